@@ -120,6 +120,8 @@ typedef enum spec_attn_kernel_variant {
 #define SPEC_ATTN_DEV_BAD_SEQ_LEN   0x2u  /* seq_len > max_seq_len or table capacity, or < W_r */
 #define SPEC_ATTN_DEV_BAD_WINDOW    0x4u  /* W_r < 0, W_r > max_w, or rows past total_q_rows */
 #define SPEC_ATTN_DEV_WAIT_TIMEOUT  0x8u  /* a pipeline wait gave up (bounded spin) */
+#define SPEC_ATTN_DEV_OUT_OF_PAGES  0x10u /* spec_attn_build_tables: fewer free pages than the step needs */
+#define SPEC_ATTN_DEV_BAD_FREE_LIST 0x20u /* spec_attn_build_tables: free and held pages exceed the pool */
 
 /* Limits of the library. */
 #define SPEC_ATTN_MAX_W 16
@@ -432,6 +434,149 @@ int spec_attn_run_noalloc(const spec_attn_plan* plan, const void* q, const void*
  * counterpart on the pages: it completes the no-alloc entry point.
  */
 int spec_attn_noalloc_check_device_status(spec_attn_stream_t stream, uint32_t* bits);
+
+/*
+ * Step tables.  spec_attn_build_tables makes, on the GPU and from the
+ * requests' lengths alone, everything the other entry points take: seq_lens,
+ * q_indptr, the grown block table, and each row's position and cache slot.  A
+ * verify step's accepted lengths are known on the GPU only; with this call no
+ * step needs them on the host.
+ *
+ * Request r has prev_seq_lens[r] keys' worth of pages in its block-table row,
+ * held_r = ceil(prev_seq_lens[r] / page_size), of which ctx_lens[r] keys are
+ * kept (ctx_lens[r] <= prev_seq_lens[r]: a rejected tail is dropped), and
+ * brings window_lens[r] new rows:
+ *   seq_lens[r] = ctx_lens[r] + window_lens[r],  need_r = ceil(seq_lens[r] / page_size)
+ *   q_indptr    = exclusive sum of window_lens, q_indptr[P] the total
+ *   row i of request r (row q_indptr[r] + i): position ctx_lens[r] + i and
+ *   slot = page * page_size + position % page_size, page its table entry.
+ * A request with ctx 0 and window 0 ends (its pages go back); one with
+ * prev_seq_lens 0 joins.  Rows from q_indptr[P] to max_rows (a padded batch)
+ * get position 0 and slot -1, which spec_attn_norm_rope_append skips.
+ *
+ * Pages.  free_pages[0 .. free_count) is a stack of free page ids.  Pages past
+ * need_r go back on top of it, in request and then table order; requests that
+ * grow then take from its top, in the same order, into their table entries
+ * held_r .. need_r - 1.  Other table entries, and stack entries outside the
+ * new part, are left as they were, so a call repeated on the same
+ * inputs writes the same values.  A page belongs to one request or to the
+ * stack, never to two (pages shared between requests are not counted).
+ *
+ * seq_lens may be prev_seq_lens or ctx_lens, and free_count may be
+ * prev_free_count (the state of a decode loop updated in place: captured once
+ * and replayed every step); no other buffer may overlap another.
+ *
+ * Device-side checks: a window below 0 or above max_w, more than max_rows rows
+ * in all (SPEC_ATTN_DEV_BAD_WINDOW); a length below 0, above max_seq_len or the
+ * table row's capacity, or ctx above prev (SPEC_ATTN_DEV_BAD_SEQ_LEN); free and
+ * held pages that exceed the pool (SPEC_ATTN_DEV_BAD_FREE_LIST); too few free
+ * pages (SPEC_ATTN_DEV_OUT_OF_PAGES).  After any of them the step is empty:
+ * q_indptr is all zero, every slot -1, every position 0, seq_lens and
+ * free_count equal their previous values, table and stack are untouched, so
+ * later calls of the step do nothing and the caller may try again.  A page id
+ * outside [0, num_pages) sets SPEC_ATTN_DEV_BAD_PAGE and gives its rows slot -1.
+ *
+ * workspace: 256 bytes, 256-byte aligned, zeroed once (spec_attn_reset_device_
+ * status); it may be a spec_attn_run workspace used on the same stream.  Calls
+ * that may overlap on the GPU need workspaces of their own.  Asynchronous on
+ * `stream`, one kernel, allocation-free, graph capturable.
+ */
+#define SPEC_ATTN_TABLES_MAX_REQS 16384
+typedef struct spec_attn_tables_problem {
+    int32_t num_reqs;            /* P: 0 .. SPEC_ATTN_TABLES_MAX_REQS */
+    int32_t max_rows;            /* entries of positions and slot_map */
+    int32_t page_size;           /* 16, 32 or 64 */
+    int32_t num_pages;           /* pages of the pool and entries of free_pages */
+    int32_t block_table_stride;  /* entries per block-table row */
+    int32_t max_w;               /* upper bound on every window, >= 1 (prompts may be long) */
+    int64_t max_seq_len;         /* upper bound on every seq_len, at most 2^31 - 1 */
+} spec_attn_tables_problem;
+
+int spec_attn_build_tables(const spec_attn_tables_problem* problem, const int32_t* ctx_lens,
+                           const int32_t* window_lens, const int32_t* prev_seq_lens,
+                           const int32_t* prev_free_count, int32_t* free_pages, int32_t* block_table,
+                           int32_t* seq_lens, int32_t* q_indptr, int32_t* free_count, int32_t* positions,
+                           int64_t* slot_map, void* workspace, size_t workspace_bytes,
+                           spec_attn_stream_t stream);
+
+/*
+ * Norm and rotation of q and k in one pass.  For each row and head with
+ * elements x_0 .. x_{d-1} (bf16, arithmetic in fp32):
+ *   y_e = x_e * w_e / sqrt(mean_e x_e^2 + eps)     (without weights: y = x)
+ *   (a, b) -> (a cos t - b sin t, a sin t + b cos t)   for each rotated pair,
+ *   t = positions[axis_j][row] * inv_freq_j,  cos and sin times rot_scale,
+ * written as bf16, rounded once.  Pair j < rot_dim / 2 is elements
+ * (j, j + rot_dim / 2), or (2 j, 2 j + 1) with interleaved = 1; elements from
+ * rot_dim on are not rotated.  Positions with several axes (time, height and
+ * width of an image or a video) give each pair the axis h_pair_axis names.
+ * The angle is reduced exactly: t in turns is a 64-bit fraction times the
+ * position, modulo one turn, so far positions lose nothing (the fp32 product
+ * would be off by up to 2^-24 of the whole angle).
+ *
+ * The plan holds the frequencies; it is a host object, reusable for any rows
+ * and layers.  The device current at its creation is the one it targets.
+ */
+typedef struct spec_attn_norm_rope_problem {
+    int32_t num_q_heads;         /* Hq >= 0 */
+    int32_t num_kv_heads;        /* Hkv >= 0; Hq + Hkv >= 1, each at most 4096 */
+    int32_t head_dim;            /* 64, 128 or 256 */
+    int32_t rot_dim;             /* rotated elements: 0 .. head_dim, a multiple of 16 */
+    int32_t interleaved;         /* pairs (2 j, 2 j + 1) instead of (j, j + rot_dim / 2) */
+    int32_t num_axes;            /* position axes, 1 .. 4 */
+    float eps;                   /* of the norm, >= 0 */
+    float rot_scale;             /* factor of cos and sin; 0 selects 1 */
+    int64_t q_row_stride;        /* elements from a row of q (k, v) to the next; 0 = dense; else a */
+    int64_t k_row_stride;        /* multiple of 8 and at least the dense row (the heads of a row */
+    int64_t v_row_stride;        /* are adjacent), e.g. views of one fused projection's output */
+    int64_t q_out_row_stride;    /* likewise for the outputs */
+    int64_t k_out_row_stride;
+    int32_t kv_dtype;            /* spec_attn_norm_rope_append only: spec_attn_kv_dtype, */
+    int32_t page_size;           /* 16, 32 or 64 (0: the plan has no cache), */
+    int32_t num_pages;           /* pages of each pool, */
+    int32_t reserved;            /* 0 */
+    int64_t kv_page_stride;      /* and page strides in bytes, as spec_attn_problem */
+    int64_t scale_page_stride;
+} spec_attn_norm_rope_problem;
+
+typedef struct spec_attn_norm_rope_plan spec_attn_norm_rope_plan;   /* opaque */
+
+/* h_inv_freq [rot_dim / 2]: radians per position, finite and >= 0, below 2^20;
+ * h_pair_axis [rot_dim / 2]: axis of each pair, below num_axes (NULL: axis 0).
+ * Host only; both are copied. */
+int spec_attn_norm_rope_plan_create(const spec_attn_norm_rope_problem* problem, const double* h_inv_freq,
+                                    const uint8_t* h_pair_axis, spec_attn_norm_rope_plan** out);
+int spec_attn_norm_rope_plan_destroy(spec_attn_norm_rope_plan* plan);
+
+/*
+ * q [num_rows, Hq, d], k [num_rows, Hkv, d] -> q_out, k_out of the same shapes,
+ * rows at the plan's strides, all 16-byte aligned.  q_weight, k_weight [d] fp32
+ * or NULL (no norm of q, of k); positions [num_axes, num_rows] int32 (any
+ * value).  q_out may be q, and k_out k, at equal strides; otherwise outputs
+ * overlap no input.  Asynchronous on `stream`, allocation-free, graph
+ * capturable.
+ */
+int spec_attn_norm_rope(const spec_attn_norm_rope_plan* plan, int32_t num_rows, const void* q, const void* k,
+                        const float* q_weight, const float* k_weight, const int32_t* positions, void* q_out,
+                        void* k_out, spec_attn_stream_t stream);
+
+/*
+ * The same pass with K and V going straight into the paged cache: row i's key
+ * heads (normalised, rotated, rounded to bf16) and value heads (v [num_rows,
+ * Hkv, d], unchanged) are written at slot slot_map[i] = page * page_size + slot
+ * within the page -- any number of rows, windows and prompts alike.  The cache
+ * bytes equal spec_attn_norm_rope followed by spec_attn_append_kv (NVFP4
+ * caches are quantised by the same rule from the bf16 values).  A row whose
+ * slot is negative is skipped whole: neither q_out nor the cache is written
+ * for it.  A slot at or past num_pages * page_size sets
+ * SPEC_ATTN_DEV_BAD_PAGE and skips the row.  Rows must have distinct slots.
+ * Pools, scales and decode scales as spec_attn_append_kv; workspace: 256 bytes
+ * holding the device-status word.
+ */
+int spec_attn_norm_rope_append(const spec_attn_norm_rope_plan* plan, int32_t num_rows, const void* q,
+                               const void* k, const void* v, const float* q_weight, const float* k_weight,
+                               const int32_t* positions, const int64_t* slot_map, void* q_out, void* k_pool,
+                               void* v_pool, void* k_scales, void* v_scales, float k_gscale, float v_gscale,
+                               void* workspace, size_t workspace_bytes, spec_attn_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -34,6 +34,7 @@ SPEC_ATTN_MASK_CAUSAL_IN_BLOCK = 0
 SPEC_ATTN_MASK_NON_CAUSAL = 1
 SPEC_ATTN_KV_BF16 = 0
 SPEC_ATTN_KV_NVFP4 = 1
+SPEC_ATTN_MAX_W = 16
 SPEC_ATTN_VARIANT_AUTO = 0
 SPEC_ATTN_VARIANT_CUDA_CORE = 1
 SPEC_ATTN_VARIANT_TCGEN05 = 2
@@ -42,6 +43,8 @@ SPEC_ATTN_DEV_BAD_PAGE = 0x1
 SPEC_ATTN_DEV_BAD_SEQ_LEN = 0x2
 SPEC_ATTN_DEV_BAD_WINDOW = 0x4
 SPEC_ATTN_DEV_WAIT_TIMEOUT = 0x8
+SPEC_ATTN_DEV_OUT_OF_PAGES = 0x10
+SPEC_ATTN_DEV_BAD_FREE_LIST = 0x20
 
 # every symbol include/spec_attn.h declares
 EXPORTED_SYMBOLS = (
@@ -50,7 +53,9 @@ EXPORTED_SYMBOLS = (
     "spec_attn_reset_device_status", "spec_attn_check_device_status",
     "spec_attn_status_string", "spec_attn_last_cuda_error", "spec_attn_version",
     "spec_attn_run_noalloc", "spec_attn_noalloc_check_device_status", "spec_attn_append_kv",
-    "spec_attn_run_append", "spec_attn_run_dense_block",
+    "spec_attn_run_append", "spec_attn_run_dense_block", "spec_attn_build_tables",
+    "spec_attn_norm_rope_plan_create", "spec_attn_norm_rope_plan_destroy", "spec_attn_norm_rope",
+    "spec_attn_norm_rope_append",
 )
 
 
@@ -84,6 +89,26 @@ class spec_attn_plan_info(ctypes.Structure):
         ("block_threads", ctypes.c_int32), ("smem_bytes", ctypes.c_int32),
         ("uses_merge", ctypes.c_int32), ("num_sms", ctypes.c_int32),
         ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class spec_attn_tables_problem(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("max_rows", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("block_table_stride", ctypes.c_int32), ("max_w", ctypes.c_int32),
+        ("max_seq_len", ctypes.c_int64),
+    ]
+
+
+class spec_attn_norm_rope_problem(ctypes.Structure):
+    _fields_ = [
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("rot_scale", ctypes.c_float), ("q_row_stride", ctypes.c_int64),
+        ("k_row_stride", ctypes.c_int64), ("v_row_stride", ctypes.c_int64), ("q_out_row_stride", ctypes.c_int64),
+        ("k_out_row_stride", ctypes.c_int64), ("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("reserved", ctypes.c_int32), ("kv_page_stride", ctypes.c_int64),
+        ("scale_page_stride", ctypes.c_int64),
     ]
 
 
@@ -139,6 +164,17 @@ def load_library(path: Optional[str] = None):
         lib.spec_attn_run_append.argtypes = [vp, vp, vp, vp] + cache_args + [vp, vp, vp, sz, vp]
         lib.spec_attn_run_dense_block.restype = i32
         lib.spec_attn_run_dense_block.argtypes = [vp] * 13 + [sz, vp]
+        lib.spec_attn_build_tables.restype = i32
+        lib.spec_attn_build_tables.argtypes = [ctypes.POINTER(spec_attn_tables_problem)] + [vp] * 12 + [sz, vp]
+        lib.spec_attn_norm_rope_plan_create.restype = i32
+        lib.spec_attn_norm_rope_plan_create.argtypes = [ctypes.POINTER(spec_attn_norm_rope_problem), vp, vp,
+                                                        ctypes.POINTER(vp)]
+        lib.spec_attn_norm_rope_plan_destroy.restype = i32
+        lib.spec_attn_norm_rope_plan_destroy.argtypes = [vp]
+        lib.spec_attn_norm_rope.restype = i32
+        lib.spec_attn_norm_rope.argtypes = [vp, i32] + [vp] * 8
+        lib.spec_attn_norm_rope_append.restype = i32
+        lib.spec_attn_norm_rope_append.argtypes = ([vp, i32] + [vp] * 12 + [ctypes.c_float, ctypes.c_float, vp, sz, vp])
         if path is None:
             _lib = lib
         return lib
@@ -384,6 +420,202 @@ def spec_attn_version() -> int:
 
 def spec_attn_last_cuda_error() -> int:
     return load_library().spec_attn_last_cuda_error()
+
+
+# --------------------------------------------------------------------------- #
+# Around the attention call: step tables, norm and rotation of q and k
+# --------------------------------------------------------------------------- #
+def _here():
+    """The current device and the handle of its current stream."""
+    import torch
+    dev = torch.cuda.current_device()
+    return dev, torch.cuda.current_stream(dev).cuda_stream
+
+
+def _bad(t, what, dtype, shape, dev):
+    """Say what is wrong with a tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on the current device, cuda:{dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have the shape {shape}, got {tuple(t.shape)}")
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _dense(t, what, dtype, shape, dev):
+    """Address of a contiguous tensor of this type and shape on the device (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _bad(t, what, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _rows(t, what, shape, row_stride, dev, dtype):
+    """Address of bf16 rows of heads [n, h, d], ``row_stride`` elements apart (0: dense)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _bad(t, what, dtype, shape, dev)
+    n, h, d = shape
+    st = t.stride()
+    if n and h and ((h > 1 and st[1] != d) or st[2] != 1 or (n > 1 and st[0] != (row_stride or h * d))):
+        raise ValueError(f"{what} must have its heads adjacent and rows {row_stride or h * d} elements apart, "
+                         f"got strides {st}")
+    return t.data_ptr()
+
+
+def spec_attn_build_tables(ctx_lens, window_lens, prev_seq_lens, prev_free_count, free_pages, block_table, seq_lens,
+                           q_indptr, free_count, positions, slot_map, workspace, *, page_size=16, max_w=SPEC_ATTN_MAX_W,
+                           max_seq_len, stream=None):
+    """seq_lens, q_indptr, the grown block table and every row's position and
+    cache slot from the requests' lengths (asynchronous).  seq_lens may be
+    prev_seq_lens or ctx_lens, free_count may be prev_free_count."""
+    import torch
+    i32 = torch.int32
+    P, rows, pages = ctx_lens.shape[0], slot_map.shape[0], free_pages.shape[0]
+    dev, cur = _here()
+    prob = spec_attn_tables_problem(P, rows, page_size, pages, block_table.shape[1], max_w, max_seq_len)
+    _check(load_library().spec_attn_build_tables(
+        ctypes.byref(prob), _dense(ctx_lens, "ctx_lens", i32, (P,), dev),
+        _dense(window_lens, "window_lens", i32, (P,), dev), _dense(prev_seq_lens, "prev_seq_lens", i32, (P,), dev),
+        _dense(prev_free_count, "prev_free_count", i32, (1,), dev), _dense(free_pages, "free_pages", i32, (pages,), dev),
+        _dense(block_table, "block_table", i32, (P, block_table.shape[1]), dev),
+        _dense(seq_lens, "seq_lens", i32, (P,), dev), _dense(q_indptr, "q_indptr", i32, (P + 1,), dev),
+        _dense(free_count, "free_count", i32, (1,), dev), _dense(positions, "positions", i32, (rows,), dev),
+        _dense(slot_map, "slot_map", torch.int64, (rows,), dev),
+        _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
+        cur if stream is None else stream.cuda_stream), "spec_attn_build_tables")
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0):
+    """The usual frequencies of rot_dim rotated elements: base^(-2 j / rot_dim)."""
+    return [base ** (-2.0 * j / rot_dim) for j in range(rot_dim // 2)]
+
+
+def rope_pair_axis(sections, interleaved: bool = False):
+    """Axis of each rotated pair for ``sections`` pairs per axis: axis by axis,
+    or (interleaved) the axes in turn while they have pairs left."""
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] -= 1
+    return out
+
+
+class NormRopePlan:
+    """Owns a spec_attn_norm_rope_plan* (destroyed with this object)."""
+
+    def __init__(self, handle, problem):
+        self._lib = load_library()
+        self.handle = handle
+        self.problem = problem
+        p = problem
+        self.q_heads, self.kv_heads, self.head_dim, self.axes = (p.num_q_heads, p.num_kv_heads, p.head_dim, p.num_axes)
+        self.strides = (p.q_row_stride, p.k_row_stride, p.v_row_stride, p.q_out_row_stride, p.k_out_row_stride)
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h is not None:
+            try:
+                self._lib.spec_attn_norm_rope_plan_destroy(h)
+            except Exception:
+                pass
+
+
+def spec_attn_norm_rope_plan_create(*, num_q_heads, num_kv_heads, head_dim, inv_freq, rot_dim=None, pair_axis=None,
+                                    num_axes=1, interleaved=0, eps=1e-6, rot_scale=1.0, q_row_stride=0,
+                                    k_row_stride=0, v_row_stride=0, q_out_row_stride=0, k_out_row_stride=0,
+                                    kv_dtype=0, page_size=0, num_pages=0, kv_page_stride=0,
+                                    scale_page_stride=0) -> NormRopePlan:
+    """``inv_freq``: rot_dim / 2 radians per position (a host sequence, doubles);
+    ``pair_axis``: the position axis of each pair.  ``page_size`` and
+    ``num_pages`` describe the cache that spec_attn_norm_rope_append writes."""
+    rot_dim = head_dim if rot_dim is None else rot_dim
+    freq = [float(x) for x in inv_freq]
+    axis = None if pair_axis is None else [int(a) for a in pair_axis]
+    if len(freq) != rot_dim // 2 or (axis is not None and len(axis) != rot_dim // 2):
+        raise ValueError(f"inv_freq and pair_axis must have rot_dim / 2 = {rot_dim // 2} entries")
+    if axis is not None and any(a < 0 or a > 255 for a in axis):
+        raise ValueError("pair_axis entries must be position axes")
+    prob = spec_attn_norm_rope_problem(
+        num_q_heads, num_kv_heads, head_dim, rot_dim, int(interleaved), num_axes, float(eps), float(rot_scale),
+        q_row_stride, k_row_stride, v_row_stride, q_out_row_stride, k_out_row_stride, kv_dtype, page_size, num_pages,
+        0, kv_page_stride, scale_page_stride)
+    handle = ctypes.c_void_p()
+    _check(load_library().spec_attn_norm_rope_plan_create(
+        ctypes.byref(prob), (ctypes.c_double * max(1, len(freq)))(*freq),
+        None if axis is None else (ctypes.c_uint8 * max(1, len(axis)))(*axis), ctypes.byref(handle)),
+        "spec_attn_norm_rope_plan_create")
+    return NormRopePlan(handle, prob)
+
+
+def _norm_rope_args(plan, q, k, q_weight, k_weight, positions, dev):
+    import torch
+    n = k.shape[0] if q is None else q.shape[0]
+    d, st = plan.head_dim, plan.strides
+    return n, [plan.handle, n, _rows(q, "q", (n, plan.q_heads, d), st[0], dev, torch.bfloat16),
+               _rows(k, "k", (n, plan.kv_heads, d), st[1], dev, torch.bfloat16)], \
+        [_dense(q_weight, "q_weight", torch.float32, (d,), dev), _dense(k_weight, "k_weight", torch.float32, (d,), dev),
+         _dense(positions, "positions", torch.int32, (plan.axes, n), dev)]
+
+
+def spec_attn_norm_rope(plan: NormRopePlan, q, k, q_weight, k_weight, positions, q_out, k_out, stream=None):
+    """Norm and rotation of q [n, Hq, d] and k [n, Hkv, d] (asynchronous).
+    ``positions`` [num_axes, n] int32; weights [d] fp32 or None (no norm);
+    the outputs may be the inputs."""
+    import torch
+    dev, cur = _here()
+    n, rows, rest = _norm_rope_args(plan, q, k, q_weight, k_weight, positions, dev)
+    _check(load_library().spec_attn_norm_rope(
+        *rows, *rest, _rows(q_out, "q_out", (n, plan.q_heads, plan.head_dim), plan.strides[3], dev, torch.bfloat16),
+        _rows(k_out, "k_out", (n, plan.kv_heads, plan.head_dim), plan.strides[4], dev, torch.bfloat16),
+        cur if stream is None else stream.cuda_stream), "spec_attn_norm_rope")
+
+
+def _pool(t, what, shape, page_stride, itemsize, dev, dtype):
+    """Address of a pool, dense or with the plan's page stride in bytes."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _bad(t, what, dtype, shape, dev)
+    if page_stride:
+        if shape[0] > 1 and t.stride(0) * itemsize != page_stride or not t[0].is_contiguous():
+            raise ValueError(f"{what} must have dense pages {page_stride} bytes apart")
+    elif not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def spec_attn_norm_rope_append(plan: NormRopePlan, q, k, v, q_weight, k_weight, positions, slot_map, q_out, k_pool,
+                               v_pool, workspace, k_scales=None, v_scales=None, k_gscale=1.0, v_gscale=1.0,
+                               stream=None):
+    """spec_attn_norm_rope with K and V written into the cache slots that
+    ``slot_map`` [n] int64 names (asynchronous); rows with a negative slot are skipped."""
+    import torch
+    dev, cur = _here()
+    p, d, hkv = plan.problem, plan.head_dim, plan.kv_heads
+    n, rows, rest = _norm_rope_args(plan, q, k, q_weight, k_weight, positions, dev)
+    fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4
+    page, kind, size = (p.num_pages, hkv, p.page_size), torch.uint8 if fp4 else torch.bfloat16, 1 if fp4 else 2
+    row = (d // 2 if fp4 else d,)
+    _check(load_library().spec_attn_norm_rope_append(
+        *rows, _rows(v, "v", (n, hkv, d), plan.strides[2], dev, torch.bfloat16), *rest,
+        _dense(slot_map, "slot_map", torch.int64, (n,), dev),
+        _rows(q_out, "q_out", (n, plan.q_heads, d), plan.strides[3], dev, torch.bfloat16),
+        _pool(k_pool, "k_pool", page + row, p.kv_page_stride, size, dev, kind),
+        _pool(v_pool, "v_pool", page + row, p.kv_page_stride, size, dev, kind),
+        _pool(k_scales, "k_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
+        _pool(v_scales, "v_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
+        k_gscale, v_gscale, _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
+        cur if stream is None else stream.cuda_stream), "spec_attn_norm_rope_append")
 
 
 # --------------------------------------------------------------------------- #

@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "nvfp4_quant.cuh"
 #include "sm100.cuh"
 
 namespace spec_attn {
@@ -45,32 +46,6 @@ __device__ __forceinline__ uint4 ld_global_nc_v4(const void* p) {
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
-}
-
-__device__ __forceinline__ void st_global_v2(void* p, uint32_t a, uint32_t b) {
-    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(a), "r"(b) : "memory");
-}
-
-// binary32 -> E4M3 byte, nearest even, saturating at +-448.
-__device__ __forceinline__ uint32_t e4m3_rn_sat(float x) {
-    unsigned short d;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(x), "f"(x));
-    return d & 0xFFu;
-}
-
-// Four pairs (t[2k] even element, t[2k+1] odd) -> four E2M1 code bytes, the
-// even element in each low nibble; nearest even, saturating at +-6.
-__device__ __forceinline__ uint32_t e2m1x8_rn_sat(const float (&t)[8]) {
-    uint32_t d;
-    asm("{ .reg .b8 c0, c1, c2, c3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c0, %2, %1;\n\t"   // first operand -> high nibble
-        "cvt.rn.satfinite.e2m1x2.f32 c1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c3, %8, %7;\n\t"
-        "mov.b32 %0, {c0, c1, c2, c3}; }"
-        : "=r"(d)
-        : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
-    return d;
 }
 
 template <int D, bool FP4>
@@ -112,29 +87,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv_kernel(const AppendP
                              (size_t)page * p.kv_page_stride + slot * (D * 2) + piece * (kUnit * 2);
         sm100::st_global_v4(dst, a);
     } else {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        float x[16];
-        float amax = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[2 * k] = __uint_as_float(w[k] << 16);
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-            amax = fmaxf(amax, fmaxf(fabsf(x[2 * k]), fabsf(x[2 * k + 1])));
-        }
-        const float g = is_v ? p.v_gscale : p.k_gscale;
-        const uint32_t sb = e4m3_rn_sat(__fdiv_rn(amax, __fmul_rn(6.0f, g)));
-        const float den = __fmul_rn(e4m3_to_float(sb), g);
-        uint32_t c0 = 0u, c1 = 0u;
-        if (den != 0.f) {
-            float t0[8], t1[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                t0[e] = __fdiv_rn(x[e], den);
-                t1[e] = __fdiv_rn(x[8 + e], den);
-            }
-            c0 = e2m1x8_rn_sat(t0);
-            c1 = e2m1x8_rn_sat(t1);
-        }
+        uint32_t c0, c1, sb;
+        nvfp4_block(a, b, is_v ? p.v_gscale : p.k_gscale, c0, c1, sb);
         uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_pool : p.k_pool) + (size_t)page * p.kv_page_stride +
                          slot * (D / 2) + piece * 8;
         uint8_t* scales = (is_v ? p.v_scales : p.k_scales) + (size_t)page * p.scale_page_stride + slot * (D / 16) +

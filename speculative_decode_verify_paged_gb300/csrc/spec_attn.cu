@@ -669,6 +669,8 @@ static int run_impl(const spec_attn_plan* plan, const void* q, const void* k_poo
 }  // extern "C"
 
 namespace spec_attn {
+int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
 int run_clearing_status(const spec_attn_plan* plan, const void* q, const void* k_pool, const void* v_pool,
                         const void* k_scales, const void* v_scales, float k_gscale, float v_gscale,
                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_indptr, void* o,

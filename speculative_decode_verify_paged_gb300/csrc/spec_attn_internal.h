@@ -145,6 +145,11 @@ constexpr unsigned int kDevBadPage = 0x1u;
 constexpr unsigned int kDevBadSeqLen = 0x2u;
 constexpr unsigned int kDevBadWindow = 0x4u;
 constexpr unsigned int kDevWaitTimeout = 0x8u;
+constexpr unsigned int kDevOutOfPages = 0x10u;
+constexpr unsigned int kDevBadFreeList = 0x20u;
+
+// Remember a CUDA error for spec_attn_last_cuda_error; returns SPEC_ATTN_E_CUDA.
+int record_cuda_error(cudaError_t e);
 
 // ---- CUDA-core split-KV kernel (split_attn_cc.cu) ----
 struct CcConfig {
@@ -198,5 +203,70 @@ int run_clearing_status(const ::spec_attn_plan* plan, const void* q, const void*
 // Always a programmatic dependent of the previous kernel in the stream (the
 // kernel waits on griddepcontrol before its first global access).
 cudaError_t append_launch(const AppendParams& p, int kv_dtype, cudaStream_t stream);
+
+// ---- step tables (step_tables.cu) ----
+struct TablesParams {
+    const int32_t* ctx_lens;        // [P]
+    const int32_t* window_lens;     // [P]
+    const int32_t* prev_seq_lens;   // [P]
+    const int32_t* prev_free_count; // [1]
+    int32_t* free_pages;            // [num_pages], a stack
+    int32_t* block_table;           // [P, bt_stride]
+    int32_t* seq_lens;              // [P]
+    int32_t* q_indptr;              // [P + 1]
+    int32_t* free_count;            // [1]
+    int32_t* positions;             // [max_rows]
+    long long* slot_map;            // [max_rows]
+    unsigned int* status;           // word 0: sticky status; word 1: the grid's ticket (0 between calls)
+    int num_reqs;
+    int max_rows;
+    int page_shift;                 // log2(page_size)
+    int num_pages;
+    int bt_stride;
+    int max_w;
+    long long max_seq_len;
+    int in_place;                   // seq_lens or free_count overwrite an input: the last CTA writes them
+};
+cudaError_t tables_launch(const TablesParams& p, cudaStream_t stream);
+
+// ---- norm and rotation of q and k, and the same into the cache (norm_rope.cu) ----
+constexpr int kMaxPairs = 128;      // rotated pairs of a head (head_dim <= 256)
+struct NormRopeParams {
+    const uint16_t* q;              // rows q_row_stride elements apart, heads adjacent, bf16 bits
+    const uint16_t* k;
+    const uint16_t* v;              // append only
+    const float* q_weight;          // [d] or nullptr (no norm)
+    const float* k_weight;
+    const int32_t* positions;       // [num_axes][pos_stride]
+    const long long* slot_map;      // append only: [num_rows]
+    uint16_t* q_out;
+    uint16_t* k_out;                // without append
+    unsigned char* k_pool;          // append only, as AppendParams
+    unsigned char* v_pool;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    float k_gscale;
+    float v_gscale;
+    unsigned int* status;           // append only
+    long long q_row_stride, k_row_stride, v_row_stride, q_out_row_stride, k_out_row_stride;   // elements
+    long long pos_stride;
+    long long num_slots;            // num_pages * page_size
+    long long kv_page_stride, scale_page_stride;   // bytes
+    int page_shift;                 // log2(page_size)
+    int num_rows;
+    int num_q_heads;
+    int num_kv_heads;
+    int rot_dim;
+    int interleaved;
+    float eps;
+    float rot_scale;
+    int iters_q, iters_k, iters_v;  // warp iterations of one row (set at launch)
+    int segs;                       // warps a row is cut into
+    int iters_per_seg;
+    unsigned long long turns[kMaxPairs];   // angle per position, in 2^-64 turns
+    uint8_t axis[kMaxPairs];               // position axis of each pair
+};
+cudaError_t norm_rope_launch(NormRopeParams& p, int head_dim, bool append, int kv_dtype, int num_sms,
+                             cudaStream_t stream);
 
 }  // namespace spec_attn
