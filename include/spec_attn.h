@@ -578,6 +578,59 @@ int spec_attn_norm_rope_append(const spec_attn_norm_rope_plan* plan, int32_t num
                                void* v_pool, void* k_scales, void* v_scales, float k_gscale, float v_gscale,
                                void* workspace, size_t workspace_bytes, spec_attn_stream_t stream);
 
+/*
+ * Cross attention: query rows of any number (a verify window, one token, a
+ * whole prompt) attend to an encoder's states of another length.  Request r's
+ * rows q_indptr[r] .. q_indptr[r+1]-1 see the kv_len[r] state rows from
+ * kv_start[r] on, all of them:
+ *   s_j = sm_scale * <q, k_j>,  O = sum_j softmax(s)_j v_j,  LSE natural log
+ * with fp32 accumulation, O bf16, LSE fp32.  kv_len[r] = 0 gives O = 0 and
+ * LSE = -infinity.  K and V are dense rows [total_kv_rows, Hkv, head_dim] bf16
+ * (not the paged cache: an encoder's states are written once and do not
+ * grow), kv_row_stride elements apart, so that a fused projection's [rows, 2,
+ * Hkv, head_dim] is taken as it is; packed states, a padded batch and states
+ * shared by several requests are all ranges of rows.  Rows outside every range
+ * may hold anything.
+ *
+ * Device-side checks: a window below 0 or above max_q_rows, or rows past
+ * total_q_rows (SPEC_ATTN_DEV_BAD_WINDOW); a range not inside the state rows, or
+ * longer than max_kv_len (SPEC_ATTN_DEV_BAD_SEQ_LEN): such a request is skipped,
+ * its rows left as they were, like rows of no request.
+ */
+typedef struct spec_attn_cross_problem {
+    int32_t num_reqs;            /* P, 0 .. 65535 */
+    int32_t total_q_rows;        /* rows of Q and O */
+    int32_t max_q_rows;          /* upper bound on a request's rows, >= 1 */
+    int32_t num_q_heads;         /* Hq */
+    int32_t num_kv_heads;        /* Hkv; Hq % Hkv == 0, Hq / Hkv <= 16 */
+    int32_t head_dim;            /* 64, 128 or 256 */
+    int32_t total_kv_rows;       /* rows of K and V */
+    int32_t max_kv_len;          /* upper bound on every kv_len */
+    float sm_scale;              /* 0 selects 1/sqrt(head_dim) */
+    int32_t force_splits;        /* 0: the library's choice; n > 0: cut the longest range n ways */
+    int64_t kv_row_stride;       /* elements; 0 = dense; else a multiple of 8, at least the dense row */
+} spec_attn_cross_problem;
+
+typedef struct spec_attn_cross_plan spec_attn_cross_plan;   /* opaque */
+
+/* Host only; the current device is the one the plan targets.
+ * *workspace_bytes (nullable) receives what spec_attn_run_cross needs. */
+int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_attn_cross_plan** out,
+                                size_t* workspace_bytes);
+int spec_attn_cross_plan_destroy(spec_attn_cross_plan* plan);
+
+/*
+ * q [total_q_rows, Hq, d], o likewise, k and v at the plan's row stride, all
+ * bf16 and 16-byte aligned; q_indptr [P+1], kv_start [P], kv_len [P] int32;
+ * lse [total_q_rows, Hq] fp32 or NULL; workspace as for spec_attn_run
+ * (256-byte aligned, its device-status word zeroed once, not shared by runs
+ * that may overlap).  Asynchronous on `stream`, allocation-free, graph
+ * capturable.
+ */
+int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const void* k, const void* v,
+                        const int32_t* q_indptr, const int32_t* kv_start, const int32_t* kv_len, void* o,
+                        float* lse, void* workspace, size_t workspace_bytes, spec_attn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -55,7 +55,8 @@ EXPORTED_SYMBOLS = (
     "spec_attn_run_noalloc", "spec_attn_noalloc_check_device_status", "spec_attn_append_kv",
     "spec_attn_run_append", "spec_attn_run_dense_block", "spec_attn_build_tables",
     "spec_attn_norm_rope_plan_create", "spec_attn_norm_rope_plan_destroy", "spec_attn_norm_rope",
-    "spec_attn_norm_rope_append",
+    "spec_attn_norm_rope_append", "spec_attn_cross_plan_create", "spec_attn_cross_plan_destroy",
+    "spec_attn_run_cross",
 )
 
 
@@ -109,6 +110,15 @@ class spec_attn_norm_rope_problem(ctypes.Structure):
         ("k_out_row_stride", ctypes.c_int64), ("kv_dtype", ctypes.c_int32), ("page_size", ctypes.c_int32),
         ("num_pages", ctypes.c_int32), ("reserved", ctypes.c_int32), ("kv_page_stride", ctypes.c_int64),
         ("scale_page_stride", ctypes.c_int64),
+    ]
+
+
+class spec_attn_cross_problem(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("total_q_rows", ctypes.c_int32), ("max_q_rows", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("total_kv_rows", ctypes.c_int32), ("max_kv_len", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+        ("force_splits", ctypes.c_int32), ("kv_row_stride", ctypes.c_int64),
     ]
 
 
@@ -175,6 +185,13 @@ def load_library(path: Optional[str] = None):
         lib.spec_attn_norm_rope.argtypes = [vp, i32] + [vp] * 8
         lib.spec_attn_norm_rope_append.restype = i32
         lib.spec_attn_norm_rope_append.argtypes = ([vp, i32] + [vp] * 12 + [ctypes.c_float, ctypes.c_float, vp, sz, vp])
+        lib.spec_attn_cross_plan_create.restype = i32
+        lib.spec_attn_cross_plan_create.argtypes = [ctypes.POINTER(spec_attn_cross_problem), ctypes.POINTER(vp),
+                                                    ctypes.POINTER(sz)]
+        lib.spec_attn_cross_plan_destroy.restype = i32
+        lib.spec_attn_cross_plan_destroy.argtypes = [vp]
+        lib.spec_attn_run_cross.restype = i32
+        lib.spec_attn_run_cross.argtypes = [vp] * 10 + [sz, vp]
         if path is None:
             _lib = lib
         return lib
@@ -616,6 +633,53 @@ def spec_attn_norm_rope_append(plan: NormRopePlan, q, k, v, q_weight, k_weight, 
         _pool(v_scales, "v_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
         k_gscale, v_gscale, _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
         cur if stream is None else stream.cuda_stream), "spec_attn_norm_rope_append")
+
+
+class CrossPlan:
+    """Owns a spec_attn_cross_plan* (destroyed with this object)."""
+
+    def __init__(self, handle, workspace_bytes, problem):
+        self._lib = load_library()
+        self.handle = handle
+        self.workspace_bytes = int(workspace_bytes)
+        self.problem = problem
+        p = problem
+        self.q_shape = (p.total_q_rows, p.num_q_heads, p.head_dim)
+        self.kv_shape = (p.total_kv_rows, p.num_kv_heads, p.head_dim)
+        self.reqs, self.kv_row_stride = p.num_reqs, p.kv_row_stride
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h is not None:
+            try:
+                self._lib.spec_attn_cross_plan_destroy(h)
+            except Exception:
+                pass
+
+
+def spec_attn_cross_plan_create(*, num_reqs, total_q_rows, max_q_rows, num_q_heads, num_kv_heads, head_dim,
+                                total_kv_rows, max_kv_len, sm_scale=0.0, force_splits=0, kv_row_stride=0) -> CrossPlan:
+    prob = spec_attn_cross_problem(num_reqs, total_q_rows, max_q_rows, num_q_heads, num_kv_heads, head_dim,
+                                   total_kv_rows, max_kv_len, float(sm_scale), force_splits, kv_row_stride)
+    handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
+    _check(load_library().spec_attn_cross_plan_create(ctypes.byref(prob), ctypes.byref(handle), ctypes.byref(ws)),
+           "spec_attn_cross_plan_create")
+    return CrossPlan(handle, ws.value, prob)
+
+
+def spec_attn_run_cross(plan: CrossPlan, q, k, v, q_indptr, kv_start, kv_len, o, lse, workspace, stream=None):
+    """Attention of each request's query rows to its range of state rows
+    (asynchronous).  ``lse`` may be None."""
+    import torch
+    dev, cur = _here()
+    bf16, i32, P = torch.bfloat16, torch.int32, plan.reqs
+    _check(load_library().spec_attn_run_cross(
+        plan.handle, _dense(q, "q", bf16, plan.q_shape, dev), _rows(k, "k", plan.kv_shape, plan.kv_row_stride, dev, bf16),
+        _rows(v, "v", plan.kv_shape, plan.kv_row_stride, dev, bf16), _dense(q_indptr, "q_indptr", i32, (P + 1,), dev),
+        _dense(kv_start, "kv_start", i32, (P,), dev), _dense(kv_len, "kv_len", i32, (P,), dev),
+        _dense(o, "o", bf16, plan.q_shape, dev), _dense(lse, "lse", torch.float32, plan.q_shape[:2], dev),
+        _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
+        cur if stream is None else stream.cuda_stream), "spec_attn_run_cross")
 
 
 # --------------------------------------------------------------------------- #

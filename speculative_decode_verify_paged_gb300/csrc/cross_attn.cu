@@ -1,0 +1,706 @@
+// Cross attention of query rows to an encoder's states (spec_attn_run_cross) on
+// 5th-generation tensor cores: dense K and V rows, a range of them for each
+// request, every query row of the request seeing the whole range.
+//
+//   s_j = sm_scale <q, k_j>,  O = sum_j softmax(s)_j v_j,  LSE = ln sum_j exp(s_j)
+//
+// in one sweep with a running maximum and sum per row (base 2, fp32; P is
+// rounded to bf16 for the second product, the sum adds the unrounded weights).
+// A request with no states gets O = 0 and LSE = -inf.
+//
+// One CTA = (NQ query tiles of 128 rows) x (one KV head) x (a split of the
+// request's states).  A tile holds wt = 128 / G whole window rows with their G
+// heads, so K and V are read once for the G heads.  NQ = 2 (windows of more
+// than one tile, d <= 128): the two tiles share every K and V tile and take
+// turns on the tensor cores, one tile's products running under the other
+// tile's softmax.  NQ = 1: the S buffer is doubled instead, so that the next
+// scores are computed under this tile's softmax.
+//
+// Warp roles:
+//   warp 0      the query tiles, then K and V tiles in turn, by TMA into one ring
+//               of slots (BN rows each, 128-byte swizzled, chunk-major).
+//   warps 1, 2  issue the products, one thread each.  NQ = 2: warp 1 + i issues
+//               both products of tile i, S_{t+1} once P_t V_t has left the buffer
+//               that S and P share.  NQ = 1: warp 1 issues S = Q K^T and warp 2 O += P V.
+//   warp 3      owns tensor memory.
+//   warps 4-7 (and 8-11 for the second tile)   softmax, a row a thread, and the
+//               epilogue.  In the last tile they also zero the V rows past the range's
+//               end (what lies there may be anything, and 0 x NaN is NaN).
+//
+// TMEM columns: O tiles [0, NQ d), two S buffers of BN columns after them, P
+// (bf16 pairs) in the first half of its S buffer.
+//
+// Every wait is bounded; on time-out the CTA sets the device-status bit, drains
+// its copies and products, frees its tensor memory and leaves.
+//
+// Splits: where the tiles alone would leave SMs idle, each request's states are
+// cut into ranges of keys_per_split; a split leaves its normalised rows in fp32
+// with their log-sum-exp, and a second kernel combines them.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include "../../include/spec_attn.h"
+#include "common.cuh"
+#include "sm100.cuh"
+#include "tc_common.cuh"
+
+namespace spec_attn {
+namespace {
+
+using namespace sm100;
+using namespace tcc;
+
+constexpr int kM = 128;
+constexpr int kMaxRing = 12;
+constexpr float kCrossRescale = 8.0f;   // log2 units: O is rescaled when a row's maximum grows by more
+
+template <int D, int NQ>
+struct CrossLayout {
+    static_assert(NQ == 1 || D <= 128, "two O tiles and two S buffers fit 512 columns up to d = 128");
+    static constexpr int kBN = D == 256 ? 64 : 128;        // states a tile
+    static constexpr int kChunks = D / 64;
+    static constexpr int kQBytes = kM * D * 2;             // one query tile
+    static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
+    static constexpr int kAux = 1024;
+    static constexpr int kMax = 232448;                    // 227 KB
+    static constexpr int kFit = (kMax - 1024 - kAux - NQ * kQBytes) / kTileBytes;
+    static constexpr int kRing = kFit > kMaxRing ? kMaxRing : kFit;
+    static constexpr int kSmem = 1024 + kAux + NQ * kQBytes + kRing * kTileBytes;
+    static constexpr int kSCol = NQ * D;                   // first column of the S buffers
+    static constexpr int kNeed = NQ * D + 2 * kBN;
+    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;
+    static constexpr int kThreads = 128 + NQ * 128;
+    static_assert(kNeed <= 512, "tensor memory");
+    static_assert(kRing >= 4, "a K and a V tile ahead of the ones in use");
+};
+
+struct CrossAux {
+    uint64_t full[kMaxRing];
+    uint64_t empty[kMaxRing];
+    uint64_t q_full[2];
+    uint64_t s_full[2];     // scores written (NQ = 2: of tile i; NQ = 1: in buffer t & 1)
+    uint64_t p_full[2];     // P written over them (four softmax warps)
+    uint64_t s_empty[2];    // NQ = 1: P V of the buffer's tile done
+    uint64_t o_done[2];     // one phase a P V
+    uint64_t o_final[2];    // after the last P V of tile i
+    uint64_t drain[2];
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(CrossAux) <= 1024, "aux region");
+
+// The request's rows and states, checked.
+struct CrossReq {
+    int row0, w, start, len;
+};
+__device__ __forceinline__ bool cross_request(const CrossParams& p, int r, unsigned int* status, CrossReq& q) {
+    const int row0 = p.q_indptr[r], row1 = p.q_indptr[r + 1];
+    q.start = p.kv_start[r];
+    q.len = p.kv_len[r];
+    q.row0 = row0;
+    if (row0 < 0 || row1 < row0 || row1 > p.total_rows || row1 - row0 > p.max_rows) {
+        if (status) atomicOr(status, kDevBadWindow);
+        return false;
+    }
+    q.w = row1 - row0;
+    if (q.len < 0 || q.len > p.max_kv_len || q.start < 0 || (long long)q.start + q.len > p.total_kv) {
+        if (status) atomicOr(status, kDevBadSeqLen);
+        return false;
+    }
+    return q.w > 0;
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(CrossLayout<D, NQ>::kThreads, 1)
+cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                  const __grid_constant__ CUtensorMap tmv) {
+    using L = CrossLayout<D, NQ>;
+    constexpr int BN = L::kBN, RING = L::kRing;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
+    const int kvh = blockIdx.y, r = blockIdx.z;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                           ~static_cast<uintptr_t>(1023));
+    unsigned char* sQ = smem;
+    unsigned char* ring = smem + NQ * L::kQBytes;
+    CrossAux* aux = reinterpret_cast<CrossAux*>(ring + RING * L::kTileBytes);
+    volatile int* abort = &aux->abort;
+
+    pdl_wait_primary();
+    CrossReq q;
+    const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
+    if (!cross_request(p, r, reporter ? p.status : nullptr, q)) return;
+    const int lo = tile * NQ * p.wt;               // first window row of the CTA
+    if (lo >= q.w) return;
+    const int nsplits = max(1, (q.len + p.keys_per_split - 1) / p.keys_per_split);
+    if (split >= nsplits) return;
+    const int G = p.group;
+    const int nact = (NQ == 2 && lo + p.wt < q.w) ? 2 : 1;
+    const int key_lo = split * p.keys_per_split;
+    const int key_hi = min(key_lo + p.keys_per_split, q.len);
+    const int T = (key_hi - key_lo + BN - 1) / BN;
+    const int tail = key_hi - (key_lo + (T - 1) * BN);     // states of the last tile
+    if (T == 0) {                                  // no states
+        const int rows = min(q.w - lo, NQ * p.wt);
+        for (int u = tid; u < rows * G * (D / 8); u += L::kThreads) {
+            const int c = u % (D / 8), m = u / (D / 8);
+            const size_t at = (size_t)(q.row0 + lo + m / G) * p.num_q_heads + kvh * G + m % G;
+            st_global_v4(p.o + at * D + c * 8, make_uint4(0u, 0u, 0u, 0u));
+            if (c == 0 && p.lse) p.lse[at] = -INFINITY;
+        }
+        return;
+    }
+
+    if (tid == 0) {
+        for (int s = 0; s < RING; ++s) {
+            mbar_init(&aux->full[s], 1);
+            mbar_init(&aux->empty[s], nact);       // every tile's products have read the slot
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&aux->q_full[i], 1);
+            mbar_init(&aux->s_full[i], 1);
+            mbar_init(&aux->p_full[i], 4);
+            mbar_init(&aux->s_empty[i], 1);
+            mbar_init(&aux->o_done[i], 1);
+            mbar_init(&aux->o_final[i], 1);
+            mbar_init(&aux->drain[i], 1);
+        }
+        aux->abort = 0;
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+    }
+    if (warp == 3) tmem_alloc(&aux->tmem_base, L::kCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = aux->tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        int issued = 0;
+        if (lane == 0) {
+            const uint32_t qbytes = static_cast<uint32_t>(L::kChunks * 128 * G * p.wt);
+            for (int i = 0; i < nact; ++i) {
+                mbar_arrive_expect_tx(&aux->q_full[i], qbytes);
+                for (int c = 0; c < L::kChunks; ++c)
+                    tma_load_3d(sQ + i * L::kQBytes + c * (kM * 128), &tmq, c * 64, kvh * G, q.row0 + lo + i * p.wt,
+                                &aux->q_full[i]);
+            }
+        }
+        __syncwarp();
+        for (int n = 0; n < 2 * T; ++n) {
+            const int slot = n % RING;
+            if (n >= RING && !warp_wait(&aux->empty[slot], ((n / RING) - 1) & 1, abort)) break;
+            if (lane == 0) {
+                unsigned char* dst = ring + slot * L::kTileBytes;
+                const CUtensorMap* map = (n & 1) ? &tmv : &tmk;
+                mbar_arrive_expect_tx(&aux->full[slot], L::kTileBytes);
+                const int row = q.start + key_lo + (n >> 1) * BN;
+                for (int c = 0; c < L::kChunks; ++c)
+                    tma_load_3d(dst + c * (BN * 128), map, c * 64, kvh, row, &aux->full[slot]);
+            }
+            __syncwarp();
+            issued = n + 1;
+        }
+        if (*abort && lane == 0) {
+            drain_copies<RING>(aux->full, issued);
+            volatile int no_abort = 0;
+            for (int i = 0; i < nact; ++i) mbar_wait(&aux->q_full[i], 0, &no_abort, kDrainLimit);
+        }
+        __syncwarp();
+    } else if (warp == 1 || (warp == 2 && (NQ == 1 || nact == 2))) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(kM, BN, 0, 0);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(kM, D, 0, 1);
+            const int i = NQ == 2 ? warp - 1 : 0;
+            const uint32_t q_addr = smem_addr(sQ + i * L::kQBytes);
+            auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(bar, parity & 1, abort, kWaitLimit); };
+            auto wait_ring = [&](int n) { return wait(&aux->full[n % RING], n / RING); };
+            auto issue_s = [&](int t, int buf) {
+                tc_fence_after();
+                const int slot = (2 * t) % RING;
+                const uint32_t k_addr = smem_addr(ring + slot * L::kTileBytes);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const int c = kk >> 2, sub = kk & 3;
+                    mma_bf16_ss(tmem + L::kSCol + buf * BN, smem_desc_sw128(q_addr + c * (kM * 128) + sub * 32, 16, 1024),
+                                smem_desc_sw128(k_addr + c * (BN * 128) + sub * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&aux->empty[slot]);
+                mma_commit(&aux->s_full[buf]);
+            };
+            auto issue_pv = [&](int t, int buf) {
+                tc_fence_after();
+                const int slot = (2 * t + 1) % RING;
+                const uint32_t v_addr = smem_addr(ring + slot * L::kTileBytes);
+                const int steps = t == T - 1 ? (tail + 15) / 16 : BN / 16;
+                for (int kk = 0; kk < steps; ++kk)
+                    mma_ts(tmem + i * D, tmem + L::kSCol + buf * BN + kk * 8,
+                           smem_desc_sw128(v_addr + kk * 2048, BN * 128, 1024), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(&aux->empty[slot]);
+                if (NQ == 1) mma_commit(&aux->s_empty[buf]);
+                mma_commit(&aux->o_done[i]);
+            };
+            bool ok = true;
+            if (NQ == 2) {
+                ok = wait(&aux->q_full[i], 0) && wait_ring(0);
+                if (ok) issue_s(0, i);
+                for (int t = 0; t < T && ok; ++t) {
+                    ok = wait(&aux->p_full[i], t) && wait_ring(2 * t + 1);
+                    if (!ok) break;
+                    issue_pv(t, i);
+                    if (t + 1 < T) {
+                        ok = wait_ring(2 * t + 2) && wait(&aux->o_done[i], t);   // P_t has been read
+                        if (ok) issue_s(t + 1, i);
+                    }
+                }
+            } else if (warp == 1) {
+                ok = wait(&aux->q_full[0], 0);
+                for (int t = 0; t < T && ok; ++t) {
+                    ok = wait_ring(2 * t) && (t < 2 || wait(&aux->s_empty[t & 1], (t >> 1) - 1));
+                    if (ok) issue_s(t, t & 1);
+                }
+            } else {
+                for (int t = 0; t < T && ok; ++t) {
+                    ok = wait(&aux->p_full[t & 1], t >> 1) && wait_ring(2 * t + 1);
+                    if (ok) issue_pv(t, t & 1);
+                }
+            }
+            if (ok && (NQ == 2 || warp == 2)) mma_commit(&aux->o_final[i]);
+            // every product this thread issued completes before the memory is released
+            uint64_t* drain = &aux->drain[warp - 1];
+            mma_commit(drain);
+            volatile int no_abort = 0;
+            mbar_wait(drain, 0, &no_abort, kDrainLimit);
+        }
+        __syncwarp();
+    } else if (warp >= 4 && (warp < 8 || nact == 2)) {
+        // ------------------------------------------------------------ softmax and epilogue
+        const int i = warp >= 8 ? 1 : 0;                   // tile
+        const int m = (warp & 3) * 32 + lane;              // row of the tile
+        const uint32_t lane_tmem = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const int wrow = lo + i * p.wt + m / G;            // window row
+        const bool valid = m < p.wt * G && wrow < q.w;
+        const float sc = p.score_scale_log2;
+        float m_ref = -INFINITY, l_sum = 0.f;
+        bool ok = true;
+        for (int t = 0; t < T; ++t) {
+            const int buf = NQ == 2 ? i : t & 1;
+            if (!(ok = warp_wait(&aux->s_full[buf], (NQ == 2 ? t : t >> 1) & 1, abort))) break;
+            tc_fence_after();
+            const uint32_t s_tmem = lane_tmem + L::kSCol + buf * BN;
+            float sv[BN];
+#pragma unroll
+            for (int h = 0; h < BN / 32; ++h) tmem_ld32(s_tmem + h * 32, *reinterpret_cast<float(*)[32]>(sv + h * 32));
+            tmem_wait_ld();
+            if (t == T - 1 && tail < BN) {
+#pragma unroll
+                for (int c = 0; c < BN; ++c) sv[c] = c < tail ? sv[c] : -INFINITY;
+            }
+            float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+            for (int c = 4; c < BN; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], sv[c]);
+            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
+            // the reference moves at the first tile, and when the maximum outgrows it
+            const bool need = mx > m_ref + kCrossRescale;
+            const float ref = need ? mx : m_ref;
+            const float alpha = need ? fast_exp2(m_ref - ref) : 1.f;   // (0 at the first tile)
+            const float nref = ref == -INFINITY ? 0.f : -ref;
+            uint32_t pk[BN / 2];
+            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < BN; c += 2) {
+                const float p0 = fast_exp2(fmaf(sv[c], sc, nref)), p1 = fast_exp2(fmaf(sv[c + 1], sc, nref));
+                ps[c & 2] += p0;
+                ps[(c & 2) + 1] += p1;
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+            l_sum = l_sum * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+            m_ref = ref;
+            if (t > 0 && __any_sync(kFullMask, valid && need)) {
+                // every earlier P V has to be in (NQ = 2: S_t was issued after the last one)
+                if (NQ == 1 && !(ok = warp_wait(&aux->o_done[0], (t - 1) & 1, abort))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float ov[32];
+                    tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                    tmem_st32(lane_tmem + i * D + ch * 32, ov);
+                }
+            }
+            if (t == T - 1 && (tail & 15) != 0) {
+                // The slot's earlier tile was consumed before these scores could be made, so the parity
+                // names this phase.  Both tiles' warps write the same zeros.
+                constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
+                const int n = 2 * T - 1, rows = ((tail + 15) & ~15) - tail;
+                if (!(ok = warp_wait(&aux->full[n % RING], (n / RING) & 1, abort))) break;
+                const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kTileBytes);
+                for (int u = m; u < rows * C8; u += 128)
+                    st_shared_v4(v_addr + ((u % C8) >> 3) * (BN * 128) + (tail + u / C8) * 128 + (u & 7) * 16,
+                                 make_uint4(0u, 0u, 0u, 0u));
+                fence_proxy_async_smem();
+            }
+#pragma unroll
+            for (int h = 0; h < BN / 64; ++h)
+                tmem_st32u(s_tmem + h * 32, *reinterpret_cast<uint32_t(*)[32]>(pk + h * 32));
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux->p_full[buf]);
+        }
+        if (ok) ok = warp_wait(&aux->o_final[i], 0, abort);
+        pdl_launch_dependents();
+        tc_fence_after();
+        if (ok) {
+            const size_t at = (size_t)(q.row0 + wrow) * p.num_q_heads + kvh * G + m % G;
+            const float inv = 1.f / l_sum, lse2 = m_ref + log2f(l_sum);
+            const bool final_out = nsplits == 1;
+            const size_t part = (size_t)split * p.total_rows * p.num_q_heads + at;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float ov[32];
+                tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                tmem_wait_ld();
+                if (!valid) continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] *= inv;
+                if (final_out) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(ov[e + 2 * k], ov[e + 2 * k + 1]);
+                            w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+                        }
+                        st_global_v4(p.o + at * D + ch * 32 + e, make_uint4(w[0], w[1], w[2], w[3]));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(p.ws_o + part * D + ch * 32 + e) =
+                            make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+                }
+            }
+            if (valid) {
+                if (!final_out) p.ws_lse[part] = lse2;
+                else if (p.lse) p.lse[at] = lse2 * kLn2;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kCols);
+    }
+    if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
+}
+
+// Combine the splits: a thread takes four elements of a (row, head).
+constexpr int kCombThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kCombThreads) cross_combine_kernel(const CrossParams p) {
+    constexpr int kVec = D / 4;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    const int r = blockIdx.y;
+    CrossReq q;
+    if (!cross_request(p, r, nullptr, q)) return;
+    const int n = (q.len + p.keys_per_split - 1) / p.keys_per_split;
+    if (n <= 1) return;
+    const size_t stride = (size_t)p.total_rows * p.num_q_heads;
+    const long long units = (long long)q.w * p.num_q_heads * kVec;
+    for (long long u = (long long)blockIdx.x * kCombThreads + threadIdx.x; u < units;
+         u += (long long)gridDim.x * kCombThreads) {
+        const size_t at = (size_t)q.row0 * p.num_q_heads + u / kVec;
+        const int c = (int)(u % kVec) * 4;
+        float mx = -INFINITY;
+        for (int s = 0; s < n; ++s) mx = fmaxf(mx, p.ws_lse[s * stride + at]);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int s = 0; s < n; ++s) {
+            const float w = fast_exp2(p.ws_lse[s * stride + at] - mx);
+            const float4 o = *reinterpret_cast<const float4*>(p.ws_o + (s * stride + at) * D + c);
+            a.x = fmaf(w, o.x, a.x); a.y = fmaf(w, o.y, a.y); a.z = fmaf(w, o.z, a.z); a.w = fmaf(w, o.w, a.w);
+            sum += w;
+        }
+        const float inv = 1.f / sum;
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.x * inv, a.y * inv);
+        const __nv_bfloat162 h1 = __floats2bfloat162_rn(a.z * inv, a.w * inv);
+        *reinterpret_cast<uint2*>(p.o + at * D + c) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
+                                                                 *reinterpret_cast<const uint32_t*>(&h1));
+        if (c == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+    }
+}
+
+using CrossKernel = void (*)(const CrossParams, const CUtensorMap, const CUtensorMap, const CUtensorMap);
+
+// What a launch of (d, query tiles a CTA) needs.
+struct CrossVariant {
+    CrossKernel kernel;
+    int threads, smem, bn;
+};
+template <int D, int NQ>
+CrossVariant variant_of() {
+    using L = CrossLayout<D, NQ>;
+    return {&cross_attn_kernel<D, NQ>, L::kThreads, L::kSmem, L::kBN};
+}
+CrossVariant cross_variant(int d, int nq) {
+    switch (d) {
+        case 64: return nq == 2 ? variant_of<64, 2>() : variant_of<64, 1>();
+        case 128: return nq == 2 ? variant_of<128, 2>() : variant_of<128, 1>();
+        default: return variant_of<256, 1>();
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 cross_encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                                         &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
+    }();
+    return fn;
+}
+
+// Rows [rows, heads, d] bf16, row_stride elements apart, as (element, head, row); box = 64 elements x
+// box_heads x box_rows, 128-byte swizzle, rows past the end zero-filled.
+bool encode_rows(CUtensorMap* map, const void* t, int rows, int heads, int d, long long row_stride, int box_heads,
+                 int box_rows) {
+    auto fn = cross_encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)row_stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(t), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+}  // namespace spec_attn
+
+struct spec_attn_cross_plan {
+    spec_attn_cross_problem prob;
+    int device;
+    int num_sms;
+    int nq;
+    int wt;
+    int tiles;
+    int keys_per_split;
+    int max_splits;
+    size_t lse_off, o_off, ws_bytes;
+    float sm_scale;
+    spec_attn::CrossVariant variant;
+    // tensor maps of the last (q, k, v): a loop on the same buffers encodes them once
+    std::mutex maps_mutex;
+    CUtensorMap maps[3];
+    const void* maps_key[3] = {nullptr, nullptr, nullptr};
+};
+
+namespace {
+
+bool cross_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// States a split takes.  Model: a CTA costs a fixed start and end plus its states at its SM's share of the HBM
+// rate, waves of num_sms CTAs; splitting adds the second kernel.
+int choose_split(const spec_attn_cross_problem& p, int tiles, int bn, int num_sms) {
+    const double key_us = 4.0 * p.head_dim / (6.5e6 / num_sms), fixed_us = 3.0, combine_us = 3.0;
+    const int64_t ctas = static_cast<int64_t>(tiles) * p.num_kv_heads * p.num_reqs;
+    const int64_t units = (static_cast<int64_t>(p.max_kv_len) + bn - 1) / bn;
+    double best = 1e300;
+    int64_t best_u = units < 1 ? 1 : units;
+    for (int64_t s = 1; s <= units && s <= 64; ++s) {
+        const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
+        const int64_t waves = (ctas * splits + num_sms - 1) / num_sms;
+        const double cost = static_cast<double>(waves) * (fixed_us + static_cast<double>(u * bn) * key_us) +
+                            (splits > 1 ? combine_us : 0.0);
+        if (cost < best * 0.999) {
+            best = cost;
+            best_u = u;
+        }
+    }
+    return static_cast<int>(best_u * bn);
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_attn_cross_plan** out,
+                                size_t* workspace_bytes) {
+    if (!out) return SPEC_ATTN_E_INVALID_ARG;
+    *out = nullptr;
+    if (!problem) return SPEC_ATTN_E_INVALID_ARG;
+    const spec_attn_cross_problem& p = *problem;
+    if (p.num_reqs < 0 || p.total_q_rows < 0 || p.max_q_rows < 1 || p.num_q_heads <= 0 || p.num_kv_heads <= 0 ||
+        p.num_q_heads % p.num_kv_heads != 0 || p.head_dim <= 0 || p.total_kv_rows < 0 || p.max_kv_len < 0 ||
+        p.force_splits < 0 || !(p.sm_scale >= 0.f) || std::isinf(p.sm_scale))
+        return SPEC_ATTN_E_INVALID_ARG;
+    if (p.head_dim != 64 && p.head_dim != 128 && p.head_dim != 256) return SPEC_ATTN_E_UNSUPPORTED;
+    const int G = p.num_q_heads / p.num_kv_heads;
+    if (G > SPEC_ATTN_MAX_GROUP || p.num_reqs > 65535 || p.num_kv_heads > 65535) return SPEC_ATTN_E_UNSUPPORTED;
+    const int64_t dense = static_cast<int64_t>(p.num_kv_heads) * p.head_dim;
+    if (p.kv_row_stride != 0 && (p.kv_row_stride < dense || p.kv_row_stride % 8 != 0)) return SPEC_ATTN_E_INVALID_ARG;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return spec_attn::record_cuda_error(e);
+    spec_attn_cross_plan* plan = new (std::nothrow) spec_attn_cross_plan();
+    if (!plan) return SPEC_ATTN_E_INVALID_ARG;
+    plan->prob = p;
+    if (p.kv_row_stride == 0) plan->prob.kv_row_stride = dense;
+    plan->device = dev;
+    plan->num_sms = sms;
+    plan->sm_scale = p.sm_scale > 0.f ? p.sm_scale : 1.0f / std::sqrt(static_cast<float>(p.head_dim));
+    plan->wt = 128 / G;
+    plan->nq = (p.head_dim <= 128 && p.max_q_rows > plan->wt) ? 2 : 1;
+    plan->tiles = static_cast<int>((static_cast<int64_t>(p.max_q_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
+    plan->variant = spec_attn::cross_variant(p.head_dim, plan->nq);
+    e = cudaFuncSetAttribute(plan->variant.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan->variant.smem);
+    if (e != cudaSuccess) {
+        delete plan;
+        return spec_attn::record_cuda_error(e);
+    }
+    const int bn = plan->variant.bn;
+    if (p.force_splits > 0) {
+        const int64_t units = (static_cast<int64_t>(p.max_kv_len) + bn - 1) / bn;
+        const int64_t u = (units + p.force_splits - 1) / p.force_splits;
+        plan->keys_per_split = static_cast<int>((u < 1 ? 1 : u) * bn);
+    } else {
+        plan->keys_per_split = choose_split(p, plan->tiles, bn, sms);
+    }
+    plan->max_splits = p.max_kv_len == 0 ? 1 : (p.max_kv_len - 1) / plan->keys_per_split + 1;
+    if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
+        delete plan;
+        return SPEC_ATTN_E_UNSUPPORTED;
+    }
+    const size_t pairs = static_cast<size_t>(p.total_q_rows) * p.num_q_heads;
+    size_t ws = 256;
+    plan->lse_off = plan->o_off = ws;
+    if (plan->max_splits > 1) {
+        ws += (plan->max_splits * pairs * sizeof(float) + 255) / 256 * 256;
+        plan->o_off = ws;
+        ws += plan->max_splits * pairs * p.head_dim * sizeof(float);
+    }
+    plan->ws_bytes = ws;
+    if (workspace_bytes) *workspace_bytes = ws;
+    *out = plan;
+    return SPEC_ATTN_OK;
+}
+
+int spec_attn_cross_plan_destroy(spec_attn_cross_plan* plan) {
+    delete plan;
+    return SPEC_ATTN_OK;
+}
+
+int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const void* k, const void* v,
+                        const int32_t* q_indptr, const int32_t* kv_start, const int32_t* kv_len, void* o, float* lse,
+                        void* workspace, size_t workspace_bytes, spec_attn_stream_t stream_handle) {
+    using namespace spec_attn;
+    if (!plan) return SPEC_ATTN_E_INVALID_ARG;
+    const spec_attn_cross_problem& p = plan->prob;
+    if (p.num_reqs == 0 || p.total_q_rows == 0) return SPEC_ATTN_OK;
+    if (!q || !o || !q_indptr || !kv_start || !kv_len || !workspace || !cross_aligned(q, 16) || !cross_aligned(o, 16) ||
+        !cross_aligned(q_indptr, 4) || !cross_aligned(kv_start, 4) || !cross_aligned(kv_len, 4) ||
+        !cross_aligned(lse, 4) || !cross_aligned(workspace, 256))
+        return SPEC_ATTN_E_INVALID_ARG;
+    if (p.total_kv_rows > 0 && (!k || !v || !cross_aligned(k, 16) || !cross_aligned(v, 16)))
+        return SPEC_ATTN_E_INVALID_ARG;
+    if (workspace_bytes < plan->ws_bytes) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    if (dev != plan->device) return SPEC_ATTN_E_INVALID_ARG;
+
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    CrossParams c = {};
+    c.q_indptr = q_indptr;
+    c.kv_start = kv_start;
+    c.kv_len = kv_len;
+    c.o = static_cast<uint16_t*>(o);
+    c.lse = lse;
+    c.ws_lse = reinterpret_cast<float*>(ws + plan->lse_off);
+    c.ws_o = reinterpret_cast<float*>(ws + plan->o_off);
+    c.status = reinterpret_cast<unsigned int*>(ws);
+    c.total_rows = p.total_q_rows;
+    c.max_rows = p.max_q_rows;
+    c.num_q_heads = p.num_q_heads;
+    c.group = p.num_q_heads / p.num_kv_heads;
+    c.wt = plan->wt;
+    c.tiles = plan->tiles;
+    c.total_kv = p.total_kv_rows;
+    c.max_kv_len = p.max_kv_len;
+    c.keys_per_split = plan->keys_per_split;
+    c.score_scale_log2 = plan->sm_scale * 1.4426950408889634f;
+
+    CUtensorMap maps[3];
+    {
+        spec_attn_cross_plan* mp = const_cast<spec_attn_cross_plan*>(plan);
+        std::lock_guard<std::mutex> lock(mp->maps_mutex);
+        const void* key[3] = {q, k, v};
+        if (std::memcmp(key, mp->maps_key, sizeof(key)) != 0) {
+            std::memset(mp->maps, 0, sizeof(mp->maps));
+            std::memset(mp->maps_key, 0, sizeof(mp->maps_key));
+            const int bn = plan->variant.bn;
+            // (with no state rows at all no copy is made: the maps stay empty)
+            if (p.total_kv_rows > 0 &&
+                !(encode_rows(&mp->maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim,
+                              static_cast<long long>(p.num_q_heads) * p.head_dim, c.group, c.wt) &&
+                  encode_rows(&mp->maps[1], k, p.total_kv_rows, p.num_kv_heads, p.head_dim, p.kv_row_stride, 1, bn) &&
+                  encode_rows(&mp->maps[2], v, p.total_kv_rows, p.num_kv_heads, p.head_dim, p.kv_row_stride, 1, bn)))
+                return SPEC_ATTN_E_INVALID_ARG;
+            std::memcpy(mp->maps_key, key, sizeof(key));
+        }
+        std::memcpy(maps, mp->maps, sizeof(maps));
+    }
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(plan->tiles * plan->max_splits), static_cast<unsigned>(p.num_kv_heads),
+                       static_cast<unsigned>(p.num_reqs));
+    cfg.blockDim = dim3(static_cast<unsigned>(plan->variant.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan->variant.smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, plan->variant.kernel, c, maps[0], maps[1], maps[2]);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    if (plan->max_splits > 1) {
+        const int64_t units = static_cast<int64_t>(p.max_q_rows) * p.num_q_heads * (p.head_dim / 4);
+        int64_t blocks = (units + kCombThreads - 1) / kCombThreads;
+        if (blocks > 1024) blocks = 1024;
+        cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.num_reqs));
+        cfg.blockDim = dim3(kCombThreads);
+        cfg.dynamicSmemBytes = 0;
+        e = p.head_dim == 64    ? cudaLaunchKernelEx(&cfg, &cross_combine_kernel<64>, c)
+            : p.head_dim == 128 ? cudaLaunchKernelEx(&cfg, &cross_combine_kernel<128>, c)
+                                : cudaLaunchKernelEx(&cfg, &cross_combine_kernel<256>, c);
+        if (e != cudaSuccess) return record_cuda_error(e);
+    }
+    return SPEC_ATTN_OK;
+}
+
+}  // extern "C"

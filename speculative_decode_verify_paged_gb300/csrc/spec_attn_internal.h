@@ -269,4 +269,26 @@ struct NormRopeParams {
 cudaError_t norm_rope_launch(NormRopeParams& p, int head_dim, bool append, int kv_dtype, int num_sms,
                              cudaStream_t stream);
 
+// ---- cross attention (cross_attn.cu) ----
+struct CrossParams {
+    const int32_t* q_indptr;    // [P + 1]
+    const int32_t* kv_start;    // [P] first state row
+    const int32_t* kv_len;      // [P]
+    uint16_t* o;                // [total_rows, Hq, d] bf16 bits
+    float* lse;                 // [total_rows, Hq] or nullptr
+    float* ws_lse;              // split partials: [split][total_rows * Hq], base 2
+    float* ws_o;                // [split][total_rows * Hq][d], normalised
+    unsigned int* status;
+    int total_rows;
+    int max_rows;               // of a request
+    int num_q_heads;
+    int group;
+    int wt;                     // window rows of a query tile: 128 / group
+    int tiles;                  // CTAs along a request's rows
+    int total_kv;
+    int max_kv_len;
+    int keys_per_split;
+    float score_scale_log2;
+};
+
 }  // namespace spec_attn

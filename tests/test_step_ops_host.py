@@ -21,7 +21,8 @@ def lib():
 
 
 STRUCTS = [("spec_attn_tables_problem", sa.spec_attn_tables_problem),
-           ("spec_attn_norm_rope_problem", sa.spec_attn_norm_rope_problem)]
+           ("spec_attn_norm_rope_problem", sa.spec_attn_norm_rope_problem),
+           ("spec_attn_cross_problem", sa.spec_attn_cross_problem)]
 
 
 @pytest.mark.parametrize("cstruct,pystruct", STRUCTS)
@@ -170,3 +171,38 @@ def test_cpu_tensors_are_refused(lib, monkeypatch):
     with pytest.raises(ValueError, match="CUDA tensor"):
         sa.spec_attn_build_tables(i, i, i, i[:1], i, i[None].expand(4, 4), i, i, i[:1], i, i.long(),
                                   torch.zeros(256, dtype=torch.uint8), max_seq_len=64)
+
+
+# --------------------------------------------------------------------------- #
+# cross attention
+# --------------------------------------------------------------------------- #
+@pytest.mark.parametrize("over,status", [
+    (dict(num_reqs=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(num_reqs=65536), sa.SPEC_ATTN_E_UNSUPPORTED),
+    (dict(total_q_rows=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(max_q_rows=0), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(num_q_heads=6, num_kv_heads=4), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(num_q_heads=34, num_kv_heads=2), sa.SPEC_ATTN_E_UNSUPPORTED),
+    (dict(head_dim=96), sa.SPEC_ATTN_E_UNSUPPORTED),
+    (dict(total_kv_rows=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(max_kv_len=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(sm_scale=-0.5), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(sm_scale=float("nan")), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(force_splits=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(kv_row_stride=248), sa.SPEC_ATTN_E_INVALID_ARG),      # below the dense row (256)
+    (dict(kv_row_stride=260), sa.SPEC_ATTN_E_INVALID_ARG),      # not a multiple of 8
+])
+def test_cross_plan_refuses_bad_problems(lib, over, status):
+    prob = dict(num_reqs=2, total_q_rows=8, max_q_rows=4, num_q_heads=8, num_kv_heads=2, head_dim=128,
+                total_kv_rows=100, max_kv_len=60, sm_scale=0.0, force_splits=0, kv_row_stride=0)
+    prob.update(over)
+    pr = sa.spec_attn_cross_problem(*[prob[f[0]] for f in sa.spec_attn_cross_problem._fields_])
+    h = ctypes.c_void_p()
+    assert lib.spec_attn_cross_plan_create(ctypes.byref(pr), ctypes.byref(h), None) == status
+    assert not h.value
+
+
+def test_cross_null_arguments(lib):
+    assert lib.spec_attn_cross_plan_create(None, None, None) == sa.SPEC_ATTN_E_INVALID_ARG
+    assert lib.spec_attn_run_cross(*([None] * 10), 0, None) == sa.SPEC_ATTN_E_INVALID_ARG
+    assert lib.spec_attn_cross_plan_destroy(None) == sa.SPEC_ATTN_OK
