@@ -11,23 +11,26 @@
 // One CTA = (NQ query tiles of 128 rows) x (one KV head) x (a split of the
 // request's states).  A tile holds wt = 128 / G whole window rows with their G
 // heads, so K and V are read once for the G heads.  NQ = 2 (windows of more
-// than one tile, d <= 128): the two tiles share every K and V tile and take
-// turns on the tensor cores, one tile's products running under the other
-// tile's softmax.  NQ = 1: the S buffer is doubled instead, so that the next
-// scores are computed under this tile's softmax.
+// than one tile, d <= 128): the two tiles share every K and V tile, one tile's
+// products running under the other tile's softmax.  Each tile's scores have two
+// buffers of 64 columns, so S_{t+1} is made while the softmax works on S_t and the
+// only chain from tile to tile is the softmax itself.  (One buffer of 128
+// columns runs the first product at its full rate, 64 instead of 96 clocks for
+// 128 states and 16 elements, but S_{t+1} then waits for softmax and P V of tile t:
+// 857 TFLOP/s at 4096 x 4096, 32/8 heads x 128.)
 //
 // Warp roles:
 //   warp 0      the query tiles, then K and V tiles in turn, by TMA into one ring
-//               of slots (BN rows each, 128-byte swizzled, chunk-major).
+//               of slots (64 rows each, 128-byte swizzled, chunk-major).
 //   warps 1, 2  issue the products, one thread each.  NQ = 2: warp 1 + i issues
-//               both products of tile i, S_{t+1} once P_t V_t has left the buffer
-//               that S and P share.  NQ = 1: warp 1 issues S = Q K^T and warp 2 O += P V.
+//               S_{t+1} and then P_t V_t of tile i.  NQ = 1: warp 1 issues S = Q K^T
+//               and warp 2 O += P V, so that a late K tile holds no P V back.
 //   warp 3      owns tensor memory.
 //   warps 4-7 (and 8-11 for the second tile)   softmax, a row a thread, and the
 //               epilogue.  In the last tile they also zero the V rows past the range's
 //               end (what lies there may be anything, and 0 x NaN is NaN).
 //
-// TMEM columns: O tiles [0, NQ d), two S buffers of BN columns after them, P
+// TMEM columns: O tiles [0, NQ d), then two S buffers of 64 columns a tile, P
 // (bf16 pairs) in the first half of its S buffer.
 //
 // Every wait is bounded; on time-out the CTA sets the device-status bit, drains
@@ -61,21 +64,25 @@ constexpr int kM = 128;
 constexpr int kMaxRing = 12;
 constexpr float kCrossRescale = 8.0f;   // log2 units: O is rescaled when a row's maximum grows by more
 
+constexpr int kBN = 64;                 // states a tile
+
 template <int D, int NQ>
 struct CrossLayout {
-    static_assert(NQ == 1 || D <= 128, "two O tiles and two S buffers fit 512 columns up to d = 128");
-    static constexpr int kBN = D == 256 ? 64 : 128;        // states a tile
+    static_assert(NQ == 1 || D <= 128, "two O tiles and four S buffers fit 512 columns up to d = 128");
     static constexpr int kChunks = D / 64;
     static constexpr int kQBytes = kM * D * 2;             // one query tile
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
     static constexpr int kAux = 1024;
-    static constexpr int kMax = 232448;                    // 227 KB
+    static constexpr int kNeed = NQ * D + NQ * 2 * kBN;
+    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;
+    // one tile up to d = 128: half of the SM's tensor memory, so two CTAs share
+    // an SM and one's start and end hide under the other's stream
+    static constexpr int kCtas = kCols == 256 ? 2 : 1;
+    static constexpr int kMax = 232448 / kCtas - (kCtas == 2 ? 1024 : 0);   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
     static constexpr int kFit = (kMax - 1024 - kAux - NQ * kQBytes) / kTileBytes;
     static constexpr int kRing = kFit > kMaxRing ? kMaxRing : kFit;
     static constexpr int kSmem = 1024 + kAux + NQ * kQBytes + kRing * kTileBytes;
-    static constexpr int kSCol = NQ * D;                   // first column of the S buffers
-    static constexpr int kNeed = NQ * D + 2 * kBN;
-    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;
+    __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (2 * i + b) * kBN; }
     static constexpr int kThreads = 128 + NQ * 128;
     static_assert(kNeed <= 512, "tensor memory");
     static_assert(kRing >= 4, "a K and a V tile ahead of the ones in use");
@@ -85,9 +92,9 @@ struct CrossAux {
     uint64_t full[kMaxRing];
     uint64_t empty[kMaxRing];
     uint64_t q_full[2];
-    uint64_t s_full[2];     // scores written (NQ = 2: of tile i; NQ = 1: in buffer t & 1)
-    uint64_t p_full[2];     // P written over them (four softmax warps)
-    uint64_t s_empty[2];    // NQ = 1: P V of the buffer's tile done
+    uint64_t s_full[2][2];  // [tile][buffer] scores written
+    uint64_t p_full[2][2];  // P written over them (four softmax warps)
+    uint64_t s_empty[2][2]; // P V has read the buffer's P
     uint64_t o_done[2];     // one phase a P V
     uint64_t o_final[2];    // after the last P V of tile i
     uint64_t drain[2];
@@ -95,6 +102,61 @@ struct CrossAux {
     int abort;
 };
 static_assert(sizeof(CrossAux) <= 1024, "aux region");
+
+// Bounded wait of a whole warp; the clock is read only when the phase is still open.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
+    return warp_wait(bar, parity, abort);
+}
+
+// Two fp32 operations in one instruction (rounded like the single ones).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// A shared-memory matrix descriptor is its high word, the same for every tile of
+// one kind, and a low word that a constant step moves along the tile: the
+// issuing thread adds to one register instead of building 64 bits each time.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+    return (saddr >> 4) | ((lbo_bytes >> 4) << 16);      // (shared addresses stay below 2^18)
+}
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 B apart, version 1, 128-byte swizzle
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi)
+        : "memory");
+}
 
 // The request's rows and states, checked.
 struct CrossReq {
@@ -118,11 +180,11 @@ __device__ __forceinline__ bool cross_request(const CrossParams& p, int r, unsig
 }
 
 template <int D, int NQ>
-__global__ void __launch_bounds__(CrossLayout<D, NQ>::kThreads, 1)
+__global__ void __launch_bounds__(CrossLayout<D, NQ>::kThreads, CrossLayout<D, NQ>::kCtas)
 cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
     using L = CrossLayout<D, NQ>;
-    constexpr int BN = L::kBN, RING = L::kRing;
+    constexpr int BN = kBN, RING = L::kRing;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
     const int kvh = blockIdx.y, r = blockIdx.z;
@@ -166,9 +228,11 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&aux->q_full[i], 1);
-            mbar_init(&aux->s_full[i], 1);
-            mbar_init(&aux->p_full[i], 4);
-            mbar_init(&aux->s_empty[i], 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&aux->s_full[i][b], 1);
+                mbar_init(&aux->p_full[i][b], 4);
+                mbar_init(&aux->s_empty[i][b], 1);
+            }
             mbar_init(&aux->o_done[i], 1);
             mbar_init(&aux->o_final[i], 1);
             mbar_init(&aux->drain[i], 1);
@@ -201,7 +265,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         __syncwarp();
         for (int n = 0; n < 2 * T; ++n) {
             const int slot = n % RING;
-            if (n >= RING && !warp_wait(&aux->empty[slot], ((n / RING) - 1) & 1, abort)) break;
+            if (n >= RING && !wait_warp(&aux->empty[slot], ((n / RING) - 1) & 1, abort)) break;
             if (lane == 0) {
                 unsigned char* dst = ring + slot * L::kTileBytes;
                 const CUtensorMap* map = (n & 1) ? &tmv : &tmk;
@@ -225,58 +289,62 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             constexpr uint32_t idesc_s = idesc_bf16_f32(kM, BN, 0, 0);
             constexpr uint32_t idesc_o = idesc_bf16_f32(kM, D, 0, 1);
             const int i = NQ == 2 ? warp - 1 : 0;
-            const uint32_t q_addr = smem_addr(sQ + i * L::kQBytes);
-            auto wait = [&](uint64_t* bar, int parity) { return mbar_wait(bar, parity & 1, abort, kWaitLimit); };
-            auto wait_ring = [&](int n) { return wait(&aux->full[n % RING], n / RING); };
-            auto issue_s = [&](int t, int buf) {
+            const uint32_t q_lo = desc_lo(smem_addr(sQ + i * L::kQBytes), 16);
+            const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), BN * 128);
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, kWaitLimit); };
+            // the ring slots of K_t and V_t, stepped along, and the parity of their phase
+            int k_slot = 0, v_slot = 1;
+            uint32_t k_par = 0, v_par = 0;
+            auto step = [](int& slot, uint32_t& par) {
+                slot += 2;
+                if (slot >= RING) {
+                    slot -= RING;
+                    par ^= 1;
+                }
+            };
+            // S_t, once K_t is here and the P that sat in S_t's buffer has been read
+            auto do_s = [&](int t) {
+                const int b = t & 1;
+                if (!wait(&aux->full[k_slot], k_par) || (t >= 2 && !wait(&aux->s_empty[i][b], ((t >> 1) - 1) & 1)))
+                    return false;
                 tc_fence_after();
-                const int slot = (2 * t) % RING;
-                const uint32_t k_addr = smem_addr(ring + slot * L::kTileBytes);
+                const uint32_t k_lo = k_lo0 + k_slot * (L::kTileBytes >> 4), d_tmem = tmem + L::s_col(i, b);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const int c = kk >> 2, sub = kk & 3;
-                    mma_bf16_ss(tmem + L::kSCol + buf * BN, smem_desc_sw128(q_addr + c * (kM * 128) + sub * 32, 16, 1024),
-                                smem_desc_sw128(k_addr + c * (BN * 128) + sub * 32, 16, 1024), idesc_s, kk > 0 ? 1u : 0u);
+                    mma_ss_lo(d_tmem, q_lo + c * (kM * 128 >> 4) + sub * 2, k_lo + c * (BN * 128 >> 4) + sub * 2, idesc_s,
+                              kk > 0);
                 }
-                mma_commit(&aux->empty[slot]);
-                mma_commit(&aux->s_full[buf]);
+                mma_commit(&aux->s_full[i][b]);
+                mma_commit(&aux->empty[k_slot]);
+                step(k_slot, k_par);
+                return true;
             };
-            auto issue_pv = [&](int t, int buf) {
+            // O += P_t V_t, once both are here
+            auto do_pv = [&](int t) {
+                const int b = t & 1;
+                if (!wait(&aux->full[v_slot], v_par) || !wait(&aux->p_full[i][b], (t >> 1) & 1)) return false;
                 tc_fence_after();
-                const int slot = (2 * t + 1) % RING;
-                const uint32_t v_addr = smem_addr(ring + slot * L::kTileBytes);
+                const uint32_t v_lo = v_lo0 + v_slot * (L::kTileBytes >> 4), p_tmem = tmem + L::s_col(i, b);
                 const int steps = t == T - 1 ? (tail + 15) / 16 : BN / 16;
-                for (int kk = 0; kk < steps; ++kk)
-                    mma_ts(tmem + i * D, tmem + L::kSCol + buf * BN + kk * 8,
-                           smem_desc_sw128(v_addr + kk * 2048, BN * 128, 1024), idesc_o, (t > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(&aux->empty[slot]);
-                if (NQ == 1) mma_commit(&aux->s_empty[buf]);
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * (2048 >> 4), idesc_o, t > 0 || kk > 0);
+                mma_commit(&aux->s_empty[i][b]);
                 mma_commit(&aux->o_done[i]);
+                mma_commit(&aux->empty[v_slot]);
+                step(v_slot, v_par);
+                return true;
             };
             bool ok = true;
+            if (NQ == 2 || warp == 1) ok = wait(&aux->q_full[i], 0);
             if (NQ == 2) {
-                ok = wait(&aux->q_full[i], 0) && wait_ring(0);
-                if (ok) issue_s(0, i);
-                for (int t = 0; t < T && ok; ++t) {
-                    ok = wait(&aux->p_full[i], t) && wait_ring(2 * t + 1);
-                    if (!ok) break;
-                    issue_pv(t, i);
-                    if (t + 1 < T) {
-                        ok = wait_ring(2 * t + 2) && wait(&aux->o_done[i], t);   // P_t has been read
-                        if (ok) issue_s(t + 1, i);
-                    }
-                }
+                ok = ok && do_s(0);
+                for (int t = 0; t < T && ok; ++t) ok = (t + 1 == T || do_s(t + 1)) && do_pv(t);
             } else if (warp == 1) {
-                ok = wait(&aux->q_full[0], 0);
-                for (int t = 0; t < T && ok; ++t) {
-                    ok = wait_ring(2 * t) && (t < 2 || wait(&aux->s_empty[t & 1], (t >> 1) - 1));
-                    if (ok) issue_s(t, t & 1);
-                }
+                for (int t = 0; t < T && ok; ++t) ok = do_s(t);
             } else {
-                for (int t = 0; t < T && ok; ++t) {
-                    ok = wait(&aux->p_full[t & 1], t >> 1) && wait_ring(2 * t + 1);
-                    if (ok) issue_pv(t, t & 1);
-                }
+                for (int t = 0; t < T && ok; ++t) ok = do_pv(t);
             }
             if (ok && (NQ == 2 || warp == 2)) mma_commit(&aux->o_final[i]);
             // every product this thread issued completes before the memory is released
@@ -296,14 +364,15 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         const float sc = p.score_scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
+        const uint64_t sc2 = pack2(sc, sc);
         for (int t = 0; t < T; ++t) {
-            const int buf = NQ == 2 ? i : t & 1;
-            if (!(ok = warp_wait(&aux->s_full[buf], (NQ == 2 ? t : t >> 1) & 1, abort))) break;
+            const int b = t & 1;
+            if (!(ok = wait_warp(&aux->s_full[i][b], (t >> 1) & 1, abort))) break;
             tc_fence_after();
-            const uint32_t s_tmem = lane_tmem + L::kSCol + buf * BN;
+            const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
             float sv[BN];
-#pragma unroll
-            for (int h = 0; h < BN / 32; ++h) tmem_ld32(s_tmem + h * 32, *reinterpret_cast<float(*)[32]>(sv + h * 32));
+            tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sv));
+            tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
             tmem_wait_ld();
             if (t == T - 1 && tail < BN) {
 #pragma unroll
@@ -311,28 +380,33 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             }
             float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
 #pragma unroll
-            for (int c = 4; c < BN; ++c) mx4[c & 3] = fmaxf(mx4[c & 3], sv[c]);
+            for (int c = 4; c < BN; c += 8) {   // (three-way maxima)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(fmaxf(mx4[k], sv[c + k]), c + 4 < BN ? sv[c + 4 + k] : mx4[k]);
+            }
             const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
             // the reference moves at the first tile, and when the maximum outgrows it
             const bool need = mx > m_ref + kCrossRescale;
             const float ref = need ? mx : m_ref;
             const float alpha = need ? fast_exp2(m_ref - ref) : 1.f;   // (0 at the first tile)
             const float nref = ref == -INFINITY ? 0.f : -ref;
+            const uint64_t nref2 = pack2(nref, nref);
             uint32_t pk[BN / 2];
-            float ps[4] = {0.f, 0.f, 0.f, 0.f};
+            uint64_t ps[2] = {0, 0};   // two fp32 zeros each
 #pragma unroll
             for (int c = 0; c < BN; c += 2) {
-                const float p0 = fast_exp2(fmaf(sv[c], sc, nref)), p1 = fast_exp2(fmaf(sv[c + 1], sc, nref));
-                ps[c & 2] += p0;
-                ps[(c & 2) + 1] += p1;
+                const float2 x = unpack2(fma2(pack2(sv[c], sv[c + 1]), sc2, nref2));
+                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], pack2(p0, p1));
                 const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
                 pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
             }
-            l_sum = l_sum * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+            const float2 psum = unpack2(add2(ps[0], ps[1]));
+            l_sum = l_sum * alpha + (psum.x + psum.y);
             m_ref = ref;
             if (t > 0 && __any_sync(kFullMask, valid && need)) {
-                // every earlier P V has to be in (NQ = 2: S_t was issued after the last one)
-                if (NQ == 1 && !(ok = warp_wait(&aux->o_done[0], (t - 1) & 1, abort))) break;
+                // every earlier P V has to be in (P V of t - 2 is: S_t was issued after it)
+                if (!(ok = wait_warp(&aux->o_done[i], (t - 1) & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
@@ -349,20 +423,18 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 // names this phase.  Both tiles' warps write the same zeros.
                 constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
                 const int n = 2 * T - 1, rows = ((tail + 15) & ~15) - tail;
-                if (!(ok = warp_wait(&aux->full[n % RING], (n / RING) & 1, abort))) break;
+                if (!(ok = wait_warp(&aux->full[n % RING], (n / RING) & 1, abort))) break;
                 const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kTileBytes);
                 for (int u = m; u < rows * C8; u += 128)
                     st_shared_v4(v_addr + ((u % C8) >> 3) * (BN * 128) + (tail + u / C8) * 128 + (u & 7) * 16,
                                  make_uint4(0u, 0u, 0u, 0u));
                 fence_proxy_async_smem();
             }
-#pragma unroll
-            for (int h = 0; h < BN / 64; ++h)
-                tmem_st32u(s_tmem + h * 32, *reinterpret_cast<uint32_t(*)[32]>(pk + h * 32));
+            tmem_st32u(s_tmem, pk);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&aux->p_full[buf]);
+            if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
         }
         if (ok) ok = warp_wait(&aux->o_final[i], 0, abort);
         pdl_launch_dependents();
@@ -455,12 +527,12 @@ using CrossKernel = void (*)(const CrossParams, const CUtensorMap, const CUtenso
 // What a launch of (d, query tiles a CTA) needs.
 struct CrossVariant {
     CrossKernel kernel;
-    int threads, smem, bn;
+    int threads, smem, ctas;
 };
 template <int D, int NQ>
 CrossVariant variant_of() {
     using L = CrossLayout<D, NQ>;
-    return {&cross_attn_kernel<D, NQ>, L::kThreads, L::kSmem, L::kBN};
+    return {&cross_attn_kernel<D, NQ>, L::kThreads, L::kSmem, L::kCtas};
 }
 CrossVariant cross_variant(int d, int nq) {
     switch (d) {
@@ -523,8 +595,9 @@ namespace {
 bool cross_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // States a split takes.  Model: a CTA costs a fixed start and end plus its states at its SM's share of the HBM
-// rate, waves of num_sms CTAs; splitting adds the second kernel.
-int choose_split(const spec_attn_cross_problem& p, int tiles, int bn, int num_sms) {
+// rate, waves of one CTA (or two) an SM; splitting adds the second kernel.
+int choose_split(const spec_attn_cross_problem& p, int tiles, int bn, int num_sms, int per_sm) {
+    num_sms *= per_sm;
     const double key_us = 4.0 * p.head_dim / (6.5e6 / num_sms), fixed_us = 3.0, combine_us = 3.0;
     const int64_t ctas = static_cast<int64_t>(tiles) * p.num_kv_heads * p.num_reqs;
     const int64_t units = (static_cast<int64_t>(p.max_kv_len) + bn - 1) / bn;
@@ -582,13 +655,13 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
         delete plan;
         return spec_attn::record_cuda_error(e);
     }
-    const int bn = plan->variant.bn;
+    const int bn = spec_attn::kBN;
     if (p.force_splits > 0) {
         const int64_t units = (static_cast<int64_t>(p.max_kv_len) + bn - 1) / bn;
         const int64_t u = (units + p.force_splits - 1) / p.force_splits;
         plan->keys_per_split = static_cast<int>((u < 1 ? 1 : u) * bn);
     } else {
-        plan->keys_per_split = choose_split(p, plan->tiles, bn, sms);
+        plan->keys_per_split = choose_split(p, plan->tiles, bn, sms, plan->variant.ctas);
     }
     plan->max_splits = p.max_kv_len == 0 ? 1 : (p.max_kv_len - 1) / plan->keys_per_split + 1;
     if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
@@ -662,7 +735,7 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
         if (std::memcmp(key, mp->maps_key, sizeof(key)) != 0) {
             std::memset(mp->maps, 0, sizeof(mp->maps));
             std::memset(mp->maps_key, 0, sizeof(mp->maps_key));
-            const int bn = plan->variant.bn;
+            const int bn = spec_attn::kBN;
             // (with no state rows at all no copy is made: the maps stay empty)
             if (p.total_kv_rows > 0 &&
                 !(encode_rows(&mp->maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim,
