@@ -79,24 +79,28 @@ struct CrossLayout {
     // an SM and one's start and end hide under the other's stream
     static constexpr int kCtas = kCols == 256 ? 2 : 1;
     static constexpr int kMax = 232448 / kCtas - (kCtas == 2 ? 1024 : 0);   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
-    static constexpr int kFit = (kMax - 1024 - kAux - NQ * kQBytes) / kTileBytes;
+    // The ring.  NQ = 1: a slot a tile, K_t and V_t in turn, each let go as soon as
+    // it has been read.  NQ = 2: a slot holds K_t and V_t, filled and let go
+    // together: one barrier to wait on and one commit less for each of the
+    // products, whose issue is what bounds long prompts.
+    static constexpr int kSlotTiles = NQ;
+    static constexpr int kSlotBytes = kSlotTiles * kTileBytes;
+    static constexpr int kFit = (kMax - 1024 - kAux - NQ * kQBytes) / kSlotBytes;
     static constexpr int kRing = kFit > kMaxRing ? kMaxRing : kFit;
-    static constexpr int kSmem = 1024 + kAux + NQ * kQBytes + kRing * kTileBytes;
+    static constexpr int kSmem = 1024 + kAux + NQ * kQBytes + kRing * kSlotBytes;
     __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (2 * i + b) * kBN; }
     static constexpr int kThreads = 128 + NQ * 128;
     static_assert(kNeed <= 512, "tensor memory");
-    static_assert(kRing >= 4, "a K and a V tile ahead of the ones in use");
+    static_assert(kRing >= 4, "tiles ahead of the ones in use");
 };
 
 struct CrossAux {
     uint64_t full[kMaxRing];
-    uint64_t empty[kMaxRing];
+    uint64_t empty[kMaxRing];           // NQ = 1
+    uint64_t pv_done[2][kMaxRing];      // P_t V_t of tile i done: O, P_t's buffer and (NQ = 2) the slot; by t mod ring
     uint64_t q_full[2];
-    uint64_t s_full[2][2];  // [tile][buffer] scores written
-    uint64_t p_full[2][2];  // P written over them (four softmax warps)
-    uint64_t s_empty[2][2]; // P V has read the buffer's P
-    uint64_t o_done[2];     // one phase a P V
-    uint64_t o_final[2];    // after the last P V of tile i
+    uint64_t s_full[2][2];              // [tile][buffer] scores written
+    uint64_t p_full[2][2];              // P written over them (four softmax warps)
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -193,7 +197,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                                                            ~static_cast<uintptr_t>(1023));
     unsigned char* sQ = smem;
     unsigned char* ring = smem + NQ * L::kQBytes;
-    CrossAux* aux = reinterpret_cast<CrossAux*>(ring + RING * L::kTileBytes);
+    CrossAux* aux = reinterpret_cast<CrossAux*>(ring + RING * L::kSlotBytes);
     volatile int* abort = &aux->abort;
 
     pdl_wait_primary();
@@ -224,17 +228,16 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     if (tid == 0) {
         for (int s = 0; s < RING; ++s) {
             mbar_init(&aux->full[s], 1);
-            mbar_init(&aux->empty[s], nact);       // every tile's products have read the slot
+            mbar_init(&aux->empty[s], 1);
+            mbar_init(&aux->pv_done[0][s], 1);
+            mbar_init(&aux->pv_done[1][s], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&aux->q_full[i], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&aux->s_full[i][b], 1);
                 mbar_init(&aux->p_full[i][b], 4);
-                mbar_init(&aux->s_empty[i][b], 1);
             }
-            mbar_init(&aux->o_done[i], 1);
-            mbar_init(&aux->o_final[i], 1);
             mbar_init(&aux->drain[i], 1);
         }
         aux->abort = 0;
@@ -263,16 +266,28 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             }
         }
         __syncwarp();
-        for (int n = 0; n < 2 * T; ++n) {
+        auto load_tile = [&](unsigned char* dst, const CUtensorMap* map, int t, uint64_t* bar) {
+            for (int c = 0; c < L::kChunks; ++c)
+                tma_load_3d(dst + c * (BN * 128), map, c * 64, kvh, q.start + key_lo + t * BN, bar);
+        };
+        for (int n = 0; n < (NQ == 2 ? T : 2 * T); ++n) {
             const int slot = n % RING;
-            if (n >= RING && !wait_warp(&aux->empty[slot], ((n / RING) - 1) & 1, abort)) break;
+            const uint32_t gone = ((n / RING) - 1) & 1;
+            if (n >= RING) {
+                if (NQ == 1 && !wait_warp(&aux->empty[slot], gone, abort)) break;
+                if (NQ == 2 && !(wait_warp(&aux->pv_done[0][slot], gone, abort) &&
+                                 (nact == 1 || wait_warp(&aux->pv_done[1][slot], gone, abort))))
+                    break;
+            }
             if (lane == 0) {
-                unsigned char* dst = ring + slot * L::kTileBytes;
-                const CUtensorMap* map = (n & 1) ? &tmv : &tmk;
-                mbar_arrive_expect_tx(&aux->full[slot], L::kTileBytes);
-                const int row = q.start + key_lo + (n >> 1) * BN;
-                for (int c = 0; c < L::kChunks; ++c)
-                    tma_load_3d(dst + c * (BN * 128), map, c * 64, kvh, row, &aux->full[slot]);
+                unsigned char* dst = ring + slot * L::kSlotBytes;
+                mbar_arrive_expect_tx(&aux->full[slot], L::kSlotBytes);
+                if (NQ == 2) {
+                    load_tile(dst, &tmk, n, &aux->full[slot]);
+                    load_tile(dst + L::kTileBytes, &tmv, n, &aux->full[slot]);
+                } else {
+                    load_tile(dst, (n & 1) ? &tmv : &tmk, n >> 1, &aux->full[slot]);
+                }
             }
             __syncwarp();
             issued = n + 1;
@@ -292,23 +307,29 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             const uint32_t q_lo = desc_lo(smem_addr(sQ + i * L::kQBytes), 16);
             const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), BN * 128);
             auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, kWaitLimit); };
-            // the ring slots of K_t and V_t, stepped along, and the parity of their phase
-            int k_slot = 0, v_slot = 1;
-            uint32_t k_par = 0, v_par = 0;
-            auto step = [](int& slot, uint32_t& par) {
-                slot += 2;
-                if (slot >= RING) {
-                    slot -= RING;
-                    par ^= 1;
+            // the ring slots of K_t and V_t, and the slot t mod ring, stepped along with the parity of their phase
+            struct Step {
+                int slot;
+                uint32_t par;
+                __device__ __forceinline__ void by(int n) {
+                    slot += n;
+                    if (slot >= RING) {
+                        slot -= RING;
+                        par ^= 1;
+                    }
                 }
             };
+            Step ks = {0, 0}, vs = {NQ == 1 ? 1 : 0, 0}, done = {0, 0}, before = {0, 0};   // (before: t - 2 of the next S)
             // S_t, once K_t is here and the P that sat in S_t's buffer has been read
             auto do_s = [&](int t) {
                 const int b = t & 1;
-                if (!wait(&aux->full[k_slot], k_par) || (t >= 2 && !wait(&aux->s_empty[i][b], ((t >> 1) - 1) & 1)))
-                    return false;
+                if (!wait(&aux->full[ks.slot], ks.par)) return false;
+                if (t >= 2) {
+                    if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
+                    before.by(1);
+                }
                 tc_fence_after();
-                const uint32_t k_lo = k_lo0 + k_slot * (L::kTileBytes >> 4), d_tmem = tmem + L::s_col(i, b);
+                const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const int c = kk >> 2, sub = kk & 3;
@@ -316,24 +337,26 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                               kk > 0);
                 }
                 mma_commit(&aux->s_full[i][b]);
-                mma_commit(&aux->empty[k_slot]);
-                step(k_slot, k_par);
+                if (NQ == 1) mma_commit(&aux->empty[ks.slot]);
+                ks.by(NQ == 1 ? 2 : 1);
                 return true;
             };
-            // O += P_t V_t, once both are here
+            // O += P_t V_t, once both are here (NQ = 2: V_t came with K_t)
             auto do_pv = [&](int t) {
                 const int b = t & 1;
-                if (!wait(&aux->full[v_slot], v_par) || !wait(&aux->p_full[i][b], (t >> 1) & 1)) return false;
+                if (NQ == 1 && !wait(&aux->full[vs.slot], vs.par)) return false;
+                if (!wait(&aux->p_full[i][b], (t >> 1) & 1)) return false;
                 tc_fence_after();
-                const uint32_t v_lo = v_lo0 + v_slot * (L::kTileBytes >> 4), p_tmem = tmem + L::s_col(i, b);
+                const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
+                const uint32_t p_tmem = tmem + L::s_col(i, b);
                 const int steps = t == T - 1 ? (tail + 15) / 16 : BN / 16;
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
                     if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * (2048 >> 4), idesc_o, t > 0 || kk > 0);
-                mma_commit(&aux->s_empty[i][b]);
-                mma_commit(&aux->o_done[i]);
-                mma_commit(&aux->empty[v_slot]);
-                step(v_slot, v_par);
+                mma_commit(&aux->pv_done[i][done.slot]);
+                if (NQ == 1) mma_commit(&aux->empty[vs.slot]);
+                vs.by(NQ == 1 ? 2 : 1);
+                done.by(1);
                 return true;
             };
             bool ok = true;
@@ -346,7 +369,6 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             } else {
                 for (int t = 0; t < T && ok; ++t) ok = do_pv(t);
             }
-            if (ok && (NQ == 2 || warp == 2)) mma_commit(&aux->o_final[i]);
             // every product this thread issued completes before the memory is released
             uint64_t* drain = &aux->drain[warp - 1];
             mma_commit(drain);
@@ -405,8 +427,8 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             l_sum = l_sum * alpha + (psum.x + psum.y);
             m_ref = ref;
             if (t > 0 && __any_sync(kFullMask, valid && need)) {
-                // every earlier P V has to be in (P V of t - 2 is: S_t was issued after it)
-                if (!(ok = wait_warp(&aux->o_done[i], (t - 1) & 1, abort))) break;
+                // every earlier P V has to be in
+                if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % RING], ((t - 1) / RING) & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
@@ -422,9 +444,9 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 // The slot's earlier tile was consumed before these scores could be made, so the parity
                 // names this phase.  Both tiles' warps write the same zeros.
                 constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
-                const int n = 2 * T - 1, rows = ((tail + 15) & ~15) - tail;
+                const int n = NQ == 2 ? T - 1 : 2 * T - 1, rows = ((tail + 15) & ~15) - tail;
                 if (!(ok = wait_warp(&aux->full[n % RING], (n / RING) & 1, abort))) break;
-                const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kTileBytes);
+                const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
                 for (int u = m; u < rows * C8; u += 128)
                     st_shared_v4(v_addr + ((u % C8) >> 3) * (BN * 128) + (tail + u / C8) * 128 + (u & 7) * 16,
                                  make_uint4(0u, 0u, 0u, 0u));
@@ -436,7 +458,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
         }
-        if (ok) ok = warp_wait(&aux->o_final[i], 0, abort);
+        if (ok) ok = wait_warp(&aux->pv_done[i][(T - 1) % RING], ((T - 1) / RING) & 1, abort);
         pdl_launch_dependents();
         tc_fence_after();
         if (ok) {
