@@ -607,7 +607,7 @@ typedef struct spec_attn_cross_problem {
     int32_t total_kv_rows;       /* rows of K and V */
     int32_t max_kv_len;          /* upper bound on every kv_len */
     float sm_scale;              /* 0 selects 1/sqrt(head_dim) */
-    int32_t force_splits;        /* 0: the library's choice; n > 0: cut the longest range n ways */
+    int32_t force_splits;        /* 0: the library's choice; 1 .. 8: cut the longest range n ways */
     int64_t kv_row_stride;       /* elements; 0 = dense; else a multiple of 8, at least the dense row */
 } spec_attn_cross_problem;
 
@@ -622,9 +622,8 @@ int spec_attn_cross_plan_destroy(spec_attn_cross_plan* plan);
 /*
  * q [total_q_rows, Hq, d], o likewise, k and v at the plan's row stride, all
  * bf16 and 16-byte aligned; q_indptr [P+1], kv_start [P], kv_len [P] int32;
- * lse [total_q_rows, Hq] fp32 or NULL; workspace as for spec_attn_run
- * (256-byte aligned, its device-status word zeroed once, not shared by runs
- * that may overlap).  Asynchronous on `stream`, allocation-free, graph
+ * lse [total_q_rows, Hq] fp32 or NULL; workspace: 256 bytes, 256-byte aligned,
+ * holding the device-status word (zeroed once).  Asynchronous on `stream`, allocation-free, graph
  * capturable.
  */
 int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const void* k, const void* v,

@@ -37,13 +37,17 @@
 // its copies and products, frees its tensor memory and leaves.
 //
 // Splits: where the tiles alone would leave SMs idle, each request's states are
-// cut into ranges of keys_per_split; a split leaves its normalised rows in fp32
-// with their log-sum-exp, and a second kernel combines them.
+// cut into up to 8 ranges, whose CTAs form a cluster.  Each leaves its
+// normalised rows in fp32 with their log-sum-exp in its own shared memory, and
+// after a cluster barrier every CTA combines a share of the rows, in split
+// order, from its peers' shared memory: no partial goes to global memory and no
+// second kernel follows.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <mutex>
@@ -62,6 +66,7 @@ using namespace tcc;
 
 constexpr int kM = 128;
 constexpr int kMaxRing = 12;
+constexpr int kMaxSplits = 8;            // CTAs of a cluster that any GPU schedules
 constexpr float kCrossRescale = 8.0f;   // log2 units: O is rescaled when a row's maximum grows by more
 
 constexpr int kBN = 64;                 // states a tile
@@ -85,9 +90,18 @@ struct CrossLayout {
     // products, whose issue is what bounds long prompts.
     static constexpr int kSlotTiles = NQ;
     static constexpr int kSlotBytes = kSlotTiles * kTileBytes;
-    static constexpr int kFit = (kMax - 1024 - kAux - NQ * kQBytes) / kSlotBytes;
-    static constexpr int kRing = kFit > kMaxRing ? kMaxRing : kFit;
-    static constexpr int kSmem = 1024 + kAux + NQ * kQBytes + kRing * kSlotBytes;
+    static constexpr int fit(int bytes) {
+        const int n = (bytes - 1024 - kAux - NQ * kQBytes) / kSlotBytes;
+        return n > kMaxRing ? kMaxRing : n;
+    }
+    static constexpr int smem(int ring) { return 1024 + kAux + NQ * kQBytes + ring * kSlotBytes; }
+    static constexpr int kRing = fit(kMax);
+    static constexpr int kDeepRing = fit(232448);          // a launch of at most one CTA an SM
+    // P V barriers in use: one a slot (NQ = 2), or enough that a phase cannot be mistaken for the next
+    static constexpr int kPv = NQ == 2 ? kRing : 4;
+    // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), and their log-sum-exps
+    static constexpr int kRowFloats = D + 4;
+    static_assert(NQ * kM * (kRowFloats + 1) * 4 <= NQ * kQBytes + kRing * kSlotBytes, "epilogue staging");
     __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (2 * i + b) * kBN; }
     static constexpr int kThreads = 128 + NQ * 128;
     static_assert(kNeed <= 512, "tensor memory");
@@ -139,7 +153,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // one kind, and a low word that a constant step moves along the tile: the
 // issuing thread adds to one register instead of building 64 bits each time.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
-    return (saddr >> 4) | ((lbo_bytes >> 4) << 16);      // (shared addresses stay below 2^18)
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);   // (in a cluster the address has the rank above bit 23)
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 B apart, version 1, 128-byte swizzle
 __device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
@@ -160,6 +174,30 @@ __device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
         "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi)
         : "memory");
+}
+
+// Thread-block cluster: all threads of all its CTAs (those that left count as
+// arrived), and shared memory of the CTA of a given rank.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ float4 ld_peer_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // The request's rows and states, checked.
@@ -188,58 +226,34 @@ __global__ void __launch_bounds__(CrossLayout<D, NQ>::kThreads, CrossLayout<D, N
 cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
     using L = CrossLayout<D, NQ>;
-    constexpr int BN = kBN, RING = L::kRing;
+    constexpr int BN = kBN, PV = L::kPv;
+    const int RING = NQ == 2 ? L::kRing : p.ring;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
+    const int tile = blockIdx.x / p.max_splits, split = blockIdx.x % p.max_splits;   // (split: the rank in the cluster)
     const int kvh = blockIdx.y, r = blockIdx.z;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
-    unsigned char* sQ = smem;
-    unsigned char* ring = smem + NQ * L::kQBytes;
-    CrossAux* aux = reinterpret_cast<CrossAux*>(ring + RING * L::kSlotBytes);
+    CrossAux* aux = reinterpret_cast<CrossAux*>(smem);
+    unsigned char* sQ = smem + L::kAux;
+    unsigned char* ring = sQ + NQ * L::kQBytes;
     volatile int* abort = &aux->abort;
-
-    pdl_wait_primary();
-    CrossReq q;
-    const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
-    if (!cross_request(p, r, reporter ? p.status : nullptr, q)) return;
-    const int lo = tile * NQ * p.wt;               // first window row of the CTA
-    if (lo >= q.w) return;
-    const int nsplits = max(1, (q.len + p.keys_per_split - 1) / p.keys_per_split);
-    if (split >= nsplits) return;
-    const int G = p.group;
-    const int nact = (NQ == 2 && lo + p.wt < q.w) ? 2 : 1;
-    const int key_lo = split * p.keys_per_split;
-    const int key_hi = min(key_lo + p.keys_per_split, q.len);
-    const int T = (key_hi - key_lo + BN - 1) / BN;
-    const int tail = key_hi - (key_lo + (T - 1) * BN);     // states of the last tile
-    if (T == 0) {                                  // no states
-        const int rows = min(q.w - lo, NQ * p.wt);
-        for (int u = tid; u < rows * G * (D / 8); u += L::kThreads) {
-            const int c = u % (D / 8), m = u / (D / 8);
-            const size_t at = (size_t)(q.row0 + lo + m / G) * p.num_q_heads + kvh * G + m % G;
-            st_global_v4(p.o + at * D + c * 8, make_uint4(0u, 0u, 0u, 0u));
-            if (c == 0 && p.lse) p.lse[at] = -INFINITY;
-        }
-        return;
-    }
 
     if (tid == 0) {
         for (int s = 0; s < RING; ++s) {
             mbar_init(&aux->full[s], 1);
             mbar_init(&aux->empty[s], 1);
-            mbar_init(&aux->pv_done[0][s], 1);
-            mbar_init(&aux->pv_done[1][s], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NQ; ++i) {
+            for (int s = 0; s < PV; ++s) mbar_init(&aux->pv_done[i][s], 1);
             mbar_init(&aux->q_full[i], 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&aux->s_full[i][b], 1);
                 mbar_init(&aux->p_full[i][b], 4);
             }
-            mbar_init(&aux->drain[i], 1);
         }
+        mbar_init(&aux->drain[0], 1);
+        mbar_init(&aux->drain[1], 1);
         aux->abort = 0;
         fence_mbarrier_init();
         fence_proxy_async_smem();
@@ -248,10 +262,40 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         tma_prefetch_desc(&tmv);
     }
     if (warp == 3) tmem_alloc(&aux->tmem_base, L::kCols);
+    // up to here the CTA touched only its own resources, while the previous kernel drains
+    pdl_wait_primary();
+    CrossReq q;
+    const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
+    bool active = cross_request(p, r, reporter ? p.status : nullptr, q);
+    const int lo = tile * NQ * p.wt;               // first window row of the CTA
+    const int nsplits = active ? max(1, (q.len + p.keys_per_split - 1) / p.keys_per_split) : 0;
+    active = active && lo < q.w && split < nsplits;
+    const int G = p.group;
+    const int nact = (NQ == 2 && lo + p.wt < q.w) ? 2 : 1;
+    const int rows = min(q.w - lo, NQ * p.wt) * G; // query rows of the CTA, wt * G of them in its first tile
+    const int key_lo = split * p.keys_per_split;
+    const int key_hi = min(key_lo + p.keys_per_split, q.len);
+    const int T = active ? (key_hi - key_lo + BN - 1) / BN : 0;
+    const int tail = key_hi - (key_lo + (T - 1) * BN);     // states of the last tile
+    // row m of the CTA: its place in O and LSE
+    auto place = [&](int m) { return (size_t)(q.row0 + lo + m / G) * p.num_q_heads + kvh * G + m % G; };
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = aux->tmem_base;
+    float* stage = reinterpret_cast<float*>(sQ);           // (epilogue)
+    float* stage_lse = stage + NQ * kM * L::kRowFloats;
+    if (T == 0) {                                  // no work, or no states
+        if (active) {
+            for (int u = tid; u < rows * (D / 8); u += L::kThreads) {
+                const size_t at = place(u / (D / 8));
+                st_global_v4(p.o + at * D + u % (D / 8) * 8, make_uint4(0u, 0u, 0u, 0u));
+                if (u % (D / 8) == 0 && p.lse) p.lse[at] = -INFINITY;
+            }
+        }
+        if (warp == 3) tmem_dealloc(tmem, L::kCols);
+        return;
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------------ copies
@@ -293,7 +337,10 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             issued = n + 1;
         }
         if (*abort && lane == 0) {
-            drain_copies<RING>(aux->full, issued);
+            for (int n = max(0, issued - RING); n < issued; ++n) {
+                volatile int go_on = 0;
+                mbar_wait(&aux->full[n % RING], (n / RING) & 1, &go_on, kDrainLimit);
+            }
             volatile int no_abort = 0;
             for (int i = 0; i < nact; ++i) mbar_wait(&aux->q_full[i], 0, &no_abort, kDrainLimit);
         }
@@ -309,17 +356,18 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, kWaitLimit); };
             // the ring slots of K_t and V_t, and the slot t mod ring, stepped along with the parity of their phase
             struct Step {
-                int slot;
+                int size, slot;
                 uint32_t par;
                 __device__ __forceinline__ void by(int n) {
                     slot += n;
-                    if (slot >= RING) {
-                        slot -= RING;
+                    if (slot >= size) {
+                        slot -= size;
                         par ^= 1;
                     }
                 }
             };
-            Step ks = {0, 0}, vs = {NQ == 1 ? 1 : 0, 0}, done = {0, 0}, before = {0, 0};   // (before: t - 2 of the next S)
+            Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
+            Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - 2 of the next S)
             // S_t, once K_t is here and the P that sat in S_t's buffer has been read
             auto do_s = [&](int t) {
                 const int b = t & 1;
@@ -428,7 +476,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             m_ref = ref;
             if (t > 0 && __any_sync(kFullMask, valid && need)) {
                 // every earlier P V has to be in
-                if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % RING], ((t - 1) / RING) & 1, abort))) break;
+                if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % PV], ((t - 1) / PV) & 1, abort))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
@@ -458,14 +506,14 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
         }
-        if (ok) ok = wait_warp(&aux->pv_done[i][(T - 1) % RING], ((T - 1) / RING) & 1, abort);
+        // both tiles' products are done: the query tiles and the ring are free
+        for (int j = 0; j < NQ; ++j)
+            if (ok && j < nact) ok = wait_warp(&aux->pv_done[j][(T - 1) % PV], ((T - 1) / PV) & 1, abort);
         pdl_launch_dependents();
         tc_fence_after();
         if (ok) {
-            const size_t at = (size_t)(q.row0 + wrow) * p.num_q_heads + kvh * G + m % G;
-            const float inv = 1.f / l_sum, lse2 = m_ref + log2f(l_sum);
-            const bool final_out = nsplits == 1;
-            const size_t part = (size_t)split * p.total_rows * p.num_q_heads + at;
+            float* row = stage + (i * p.wt * G + m) * L::kRowFloats;   // (rows past the tile's wt * G are not written)
+            const float inv = 1.f / l_sum;
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
                 float ov[32];
@@ -473,29 +521,11 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 tmem_wait_ld();
                 if (!valid) continue;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) ov[e] *= inv;
-                if (final_out) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const __nv_bfloat162 h2 = __floats2bfloat162_rn(ov[e + 2 * k], ov[e + 2 * k + 1]);
-                            w[k] = *reinterpret_cast<const uint32_t*>(&h2);
-                        }
-                        st_global_v4(p.o + at * D + ch * 32 + e, make_uint4(w[0], w[1], w[2], w[3]));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(p.ws_o + part * D + ch * 32 + e) =
-                            make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
-                }
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4*>(row + ch * 32 + e) =
+                        make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
             }
-            if (valid) {
-                if (!final_out) p.ws_lse[part] = lse2;
-                else if (p.lse) p.lse[at] = lse2 * kLn2;
-            }
+            if (valid) stage_lse[i * p.wt * G + m] = m_ref + log2f(l_sum);
         }
     }
     tc_fence_before();
@@ -505,43 +535,59 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         tmem_dealloc(tmem, L::kCols);
     }
     if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
-}
-
-// Combine the splits: a thread takes four elements of a (row, head).
-constexpr int kCombThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kCombThreads) cross_combine_kernel(const CrossParams p) {
-    constexpr int kVec = D / 4;
-    pdl_wait_primary();
-    pdl_launch_dependents();
-    const int r = blockIdx.y;
-    CrossReq q;
-    if (!cross_request(p, r, nullptr, q)) return;
-    const int n = (q.len + p.keys_per_split - 1) / p.keys_per_split;
-    if (n <= 1) return;
-    const size_t stride = (size_t)p.total_rows * p.num_q_heads;
-    const long long units = (long long)q.w * p.num_q_heads * kVec;
-    for (long long u = (long long)blockIdx.x * kCombThreads + threadIdx.x; u < units;
-         u += (long long)gridDim.x * kCombThreads) {
-        const size_t at = (size_t)q.row0 * p.num_q_heads + u / kVec;
-        const int c = (int)(u % kVec) * 4;
-        float mx = -INFINITY;
-        for (int s = 0; s < n; ++s) mx = fmaxf(mx, p.ws_lse[s * stride + at]);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        for (int s = 0; s < n; ++s) {
-            const float w = fast_exp2(p.ws_lse[s * stride + at] - mx);
-            const float4 o = *reinterpret_cast<const float4*>(p.ws_o + (s * stride + at) * D + c);
-            a.x = fmaf(w, o.x, a.x); a.y = fmaf(w, o.y, a.y); a.z = fmaf(w, o.z, a.z); a.w = fmaf(w, o.w, a.w);
-            sum += w;
+    // ---------------------------------------------------------------- rows out, 8 elements a thread
+    constexpr int C8 = D / 8;
+    auto put = [&](int m, int c, const float4& a, const float4& b) {
+        uint4 v;
+        const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.x, a.y), h1 = __floats2bfloat162_rn(a.z, a.w);
+        const __nv_bfloat162 h2 = __floats2bfloat162_rn(b.x, b.y), h3 = __floats2bfloat162_rn(b.z, b.w);
+        v.x = *reinterpret_cast<const uint32_t*>(&h0);
+        v.y = *reinterpret_cast<const uint32_t*>(&h1);
+        v.z = *reinterpret_cast<const uint32_t*>(&h2);
+        v.w = *reinterpret_cast<const uint32_t*>(&h3);
+        st_global_v4(p.o + place(m) * D + c * 8, v);
+    };
+    if (nsplits == 1) {
+        if (*abort) return;
+        for (int u = tid; u < rows * C8; u += L::kThreads) {
+            const int m = u / C8, c = u % C8;
+            const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
+            put(m, c, src[0], src[1]);
+            if (c == 0 && p.lse) p.lse[place(m)] = stage_lse[m] * kLn2;
         }
-        const float inv = 1.f / sum;
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.x * inv, a.y * inv);
-        const __nv_bfloat162 h1 = __floats2bfloat162_rn(a.z * inv, a.w * inv);
-        *reinterpret_cast<uint2*>(p.o + at * D + c) = make_uint2(*reinterpret_cast<const uint32_t*>(&h0),
-                                                                 *reinterpret_cast<const uint32_t*>(&h1));
-        if (c == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+        return;
     }
+    __syncwarp();
+    cluster_sync();                                // every split's rows are in its shared memory
+    if (!*abort) {
+        const uint32_t rows_at = smem_addr(stage), lse_at = smem_addr(stage_lse);
+        for (int u = split * L::kThreads + tid; u < rows * C8; u += nsplits * L::kThreads) {
+            const int m = u / C8, c = u % C8;
+            float ls[kMaxSplits], mx = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                ls[k] = k < nsplits ? ld_peer(peer_addr(lse_at + m * 4, k)) : -INFINITY;
+                mx = fmaxf(mx, ls[k]);
+            }
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll
+            for (int k = 0; k < kMaxSplits; ++k) {
+                if (k >= nsplits) break;
+                const uint32_t from = peer_addr(rows_at + (m * L::kRowFloats + c * 8) * 4, k);
+                const float4 x = ld_peer_v4(from), y = ld_peer_v4(from + 16);
+                const float w = fast_exp2(ls[k] - mx);
+                a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
+                b.x = fmaf(w, y.x, b.x); b.y = fmaf(w, y.y, b.y); b.z = fmaf(w, y.z, b.z); b.w = fmaf(w, y.w, b.w);
+                sum += w;
+            }
+            const float inv = 1.f / sum;
+            put(m, c, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
+                make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv));
+            if (c == 0 && p.lse) p.lse[place(m)] = (mx + log2f(sum)) * kLn2;
+        }
+    }
+    __syncwarp();
+    cluster_sync();                                // no CTA leaves while its rows are being read
 }
 
 using CrossKernel = void (*)(const CrossParams, const CUtensorMap, const CUtensorMap, const CUtensorMap);
@@ -549,12 +595,14 @@ using CrossKernel = void (*)(const CrossParams, const CUtensorMap, const CUtenso
 // What a launch of (d, query tiles a CTA) needs.
 struct CrossVariant {
     CrossKernel kernel;
-    int threads, smem, ctas;
+    int threads, ctas;             // CTAs an SM holds at the shallow ring
+    int ring, smem, deep_ring, deep_smem;
 };
 template <int D, int NQ>
 CrossVariant variant_of() {
     using L = CrossLayout<D, NQ>;
-    return {&cross_attn_kernel<D, NQ>, L::kThreads, L::kSmem, L::kCtas};
+    return {&cross_attn_kernel<D, NQ>, L::kThreads, L::kCtas, L::kRing, L::smem(L::kRing),
+            NQ == 2 ? L::kRing : L::kDeepRing, NQ == 2 ? L::smem(L::kRing) : L::smem(L::kDeepRing)};
 }
 CrossVariant cross_variant(int d, int nq) {
     switch (d) {
@@ -603,7 +651,7 @@ struct spec_attn_cross_plan {
     int tiles;
     int keys_per_split;
     int max_splits;
-    size_t lse_off, o_off, ws_bytes;
+    int ring, smem;
     float sm_scale;
     spec_attn::CrossVariant variant;
     // tensor maps of the last (q, k, v): a loop on the same buffers encodes them once
@@ -616,26 +664,28 @@ namespace {
 
 bool cross_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
-// States a split takes.  Model: a CTA costs a fixed start and end plus its states at its SM's share of the HBM
-// rate, waves of one CTA (or two) an SM; splitting adds the second kernel.
-int choose_split(const spec_attn_cross_problem& p, int tiles, int bn, int num_sms, int per_sm) {
-    num_sms *= per_sm;
-    const double key_us = 4.0 * p.head_dim / (6.5e6 / num_sms), fixed_us = 3.0, combine_us = 3.0;
-    const int64_t ctas = static_cast<int64_t>(tiles) * p.num_kv_heads * p.num_reqs;
-    const int64_t units = (static_cast<int64_t>(p.max_kv_len) + bn - 1) / bn;
+// States a split takes (a multiple of the tile).
+int choose_split(const spec_attn_cross_problem& p, const spec_attn_cross_plan& plan) {
+    const int64_t units = (static_cast<int64_t>(p.max_kv_len) + spec_attn::kBN - 1) / spec_attn::kBN;
+    const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
+    // Model (us): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
+    // cluster's barriers; the states come from HBM at best at its rate.
+    const double fixed = 3.0, tile = plan.nq == 2 ? 0.85 : 0.5, cluster = 1.0;
+    const double hbm = static_cast<double>(p.num_reqs) * p.max_kv_len * p.num_kv_heads * p.head_dim * 4.0 / 6.5e6;
     double best = 1e300;
     int64_t best_u = units < 1 ? 1 : units;
-    for (int64_t s = 1; s <= units && s <= 64; ++s) {
+    for (int64_t s = 1; s <= units && s <= spec_attn::kMaxSplits; ++s) {
         const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
-        const int64_t waves = (ctas * splits + num_sms - 1) / num_sms;
-        const double cost = static_cast<double>(waves) * (fixed_us + static_cast<double>(u * bn) * key_us) +
-                            (splits > 1 ? combine_us : 0.0);
-        if (cost < best * 0.999) {
+        const int64_t slots = static_cast<int64_t>(plan.num_sms) * (ctas * splits <= plan.num_sms ? 1 : plan.variant.ctas);
+        const int64_t waves = (ctas * splits + slots - 1) / slots;
+        const double cta = fixed + static_cast<double>(u) * tile + (splits > 1 ? cluster : 0.0);
+        const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed);
+        if (cost < best * 0.98) {
             best = cost;
             best_u = u;
         }
     }
-    return static_cast<int>(best_u * bn);
+    return static_cast<int>(best_u * spec_attn::kBN);
 }
 
 }  // namespace
@@ -654,7 +704,7 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
         return SPEC_ATTN_E_INVALID_ARG;
     if (p.head_dim != 64 && p.head_dim != 128 && p.head_dim != 256) return SPEC_ATTN_E_UNSUPPORTED;
     const int G = p.num_q_heads / p.num_kv_heads;
-    if (G > SPEC_ATTN_MAX_GROUP || p.num_reqs > 65535 || p.num_kv_heads > 65535) return SPEC_ATTN_E_UNSUPPORTED;
+    if (p.force_splits > spec_attn::kMaxSplits || G > SPEC_ATTN_MAX_GROUP || p.num_reqs > 65535 || p.num_kv_heads > 65535) return SPEC_ATTN_E_UNSUPPORTED;
     const int64_t dense = static_cast<int64_t>(p.num_kv_heads) * p.head_dim;
     if (p.kv_row_stride != 0 && (p.kv_row_stride < dense || p.kv_row_stride % 8 != 0)) return SPEC_ATTN_E_INVALID_ARG;
     int dev = 0, sms = 0;
@@ -672,34 +722,29 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     plan->nq = (p.head_dim <= 128 && p.max_q_rows > plan->wt) ? 2 : 1;
     plan->tiles = static_cast<int>((static_cast<int64_t>(p.max_q_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
     plan->variant = spec_attn::cross_variant(p.head_dim, plan->nq);
-    e = cudaFuncSetAttribute(plan->variant.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan->variant.smem);
+    e = cudaFuncSetAttribute(plan->variant.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             plan->variant.deep_smem);
     if (e != cudaSuccess) {
         delete plan;
         return spec_attn::record_cuda_error(e);
     }
-    const int bn = spec_attn::kBN;
     if (p.force_splits > 0) {
-        const int64_t units = (static_cast<int64_t>(p.max_kv_len) + bn - 1) / bn;
+        const int64_t units = (static_cast<int64_t>(p.max_kv_len) + spec_attn::kBN - 1) / spec_attn::kBN;
         const int64_t u = (units + p.force_splits - 1) / p.force_splits;
-        plan->keys_per_split = static_cast<int>((u < 1 ? 1 : u) * bn);
+        plan->keys_per_split = static_cast<int>((u < 1 ? 1 : u) * spec_attn::kBN);
     } else {
-        plan->keys_per_split = choose_split(p, plan->tiles, bn, sms, plan->variant.ctas);
+        plan->keys_per_split = choose_split(p, *plan);
     }
     plan->max_splits = p.max_kv_len == 0 ? 1 : (p.max_kv_len - 1) / plan->keys_per_split + 1;
     if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
         delete plan;
         return SPEC_ATTN_E_UNSUPPORTED;
     }
-    const size_t pairs = static_cast<size_t>(p.total_q_rows) * p.num_q_heads;
-    size_t ws = 256;
-    plan->lse_off = plan->o_off = ws;
-    if (plan->max_splits > 1) {
-        ws += (plan->max_splits * pairs * sizeof(float) + 255) / 256 * 256;
-        plan->o_off = ws;
-        ws += plan->max_splits * pairs * p.head_dim * sizeof(float);
-    }
-    plan->ws_bytes = ws;
-    if (workspace_bytes) *workspace_bytes = ws;
+    // one CTA an SM at most: a deeper ring hides the latency that a second CTA would
+    const bool deep = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms;
+    plan->ring = deep ? plan->variant.deep_ring : plan->variant.ring;
+    plan->smem = deep ? plan->variant.deep_smem : plan->variant.smem;
+    if (workspace_bytes) *workspace_bytes = 256;
     *out = plan;
     return SPEC_ATTN_OK;
 }
@@ -722,28 +767,26 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
         return SPEC_ATTN_E_INVALID_ARG;
     if (p.total_kv_rows > 0 && (!k || !v || !cross_aligned(k, 16) || !cross_aligned(v, 16)))
         return SPEC_ATTN_E_INVALID_ARG;
-    if (workspace_bytes < plan->ws_bytes) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < 256) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return record_cuda_error(e);
     if (dev != plan->device) return SPEC_ATTN_E_INVALID_ARG;
 
-    unsigned char* ws = static_cast<unsigned char*>(workspace);
     CrossParams c = {};
     c.q_indptr = q_indptr;
     c.kv_start = kv_start;
     c.kv_len = kv_len;
     c.o = static_cast<uint16_t*>(o);
     c.lse = lse;
-    c.ws_lse = reinterpret_cast<float*>(ws + plan->lse_off);
-    c.ws_o = reinterpret_cast<float*>(ws + plan->o_off);
-    c.status = reinterpret_cast<unsigned int*>(ws);
+    c.status = static_cast<unsigned int*>(workspace);
     c.total_rows = p.total_q_rows;
     c.max_rows = p.max_q_rows;
     c.num_q_heads = p.num_q_heads;
     c.group = p.num_q_heads / p.num_kv_heads;
     c.wt = plan->wt;
-    c.tiles = plan->tiles;
+    c.max_splits = plan->max_splits;
+    c.ring = plan->ring;
     c.total_kv = p.total_kv_rows;
     c.max_kv_len = p.max_kv_len;
     c.keys_per_split = plan->keys_per_split;
@@ -757,7 +800,7 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
         if (std::memcmp(key, mp->maps_key, sizeof(key)) != 0) {
             std::memset(mp->maps, 0, sizeof(mp->maps));
             std::memset(mp->maps_key, 0, sizeof(mp->maps_key));
-            const int bn = spec_attn::kBN;
+            const int bn = kBN;
             // (with no state rows at all no copy is made: the maps stay empty)
             if (p.total_kv_rows > 0 &&
                 !(encode_rows(&mp->maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim,
@@ -774,27 +817,19 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     cfg.gridDim = dim3(static_cast<unsigned>(plan->tiles * plan->max_splits), static_cast<unsigned>(p.num_kv_heads),
                        static_cast<unsigned>(p.num_reqs));
     cfg.blockDim = dim3(static_cast<unsigned>(plan->variant.threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(plan->variant.smem);
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan->smem);
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan->max_splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = plan->max_splits > 1 ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, plan->variant.kernel, c, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess) return record_cuda_error(e);
-    if (plan->max_splits > 1) {
-        const int64_t units = static_cast<int64_t>(p.max_q_rows) * p.num_q_heads * (p.head_dim / 4);
-        int64_t blocks = (units + kCombThreads - 1) / kCombThreads;
-        if (blocks > 1024) blocks = 1024;
-        cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(p.num_reqs));
-        cfg.blockDim = dim3(kCombThreads);
-        cfg.dynamicSmemBytes = 0;
-        e = p.head_dim == 64    ? cudaLaunchKernelEx(&cfg, &cross_combine_kernel<64>, c)
-            : p.head_dim == 128 ? cudaLaunchKernelEx(&cfg, &cross_combine_kernel<128>, c)
-                                : cudaLaunchKernelEx(&cfg, &cross_combine_kernel<256>, c);
-        if (e != cudaSuccess) return record_cuda_error(e);
-    }
     return SPEC_ATTN_OK;
 }
 

@@ -276,15 +276,14 @@ struct CrossParams {
     const int32_t* kv_len;      // [P]
     uint16_t* o;                // [total_rows, Hq, d] bf16 bits
     float* lse;                 // [total_rows, Hq] or nullptr
-    float* ws_lse;              // split partials: [split][total_rows * Hq], base 2
-    float* ws_o;                // [split][total_rows * Hq][d], normalised
     unsigned int* status;
     int total_rows;
     int max_rows;               // of a request
     int num_q_heads;
     int group;
     int wt;                     // window rows of a query tile: 128 / group
-    int tiles;                  // CTAs along a request's rows
+    int max_splits;             // CTAs of a cluster
+    int ring;                   // ring slots of a one-tile CTA
     int total_kv;
     int max_kv_len;
     int keys_per_split;

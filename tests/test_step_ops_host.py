@@ -189,6 +189,7 @@ def test_cpu_tensors_are_refused(lib, monkeypatch):
     (dict(sm_scale=-0.5), sa.SPEC_ATTN_E_INVALID_ARG),
     (dict(sm_scale=float("nan")), sa.SPEC_ATTN_E_INVALID_ARG),
     (dict(force_splits=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(force_splits=9), sa.SPEC_ATTN_E_UNSUPPORTED),           # a cluster has at most 8 CTAs
     (dict(kv_row_stride=248), sa.SPEC_ATTN_E_INVALID_ARG),      # below the dense row (256)
     (dict(kv_row_stride=260), sa.SPEC_ATTN_E_INVALID_ARG),      # not a multiple of 8
 ])
