@@ -78,11 +78,14 @@ struct CrossLayout {
     static constexpr int kQBytes = kM * D * 2;             // one query tile
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
     static constexpr int kAux = 1024;
-    static constexpr int kNeed = NQ * D + NQ * 2 * kBN;
-    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;
-    // one tile up to d = 128: half of the SM's tensor memory, so two CTAs share
-    // an SM and one's start and end hide under the other's stream
-    static constexpr int kCtas = kCols == 256 ? 2 : 1;
+    // S buffers of a tile, as a power of two.  Two tiles: two each (all there is at d = 128).
+    // One tile: four, so that S_{t+1} does not wait for P V of tile t - 1; but up to d = 128 a
+    // launch of more CTAs than SMs takes two buffers, half of the SM's tensor memory, and two CTAs
+    // share an SM, one's start, end and waits under the other's work.
+    static constexpr int kCtas = (NQ == 1 && D <= 128) ? 2 : 1;
+    __host__ __device__ static constexpr int buf_shift(bool deep) { return NQ == 1 && (deep || D == 256) ? 2 : 1; }
+    __host__ __device__ static constexpr int cols(bool deep) { return NQ * (D + (kBN << buf_shift(deep))) <= 256 ? 256 : 512; }
+    static_assert(NQ * (D + (kBN << buf_shift(true))) <= 512 && cols(false) * kCtas <= 512, "tensor memory");
     static constexpr int kMax = 232448 / kCtas - (kCtas == 2 ? 1024 : 0);   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
     // The ring.  NQ = 1: a slot a tile, K_t and V_t in turn, each let go as soon as
     // it has been read.  NQ = 2: a slot holds K_t and V_t, filled and let go
@@ -97,14 +100,14 @@ struct CrossLayout {
     static constexpr int smem(int ring) { return 1024 + kAux + NQ * kQBytes + ring * kSlotBytes; }
     static constexpr int kRing = fit(kMax);
     static constexpr int kDeepRing = fit(232448);          // a launch of at most one CTA an SM
-    // P V barriers in use: one a slot (NQ = 2), or enough that a phase cannot be mistaken for the next
+    // P V barriers in use: one a slot (NQ = 2), or one an S buffer
     static constexpr int kPv = NQ == 2 ? kRing : 4;
     // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), and their log-sum-exps
     static constexpr int kRowFloats = D + 4;
     static_assert(NQ * kM * (kRowFloats + 1) * 4 <= NQ * kQBytes + kRing * kSlotBytes, "epilogue staging");
+    // first column of buffer b of tile i (one tile: any number of buffers)
     __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (2 * i + b) * kBN; }
     static constexpr int kThreads = 128 + NQ * 128;
-    static_assert(kNeed <= 512, "tensor memory");
     static_assert(kRing >= 4, "tiles ahead of the ones in use");
 };
 
@@ -113,8 +116,8 @@ struct CrossAux {
     uint64_t empty[kMaxRing];           // NQ = 1
     uint64_t pv_done[2][kMaxRing];      // P_t V_t of tile i done: O, P_t's buffer and (NQ = 2) the slot; by t mod ring
     uint64_t q_full[2];
-    uint64_t s_full[2][2];              // [tile][buffer] scores written
-    uint64_t p_full[2][2];              // P written over them (four softmax warps)
+    uint64_t s_full[2][4];              // [tile][buffer] scores written
+    uint64_t p_full[2][4];              // P written over them (four softmax warps)
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -228,6 +231,8 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     using L = CrossLayout<D, NQ>;
     constexpr int BN = kBN, PV = L::kPv;
     const int RING = NQ == 2 ? L::kRing : p.ring;
+    const int SH = (NQ == 2 || D == 256) ? L::buf_shift(true) : p.buf_shift, NB = 1 << SH;   // S buffers of a tile
+    const uint32_t cols = (NQ == 2 || D == 256) ? 512u : L::cols(SH == 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x / p.max_splits, split = blockIdx.x % p.max_splits;   // (split: the rank in the cluster)
     const int kvh = blockIdx.y, r = blockIdx.z;
@@ -247,7 +252,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         for (int i = 0; i < NQ; ++i) {
             for (int s = 0; s < PV; ++s) mbar_init(&aux->pv_done[i][s], 1);
             mbar_init(&aux->q_full[i], 1);
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 mbar_init(&aux->s_full[i][b], 1);
                 mbar_init(&aux->p_full[i][b], 4);
             }
@@ -261,7 +266,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    if (warp == 3) tmem_alloc(&aux->tmem_base, L::kCols);
+    if (warp == 3) tmem_alloc(&aux->tmem_base, cols);
     // up to here the CTA touched only its own resources, while the previous kernel drains
     pdl_wait_primary();
     CrossReq q;
@@ -293,7 +298,8 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 if (u % (D / 8) == 0 && p.lse) p.lse[at] = -INFINITY;
             }
         }
-        if (warp == 3) tmem_dealloc(tmem, L::kCols);
+        __syncwarp();
+        if (warp == 3) tmem_dealloc(tmem, cols);
         return;
     }
 
@@ -367,15 +373,19 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 }
             };
             Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
-            Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - 2 of the next S)
+            // S may lead P V by as many tiles as it has buffers.  An odd ring puts K_t where V of tile
+            // t - (RING + 1) / 2 was, and that V has to be gone before its slot's next phase is waited for
+            // (a wait two phases ahead would take the older one for it).
+            const int lead = min(NB, (RING + 1) / 2);
+            Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - lead of the next S)
             // S_t, once K_t is here and the P that sat in S_t's buffer has been read
             auto do_s = [&](int t) {
-                const int b = t & 1;
-                if (!wait(&aux->full[ks.slot], ks.par)) return false;
-                if (t >= 2) {
+                const int b = t & (NB - 1);
+                if (t >= lead) {
                     if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
                     before.by(1);
                 }
+                if (!wait(&aux->full[ks.slot], ks.par)) return false;
                 tc_fence_after();
                 const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
 #pragma unroll
@@ -391,9 +401,9 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             };
             // O += P_t V_t, once both are here (NQ = 2: V_t came with K_t)
             auto do_pv = [&](int t) {
-                const int b = t & 1;
+                const int b = t & (NB - 1);
                 if (NQ == 1 && !wait(&aux->full[vs.slot], vs.par)) return false;
-                if (!wait(&aux->p_full[i][b], (t >> 1) & 1)) return false;
+                if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
                 tc_fence_after();
                 const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
                 const uint32_t p_tmem = tmem + L::s_col(i, b);
@@ -431,62 +441,71 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         const uint32_t lane_tmem = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const int wrow = lo + i * p.wt + m / G;            // window row
         const bool valid = m < p.wt * G && wrow < q.w;
+        // a warp without rows leaves its scores as they are: they weigh on no other row
+        const bool live = __any_sync(kFullMask, valid);
         const float sc = p.score_scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
         bool ok = true;
         const uint64_t sc2 = pack2(sc, sc);
         for (int t = 0; t < T; ++t) {
-            const int b = t & 1;
-            if (!(ok = wait_warp(&aux->s_full[i][b], (t >> 1) & 1, abort))) break;
+            const int b = t & (NB - 1);
+            if (!(ok = wait_warp(&aux->s_full[i][b], (t >> SH) & 1, abort))) break;
             tc_fence_after();
             const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
-            float sv[BN];
-            tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sv));
-            tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
-            tmem_wait_ld();
-            if (t == T - 1 && tail < BN) {
+            if (live) {
+                __syncwarp();
+                float sv[BN];
+                tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sv));
+                tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+                tmem_wait_ld();
+                if (t == T - 1 && tail < BN) {
 #pragma unroll
-                for (int c = 0; c < BN; ++c) sv[c] = c < tail ? sv[c] : -INFINITY;
-            }
-            float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-            for (int c = 4; c < BN; c += 8) {   // (three-way maxima)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) mx4[k] = fmaxf(fmaxf(mx4[k], sv[c + k]), c + 4 < BN ? sv[c + 4 + k] : mx4[k]);
-            }
-            const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
-            // the reference moves at the first tile, and when the maximum outgrows it
-            const bool need = mx > m_ref + kCrossRescale;
-            const float ref = need ? mx : m_ref;
-            const float alpha = need ? fast_exp2(m_ref - ref) : 1.f;   // (0 at the first tile)
-            const float nref = ref == -INFINITY ? 0.f : -ref;
-            const uint64_t nref2 = pack2(nref, nref);
-            uint32_t pk[BN / 2];
-            uint64_t ps[2] = {0, 0};   // two fp32 zeros each
-#pragma unroll
-            for (int c = 0; c < BN; c += 2) {
-                const float2 x = unpack2(fma2(pack2(sv[c], sv[c + 1]), sc2, nref2));
-                const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
-                ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], pack2(p0, p1));
-                const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
-                pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
-            }
-            const float2 psum = unpack2(add2(ps[0], ps[1]));
-            l_sum = l_sum * alpha + (psum.x + psum.y);
-            m_ref = ref;
-            if (t > 0 && __any_sync(kFullMask, valid && need)) {
-                // every earlier P V has to be in
-                if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % PV], ((t - 1) / PV) & 1, abort))) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    float ov[32];
-                    tmem_ld32(lane_tmem + i * D + ch * 32, ov);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                    tmem_st32(lane_tmem + i * D + ch * 32, ov);
+                    for (int c = 0; c < BN; ++c) sv[c] = c < tail ? sv[c] : -INFINITY;
                 }
+                float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+                for (int c = 4; c < BN; c += 8) {   // (three-way maxima)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx4[k] = fmaxf(fmaxf(mx4[k], sv[c + k]), c + 4 < BN ? sv[c + 4 + k] : mx4[k]);
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
+                // the reference moves at the first tile, and when the maximum outgrows it
+                const bool need = mx > m_ref + kCrossRescale;
+                const float ref = need ? mx : m_ref;
+                const float alpha = need ? fast_exp2(m_ref - ref) : 1.f;   // (0 at the first tile)
+                const float nref = ref == -INFINITY ? 0.f : -ref;
+                const uint64_t nref2 = pack2(nref, nref);
+                uint32_t pk[BN / 2];
+                uint64_t ps[2] = {0, 0};   // two fp32 zeros each
+#pragma unroll
+                for (int c = 0; c < BN; c += 2) {
+                    const float2 x = unpack2(fma2(pack2(sv[c], sv[c + 1]), sc2, nref2));
+                    const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                    ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], pack2(p0, p1));
+                    const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                    pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
+                }
+                const float2 psum = unpack2(add2(ps[0], ps[1]));
+                l_sum = l_sum * alpha + (psum.x + psum.y);
+                m_ref = ref;
+                if (t > 0 && __any_sync(kFullMask, valid && need)) {
+                    // every earlier P V has to be in
+                    if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % PV], ((t - 1) / PV) & 1, abort))) break;
+                    tc_fence_after();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        float ov[32];
+                        tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                        tmem_st32(lane_tmem + i * D + ch * 32, ov);
+                    }
+                }
+                tmem_st32u(s_tmem, pk);
+                tmem_wait_st();
             }
             if (t == T - 1 && (tail & 15) != 0) {
                 // The slot's earlier tile was consumed before these scores could be made, so the parity
@@ -500,8 +519,6 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                                  make_uint4(0u, 0u, 0u, 0u));
                 fence_proxy_async_smem();
             }
-            tmem_st32u(s_tmem, pk);
-            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
@@ -514,16 +531,20 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         if (ok) {
             float* row = stage + (i * p.wt * G + m) * L::kRowFloats;   // (rows past the tile's wt * G are not written)
             const float inv = 1.f / l_sum;
+            if (live) {
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-                float ov[32];
-                tmem_ld32(lane_tmem + i * D + ch * 32, ov);
-                tmem_wait_ld();
-                if (!valid) continue;
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float ov[32];
+                    tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                    tmem_wait_ld();
+                    if (valid) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4*>(row + ch * 32 + e) =
-                        make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(row + ch * 32 + e) =
+                                make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
+                    }
+                    __syncwarp();   // the next load takes the whole warp at once
+                }
             }
             if (valid) stage_lse[i * p.wt * G + m] = m_ref + log2f(l_sum);
         }
@@ -532,7 +553,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     __syncthreads();
     if (warp == 3) {
         tc_fence_after();
-        tmem_dealloc(tmem, L::kCols);
+        tmem_dealloc(tmem, cols);
     }
     if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
     // ---------------------------------------------------------------- rows out, 8 elements a thread
@@ -651,7 +672,7 @@ struct spec_attn_cross_plan {
     int tiles;
     int keys_per_split;
     int max_splits;
-    int ring, smem;
+    int ring, smem, buf_shift;
     float sm_scale;
     spec_attn::CrossVariant variant;
     // tensor maps of the last (q, k, v): a loop on the same buffers encodes them once
@@ -670,7 +691,7 @@ int choose_split(const spec_attn_cross_problem& p, const spec_attn_cross_plan& p
     const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
     // Model (us): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
     // cluster's barriers; the states come from HBM at best at its rate.
-    const double fixed = 3.0, tile = plan.nq == 2 ? 0.85 : 0.5, cluster = 1.0;
+    const double fixed = 3.0, tile = plan.nq == 2 ? 0.85 : 0.45, cluster = 1.0;
     const double hbm = static_cast<double>(p.num_reqs) * p.max_kv_len * p.num_kv_heads * p.head_dim * 4.0 / 6.5e6;
     double best = 1e300;
     int64_t best_u = units < 1 ? 1 : units;
@@ -744,6 +765,7 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     const bool deep = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms;
     plan->ring = deep ? plan->variant.deep_ring : plan->variant.ring;
     plan->smem = deep ? plan->variant.deep_smem : plan->variant.smem;
+    plan->buf_shift = deep ? 2 : 1;   // (one tile, d <= 128; the other variants fix theirs)
     if (workspace_bytes) *workspace_bytes = 256;
     *out = plan;
     return SPEC_ATTN_OK;
@@ -787,6 +809,7 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     c.wt = plan->wt;
     c.max_splits = plan->max_splits;
     c.ring = plan->ring;
+    c.buf_shift = plan->buf_shift;
     c.total_kv = p.total_kv_rows;
     c.max_kv_len = p.max_kv_len;
     c.keys_per_split = plan->keys_per_split;
