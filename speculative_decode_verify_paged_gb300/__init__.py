@@ -442,11 +442,18 @@ def spec_attn_last_cuda_error() -> int:
 # --------------------------------------------------------------------------- #
 # Around the attention call: step tables, norm and rotation of q and k
 # --------------------------------------------------------------------------- #
-def _here():
-    """The current device and the handle of its current stream."""
-    import torch
-    dev = torch.cuda.current_device()
-    return dev, torch.cuda.current_stream(dev).cuda_stream
+_torch = None
+
+
+def _here(stream):
+    """torch, the current device, the handle of ``stream`` (None: the device's current stream) and the library."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    dev = _torch.cuda.current_device()
+    raw = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _torch, dev, raw, _lib or load_library()
 
 
 def _bad(t, what, dtype, shape, dev):
@@ -466,9 +473,9 @@ def _dense(t, what, dtype, shape, dev):
     """Address of a contiguous tensor of this type and shape on the device (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _bad(t, what, dtype, shape, dev)
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _bad(t, what, dtype, shape, dev)
 
 
 def _rows(t, what, shape, row_stride, dev, dtype):
@@ -491,21 +498,20 @@ def spec_attn_build_tables(ctx_lens, window_lens, prev_seq_lens, prev_free_count
     """seq_lens, q_indptr, the grown block table and every row's position and
     cache slot from the requests' lengths (asynchronous).  seq_lens may be
     prev_seq_lens or ctx_lens, free_count may be prev_free_count."""
-    import torch
+    torch, dev, cur, lib = _here(stream)
     i32 = torch.int32
-    P, rows, pages = ctx_lens.shape[0], slot_map.shape[0], free_pages.shape[0]
-    dev, cur = _here()
-    prob = spec_attn_tables_problem(P, rows, page_size, pages, block_table.shape[1], max_w, max_seq_len)
-    _check(load_library().spec_attn_build_tables(
+    P, rows, pages, stride = ctx_lens.shape[0], slot_map.shape[0], free_pages.shape[0], block_table.shape[1]
+    prob = spec_attn_tables_problem(P, rows, page_size, pages, stride, max_w, max_seq_len)
+    _check(lib.spec_attn_build_tables(
         ctypes.byref(prob), _dense(ctx_lens, "ctx_lens", i32, (P,), dev),
         _dense(window_lens, "window_lens", i32, (P,), dev), _dense(prev_seq_lens, "prev_seq_lens", i32, (P,), dev),
         _dense(prev_free_count, "prev_free_count", i32, (1,), dev), _dense(free_pages, "free_pages", i32, (pages,), dev),
-        _dense(block_table, "block_table", i32, (P, block_table.shape[1]), dev),
+        _dense(block_table, "block_table", i32, (P, stride), dev),
         _dense(seq_lens, "seq_lens", i32, (P,), dev), _dense(q_indptr, "q_indptr", i32, (P + 1,), dev),
         _dense(free_count, "free_count", i32, (1,), dev), _dense(positions, "positions", i32, (rows,), dev),
         _dense(slot_map, "slot_map", torch.int64, (rows,), dev),
         _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
-        cur if stream is None else stream.cuda_stream), "spec_attn_build_tables")
+        cur), "spec_attn_build_tables")
 
 
 def rope_inv_freq(rot_dim: int, base: float = 10000.0):
@@ -574,8 +580,7 @@ def spec_attn_norm_rope_plan_create(*, num_q_heads, num_kv_heads, head_dim, inv_
     return NormRopePlan(handle, prob)
 
 
-def _norm_rope_args(plan, q, k, q_weight, k_weight, positions, dev):
-    import torch
+def _norm_rope_args(torch, plan, q, k, q_weight, k_weight, positions, dev):
     n = k.shape[0] if q is None else q.shape[0]
     d, st = plan.head_dim, plan.strides
     return n, [plan.handle, n, _rows(q, "q", (n, plan.q_heads, d), st[0], dev, torch.bfloat16),
@@ -588,13 +593,12 @@ def spec_attn_norm_rope(plan: NormRopePlan, q, k, q_weight, k_weight, positions,
     """Norm and rotation of q [n, Hq, d] and k [n, Hkv, d] (asynchronous).
     ``positions`` [num_axes, n] int32; weights [d] fp32 or None (no norm);
     the outputs may be the inputs."""
-    import torch
-    dev, cur = _here()
-    n, rows, rest = _norm_rope_args(plan, q, k, q_weight, k_weight, positions, dev)
-    _check(load_library().spec_attn_norm_rope(
+    torch, dev, cur, lib = _here(stream)
+    n, rows, rest = _norm_rope_args(torch, plan, q, k, q_weight, k_weight, positions, dev)
+    _check(lib.spec_attn_norm_rope(
         *rows, *rest, _rows(q_out, "q_out", (n, plan.q_heads, plan.head_dim), plan.strides[3], dev, torch.bfloat16),
         _rows(k_out, "k_out", (n, plan.kv_heads, plan.head_dim), plan.strides[4], dev, torch.bfloat16),
-        cur if stream is None else stream.cuda_stream), "spec_attn_norm_rope")
+        cur), "spec_attn_norm_rope")
 
 
 def _pool(t, what, shape, page_stride, itemsize, dev, dtype):
@@ -616,14 +620,13 @@ def spec_attn_norm_rope_append(plan: NormRopePlan, q, k, v, q_weight, k_weight, 
                                stream=None):
     """spec_attn_norm_rope with K and V written into the cache slots that
     ``slot_map`` [n] int64 names (asynchronous); rows with a negative slot are skipped."""
-    import torch
-    dev, cur = _here()
+    torch, dev, cur, lib = _here(stream)
     p, d, hkv = plan.problem, plan.head_dim, plan.kv_heads
-    n, rows, rest = _norm_rope_args(plan, q, k, q_weight, k_weight, positions, dev)
+    n, rows, rest = _norm_rope_args(torch, plan, q, k, q_weight, k_weight, positions, dev)
     fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4
     page, kind, size = (p.num_pages, hkv, p.page_size), torch.uint8 if fp4 else torch.bfloat16, 1 if fp4 else 2
     row = (d // 2 if fp4 else d,)
-    _check(load_library().spec_attn_norm_rope_append(
+    _check(lib.spec_attn_norm_rope_append(
         *rows, _rows(v, "v", (n, hkv, d), plan.strides[2], dev, torch.bfloat16), *rest,
         _dense(slot_map, "slot_map", torch.int64, (n,), dev),
         _rows(q_out, "q_out", (n, plan.q_heads, d), plan.strides[3], dev, torch.bfloat16),
@@ -632,7 +635,7 @@ def spec_attn_norm_rope_append(plan: NormRopePlan, q, k, v, q_weight, k_weight, 
         _pool(k_scales, "k_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
         _pool(v_scales, "v_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
         k_gscale, v_gscale, _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
-        cur if stream is None else stream.cuda_stream), "spec_attn_norm_rope_append")
+        cur), "spec_attn_norm_rope_append")
 
 
 class CrossPlan:
@@ -670,16 +673,15 @@ def spec_attn_cross_plan_create(*, num_reqs, total_q_rows, max_q_rows, num_q_hea
 def spec_attn_run_cross(plan: CrossPlan, q, k, v, q_indptr, kv_start, kv_len, o, lse, workspace, stream=None):
     """Attention of each request's query rows to its range of state rows
     (asynchronous).  ``lse`` may be None."""
-    import torch
-    dev, cur = _here()
+    torch, dev, cur, lib = _here(stream)
     bf16, i32, P = torch.bfloat16, torch.int32, plan.reqs
-    _check(load_library().spec_attn_run_cross(
+    _check(lib.spec_attn_run_cross(
         plan.handle, _dense(q, "q", bf16, plan.q_shape, dev), _rows(k, "k", plan.kv_shape, plan.kv_row_stride, dev, bf16),
         _rows(v, "v", plan.kv_shape, plan.kv_row_stride, dev, bf16), _dense(q_indptr, "q_indptr", i32, (P + 1,), dev),
         _dense(kv_start, "kv_start", i32, (P,), dev), _dense(kv_len, "kv_len", i32, (P,), dev),
         _dense(o, "o", bf16, plan.q_shape, dev), _dense(lse, "lse", torch.float32, plan.q_shape[:2], dev),
         _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
-        cur if stream is None else stream.cuda_stream), "spec_attn_run_cross")
+        cur), "spec_attn_run_cross")
 
 
 # --------------------------------------------------------------------------- #

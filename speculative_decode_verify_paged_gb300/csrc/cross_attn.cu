@@ -71,44 +71,47 @@ constexpr float kCrossRescale = 8.0f;   // log2 units: O is rescaled when a row'
 
 constexpr int kBN = 64;                 // states a tile
 
-template <int D, int NQ>
+// DEEP (one tile, d <= 128): the launch has no more CTAs than SMs, and a CTA
+// takes the whole SM; otherwise two CTAs share it, one's start, end and waits
+// under the other's work.  (d = 256 and two tiles always take the whole SM.)
+template <int D, int NQ, bool DEEP>
 struct CrossLayout {
     static_assert(NQ == 1 || D <= 128, "two O tiles and four S buffers fit 512 columns up to d = 128");
     static constexpr int kChunks = D / 64;
     static constexpr int kQBytes = kM * D * 2;             // one query tile
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
     static constexpr int kAux = 1024;
-    // S buffers of a tile, as a power of two.  Two tiles: two each (all there is at d = 128).
-    // One tile: four, so that S_{t+1} does not wait for P V of tile t - 1; but up to d = 128 a
-    // launch of more CTAs than SMs takes two buffers, half of the SM's tensor memory, and two CTAs
-    // share an SM, one's start, end and waits under the other's work.
-    static constexpr int kCtas = (NQ == 1 && D <= 128) ? 2 : 1;
-    __host__ __device__ static constexpr int buf_shift(bool deep) { return NQ == 1 && (deep || D == 256) ? 2 : 1; }
-    __host__ __device__ static constexpr int cols(bool deep) { return NQ * (D + (kBN << buf_shift(deep))) <= 256 ? 256 : 512; }
-    static_assert(NQ * (D + (kBN << buf_shift(true))) <= 512 && cols(false) * kCtas <= 512, "tensor memory");
-    static constexpr int kMax = 232448 / kCtas - (kCtas == 2 ? 1024 : 0);   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
+    static constexpr int kCtas = DEEP ? 1 : 2;
+    // S buffers of a tile (a power of two): two, or four for a lone tile with the SM to itself, whose
+    // S_{t+1} then does not wait for P V of tile t - 1
+    static constexpr int kBufShift = NQ == 1 && DEEP ? 2 : 1;
+    static constexpr int kBufs = 1 << kBufShift;
+    static constexpr int kNeed = NQ * (D + kBufs * kBN);
+    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;   // (a constant at the allocation: the driver counts it)
+    static_assert(kNeed <= 512 && kCols * kCtas <= 512, "tensor memory");
+    // first column of buffer b of tile i
+    __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (kBufs * i + b) * kBN; }
     // The ring.  NQ = 1: a slot a tile, K_t and V_t in turn, each let go as soon as
     // it has been read.  NQ = 2: a slot holds K_t and V_t, filled and let go
     // together: one barrier to wait on and one commit less for each of the
     // products, whose issue is what bounds long prompts.
     static constexpr int kSlotTiles = NQ;
     static constexpr int kSlotBytes = kSlotTiles * kTileBytes;
-    static constexpr int fit(int bytes) {
-        const int n = (bytes - 1024 - kAux - NQ * kQBytes) / kSlotBytes;
-        return n > kMaxRing ? kMaxRing : n;
-    }
-    static constexpr int smem(int ring) { return 1024 + kAux + NQ * kQBytes + ring * kSlotBytes; }
-    static constexpr int kRing = fit(kMax);
-    static constexpr int kDeepRing = fit(232448);          // a launch of at most one CTA an SM
-    // P V barriers in use: one a slot (NQ = 2), or one an S buffer
+    static constexpr int kMax = DEEP ? 232448 : 232448 / 2 - 1024;   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
+    static constexpr int kFit = (kMax - 1024 - kAux - NQ * kQBytes) / kSlotBytes;
+    static constexpr int kRing = kFit > kMaxRing ? kMaxRing : kFit;
+    static constexpr int kSmem = 1024 + kAux + NQ * kQBytes + kRing * kSlotBytes;
+    static_assert(kRing >= 4, "tiles ahead of the ones in use");
+    // S may lead P V by as many tiles as it has buffers.  An odd ring puts K_t where V of tile
+    // t - (ring + 1) / 2 was, and that V has to be gone before its slot's next phase is waited for
+    // (a wait two phases ahead would take the older one for it).
+    static constexpr int kLead = (NQ == 2 || kBufs <= (kRing + 1) / 2) ? kBufs : (kRing + 1) / 2;
+    // P V barriers in use: one a slot (NQ = 2), or one an S buffer and at least four
     static constexpr int kPv = NQ == 2 ? kRing : 4;
     // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), and their log-sum-exps
     static constexpr int kRowFloats = D + 4;
     static_assert(NQ * kM * (kRowFloats + 1) * 4 <= NQ * kQBytes + kRing * kSlotBytes, "epilogue staging");
-    // first column of buffer b of tile i (one tile: any number of buffers)
-    __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (2 * i + b) * kBN; }
     static constexpr int kThreads = 128 + NQ * 128;
-    static_assert(kRing >= 4, "tiles ahead of the ones in use");
 };
 
 struct CrossAux {
@@ -224,15 +227,12 @@ __device__ __forceinline__ bool cross_request(const CrossParams& p, int r, unsig
     return q.w > 0;
 }
 
-template <int D, int NQ>
-__global__ void __launch_bounds__(CrossLayout<D, NQ>::kThreads, CrossLayout<D, NQ>::kCtas)
+template <int D, int NQ, bool DEEP>
+__global__ void __launch_bounds__(CrossLayout<D, NQ, DEEP>::kThreads, CrossLayout<D, NQ, DEEP>::kCtas)
 cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                   const __grid_constant__ CUtensorMap tmv) {
-    using L = CrossLayout<D, NQ>;
-    constexpr int BN = kBN, PV = L::kPv;
-    const int RING = NQ == 2 ? L::kRing : p.ring;
-    const int SH = (NQ == 2 || D == 256) ? L::buf_shift(true) : p.buf_shift, NB = 1 << SH;   // S buffers of a tile
-    const uint32_t cols = (NQ == 2 || D == 256) ? 512u : L::cols(SH == 2);
+    using L = CrossLayout<D, NQ, DEEP>;
+    constexpr int BN = kBN, PV = L::kPv, RING = L::kRing, SH = L::kBufShift, NB = L::kBufs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x / p.max_splits, split = blockIdx.x % p.max_splits;   // (split: the rank in the cluster)
     const int kvh = blockIdx.y, r = blockIdx.z;
@@ -266,9 +266,10 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
     }
-    if (warp == 3) tmem_alloc(&aux->tmem_base, cols);
+    if (warp == 3) tmem_alloc(&aux->tmem_base, L::kCols);
     // up to here the CTA touched only its own resources, while the previous kernel drains
     pdl_wait_primary();
+    pdl_launch_dependents();   // (the next kernel's CTAs set up as these leave their SMs)
     CrossReq q;
     const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
     bool active = cross_request(p, r, reporter ? p.status : nullptr, q);
@@ -299,7 +300,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
             }
         }
         __syncwarp();
-        if (warp == 3) tmem_dealloc(tmem, cols);
+        if (warp == 3) tmem_dealloc(tmem, L::kCols);
         return;
     }
 
@@ -373,15 +374,11 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 }
             };
             Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
-            // S may lead P V by as many tiles as it has buffers.  An odd ring puts K_t where V of tile
-            // t - (RING + 1) / 2 was, and that V has to be gone before its slot's next phase is waited for
-            // (a wait two phases ahead would take the older one for it).
-            const int lead = min(NB, (RING + 1) / 2);
             Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - lead of the next S)
             // S_t, once K_t is here and the P that sat in S_t's buffer has been read
             auto do_s = [&](int t) {
                 const int b = t & (NB - 1);
-                if (t >= lead) {
+                if (t >= L::kLead) {
                     if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
                     before.by(1);
                 }
@@ -526,7 +523,6 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         // both tiles' products are done: the query tiles and the ring are free
         for (int j = 0; j < NQ; ++j)
             if (ok && j < nact) ok = wait_warp(&aux->pv_done[j][(T - 1) % PV], ((T - 1) / PV) & 1, abort);
-        pdl_launch_dependents();
         tc_fence_after();
         if (ok) {
             float* row = stage + (i * p.wt * G + m) * L::kRowFloats;   // (rows past the tile's wt * G are not written)
@@ -553,7 +549,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     __syncthreads();
     if (warp == 3) {
         tc_fence_after();
-        tmem_dealloc(tmem, cols);
+        tmem_dealloc(tmem, L::kCols);
     }
     if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
     // ---------------------------------------------------------------- rows out, 8 elements a thread
@@ -616,21 +612,18 @@ using CrossKernel = void (*)(const CrossParams, const CUtensorMap, const CUtenso
 // What a launch of (d, query tiles a CTA) needs.
 struct CrossVariant {
     CrossKernel kernel;
-    int threads, ctas;             // CTAs an SM holds at the shallow ring
-    int ring, smem, deep_ring, deep_smem;
+    int threads, smem, ctas;   // ctas: on one SM
 };
-template <int D, int NQ>
+template <int D, int NQ, bool DEEP>
 CrossVariant variant_of() {
-    using L = CrossLayout<D, NQ>;
-    return {&cross_attn_kernel<D, NQ>, L::kThreads, L::kCtas, L::kRing, L::smem(L::kRing),
-            NQ == 2 ? L::kRing : L::kDeepRing, NQ == 2 ? L::smem(L::kRing) : L::smem(L::kDeepRing)};
+    using L = CrossLayout<D, NQ, DEEP>;
+    return {&cross_attn_kernel<D, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas};
 }
-CrossVariant cross_variant(int d, int nq) {
-    switch (d) {
-        case 64: return nq == 2 ? variant_of<64, 2>() : variant_of<64, 1>();
-        case 128: return nq == 2 ? variant_of<128, 2>() : variant_of<128, 1>();
-        default: return variant_of<256, 1>();
-    }
+CrossVariant cross_variant(int d, int nq, bool deep) {
+    if (d == 256) return variant_of<256, 1, true>();
+    if (nq == 2) return d == 64 ? variant_of<64, 2, true>() : variant_of<128, 2, true>();
+    if (d == 64) return deep ? variant_of<64, 1, true>() : variant_of<64, 1, false>();
+    return deep ? variant_of<128, 1, true>() : variant_of<128, 1, false>();
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 cross_encode_fn() {
@@ -672,7 +665,6 @@ struct spec_attn_cross_plan {
     int tiles;
     int keys_per_split;
     int max_splits;
-    int ring, smem, buf_shift;
     float sm_scale;
     spec_attn::CrossVariant variant;
     // tensor maps of the last (q, k, v): a loop on the same buffers encodes them once
@@ -687,6 +679,7 @@ bool cross_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>
 
 // States a split takes (a multiple of the tile).
 int choose_split(const spec_attn_cross_problem& p, const spec_attn_cross_plan& plan) {
+    const int shared = spec_attn::cross_variant(p.head_dim, plan.nq, false).ctas;   // CTAs an SM of a larger launch holds
     const int64_t units = (static_cast<int64_t>(p.max_kv_len) + spec_attn::kBN - 1) / spec_attn::kBN;
     const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
     // Model (us): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
@@ -697,7 +690,7 @@ int choose_split(const spec_attn_cross_problem& p, const spec_attn_cross_plan& p
     int64_t best_u = units < 1 ? 1 : units;
     for (int64_t s = 1; s <= units && s <= spec_attn::kMaxSplits; ++s) {
         const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
-        const int64_t slots = static_cast<int64_t>(plan.num_sms) * (ctas * splits <= plan.num_sms ? 1 : plan.variant.ctas);
+        const int64_t slots = static_cast<int64_t>(plan.num_sms) * (ctas * splits <= plan.num_sms ? 1 : shared);
         const int64_t waves = (ctas * splits + slots - 1) / slots;
         const double cta = fixed + static_cast<double>(u) * tile + (splits > 1 ? cluster : 0.0);
         const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed);
@@ -742,13 +735,6 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     plan->wt = 128 / G;
     plan->nq = (p.head_dim <= 128 && p.max_q_rows > plan->wt) ? 2 : 1;
     plan->tiles = static_cast<int>((static_cast<int64_t>(p.max_q_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
-    plan->variant = spec_attn::cross_variant(p.head_dim, plan->nq);
-    e = cudaFuncSetAttribute(plan->variant.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             plan->variant.deep_smem);
-    if (e != cudaSuccess) {
-        delete plan;
-        return spec_attn::record_cuda_error(e);
-    }
     if (p.force_splits > 0) {
         const int64_t units = (static_cast<int64_t>(p.max_kv_len) + spec_attn::kBN - 1) / spec_attn::kBN;
         const int64_t u = (units + p.force_splits - 1) / p.force_splits;
@@ -761,11 +747,13 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
         delete plan;
         return SPEC_ATTN_E_UNSUPPORTED;
     }
-    // one CTA an SM at most: a deeper ring hides the latency that a second CTA would
-    const bool deep = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms;
-    plan->ring = deep ? plan->variant.deep_ring : plan->variant.ring;
-    plan->smem = deep ? plan->variant.deep_smem : plan->variant.smem;
-    plan->buf_shift = deep ? 2 : 1;   // (one tile, d <= 128; the other variants fix theirs)
+    plan->variant = spec_attn::cross_variant(
+        p.head_dim, plan->nq, static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms);
+    e = cudaFuncSetAttribute(plan->variant.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan->variant.smem);
+    if (e != cudaSuccess) {
+        delete plan;
+        return spec_attn::record_cuda_error(e);
+    }
     if (workspace_bytes) *workspace_bytes = 256;
     *out = plan;
     return SPEC_ATTN_OK;
@@ -808,8 +796,6 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     c.group = p.num_q_heads / p.num_kv_heads;
     c.wt = plan->wt;
     c.max_splits = plan->max_splits;
-    c.ring = plan->ring;
-    c.buf_shift = plan->buf_shift;
     c.total_kv = p.total_kv_rows;
     c.max_kv_len = p.max_kv_len;
     c.keys_per_split = plan->keys_per_split;
@@ -840,7 +826,7 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     cfg.gridDim = dim3(static_cast<unsigned>(plan->tiles * plan->max_splits), static_cast<unsigned>(p.num_kv_heads),
                        static_cast<unsigned>(p.num_reqs));
     cfg.blockDim = dim3(static_cast<unsigned>(plan->variant.threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(plan->smem);
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan->variant.smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

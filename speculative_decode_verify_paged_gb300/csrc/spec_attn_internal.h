@@ -283,8 +283,6 @@ struct CrossParams {
     int group;
     int wt;                     // window rows of a query tile: 128 / group
     int max_splits;             // CTAs of a cluster
-    int ring;                   // ring slots of a one-tile CTA
-    int buf_shift;              // log2 of its S buffers
     int total_kv;
     int max_kv_len;
     int keys_per_split;

@@ -166,7 +166,7 @@ def test_rope_helpers():
 
 
 def test_cpu_tensors_are_refused(lib, monkeypatch):
-    monkeypatch.setattr(sa, "_here", lambda: (0, 0))
+    monkeypatch.setattr(sa, "_here", lambda stream: (torch, 0, 0, lib))
     i = torch.zeros(4, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA tensor"):
         sa.spec_attn_build_tables(i, i, i, i[:1], i, i[None].expand(4, 4), i, i, i[:1], i, i.long(),
