@@ -266,6 +266,7 @@ struct NormRopeParams {
     unsigned long long turns[kMaxPairs];   // angle per position, in 2^-64 turns
     uint8_t axis[kMaxPairs];               // position axis of each pair
 };
+cudaError_t norm_rope_prepare(int head_dim);   // the kernels' shared memory, on the current device
 cudaError_t norm_rope_launch(NormRopeParams& p, int head_dim, bool append, int kv_dtype, int num_sms,
                              cudaStream_t stream);
 
