@@ -20,11 +20,12 @@
 // Layout.  A head of d elements is taken by d / 16 adjacent lanes, 16 elements
 // each in two 16-byte pieces: with half-split pairs the pieces at l and l +
 // rot / 16, so that a rotation needs no exchange between lanes; otherwise
-// pieces 2 l and 2 l + 1.  A warp iteration is 512 elements: 2, 4 or 8 heads.  A
-// warp takes one row (or a segment of its heads): its lanes compute the row's
-// cos and sin once, two or four pairs each, and share them through shared
-// memory; every lane then keeps its 8 pairs in registers over the row's heads,
-// and its weights for the whole launch.
+// pieces 2 l and 2 l + 1.  A warp iteration is 512 elements: 2, 4 or 8 heads.  The
+// launch's iterations are dealt out in even runs, one a resident warp (whole
+// rows would leave the last round mostly idle: 4097 rows on 2432 warps).  At
+// each row the lanes compute its cos and sin, two or four pairs each, and share
+// them through shared memory; every lane then keeps its 8 pairs in registers
+// over the row's heads.
 //
 // Loads run kAhead iterations ahead of the arithmetic, across heads, kinds and
 // rows, as asynchronous copies of whole 1 KB iterations into a ring of the
@@ -58,7 +59,7 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
-constexpr int kAhead = 8;               // warp iterations whose loads are in flight (a power of two)
+constexpr int kAhead = 3;               // warp iterations whose loads are in flight
 constexpr int kResident = 2;            // CTAs an SM holds (128 registers a thread)
 
 // 16 bytes into shared memory, not through L1 (in place, this kernel writes what it reads).
@@ -71,33 +72,64 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[16], int at) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A lane's 16 elements as pairs (A_j, B_j), j < 8, two j to a register pair: the
+// two pieces (half-split), or the even and the odd elements (interleaved).
+struct Pairs {
+    uint64_t a[4], b[4];
+};
+__device__ __forceinline__ uint64_t lows(uint32_t v, uint32_t w) { return pack2(v << 16, w << 16); }
+__device__ __forceinline__ uint64_t highs(uint32_t v, uint32_t w) { return pack2(v & 0xFFFF0000u, w & 0xFFFF0000u); }
+__device__ __forceinline__ Pairs unpack16(const uint4& va, const uint4& vb, bool interleaved) {
+    const uint32_t u[4] = {va.x, va.y, va.z, va.w}, w[4] = {vb.x, vb.y, vb.z, vb.w};
+    Pairs x;
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[at + 2 * i] = __uint_as_float(w[i] << 16);
-        x[at + 2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        for (int i = 0; i < 2; ++i) {
+            x.a[i] = lows(u[2 * i], u[2 * i + 1]);
+            x.b[i] = highs(u[2 * i], u[2 * i + 1]);
+            x.a[2 + i] = lows(w[2 * i], w[2 * i + 1]);
+            x.b[2 + i] = highs(w[2 * i], w[2 * i + 1]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x.a[i] = pack2(u[i] << 16, u[i] & 0xFFFF0000u);
+            x.b[i] = pack2(w[i] << 16, w[i] & 0xFFFF0000u);
+        }
     }
+    return x;
 }
-
-__device__ __forceinline__ uint4 pack8(const float (&x)[16], int at) {
-    uint32_t w[4];
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void pack16(const Pairs& x, bool interleaved, uint4& va, uint4& vb) {
+    uint32_t u[4], w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[at + 2 * i], x[at + 2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        const float2 a = unpack2(x.a[i]), b = unpack2(x.b[i]);
+        if (interleaved) {
+            (i < 2 ? u : w)[2 * (i & 1)] = bf16x2(a.x, b.x);
+            (i < 2 ? u : w)[2 * (i & 1) + 1] = bf16x2(a.y, b.y);
+        } else {
+            u[i] = bf16x2(a.x, a.y);
+            w[i] = bf16x2(b.x, b.y);
+        }
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    va = make_uint4(u[0], u[1], u[2], u[3]);
+    vb = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 struct NrShared {
     uint4 ring[kNrWarps][kAhead][64];              // [iteration]: 512 elements of adjacent heads, in order
+    ulonglong2 w[2][64];                           // weights of q and k, four a lane: [four][lane of the head]
     unsigned long long turns[kMaxPairs];
     float cs[kNrWarps][2][kMaxPairs];              // cos and sin of the warp's row
     uint8_t axis[kMaxPairs];
 };
 
 enum Kind { kQ = 0, kK = 1, kV = 2 };
+enum Mode { kWhole, kPart, kInterleaved };   // half-split pairs over the whole head or part of it, pairs side by side
 
 template <int D, bool APPEND, bool FP4>
 struct Row {
@@ -109,9 +141,7 @@ struct Row {
     int warp, lane, l, sub;                        // l: lane within the head; sub: head within the iteration
     int ea, eb;                                    // first elements of the two pieces
     bool turn;                                     // this lane's pairs rotate
-    bool relay;                                    // results leave through the ring
-    float qw[16], kw[16];
-    float c[8], s[8];
+    float c[8], s[8];                              // cos and sin of the lane's pairs
     int row;
     long long slot;
     int pos[kMaxPairs / 32];                       // of the row to come, this lane's pairs
@@ -122,48 +152,74 @@ struct Row {
         return it * kHeads + j * (kHeads / 2) + lane / (D / 8);
     }
 
-    // ---- loads: the warp's items from `item` on, iteration by iteration
-    unsigned items, step, item;                    // item: (row, segment)
-    int load_row, load_it, load_end;               // of the item being loaded
-    unsigned loads, uses;                          // iterations asked for and used so far
-
-    __device__ __forceinline__ void split(unsigned i, int& r, int& it0, int& it1) const {
-        if (p.segs == 1) {
-            r = (int)i;
-            it0 = 0;
-            it1 = p.iters_q + p.iters_k + p.iters_v;
-        } else {
-            r = (int)(i / (unsigned)p.segs);
-            it0 = (int)(i % (unsigned)p.segs) * p.iters_per_seg;
-            it1 = min(it0 + p.iters_per_seg, p.iters_q + p.iters_k + p.iters_v);
+    // ---- the warp's run of iterations, `left` of them from iteration `it` of row `row` on; the loads' own copy of it
+    struct Run {
+        int row, it, end;                          // [it, end): the run's part of the row
+        long long left;                            // beyond this row
+        __device__ __forceinline__ void start(long long from, long long count, int iters) {
+            row = (int)(from / iters);
+            it = (int)(from % iters);
+            left = count;
+            trim(iters);
         }
+        __device__ __forceinline__ void trim(int iters) {
+            end = (int)min((long long)iters, it + left);
+            left -= end - it;
+        }
+        __device__ __forceinline__ bool next(int iters) {
+            if (left == 0) return false;
+            ++row;
+            it = 0;
+            trim(iters);
+            return true;
+        }
+    };
+    Run load;
+    int iters;                                     // of a row
+    bool more;                                     // loads left to ask for
+    int load_slot, use_slot;                       // ring
+    const uint16_t* load_at;                       // this lane's first piece of the next iteration
+    int load_head, load_heads;                     // its head, and the heads of its kind
+    int load_left;                                 // iterations left of the kind
+
+    // the row's iterations of one kind, from load.it on
+    __device__ __forceinline__ void load_kind() {
+        const int q1 = p.iters_q, k1 = q1 + p.iters_k, it = load.it;
+        const int base = it < q1 ? 0 : it < k1 ? q1 : k1;
+        const int stop = min(load.end, it < q1 ? q1 : it < k1 ? k1 : load.end);
+        const uint16_t* src = it < q1 ? p.q : it < k1 ? p.k : p.v;
+        src += (size_t)load.row * (it < q1 ? p.q_row_stride : it < k1 ? p.k_row_stride : p.v_row_stride);
+        load_at = src + (it - base) * 512 + lane * 8;
+        load_head = head_of(it - base, 0);
+        load_heads = it < q1 ? p.num_q_heads : p.num_kv_heads;
+        load_left = stop - it;
+        load.it = stop;
     }
     __device__ __forceinline__ void load_next() {
-        if (item < items) {
-            const int it = load_it;
-            const bool is_q = it < p.iters_q, is_k = it < p.iters_q + p.iters_k;
-            const int i = is_q ? it : is_k ? it - p.iters_q : it - p.iters_q - p.iters_k;   // of its kind
-            const int H = is_q ? p.num_q_heads : p.num_kv_heads;
-            const uint16_t* src = is_q ? p.q : is_k ? p.k : p.v;
-            src += (size_t)load_row * (is_q ? p.q_row_stride : is_k ? p.k_row_stride : p.v_row_stride) + i * 512;
-            const uint32_t dst = sm100::smem_addr(sh.ring[warp][loads % kAhead]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (head_of(i, j) < H) copy16(dst + (lane + 32 * j) * 16, src + (lane + 32 * j) * 8);
-            ++loads;
-            if (++load_it == load_end) {
-                item += step;
-                if (item < items) split(item, load_row, load_it, load_end);
+        if (more) {
+            const uint32_t dst = sm100::smem_addr(&sh.ring[warp][load_slot][lane]);
+            if (load_head < load_heads) copy16(dst, load_at);
+            if (load_head + kHeads / 2 < load_heads) copy16(dst + 512, load_at + 256);
+            load_at += 512;
+            load_head += kHeads;
+            load_slot = load_slot + 1 == kAhead ? 0 : load_slot + 1;
+            if (--load_left == 0) {
+                if (load.it == load.end) more = load.next(iters);
+                if (more) load_kind();
             }
         }
         copies_commit();                           // (one group a call, empty ones too)
     }
+    __device__ __forceinline__ uint4* arrived() {
+        copies_wait<kAhead - 1>();
+        __syncwarp();                              // every lane's copies are in
+        uint4* r = sh.ring[warp][use_slot];
+        use_slot = use_slot + 1 == kAhead ? 0 : use_slot + 1;
+        return r;
+    }
 
     // ---- a row's positions and slot, asked for a row ahead
-    __device__ __forceinline__ void ask(unsigned i) {
-        if (i >= items) return;
-        int r, it0, it1;
-        split(i, r, it0, it1);
+    __device__ __forceinline__ void ask(int r) {
         if (APPEND) next_slot = p.slot_map[r];
 #pragma unroll
         for (int k = 0; k < kMaxPairs / 32; ++k) {
@@ -199,124 +255,138 @@ struct Row {
         }
     }
 
-    __device__ __forceinline__ void rotate(float& a, float& b, int j) const {
-        const float t = a;
-        a = t * c[j] - b * s[j];
-        b = t * s[j] + b * c[j];
+    // w: the kind's weights in shared memory, in the lane's order (nullptr: no norm); ALL: every lane's pairs turn
+    template <bool ALL>
+    __device__ __forceinline__ void norm_rotate(Pairs& x, const ulonglong2* w) const {
+        if (w) {
+            uint64_t s0 = 0, s1 = 0;               // two fp32 zeros each
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s0 = fma2(x.a[i], x.a[i], s0);
+                s1 = fma2(x.b[i], x.b[i], s1);
+            }
+            const float2 st = unpack2(add2(s0, s1));
+            float ss = st.x + st.y;
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+            const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+            const uint64_t r2 = pack2(r, r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const ulonglong2 wa = w[i * kLanes + l], wb = w[(2 + i) * kLanes + l];
+                x.a[2 * i] = mul2(x.a[2 * i], mul2(r2, wa.x));
+                x.a[2 * i + 1] = mul2(x.a[2 * i + 1], mul2(r2, wa.y));
+                x.b[2 * i] = mul2(x.b[2 * i], mul2(r2, wb.x));
+                x.b[2 * i + 1] = mul2(x.b[2 * i + 1], mul2(r2, wb.y));
+            }
+        }
+        if (ALL || turn) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = unpack2(x.a[i]), b = unpack2(x.b[i]);
+                x.a[i] = pack2(a.x * c[2 * i] - b.x * s[2 * i], a.y * c[2 * i + 1] - b.y * s[2 * i + 1]);
+                x.b[i] = pack2(a.x * s[2 * i] + b.x * c[2 * i], a.y * s[2 * i + 1] + b.y * c[2 * i + 1]);
+            }
+        }
     }
 
-    // Warp iterations [it0, it1) of one kind; a row that is skipped is only drained from the ring.
+    // Warp iterations [it0, it1) of one kind.
     template <int KIND>
     __device__ __forceinline__ void heads(int it0, int it1, bool skip) {
+        if (it0 >= it1) return;                    // (every branch here is uniform over the warp)
+        if (skip) {                                // the row is only drained from the ring
+            for (int it = it0; it < it1; ++it) {
+                arrived();
+                load_next();
+            }
+        } else if (KIND == kV) {
+            loop<KIND, kWhole>(it0, it1);
+        } else if (p.interleaved) {
+            loop<KIND, kInterleaved>(it0, it1);
+        } else if (p.rot_dim < D) {
+            loop<KIND, kPart>(it0, it1);
+        } else {
+            loop<KIND, kWhole>(it0, it1);
+        }
+    }
+    template <int KIND, int MODE>
+    __device__ __forceinline__ void loop(int it0, int it1) {
+        constexpr bool kCache = APPEND && KIND != kQ;
+        constexpr bool kQuant = kCache && FP4;     // blocks of 16 adjacent elements: the pieces 2 l and 2 l + 1
         const int H = KIND == kQ ? p.num_q_heads : p.num_kv_heads;
-        const bool norm = KIND == kQ ? p.q_weight != nullptr : p.k_weight != nullptr;
-        // (V is copied: whichever pieces; an NVFP4 block is the pieces 2 l and 2 l + 1)
-        const int a = KIND == kV ? 16 * l : ea, b = KIND == kV ? 16 * l + 8 : eb;
+        const ulonglong2* w = (KIND == kQ ? p.q_weight : p.k_weight) ? &sh.w[KIND == kQ ? 0 : 1][0] : nullptr;
+        constexpr bool interleaved = MODE == kInterleaved;
+        // where the lane's two results go: its own pieces of head it * kHeads + sub, or (in order) the
+        // iteration's pieces lane and lane + 32
+        constexpr bool in_order = !kQuant && (KIND == kV || MODE != kWhole);
+        const int pa = (sub * D + ea) / 8, pb = (sub * D + eb) / 8;             // in the ring, read
+        const int oa = kQuant ? (sub * D + 16 * l) / 8 : in_order ? lane : pa;  // and sent
+        const int ob = kQuant ? oa + 1 : in_order ? lane + 32 : pb;
+        int h0 = it0 * kHeads + oa / (D / 8), h1 = it0 * kHeads + ob / (D / 8);
+        unsigned char *d0, *d1;                    // (quantised: codes, scales)
+        size_t inc0, inc1;
+        if constexpr (!kCache) {
+            uint16_t* out = KIND == kQ ? p.q_out + (size_t)row * p.q_out_row_stride
+                                       : p.k_out + (size_t)row * p.k_out_row_stride;
+            d0 = reinterpret_cast<unsigned char*>(out + it0 * 512 + oa * 8);
+            d1 = reinterpret_cast<unsigned char*>(out + it0 * 512 + ob * 8);
+            inc0 = inc1 = 1024;
+        } else {
+            const long long page = slot >> p.page_shift;
+            const int in_page = (int)(slot & ((1 << p.page_shift) - 1));
+            unsigned char* pool = (KIND == kK ? p.k_pool : p.v_pool) + page * p.kv_page_stride;
+            auto at = [&](int g) { return ((size_t)g << p.page_shift) + in_page; };   // head g's row of the page
+            const size_t rows = (size_t)kHeads << p.page_shift;
+            if constexpr (!kQuant) {
+                d0 = pool + at(h0) * (2 * D) + oa % (D / 8) * 16;
+                d1 = pool + at(h1) * (2 * D) + ob % (D / 8) * 16;
+                inc0 = inc1 = rows * (2 * D);
+            } else {
+                d0 = pool + at(h0) * (D / 2) + l * 8;
+                d1 = (KIND == kK ? p.k_scales : p.v_scales) + page * p.scale_page_stride + at(h0) * (D / 16) + l;
+                inc0 = rows * (D / 2);
+                inc1 = rows * (D / 16);
+            }
+        }
 #pragma unroll 1
         for (int it = it0; it < it1; ++it) {
-            copies_wait<kAhead - 1>();
-            __syncwarp();                          // every lane's copies are in
-            uint4* ring = sh.ring[warp][uses % kAhead];
-            ++uses;
-            const int pa = (sub * D + a) / 8, pb = (sub * D + b) / 8;
-            uint4 va = ring[pa], vb = ring[pb];
-            if (skip) {                            // uniform over the warp
-                __syncwarp();
-                load_next();
-                continue;
-            }
-            const int h = it * kHeads + sub;
-            if (KIND != kV) {
-                float x[16];
-                unpack8(va, x, 0);
-                unpack8(vb, x, 8);
-                if (norm) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-                    const float r = rsqrtf(ss * (1.0f / D) + p.eps);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) x[e] *= r * (KIND == kQ ? qw[e] : kw[e]);
-                }
-                if (turn) {
-                    if (p.interleaved) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) rotate(x[2 * j], x[2 * j + 1], j);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) rotate(x[j], x[8 + j], j);
-                    }
-                }
-                va = pack8(x, 0);
-                vb = pack8(x, 8);
-            }
-            if (KIND == kV ? !FP4 : relay || (APPEND && FP4 && KIND == kK)) {
-                if (KIND != kV) {
+            uint4* ring = arrived();
+            uint4 va, vb;
+            if (KIND == kV) {
+                va = ring[oa];
+                vb = ring[ob];
+            } else {
+                va = ring[pa];
+                vb = ring[pb];
+                Pairs x = unpack16(va, vb, interleaved);
+                norm_rotate<MODE == kWhole>(x, w);
+                pack16(x, interleaved, va, vb);
+                if (kQuant || in_order) {
                     ring[pa] = va;
                     ring[pb] = vb;
                     __syncwarp();
-                }
-                if (!(FP4 && KIND == kK)) {        // pieces lane and lane + 32, in the order of memory
-                    va = ring[lane];
-                    vb = ring[lane + 32];
-                } else {                           // whole blocks of 16
-                    va = ring[(sub * D + 16 * l) / 8];
-                    vb = ring[(sub * D + 16 * l) / 8 + 1];
+                    va = ring[oa];
+                    vb = ring[ob];
                 }
             }
             __syncwarp();                          // the slot is free
             load_next();
-            // (in_order: the lane holds pieces lane and lane + 32, else its own two of head h)
-            const bool in_order = KIND == kV || relay;
-            if constexpr (KIND == kQ || !APPEND) {
-                uint16_t* dst = KIND == kQ ? p.q_out + (size_t)row * p.q_out_row_stride
-                                           : p.k_out + (size_t)row * p.k_out_row_stride;
-                if (in_order) {
-                    dst += it * 512;
-                    if (head_of(it, 0) < H) sm100::st_global_v4(dst + lane * 8, va);
-                    if (head_of(it, 1) < H) sm100::st_global_v4(dst + (lane + 32) * 8, vb);
-                } else if (h < H) {
-                    sm100::st_global_v4(dst + (size_t)h * D + a, va);
-                    sm100::st_global_v4(dst + (size_t)h * D + b, vb);
-                }
-            } else {
-                // row `at` of the page, for the slot's place in head g
-                const long long page = slot >> p.page_shift;
-                const int in_page = (int)(slot & ((1 << p.page_shift) - 1));
-                auto at = [&](int g) { return ((size_t)g << p.page_shift) + in_page; };
-                unsigned char* pool = (KIND == kK ? p.k_pool : p.v_pool) + page * p.kv_page_stride;
-                if constexpr (!FP4) {
-                    if (in_order) {
-                        const int e = lane % (D / 8) * 16;      // bytes into the head's row
-                        const int g0 = head_of(it, 0), g1 = head_of(it, 1);
-                        if (g0 < H) sm100::st_global_v4(pool + at(g0) * (2 * D) + e, va);
-                        if (g1 < H) sm100::st_global_v4(pool + at(g1) * (2 * D) + e, vb);
-                    } else if (h < H) {
-                        sm100::st_global_v4(pool + at(h) * (2 * D) + 2 * a, va);
-                        sm100::st_global_v4(pool + at(h) * (2 * D) + 2 * b, vb);
-                    }
-                } else if (h < H) {
-                    uint32_t c0, c1, sb;
-                    nvfp4_block(va, vb, KIND == kK ? p.k_gscale : p.v_gscale, c0, c1, sb);
-                    st_global_v2(pool + at(h) * (D / 2) + l * 8, c0, c1);
-                    uint8_t* sc = (KIND == kK ? p.k_scales : p.v_scales) + page * p.scale_page_stride;
-                    sc[at(h) * (D / 16) + l] = static_cast<uint8_t>(sb);
-                }
+            if constexpr (!kQuant) {
+                if (h0 < H) sm100::st_global_v4(d0, va);
+                if (h1 < H) sm100::st_global_v4(d1, vb);
+            } else if (h0 < H) {
+                uint32_t c0, c1, sb;
+                nvfp4_block(va, vb, KIND == kK ? p.k_gscale : p.v_gscale, c0, c1, sb);
+                st_global_v2(d0, c0, c1);
+                *d1 = static_cast<uint8_t>(sb);
             }
+            d0 += inc0;
+            d1 += inc1;
+            h0 += kHeads;
+            h1 += kHeads;
         }
     }
 };
-
-__device__ __forceinline__ void load_weights(const float* w, int a, int b, float (&out)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
-        if (w) f = __ldg(reinterpret_cast<const float4*>(w + (i < 2 ? a : b)) + (i & 1));
-        out[4 * i] = f.x; out[4 * i + 1] = f.y; out[4 * i + 2] = f.z; out[4 * i + 3] = f.w;
-    }
-}
 
 template <int D, bool APPEND, bool FP4>
 __global__ void __launch_bounds__(kNrThreads, kResident) norm_rope_kernel(const __grid_constant__ NormRopeParams p) {
@@ -340,37 +410,54 @@ __global__ void __launch_bounds__(kNrThreads, kResident) norm_rope_kernel(const 
     const int nr = p.rot_dim / 16;                 // lanes of a head that rotate
     t.turn = t.l < nr;
     const bool halves = t.turn && !p.interleaved;
-    t.relay = p.interleaved || p.rot_dim < D;
     t.ea = halves ? 8 * t.l : 16 * t.l;
     t.eb = halves ? 8 * (t.l + nr) : 16 * t.l + 8;
-    t.items = (unsigned)p.num_rows * (unsigned)p.segs;
-    t.step = gridDim.x * kNrWarps;
-    t.item = blockIdx.x * kNrWarps + warp;
-    t.loads = t.uses = 0;
+    // the launch's iterations in even runs, one a warp (a run begins and ends within a row)
+    t.iters = p.iters_q + p.iters_k + p.iters_v;
+    const long long total = (long long)p.num_rows * t.iters, warps = (long long)gridDim.x * kNrWarps;
+    const long long me = (long long)blockIdx.x * kNrWarps + warp;
+    const long long from = total * me / warps, count = total * (me + 1) / warps - from;
+    t.load_slot = t.use_slot = 0;
     t.slot = t.next_slot = 0;
-    const unsigned first = t.item;
-    if (first >= t.items) return;
-    t.split(first, t.load_row, t.load_it, t.load_end);
-    t.ask(first);
+    // the weights, fours of one kind of pair (A, A, B, B) for each lane of a head, as unpack16 lays out its elements
+    for (int u = tid; u < 2 * 4 * R::kLanes; u += kNrThreads) {
+        const int kind = u / (4 * R::kLanes), f = u / R::kLanes % 4, l = u % R::kLanes;
+        const float* w = kind ? p.k_weight : p.q_weight;
+        if (!w) continue;
+        const bool hv = l < nr && !p.interleaved;
+        const int ea = hv ? 8 * l : 16 * l, eb = hv ? 8 * (l + nr) : 16 * l + 8;
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = 4 * (f & 1) + i;         // pair of the lane
+            x[i] = p.interleaved ? w[16 * l + 2 * j + (f >> 1)] : w[(f < 2 ? ea : eb) + j];
+        }
+        sh.w[kind][f * R::kLanes + l] = make_ulonglong2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+    }
+    __syncthreads();
+    if (count == 0) return;
+    typename R::Run run;
+    run.start(from, count, t.iters);
+    t.load = run;
+    t.more = true;
+    t.load_kind();
+    t.ask(run.row);
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) t.load_next();
-    load_weights(p.q_weight, t.ea, t.eb, t.qw);
-    load_weights(p.k_weight, t.ea, t.eb, t.kw);
     const int q1 = p.iters_q, k1 = q1 + p.iters_k;
-    for (unsigned i = first; i < t.items; i += t.step) {
-        int it0, it1;
-        t.split(i, t.row, it0, it1);
+    do {
+        t.row = run.row;
         t.take();
-        t.ask(i + t.step);
+        if (run.left > 0) t.ask(run.row + 1);
         bool skip = false;
         if (APPEND) {
             skip = t.slot < 0 || t.slot >= p.num_slots;      // a padded row, or a bad slot
             if (t.slot >= p.num_slots && lane == 0) atomicOr(p.status, kDevBadPage);
         }
-        t.template heads<kQ>(min(it0, q1), min(it1, q1), skip);
-        t.template heads<kK>(max(it0, q1) - q1, min(it1, k1) - q1, skip);
-        if (APPEND) t.template heads<kV>(max(it0, k1) - k1, it1 - k1, skip);
-    }
+        t.template heads<kQ>(min(run.it, q1), min(run.end, q1), skip);
+        t.template heads<kK>(max(run.it, q1) - q1, min(run.end, k1) - q1, skip);
+        if (APPEND) t.template heads<kV>(max(run.it, k1) - k1, run.end - k1, skip);
+    } while (run.next(t.iters));
 }
 
 template <int D>
@@ -414,26 +501,9 @@ cudaError_t norm_rope_launch(NormRopeParams& p, int head_dim, bool append, int k
     p.iters_q = (p.num_q_heads + per - 1) / per;
     p.iters_k = (p.num_kv_heads + per - 1) / per;
     p.iters_v = append ? p.iters_k : 0;
-    const int iters = p.iters_q + p.iters_k + p.iters_v;
-    // Segments of a row: few rows are cut into as many as there are warps for, others so that the last
-    // round of the resident warps is not mostly idle.  A segment costs its iterations and about one more
-    // for its cos and sin.  (5001 rows x 14 iterations on 2432 warps: 3 rounds of 15, or 5 of 8 in halves.)
-    const long long resident = (long long)num_sms * kResident * kNrWarps;
-    const long long most = std::max<long long>(1, std::min<long long>(iters, resident / std::max(p.num_rows, 1)));
-    long long best = -1, best_per = iters;
-    for (long long k = 0; k <= 8; ++k) {
-        const long long s = k == 0 ? most : std::min<long long>(k, iters);
-        const long long per_seg = (iters + s - 1) / s, segs = (iters + per_seg - 1) / per_seg;
-        const long long rounds = (p.num_rows * segs + resident - 1) / resident;
-        const long long cost = rounds * (per_seg + 1);
-        if (best < 0 || cost < best) {
-            best = cost;
-            best_per = per_seg;
-        }
-    }
-    p.iters_per_seg = (int)best_per;
-    p.segs = (int)((iters + best_per - 1) / best_per);
-    long long ctas = ((long long)p.num_rows * p.segs + kNrWarps - 1) / kNrWarps;
+    // as many warps as there are iterations, up to those resident
+    const long long total = (long long)p.num_rows * (p.iters_q + p.iters_k + p.iters_v);
+    long long ctas = (total + kNrWarps - 1) / kNrWarps;
     if (ctas > (long long)num_sms * kResident) ctas = (long long)num_sms * kResident;
     const dim3 grid(static_cast<unsigned>(ctas));
     switch (head_dim) {

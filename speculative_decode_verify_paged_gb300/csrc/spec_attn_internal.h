@@ -261,8 +261,6 @@ struct NormRopeParams {
     float eps;
     float rot_scale;
     int iters_q, iters_k, iters_v;  // warp iterations of one row (set at launch)
-    int segs;                       // warps a row is cut into
-    int iters_per_seg;
     unsigned long long turns[kMaxPairs];   // angle per position, in 2^-64 turns
     uint8_t axis[kMaxPairs];               // position axis of each pair
 };
