@@ -52,6 +52,7 @@
 #include <cstring>
 #include <mutex>
 #include <new>
+#include <type_traits>
 
 #include "../../include/spec_attn.h"
 #include "common.cuh"
@@ -66,6 +67,7 @@ using namespace tcc;
 
 constexpr int kM = 128;
 constexpr int kMaxRing = 12;
+constexpr int kMaxSorted = 256;          // requests put in order by one CTA's threads
 constexpr int kMaxSplits = 8;            // CTAs of a cluster that any GPU schedules
 constexpr float kCrossRescale = 8.0f;   // log2 units: O is rescaled when a row's maximum grows by more
 
@@ -80,7 +82,7 @@ struct CrossLayout {
     static constexpr int kChunks = D / 64;
     static constexpr int kQBytes = kM * D * 2;             // one query tile
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
-    static constexpr int kAux = 1024;
+    static constexpr int kAux = 2048;
     static constexpr int kCtas = DEEP ? 1 : 2;
     // S buffers of a tile (a power of two): two, or four for a lone tile with the SM to itself, whose
     // S_{t+1} then does not wait for P V of tile t - 1
@@ -124,8 +126,10 @@ struct CrossAux {
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
+    int request;                        // longest-first order: the CTA's request
+    int lens[kMaxSorted];
 };
-static_assert(sizeof(CrossAux) <= 1024, "aux region");
+static_assert(sizeof(CrossAux) <= 2048, "aux region");
 
 // Bounded wait of a whole warp; the clock is read only when the phase is still open.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
@@ -213,7 +217,8 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     constexpr int BN = kBN, PV = L::kPv, RING = L::kRing, SH = L::kBufShift, NB = L::kBufs;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x / p.max_splits, split = blockIdx.x % p.max_splits;   // (split: the rank in the cluster)
-    const int kvh = blockIdx.y, r = blockIdx.z;
+    const int kvh = blockIdx.y;
+    int r = blockIdx.z;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                            ~static_cast<uintptr_t>(1023));
@@ -248,6 +253,20 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     // up to here the CTA touched only its own resources, while the previous kernel drains
     pdl_wait_primary();
     pdl_launch_dependents();   // (the next kernel's CTAs set up as these leave their SMs)
+    if (p.longest_first) {
+        // More CTAs than the GPU holds: the requests with the most states go first, so that the last CTAs to
+        // start are short ones.  Each CTA ranks the lengths itself (ties by index).
+        if (tid < p.longest_first) aux->lens[tid] = p.kv_len[tid];
+        __syncthreads();
+        if (tid < p.longest_first) {
+            const int mine = aux->lens[tid];
+            int rank = 0;
+            for (int j = 0; j < p.longest_first; ++j) rank += aux->lens[j] > mine || (aux->lens[j] == mine && j < tid);
+            if (rank == blockIdx.z) aux->request = tid;
+        }
+        __syncthreads();
+        r = aux->request;
+    }
     CrossReq q;
     const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
     bool active = cross_request(p, r, reporter ? p.status : nullptr, q);
@@ -555,31 +574,52 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
     __syncwarp();
     cluster_sync();                                // every split's rows are in its shared memory
     if (!*abort) {
-        const uint32_t rows_at = smem_addr(stage), lse_at = smem_addr(stage_lse);
-        for (int u = split * L::kThreads + tid; u < rows * C8; u += nsplits * L::kThreads) {
-            const int m = u / C8, c = u % C8;
-            float ls[kMaxSplits], mx = -INFINITY, sum = 0.f;
+        auto combine = [&](auto most) {
+            constexpr int N = decltype(most)::value;
+            // Every load of a unit is on its way before the first is used, and each CTA begins with its own
+            // rows: were all to begin with rank 0, they would queue at one SM.
+            uint32_t rows_at[N], lse_at[N];
 #pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) {
-                ls[k] = k < nsplits ? ld_peer(peer_addr(lse_at + m * 4, k)) : -INFINITY;
-                mx = fmaxf(mx, ls[k]);
+            for (int k = 0; k < N; ++k) {
+                const int from = split + k < nsplits ? split + k : split + k - nsplits;
+                rows_at[k] = peer_addr(smem_addr(stage), k < nsplits ? from : split);
+                lse_at[k] = peer_addr(smem_addr(stage_lse), k < nsplits ? from : split);
             }
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+            for (int u = split * L::kThreads + tid; u < rows * C8; u += nsplits * L::kThreads) {
+                const int m = u / C8, c = u % C8;
+                float ls[N];
+                float4 x[N], y[N];
 #pragma unroll
-            for (int k = 0; k < kMaxSplits; ++k) {
-                if (k >= nsplits) break;
-                const uint32_t from = peer_addr(rows_at + (m * L::kRowFloats + c * 8) * 4, k);
-                const float4 x = ld_peer_v4(from), y = ld_peer_v4(from + 16);
-                const float w = fast_exp2(ls[k] - mx);
-                a.x = fmaf(w, x.x, a.x); a.y = fmaf(w, x.y, a.y); a.z = fmaf(w, x.z, a.z); a.w = fmaf(w, x.w, a.w);
-                b.x = fmaf(w, y.x, b.x); b.y = fmaf(w, y.y, b.y); b.z = fmaf(w, y.z, b.z); b.w = fmaf(w, y.w, b.w);
-                sum += w;
+                for (int k = 0; k < N; ++k) {
+                    ls[k] = ld_peer(lse_at[k] + m * 4);
+                    x[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 8) * 4);
+                    y[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 8 + 4) * 4);
+                }
+                float mx = ls[0], sum = 0.f;
+#pragma unroll
+                for (int k = 1; k < N; ++k) {
+                    if (k >= nsplits) ls[k] = -INFINITY;
+                    mx = fmaxf(mx, ls[k]);
+                }
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const float w = fast_exp2(ls[k] - mx);
+                    a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
+                    a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);
+                    b.x = fmaf(w, y[k].x, b.x); b.y = fmaf(w, y[k].y, b.y);
+                    b.z = fmaf(w, y[k].z, b.z); b.w = fmaf(w, y[k].w, b.w);
+                    sum += w;
+                }
+                const float inv = 1.f / sum;
+                put(m, c, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
+                    make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv));
+                if (c == 0 && p.lse) p.lse[place(m)] = (mx + log2f(sum)) * kLn2;
             }
-            const float inv = 1.f / sum;
-            put(m, c, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
-                make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv));
-            if (c == 0 && p.lse) p.lse[place(m)] = (mx + log2f(sum)) * kLn2;
-        }
+        };
+        if (nsplits <= 2) combine(std::integral_constant<int, 2>());
+        else if (nsplits <= 4) combine(std::integral_constant<int, 4>());
+        else combine(std::integral_constant<int, kMaxSplits>());
     }
     __syncwarp();
     cluster_sync();                                // no CTA leaves while its rows are being read
@@ -774,6 +814,12 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     c.group = p.num_q_heads / p.num_kv_heads;
     c.wt = plan->wt;
     c.max_splits = plan->max_splits;
+    // (one request, or all CTAs at once: nothing to order)
+    const int64_t ctas = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs;
+    c.longest_first = p.num_reqs > 1 && p.num_reqs <= kMaxSorted &&
+                              ctas > static_cast<int64_t>(plan->num_sms) * plan->variant.ctas
+                          ? p.num_reqs
+                          : 0;
     c.total_kv = p.total_kv_rows;
     c.max_kv_len = p.max_kv_len;
     c.keys_per_split = plan->keys_per_split;

@@ -282,6 +282,7 @@ struct CrossParams {
     int group;
     int wt;                     // window rows of a query tile: 128 / group
     int max_splits;             // CTAs of a cluster
+    int longest_first;          // requests to put in order of length (0: as they come)
     int total_kv;
     int max_kv_len;
     int keys_per_split;
