@@ -3,7 +3,9 @@
 A thin ctypes binding over ``libspec_attn.so`` (C ABI in ``include/spec_attn.h``).
 Every step of the computation runs in the library's CUDA kernels; this module
 only marshals arguments: torch tensors are passed as device pointers and the
-current torch CUDA stream is used unless another is given.  There is no CPU
+current torch CUDA stream is used unless another is given.  The calls around
+the attention (step tables, norm and rotation, cross attention) go through a
+small extension module (``csrc/binding.c``) with the same checks.  There is no CPU
 path: if the library is missing, every call raises.
 
 Names follow the C ABI::
@@ -442,54 +444,28 @@ def spec_attn_last_cuda_error() -> int:
 # --------------------------------------------------------------------------- #
 # Around the attention call: step tables, norm and rotation of q and k
 # --------------------------------------------------------------------------- #
-_torch = None
+_calls = None
 
 
-def _here(stream):
-    """torch, the current device, the handle of ``stream`` (None: the device's current stream) and the library."""
-    global _torch
-    if _torch is None:
+def _native():
+    """The extension module that checks these calls' tensors and makes them."""
+    global _calls
+    if _calls is None:
+        import importlib.machinery
+        import importlib.util
         import torch
-        _torch = torch
-    dev = _torch.cuda.current_device()
-    raw = _torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    return _torch, dev, raw, _lib or load_library()
-
-
-def _bad(t, what, dtype, shape, dev):
-    """Say what is wrong with a tensor."""
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{what} must be on the current device, cuda:{dev}, got {t.device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have the shape {shape}, got {tuple(t.shape)}")
-    raise ValueError(f"{what} must be contiguous")
-
-
-def _dense(t, what, dtype, shape, dev):
-    """Address of a contiguous tensor of this type and shape on the device (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
-        return t.data_ptr()
-    _bad(t, what, dtype, shape, dev)
-
-
-def _rows(t, what, shape, row_stride, dev, dtype):
-    """Address of bf16 rows of heads [n, h, d], ``row_stride`` elements apart (0: dense)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _bad(t, what, dtype, shape, dev)
-    n, h, d = shape
-    st = t.stride()
-    if n and h and ((h > 1 and st[1] != d) or st[2] != 1 or (n > 1 and st[0] != (row_stride or h * d))):
-        raise ValueError(f"{what} must have its heads adjacent and rows {row_stride or h * d} elements apart, "
-                         f"got strides {st}")
-    return t.data_ptr()
+        load_library()
+        path = os.path.join(HERE, "_build", "spec_attn_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"spec_attn_calls.so not found at {path}; build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("spec_attn_calls", path)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("spec_attn_calls", loader))
+        loader.exec_module(mod)
+        mod.setup(torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8, torch.cuda.current_device,
+                  torch._C._cuda_getCurrentRawStream)
+        _calls = mod
+    return _calls
 
 
 def spec_attn_build_tables(ctx_lens, window_lens, prev_seq_lens, prev_free_count, free_pages, block_table, seq_lens,
@@ -498,20 +474,9 @@ def spec_attn_build_tables(ctx_lens, window_lens, prev_seq_lens, prev_free_count
     """seq_lens, q_indptr, the grown block table and every row's position and
     cache slot from the requests' lengths (asynchronous).  seq_lens may be
     prev_seq_lens or ctx_lens, free_count may be prev_free_count."""
-    torch, dev, cur, lib = _here(stream)
-    i32 = torch.int32
-    P, rows, pages, stride = ctx_lens.shape[0], slot_map.shape[0], free_pages.shape[0], block_table.shape[1]
-    prob = spec_attn_tables_problem(P, rows, page_size, pages, stride, max_w, max_seq_len)
-    _check(lib.spec_attn_build_tables(
-        ctypes.byref(prob), _dense(ctx_lens, "ctx_lens", i32, (P,), dev),
-        _dense(window_lens, "window_lens", i32, (P,), dev), _dense(prev_seq_lens, "prev_seq_lens", i32, (P,), dev),
-        _dense(prev_free_count, "prev_free_count", i32, (1,), dev), _dense(free_pages, "free_pages", i32, (pages,), dev),
-        _dense(block_table, "block_table", i32, (P, stride), dev),
-        _dense(seq_lens, "seq_lens", i32, (P,), dev), _dense(q_indptr, "q_indptr", i32, (P + 1,), dev),
-        _dense(free_count, "free_count", i32, (1,), dev), _dense(positions, "positions", i32, (rows,), dev),
-        _dense(slot_map, "slot_map", torch.int64, (rows,), dev),
-        _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
-        cur), "spec_attn_build_tables")
+    _check((_calls or _native()).build_tables(
+        (page_size, max_w, max_seq_len), ctx_lens, window_lens, prev_seq_lens, prev_free_count, free_pages, block_table,
+        seq_lens, q_indptr, free_count, positions, slot_map, workspace, stream), "spec_attn_build_tables")
 
 
 def rope_inv_freq(rot_dim: int, base: float = 10000.0):
@@ -541,8 +506,10 @@ class NormRopePlan:
         self.handle = handle
         self.problem = problem
         p = problem
-        self.q_heads, self.kv_heads, self.head_dim, self.axes = (p.num_q_heads, p.num_kv_heads, p.head_dim, p.num_axes)
-        self.strides = (p.q_row_stride, p.k_row_stride, p.v_row_stride, p.q_out_row_stride, p.k_out_row_stride)
+        # (in the order the native calls read them)
+        self.spec = (handle.value, p.num_q_heads, p.num_kv_heads, p.head_dim, p.num_axes, p.q_row_stride, p.k_row_stride,
+                     p.v_row_stride, p.q_out_row_stride, p.k_out_row_stride, p.kv_dtype, p.page_size, p.num_pages,
+                     p.kv_page_stride, p.scale_page_stride)
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -580,39 +547,12 @@ def spec_attn_norm_rope_plan_create(*, num_q_heads, num_kv_heads, head_dim, inv_
     return NormRopePlan(handle, prob)
 
 
-def _norm_rope_args(torch, plan, q, k, q_weight, k_weight, positions, dev):
-    n = k.shape[0] if q is None else q.shape[0]
-    d, st = plan.head_dim, plan.strides
-    return n, [plan.handle, n, _rows(q, "q", (n, plan.q_heads, d), st[0], dev, torch.bfloat16),
-               _rows(k, "k", (n, plan.kv_heads, d), st[1], dev, torch.bfloat16)], \
-        [_dense(q_weight, "q_weight", torch.float32, (d,), dev), _dense(k_weight, "k_weight", torch.float32, (d,), dev),
-         _dense(positions, "positions", torch.int32, (plan.axes, n), dev)]
-
-
 def spec_attn_norm_rope(plan: NormRopePlan, q, k, q_weight, k_weight, positions, q_out, k_out, stream=None):
     """Norm and rotation of q [n, Hq, d] and k [n, Hkv, d] (asynchronous).
     ``positions`` [num_axes, n] int32; weights [d] fp32 or None (no norm);
     the outputs may be the inputs."""
-    torch, dev, cur, lib = _here(stream)
-    n, rows, rest = _norm_rope_args(torch, plan, q, k, q_weight, k_weight, positions, dev)
-    _check(lib.spec_attn_norm_rope(
-        *rows, *rest, _rows(q_out, "q_out", (n, plan.q_heads, plan.head_dim), plan.strides[3], dev, torch.bfloat16),
-        _rows(k_out, "k_out", (n, plan.kv_heads, plan.head_dim), plan.strides[4], dev, torch.bfloat16),
-        cur), "spec_attn_norm_rope")
-
-
-def _pool(t, what, shape, page_stride, itemsize, dev, dtype):
-    """Address of a pool, dense or with the plan's page stride in bytes."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _bad(t, what, dtype, shape, dev)
-    if page_stride:
-        if shape[0] > 1 and t.stride(0) * itemsize != page_stride or not t[0].is_contiguous():
-            raise ValueError(f"{what} must have dense pages {page_stride} bytes apart")
-    elif not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
-    return t.data_ptr()
+    _check((_calls or _native()).norm_rope(plan.spec, q, k, q_weight, k_weight, positions, q_out, k_out, stream),
+           "spec_attn_norm_rope")
 
 
 def spec_attn_norm_rope_append(plan: NormRopePlan, q, k, v, q_weight, k_weight, positions, slot_map, q_out, k_pool,
@@ -620,22 +560,9 @@ def spec_attn_norm_rope_append(plan: NormRopePlan, q, k, v, q_weight, k_weight, 
                                stream=None):
     """spec_attn_norm_rope with K and V written into the cache slots that
     ``slot_map`` [n] int64 names (asynchronous); rows with a negative slot are skipped."""
-    torch, dev, cur, lib = _here(stream)
-    p, d, hkv = plan.problem, plan.head_dim, plan.kv_heads
-    n, rows, rest = _norm_rope_args(torch, plan, q, k, q_weight, k_weight, positions, dev)
-    fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4
-    page, kind, size = (p.num_pages, hkv, p.page_size), torch.uint8 if fp4 else torch.bfloat16, 1 if fp4 else 2
-    row = (d // 2 if fp4 else d,)
-    _check(lib.spec_attn_norm_rope_append(
-        *rows, _rows(v, "v", (n, hkv, d), plan.strides[2], dev, torch.bfloat16), *rest,
-        _dense(slot_map, "slot_map", torch.int64, (n,), dev),
-        _rows(q_out, "q_out", (n, plan.q_heads, d), plan.strides[3], dev, torch.bfloat16),
-        _pool(k_pool, "k_pool", page + row, p.kv_page_stride, size, dev, kind),
-        _pool(v_pool, "v_pool", page + row, p.kv_page_stride, size, dev, kind),
-        _pool(k_scales, "k_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
-        _pool(v_scales, "v_scales", page + (d // 16,), p.scale_page_stride, 1, dev, torch.uint8),
-        k_gscale, v_gscale, _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
-        cur), "spec_attn_norm_rope_append")
+    _check((_calls or _native()).norm_rope_append(
+        plan.spec, q, k, v, q_weight, k_weight, positions, slot_map, q_out, k_pool, v_pool, workspace, k_scales, v_scales,
+        k_gscale, v_gscale, stream), "spec_attn_norm_rope_append")
 
 
 class CrossPlan:
@@ -647,9 +574,8 @@ class CrossPlan:
         self.workspace_bytes = int(workspace_bytes)
         self.problem = problem
         p = problem
-        self.q_shape = (p.total_q_rows, p.num_q_heads, p.head_dim)
-        self.kv_shape = (p.total_kv_rows, p.num_kv_heads, p.head_dim)
-        self.reqs, self.kv_row_stride = p.num_reqs, p.kv_row_stride
+        self.spec = (handle.value, p.num_reqs, p.total_q_rows, p.num_q_heads, p.num_kv_heads, p.head_dim,
+                     p.total_kv_rows, p.kv_row_stride)   # (in the order the native call reads them)
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None
@@ -673,15 +599,8 @@ def spec_attn_cross_plan_create(*, num_reqs, total_q_rows, max_q_rows, num_q_hea
 def spec_attn_run_cross(plan: CrossPlan, q, k, v, q_indptr, kv_start, kv_len, o, lse, workspace, stream=None):
     """Attention of each request's query rows to its range of state rows
     (asynchronous).  ``lse`` may be None."""
-    torch, dev, cur, lib = _here(stream)
-    bf16, i32, P = torch.bfloat16, torch.int32, plan.reqs
-    _check(lib.spec_attn_run_cross(
-        plan.handle, _dense(q, "q", bf16, plan.q_shape, dev), _rows(k, "k", plan.kv_shape, plan.kv_row_stride, dev, bf16),
-        _rows(v, "v", plan.kv_shape, plan.kv_row_stride, dev, bf16), _dense(q_indptr, "q_indptr", i32, (P + 1,), dev),
-        _dense(kv_start, "kv_start", i32, (P,), dev), _dense(kv_len, "kv_len", i32, (P,), dev),
-        _dense(o, "o", bf16, plan.q_shape, dev), _dense(lse, "lse", torch.float32, plan.q_shape[:2], dev),
-        _dense(workspace, "workspace", torch.uint8, workspace.shape, dev), workspace.shape[0],
-        cur), "spec_attn_run_cross")
+    _check((_calls or _native()).run_cross(plan.spec, q, k, v, q_indptr, kv_start, kv_len, o, lse, workspace, stream),
+           "spec_attn_run_cross")
 
 
 # --------------------------------------------------------------------------- #

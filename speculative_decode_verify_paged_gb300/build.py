@@ -2,7 +2,9 @@
 
 Each CUDA translation unit under csrc/ is compiled in parallel into
 _build/*.o, then linked into _build/libspec_attn.so (CUDA runtime linked
-statically, so the library needs only the driver).  No cmake.
+statically, so the library needs only the driver).  The native side of the
+Python binding, csrc/binding.c, becomes the extension module
+_build/spec_attn_calls.so, linked against that library.  No cmake.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -19,6 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libspec_attn.so")
+CALLS = os.path.join(BUILD, "spec_attn_calls.so")
+BINDING = os.path.join(CSRC, "binding.c")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -36,7 +41,7 @@ def sources():
 
 def _deps():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
+                  glob.glob(os.path.join(CSRC, "*.h")) + [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h")) +
                   [os.path.abspath(__file__)])
 
 
@@ -56,6 +61,17 @@ def _compile(src, extra):
     return obj, res.stderr
 
 
+def _build_binding():
+    """The extension module: plain C against the running interpreter's headers, finding the library beside it."""
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CC", "gcc"), "-shared", "-fPIC", "-O2", "-std=c11", "-Wall", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], BINDING, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     """Compile every CUDA source and link the shared library; return its path."""
     os.makedirs(BUILD, exist_ok=True)
@@ -65,7 +81,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     stamp = os.path.join(BUILD, "sources.txt")
     listing = "\n".join(os.path.basename(s) for s in srcs)
     same_set = os.path.exists(stamp) and open(stamp).read() == listing
-    if not force and not extra_flags and same_set and not _stale(LIB, deps):
+    if not force and not extra_flags and same_set and not _stale(LIB, deps) and not _stale(CALLS, deps):
         return LIB
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(lambda s: _compile(s, extra_flags), srcs))
@@ -75,11 +91,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if log:
                 sys.stderr.write(log)
     tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
+    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-Xlinker", "-soname=libspec_attn.so", "-o", tmp] + objs
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _build_binding()
     with open(stamp, "w") as f:
         f.write(listing)
     return LIB

@@ -169,6 +169,17 @@ def test_random_batches():
         c.check()
 
 
+@pytest.mark.parametrize("hq,hkv,d,P,rows", [(6, 1, 256, 190, 1), (4, 2, 128, 250, 3), (8, 1, 64, 256, 2), (3, 3, 64, 257, 1),
+                                              (16, 1, 128, 160, 9)])
+def test_more_ctas_than_the_gpu_holds(hq, hkv, d, P, rows):
+    """Uneven lengths, equal ones and empty ones among them: the CTAs run in order of length, the rows stay in place."""
+    rng = random.Random(P)
+    lens = [rng.choice((0, 1, 64, 64, 100, rng.randint(1, 400))) for _ in range(P)]
+    c = Case([rng.choice((0, rows, rows)) for _ in range(P)], lens, hq, hkv, d, seed=P, max_q=rows)
+    c.run()
+    c.check()
+
+
 @pytest.mark.parametrize("field,value,bits", [
     ("kv_len", -1, sa.SPEC_ATTN_DEV_BAD_SEQ_LEN), ("kv_len", 201, sa.SPEC_ATTN_DEV_BAD_SEQ_LEN),
     ("kv_start", -1, sa.SPEC_ATTN_DEV_BAD_SEQ_LEN), ("kv_start", 2 ** 31 - 1, sa.SPEC_ATTN_DEV_BAD_SEQ_LEN),

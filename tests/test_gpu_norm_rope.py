@@ -294,12 +294,13 @@ def test_refused_calls_write_nothing():
     slot = torch.arange(4, device="cuda")
     ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
     no_cache = Case(4, 4, 2, 64, seed=15)
-    with pytest.raises(sa.SpecAttnError) as e:          # the plan has no cache
-        sa.load_library()
-        p = no_cache.plan.problem
-        p.num_pages, p.page_size = 2, 16                # (past the binding's shape check)
+    lib = sa.load_library()
+    st = lib.spec_attn_norm_rope_append(            # the plan has no cache
+        no_cache.plan.handle, 4, *[t.data_ptr() for t in (c.q, c.k, c.v, c.qw, c.kw, c.pos, slot, c.q_out, *pools)], None,
+        None, 1.0, 1.0, ws.data_ptr(), 256, None)
+    assert st == sa.SPEC_ATTN_E_INVALID_ARG
+    with pytest.raises(ValueError):                     # (nor do its shapes fit)
         sa.spec_attn_norm_rope_append(no_cache.plan, c.q, c.k, c.v, c.qw, c.kw, c.pos, slot, c.q_out, *pools, ws)
-    assert e.value.status == sa.SPEC_ATTN_E_INVALID_ARG
     with pytest.raises(ValueError):                     # positions of another length
         sa.spec_attn_norm_rope(c.plan, c.q, c.k, c.qw, c.kw, c.pos[:, :3].contiguous(), c.q_out, c.k_out)
     with pytest.raises(ValueError):                     # weights in another type
@@ -310,7 +311,6 @@ def test_refused_calls_write_nothing():
         sa.spec_attn_norm_rope_append(c.plan, c.q, c.k, c.v, c.qw, c.kw, c.pos, slot.int(), c.q_out, *pools, ws)
     with pytest.raises(sa.SpecAttnError):               # in place at another stride
         other = Case(4, 4, 2, 64, seed=15, q_out_row_stride=512)
-        lib = sa.load_library()
         sa._check(lib.spec_attn_norm_rope(other.plan.handle, 4, c.q.data_ptr(), c.k.data_ptr(), None, None,
                                           c.pos.data_ptr(), c.q.data_ptr(), c.k_out.data_ptr(), None), "in place")
     torch.cuda.synchronize()

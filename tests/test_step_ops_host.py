@@ -165,12 +165,20 @@ def test_rope_helpers():
     assert sa.rope_pair_axis((2, 3, 1), interleaved=True) == [0, 1, 2, 0, 1, 1]
 
 
-def test_cpu_tensors_are_refused(lib, monkeypatch):
-    monkeypatch.setattr(sa, "_here", lambda stream: (torch, 0, 0, lib))
+def test_cpu_tensors_are_refused(lib):
     i = torch.zeros(4, dtype=torch.int32)
-    with pytest.raises(ValueError, match="CUDA tensor"):
+    with pytest.raises(ValueError, match="ctx_lens must be a CUDA tensor"):
         sa.spec_attn_build_tables(i, i, i, i[:1], i, i[None].expand(4, 4), i, i, i[:1], i, i.long(),
                                   torch.zeros(256, dtype=torch.uint8), max_seq_len=64)
+
+
+def test_native_calls_count_their_arguments(lib):
+    calls = sa._native()
+    for f in (calls.build_tables, calls.norm_rope, calls.norm_rope_append, calls.run_cross):
+        with pytest.raises(TypeError):
+            f(())
+    with pytest.raises(TypeError, match="not a plan"):
+        calls.norm_rope((1, 2), *([None] * 8))
 
 
 # --------------------------------------------------------------------------- #
