@@ -15,7 +15,9 @@
 // frac(f) as a 64-bit fixed-point fraction, and its product with the position
 // modulo 2^64 is the angle modulo one turn, exact for every 32-bit position
 // (the fraction itself is within 2^-53 f of the double it came from).  As a
-// signed fraction it is rounded once to fp32, for sincospi.
+// signed fraction it is rounded to fp32 for sincospi, and the part that this
+// leaves out (up to 9e-8 radians, as much as the functions' own error) turns
+// the result once more to first order.
 //
 // Layout.  A head of d elements is taken by d / 16 adjacent lanes, 16 elements
 // each in two 16-byte pieces: with half-split pairs the pieces at l and l +
@@ -237,10 +239,14 @@ struct Row {
             if (j < p.rot_dim / 2) {
                 // the angle in turns, modulo one: -1/2 .. 1/2
                 const unsigned long long u = sh.turns[j] * (unsigned long long)(long long)pos[k];
+                const long long v = (long long)u;
+                const float top = (float)v;
+                // what rounding the angle to fp32 left out, in radians, turns (cos, sin) by itself
+                const float rest = (float)(v - __float2ll_rz(top)) * 3.4061215800865545e-19f;   // 2^-63 pi
                 float sn, cn;
-                sincospif((float)(long long)u * 1.0842021724855044e-19f, &sn, &cn);   // 2^-63: in half turns
-                cs[j] = cn * p.rot_scale;
-                cs[kMaxPairs + j] = sn * p.rot_scale;
+                sincospif(top * 1.0842021724855044e-19f, &sn, &cn);                             // 2^-63: in half turns
+                cs[j] = fmaf(-rest, sn, cn) * p.rot_scale;
+                cs[kMaxPairs + j] = fmaf(rest, cn, sn) * p.rot_scale;
             }
         }
         __syncwarp();

@@ -34,9 +34,22 @@ __device__ __forceinline__ uint32_t e2m1x8_rn_sat(const float (&t)[8]) {
     return d;
 }
 
+// (a call: the rare path of a block stays out of its caller's code)
+static __device__ __noinline__ float quotient(float x, float y) { return __fdiv_rn(x, y); }
+
 // The block's 16 bf16 elements (a, then b) -> 8 code bytes (c0, c1) and the
 // scale byte sb: scale = E4M3(amax / (6 g)), den = scale * g, code = den == 0 ?
 // 0 : E2M1(x / den), every product and quotient in binary32 to nearest even.
+//
+// The 16 quotients share their divisor.  With r = 1 / den to nearest, q = x r
+// is within an ulp of x / den, its residual x - q den is exact in one fused
+// multiply-add, and q + r (x - q den) in another is the quotient rounded to
+// nearest (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990) while nothing overflows or loses bits below
+// the normal range: three instructions for each element instead of a division.
+// The theorem excludes a divisor whose significand is all ones.  Such a den, one
+// outside 2^-60 .. 2^60, and a block whose largest quotient passes 2^20 take the
+// division itself; elements below 2^-40 den are far from every rounding border.
 __device__ __forceinline__ void nvfp4_block(const uint4& a, const uint4& b, float g, uint32_t& c0, uint32_t& c1,
                                             uint32_t& sb) {
     const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -53,10 +66,25 @@ __device__ __forceinline__ void nvfp4_block(const uint4& a, const uint4& b, floa
     c0 = c1 = 0u;
     if (den != 0.f) {
         float t0[8], t1[8];
+        const bool plain = den >= 8.673617379884035e-19f && den <= 1.152921504606847e18f && amax <= den * 1048576.0f &&
+                           (__float_as_uint(den) & 0x7FFFFFu) != 0x7FFFFFu;
+        if (plain) {
+            const float r = __frcp_rn(den);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            t0[e] = __fdiv_rn(x[e], den);
-            t1[e] = __fdiv_rn(x[8 + e], den);
+            for (int e = 0; e < 8; ++e) {
+                const float q0 = __fmul_rn(x[e], r), q1 = __fmul_rn(x[8 + e], r);
+                t0[e] = __fmaf_rn(__fmaf_rn(-q0, den, x[e]), r, q0);
+                t1[e] = __fmaf_rn(__fmaf_rn(-q1, den, x[8 + e]), r, q1);
+                // (a zero keeps its sign)
+                if (x[e] == 0.f) t0[e] = x[e];
+                if (x[8 + e] == 0.f) t1[e] = x[8 + e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                t0[e] = quotient(x[e], den);
+                t1[e] = quotient(x[8 + e], den);
+            }
         }
         c0 = e2m1x8_rn_sat(t0);
         c1 = e2m1x8_rn_sat(t1);

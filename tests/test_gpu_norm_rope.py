@@ -371,3 +371,30 @@ def test_tables_then_append_then_attention(kv):
         for i in range(n):
             s = int(slot[i])
             assert torch.equal(pools[0][s // ps, :, s % ps], k_rot[i]) and torch.equal(pools[1][s // ps, :, s % ps], v[i])
+
+
+@pytest.mark.parametrize("seed,gscale", [(0, 2.0 ** -6), (1, 0.3), (2, 1.0 / 2688), (3, 7.5e-6), (4, 1e-25), (5, 3e24),
+                                         (6, 2.0 ** -8 * (2 - 2.0 ** -23))])
+def test_quantised_values_of_every_range(seed, gscale):
+    """V goes into a 4-bit cache as it is: rows of wide range, dyadic values on rounding borders, zeros of both signs,
+    tiny and clipped blocks, against the oracle's own divisions, byte for byte -- for decode scales in the middle of
+    the range, at its ends (where a block's quotients are divisions) and with a significand of ones."""
+    hkv, d, ps, n = 4, 256, 16, 512
+    k, v = W.window_kv_rows(n, hkv, d, seed=60 + seed)
+    pools = _cache(n // ps, hkv, ps, d, W.KV_NVFP4, False)
+    host = [p.cpu().contiguous() for p in pools]
+    plan = sa.spec_attn_norm_rope_plan_create(num_q_heads=1, num_kv_heads=hkv, head_dim=d, rot_dim=0, inv_freq=[],
+                                              kv_dtype=1, page_size=ps, num_pages=n // ps)
+    q = torch.zeros(n, 1, d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    sa.spec_attn_norm_rope_append(plan, q, k.cuda(), v.cuda(), None, None, torch.zeros(1, n, dtype=torch.int32, device="cuda"),
+                                  torch.arange(n, device="cuda"), q, *pools[:2], ws, *pools[2:], gscale, gscale)
+    assert sa.spec_attn_check_device_status(ws) == 0
+    # (32 requests of 16 rows at context 0: their slots are the rows' numbers)
+    ref = oracle.append_kv(num_kv_heads=hkv, head_dim=d, page_size=ps, kv_dtype=1, k_new=k, v_new=v, k_pool=host[0],
+                           v_pool=host[1], k_scales=host[2], v_scales=host[3], k_gscale=gscale, v_gscale=gscale,
+                           block_table=torch.arange(n // 16, dtype=torch.int32)[:, None].contiguous(),
+                           seq_lens=torch.full((n // 16,), 16, dtype=torch.int32),
+                           q_indptr=torch.arange(n // 16 + 1, dtype=torch.int32) * 16)
+    for got, want in zip(pools, ref):
+        assert np.array_equal(_bytes(got), want.view(np.uint8).reshape(-1))
