@@ -472,8 +472,10 @@ int spec_attn_noalloc_check_device_status(spec_attn_stream_t stream, uint32_t* b
  * held pages that exceed the pool (SPEC_ATTN_DEV_BAD_FREE_LIST); too few free
  * pages (SPEC_ATTN_DEV_OUT_OF_PAGES).  After any of them the step is empty:
  * q_indptr is all zero, every slot -1, every position 0, seq_lens and
- * free_count equal their previous values, table and stack are untouched, so
- * later calls of the step do nothing and the caller may try again.  A page id
+ * free_count equal their previous values (prev_seq_lens and prev_free_count),
+ * table and stack are untouched, so later calls of the step do nothing and the
+ * caller may try again (where seq_lens is ctx_lens, with ctx_lens set anew: it
+ * holds prev_seq_lens now).  A page id
  * outside [0, num_pages) sets SPEC_ATTN_DEV_BAD_PAGE and gives its rows slot -1.
  *
  * workspace: 256 bytes, 256-byte aligned, zeroed once (spec_attn_reset_device_
@@ -599,12 +601,12 @@ int spec_attn_norm_rope_append(const spec_attn_norm_rope_plan* plan, int32_t num
  */
 typedef struct spec_attn_cross_problem {
     int32_t num_reqs;            /* P, 0 .. 65535 */
-    int32_t total_q_rows;        /* rows of Q and O */
+    int32_t total_q_rows;        /* rows of Q and O, at most 2^30 */
     int32_t max_q_rows;          /* upper bound on a request's rows, >= 1 */
     int32_t num_q_heads;         /* Hq */
     int32_t num_kv_heads;        /* Hkv; Hq % Hkv == 0, Hq / Hkv <= 16 */
     int32_t head_dim;            /* 64, 128 or 256 */
-    int32_t total_kv_rows;       /* rows of K and V */
+    int32_t total_kv_rows;       /* rows of K and V, at most 2^30 */
     int32_t max_kv_len;          /* upper bound on every kv_len */
     float sm_scale;              /* 0 selects 1/sqrt(head_dim) */
     int32_t force_splits;        /* 0: the library's choice; 1 .. 8: cut the longest range n ways */
@@ -622,9 +624,9 @@ int spec_attn_cross_plan_destroy(spec_attn_cross_plan* plan);
 /*
  * q [total_q_rows, Hq, d], o likewise, k and v at the plan's row stride, all
  * bf16 and 16-byte aligned; q_indptr [P+1], kv_start [P], kv_len [P] int32;
- * lse [total_q_rows, Hq] fp32 or NULL; workspace: 256 bytes, 256-byte aligned,
- * holding the device-status word (zeroed once).  Asynchronous on `stream`, allocation-free, graph
- * capturable.
+ * lse [total_q_rows, Hq] fp32 or NULL; outputs overlap no input.  workspace:
+ * 256 bytes, 256-byte aligned, holding the device-status word (zeroed once).
+ * Asynchronous on `stream`, allocation-free, graph capturable.
  */
 int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const void* k, const void* v,
                         const int32_t* q_indptr, const int32_t* kv_start, const int32_t* kv_len, void* o,

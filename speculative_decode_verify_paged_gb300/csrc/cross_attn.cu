@@ -49,8 +49,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
-#include <mutex>
 #include <new>
 #include <type_traits>
 
@@ -89,7 +87,7 @@ struct CrossLayout {
     static constexpr int kBufShift = NQ == 1 && DEEP ? 2 : 1;
     static constexpr int kBufs = 1 << kBufShift;
     static constexpr int kNeed = NQ * (D + kBufs * kBN);
-    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;   // (a constant at the allocation: the driver counts it)
+    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;   // allocated: a power of two
     static_assert(kNeed <= 512 && kCols * kCtas <= 512, "tensor memory");
     // first column of buffer b of tile i
     __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (kBufs * i + b) * kBN; }
@@ -685,25 +683,23 @@ struct spec_attn_cross_plan {
     int max_splits;
     float sm_scale;
     spec_attn::CrossVariant variant;
-    // tensor maps of the last (q, k, v): a loop on the same buffers encodes them once
-    std::mutex maps_mutex;
-    CUtensorMap maps[3];
-    const void* maps_key[3] = {nullptr, nullptr, nullptr};
 };
 
 namespace {
 
+constexpr int32_t kMaxCrossRows = 1 << 30;
+
 bool cross_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // States a split takes (a multiple of the tile).
-int choose_split(const spec_attn_cross_problem& p, const spec_attn_cross_plan& plan) {
+int choose_split(const spec_attn_cross_problem& p, int max_len, const spec_attn_cross_plan& plan) {
     const int shared = spec_attn::cross_variant(p.head_dim, plan.nq, false).ctas;   // CTAs an SM of a larger launch holds
-    const int64_t units = (static_cast<int64_t>(p.max_kv_len) + spec_attn::kBN - 1) / spec_attn::kBN;
+    const int64_t units = (static_cast<int64_t>(max_len) + spec_attn::kBN - 1) / spec_attn::kBN;
     const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
     // Model (us): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
     // cluster's barriers; the states come from HBM at best at its rate.
     const double fixed = 3.0, tile = plan.nq == 2 ? 0.85 : 0.45, cluster = 1.0;
-    const double hbm = static_cast<double>(p.num_reqs) * p.max_kv_len * p.num_kv_heads * p.head_dim * 4.0 / 6.5e6;
+    const double hbm = static_cast<double>(p.num_reqs) * max_len * p.num_kv_heads * p.head_dim * 4.0 / 6.5e6;
     double best = 1e300;
     int64_t best_u = units < 1 ? 1 : units;
     for (int64_t s = 1; s <= units && s <= spec_attn::kMaxSplits; ++s) {
@@ -736,7 +732,10 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
         return SPEC_ATTN_E_INVALID_ARG;
     if (p.head_dim != 64 && p.head_dim != 128 && p.head_dim != 256) return SPEC_ATTN_E_UNSUPPORTED;
     const int G = p.num_q_heads / p.num_kv_heads;
-    if (p.force_splits > spec_attn::kMaxSplits || G > SPEC_ATTN_MAX_GROUP || p.num_reqs > 65535 || p.num_kv_heads > 65535) return SPEC_ATTN_E_UNSUPPORTED;
+    if (p.force_splits > spec_attn::kMaxSplits || G > SPEC_ATTN_MAX_GROUP || p.num_reqs > 65535 || p.num_kv_heads > 65535)
+        return SPEC_ATTN_E_UNSUPPORTED;
+    // (2^30 rows of the smallest head are 128 GiB of K: a limit that keeps every index of the kernel in 32 bits)
+    if (p.total_q_rows > kMaxCrossRows || p.total_kv_rows > kMaxCrossRows) return SPEC_ATTN_E_UNSUPPORTED;
     const int64_t dense = static_cast<int64_t>(p.num_kv_heads) * p.head_dim;
     if (p.kv_row_stride != 0 && (p.kv_row_stride < dense || p.kv_row_stride % 8 != 0)) return SPEC_ATTN_E_INVALID_ARG;
     int dev = 0, sms = 0;
@@ -747,20 +746,23 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     if (!plan) return SPEC_ATTN_E_INVALID_ARG;
     plan->prob = p;
     if (p.kv_row_stride == 0) plan->prob.kv_row_stride = dense;
+    // bounds beyond the rows there are (INT32_MAX for "any") size nothing
+    const int max_rows = std::max(1, std::min(p.max_q_rows, p.total_q_rows));
+    const int max_len = std::min(p.max_kv_len, p.total_kv_rows);
     plan->device = dev;
     plan->num_sms = sms;
     plan->sm_scale = p.sm_scale > 0.f ? p.sm_scale : 1.0f / std::sqrt(static_cast<float>(p.head_dim));
     plan->wt = 128 / G;
-    plan->nq = (p.head_dim <= 128 && p.max_q_rows > plan->wt) ? 2 : 1;
-    plan->tiles = static_cast<int>((static_cast<int64_t>(p.max_q_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
+    plan->nq = (p.head_dim <= 128 && max_rows > plan->wt) ? 2 : 1;
+    plan->tiles = static_cast<int>((static_cast<int64_t>(max_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
     if (p.force_splits > 0) {
-        const int64_t units = (static_cast<int64_t>(p.max_kv_len) + spec_attn::kBN - 1) / spec_attn::kBN;
+        const int64_t units = (static_cast<int64_t>(max_len) + spec_attn::kBN - 1) / spec_attn::kBN;
         const int64_t u = (units + p.force_splits - 1) / p.force_splits;
         plan->keys_per_split = static_cast<int>((u < 1 ? 1 : u) * spec_attn::kBN);
     } else {
-        plan->keys_per_split = choose_split(p, *plan);
+        plan->keys_per_split = choose_split(p, max_len, *plan);
     }
-    plan->max_splits = p.max_kv_len == 0 ? 1 : (p.max_kv_len - 1) / plan->keys_per_split + 1;
+    plan->max_splits = max_len == 0 ? 1 : (max_len - 1) / plan->keys_per_split + 1;
     if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
         delete plan;
         return SPEC_ATTN_E_UNSUPPORTED;
@@ -825,25 +827,19 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     c.keys_per_split = plan->keys_per_split;
     c.score_scale_log2 = plan->sm_scale * 1.4426950408889634f;
 
-    CUtensorMap maps[3];
-    {
-        spec_attn_cross_plan* mp = const_cast<spec_attn_cross_plan*>(plan);
-        std::lock_guard<std::mutex> lock(mp->maps_mutex);
-        const void* key[3] = {q, k, v};
-        if (std::memcmp(key, mp->maps_key, sizeof(key)) != 0) {
-            std::memset(mp->maps, 0, sizeof(mp->maps));
-            std::memset(mp->maps_key, 0, sizeof(mp->maps_key));
-            const int bn = kBN;
-            // (with no state rows at all no copy is made: the maps stay empty)
-            if (p.total_kv_rows > 0 &&
-                !(encode_rows(&mp->maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim,
-                              static_cast<long long>(p.num_q_heads) * p.head_dim, c.group, c.wt) &&
-                  encode_rows(&mp->maps[1], k, p.total_kv_rows, p.num_kv_heads, p.head_dim, p.kv_row_stride, 1, bn) &&
-                  encode_rows(&mp->maps[2], v, p.total_kv_rows, p.num_kv_heads, p.head_dim, p.kv_row_stride, 1, bn)))
-                return SPEC_ATTN_E_INVALID_ARG;
-            std::memcpy(mp->maps_key, key, sizeof(key));
-        }
-        std::memcpy(maps, mp->maps, sizeof(maps));
+    CUtensorMap maps[3] = {};
+    auto encode = [&] {
+        return encode_rows(&maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim,
+                           static_cast<long long>(p.num_q_heads) * p.head_dim, c.group, c.wt) &&
+               encode_rows(&maps[1], k, p.total_kv_rows, p.num_kv_heads, p.head_dim, p.kv_row_stride, 1, kBN) &&
+               encode_rows(&maps[2], v, p.total_kv_rows, p.num_kv_heads, p.head_dim, p.kv_row_stride, 1, kBN);
+    };
+    // (with no state rows at all no copy is made: the maps stay empty)
+    if (p.total_kv_rows > 0 && !encode()) {
+        // a thread's first CUDA call has no context to encode in yet: bind the device's and try once more
+        e = cudaSetDevice(dev);
+        if (e != cudaSuccess) return record_cuda_error(e);
+        if (!encode()) return SPEC_ATTN_E_INVALID_ARG;
     }
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_handle);
     cudaLaunchConfig_t cfg = {};

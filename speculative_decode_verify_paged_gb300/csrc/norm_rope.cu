@@ -547,7 +547,7 @@ int prepare_call(const spec_attn_norm_rope_plan* plan, int32_t num_rows, const v
     if (p.num_q_heads > 0 && (!q || !q_out || !nr_aligned(q, 16) || !nr_aligned(q_out, 16)))
         return SPEC_ATTN_E_INVALID_ARG;
     if (p.num_kv_heads > 0 && (!k || !nr_aligned(k, 16))) return SPEC_ATTN_E_INVALID_ARG;
-    if (!nr_aligned(q_weight, 16) || !nr_aligned(k_weight, 16)) return SPEC_ATTN_E_INVALID_ARG;
+    if (!nr_aligned(q_weight, 4) || !nr_aligned(k_weight, 4)) return SPEC_ATTN_E_INVALID_ARG;
     if (p.rot_dim > 0 && (!positions || !nr_aligned(positions, 4))) return SPEC_ATTN_E_INVALID_ARG;
     int dev = -1;
     const cudaError_t e = cudaGetDevice(&dev);
@@ -658,7 +658,8 @@ int spec_attn_norm_rope(const spec_attn_norm_rope_plan* plan, int32_t num_rows, 
     if (st != SPEC_ATTN_OK) return st;
     if (p.num_kv_heads > 0 && (!k_out || !nr_aligned(k_out, 16))) return SPEC_ATTN_E_INVALID_ARG;
     // in place only where every element is written where it was read
-    if ((q_out == q && c.q_out_row_stride != c.q_row_stride) || (k_out == k && k && c.k_out_row_stride != c.k_row_stride))
+    if ((q_out == q && q && c.q_out_row_stride != c.q_row_stride) ||
+        (k_out == k && k && c.k_out_row_stride != c.k_row_stride))
         return SPEC_ATTN_E_INVALID_ARG;
     c.k_out = static_cast<uint16_t*>(k_out);
     const cudaError_t e = spec_attn::norm_rope_launch(c, p.head_dim, false, 0, plan->num_sms,

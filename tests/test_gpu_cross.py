@@ -12,6 +12,7 @@ moves O by at most 2^-8 A, rounding O itself by 2^-8 |O|:
   |got - want| <= 2^-8 (1 + 2^-6) (|O| + A) + 2 e A."""
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -155,6 +156,34 @@ def test_plan_bounds_above_the_batch():
     c = Case([5, 1], [77, 500], 32, 8, 128, max_q=500, max_kv=9000, seed=5)
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(24, 4, 256), (32, 8, 128), (8, 8, 64)])
+def test_bounds_that_bound_nothing(hq, hkv, d):
+    """The largest bounds there are: the rows themselves size the launch."""
+    c = Case([5, 1], [77, 500], hq, hkv, d, max_q=2 ** 31 - 1, max_kv=2 ** 31 - 1, seed=5)
+    c.run()
+    c.check()
+
+
+def test_two_calls_at_once():
+    """One plan from two threads on two streams, each with its buffers and workspace."""
+    cases = [Case([9, 200], [300, 900], 8, 2, 128, seed=s) for s in (20, 21)]
+    cases[1].plan = cases[0].plan
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+
+    def loop(c, s):
+        for _ in range(50):
+            c.run(stream=s)
+    threads = [threading.Thread(target=loop, args=a) for a in zip(cases, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for c in cases:
+        c.check()
 
 
 def test_random_batches():

@@ -170,6 +170,21 @@ def test_one_side_alone_and_no_rows():
     e.run()
 
 
+def test_weights_of_a_larger_buffer():
+    """Weights need no more than their type's alignment; a side without heads has no rows to be in place."""
+    c = Case(33, 8, 2, 128, seed=31)
+    c.run()
+    want = c.q_out.clone(), c.k_out.clone()
+    packed = torch.zeros(2 * 128 + 3, device="cuda")
+    packed[1:129], packed[130:258] = c.qw, c.kw
+    c.q_out.fill_(77.0), c.k_out.fill_(77.0)
+    sa.spec_attn_norm_rope(c.plan, c.q, c.k, packed[1:129], packed[130:258], c.pos, c.q_out, c.k_out)
+    assert torch.equal(c.q_out, want[0]) and torch.equal(c.k_out, want[1])
+    plan = sa.spec_attn_norm_rope_plan_create(num_q_heads=0, num_kv_heads=2, head_dim=128, rot_dim=0, inv_freq=[],
+                                              q_row_stride=512)
+    sa.spec_attn_norm_rope(plan, None, c.k, None, c.kw, None, None, c.k_out)
+
+
 def test_graph_replay_and_another_stream():
     c = Case(50, 24, 4, 256, seed=8)
     c.run()

@@ -193,6 +193,8 @@ def test_native_calls_count_their_arguments(lib):
     (dict(num_q_heads=34, num_kv_heads=2), sa.SPEC_ATTN_E_UNSUPPORTED),
     (dict(head_dim=96), sa.SPEC_ATTN_E_UNSUPPORTED),
     (dict(total_kv_rows=-1), sa.SPEC_ATTN_E_INVALID_ARG),
+    (dict(total_q_rows=2 ** 30 + 1), sa.SPEC_ATTN_E_UNSUPPORTED),
+    (dict(total_kv_rows=2 ** 30 + 1), sa.SPEC_ATTN_E_UNSUPPORTED),
     (dict(max_kv_len=-1), sa.SPEC_ATTN_E_INVALID_ARG),
     (dict(sm_scale=-0.5), sa.SPEC_ATTN_E_INVALID_ARG),
     (dict(sm_scale=float("nan")), sa.SPEC_ATTN_E_INVALID_ARG),
