@@ -547,24 +547,19 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         tmem_dealloc(tmem, L::kCols);
     }
     if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
-    // ---------------------------------------------------------------- rows out, 8 elements a thread
-    constexpr int C8 = D / 8;
-    auto put = [&](int m, int c, const float4& a, const float4& b) {
-        uint4 v;
-        const __nv_bfloat162 h0 = __floats2bfloat162_rn(a.x, a.y), h1 = __floats2bfloat162_rn(a.z, a.w);
-        const __nv_bfloat162 h2 = __floats2bfloat162_rn(b.x, b.y), h3 = __floats2bfloat162_rn(b.z, b.w);
-        v.x = *reinterpret_cast<const uint32_t*>(&h0);
-        v.y = *reinterpret_cast<const uint32_t*>(&h1);
-        v.z = *reinterpret_cast<const uint32_t*>(&h2);
-        v.w = *reinterpret_cast<const uint32_t*>(&h3);
-        st_global_v4(p.o + place(m) * D + c * 8, v);
+    // ---------------------------------------------------------------- rows out
+    auto pair = [](float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
     };
     if (nsplits == 1) {
         if (*abort) return;
+        constexpr int C8 = D / 8;
         for (int u = tid; u < rows * C8; u += L::kThreads) {
             const int m = u / C8, c = u % C8;
             const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
-            put(m, c, src[0], src[1]);
+            const float4 a = src[0], b = src[1];
+            st_global_v4(p.o + place(m) * D + c * 8, make_uint4(pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)));
             if (c == 0 && p.lse) p.lse[place(m)] = stage_lse[m] * kLn2;
         }
         return;
@@ -575,7 +570,9 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         auto combine = [&](auto most) {
             constexpr int N = decltype(most)::value;
             // Every load of a unit is on its way before the first is used, and each CTA begins with its own
-            // rows: were all to begin with rank 0, they would queue at one SM.
+            // rows: were all to begin with rank 0, they would queue at one SM.  Units of 4 elements: with 8, half
+            // the threads had none (16 rows of 32/8 heads x 128 over 4096 states in 8 splits 12.6 us, now 11.0).
+            constexpr int C4 = D / 4;
             uint32_t rows_at[N], lse_at[N];
 #pragma unroll
             for (int k = 0; k < N; ++k) {
@@ -583,15 +580,14 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 rows_at[k] = peer_addr(smem_addr(stage), k < nsplits ? from : split);
                 lse_at[k] = peer_addr(smem_addr(stage_lse), k < nsplits ? from : split);
             }
-            for (int u = split * L::kThreads + tid; u < rows * C8; u += nsplits * L::kThreads) {
-                const int m = u / C8, c = u % C8;
+            for (int u = split * L::kThreads + tid; u < rows * C4; u += nsplits * L::kThreads) {
+                const int m = u / C4, c = u % C4;
                 float ls[N];
-                float4 x[N], y[N];
+                float4 x[N];
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
                     ls[k] = ld_peer(lse_at[k] + m * 4);
-                    x[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 8) * 4);
-                    y[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 8 + 4) * 4);
+                    x[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 4) * 4);
                 }
                 float mx = ls[0], sum = 0.f;
 #pragma unroll
@@ -599,19 +595,17 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                     if (k >= nsplits) ls[k] = -INFINITY;
                     mx = fmaxf(mx, ls[k]);
                 }
-                float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
                     const float w = fast_exp2(ls[k] - mx);
                     a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
                     a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);
-                    b.x = fmaf(w, y[k].x, b.x); b.y = fmaf(w, y[k].y, b.y);
-                    b.z = fmaf(w, y[k].z, b.z); b.w = fmaf(w, y[k].w, b.w);
                     sum += w;
                 }
                 const float inv = 1.f / sum;
-                put(m, c, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv),
-                    make_float4(b.x * inv, b.y * inv, b.z * inv, b.w * inv));
+                *reinterpret_cast<uint2*>(p.o + place(m) * D + c * 4) =
+                    make_uint2(pair(a.x * inv, a.y * inv), pair(a.z * inv, a.w * inv));
                 if (c == 0 && p.lse) p.lse[place(m)] = (mx + log2f(sum)) * kLn2;
             }
         };
@@ -691,9 +685,32 @@ constexpr int32_t kMaxCrossRows = 1 << 30;
 
 bool cross_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
+// Clusters of `size` CTAs that the GPU holds at once: a cluster stays within one group of SMs (GPC), so CTAs that would
+// fit singly may not fit as clusters (16 clusters of 8 on 152 SMs: 25.4 us where 16 of 6 take 20.6).
+int resident_clusters(const spec_attn::CrossVariant& v, int size, int num_sms) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, v.kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, num_sms / size);
+    }
+    return n * v.ctas;   // (counted at one CTA an SM for kernels with tensor memory)
+}
+
 // States a split takes (a multiple of the tile).
 int choose_split(const spec_attn_cross_problem& p, int max_len, const spec_attn_cross_plan& plan) {
-    const int shared = spec_attn::cross_variant(p.head_dim, plan.nq, false).ctas;   // CTAs an SM of a larger launch holds
+    const spec_attn::CrossVariant deep = spec_attn::cross_variant(p.head_dim, plan.nq, true);
+    const spec_attn::CrossVariant shared = spec_attn::cross_variant(p.head_dim, plan.nq, false);
     const int64_t units = (static_cast<int64_t>(max_len) + spec_attn::kBN - 1) / spec_attn::kBN;
     const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
     // Model (us): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
@@ -704,8 +721,11 @@ int choose_split(const spec_attn_cross_problem& p, int max_len, const spec_attn_
     int64_t best_u = units < 1 ? 1 : units;
     for (int64_t s = 1; s <= units && s <= spec_attn::kMaxSplits; ++s) {
         const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
-        const int64_t slots = static_cast<int64_t>(plan.num_sms) * (ctas * splits <= plan.num_sms ? 1 : shared);
-        const int64_t waves = (ctas * splits + slots - 1) / slots;
+        if (splits < s) continue;                  // (as an earlier s)
+        const spec_attn::CrossVariant& v = ctas * splits <= plan.num_sms ? deep : shared;
+        const int64_t at_once = splits == 1 ? static_cast<int64_t>(plan.num_sms) * v.ctas
+                                            : resident_clusters(v, static_cast<int>(splits), plan.num_sms);
+        const int64_t waves = (ctas + at_once - 1) / at_once;
         const double cta = fixed + static_cast<double>(u) * tile + (splits > 1 ? cluster : 0.0);
         const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed);
         if (cost < best * 0.98) {
@@ -755,6 +775,14 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     plan->wt = 128 / G;
     plan->nq = (p.head_dim <= 128 && max_rows > plan->wt) ? 2 : 1;
     plan->tiles = static_cast<int>((static_cast<int64_t>(max_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
+    for (const bool deep : {true, false}) {
+        const spec_attn::CrossVariant v = spec_attn::cross_variant(p.head_dim, plan->nq, deep);
+        e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e != cudaSuccess) {
+            delete plan;
+            return spec_attn::record_cuda_error(e);
+        }
+    }
     if (p.force_splits > 0) {
         const int64_t units = (static_cast<int64_t>(max_len) + spec_attn::kBN - 1) / spec_attn::kBN;
         const int64_t u = (units + p.force_splits - 1) / p.force_splits;
@@ -769,11 +797,6 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     }
     plan->variant = spec_attn::cross_variant(
         p.head_dim, plan->nq, static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms);
-    e = cudaFuncSetAttribute(plan->variant.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, plan->variant.smem);
-    if (e != cudaSuccess) {
-        delete plan;
-        return spec_attn::record_cuda_error(e);
-    }
     if (workspace_bytes) *workspace_bytes = 256;
     *out = plan;
     return SPEC_ATTN_OK;
