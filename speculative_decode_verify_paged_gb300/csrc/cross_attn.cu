@@ -142,24 +142,45 @@ __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) 
     return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);   // (in a cluster the address has the rank above bit 23)
 }
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 B apart, version 1, 128-byte swizzle
-__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+// Products and commits are issued by the one thread whose `go` is set, under a
+// predicate: the whole warp runs the issuing loop and its waits.  (With the loop
+// in a branch of one thread, each wait cost the next product 200 clocks: 8 + 4
+// instructions with a wait before each kind took 1053 clocks, and 621 like this.)
+__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate,
+                                          uint32_t go) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "{\n\t.reg .pred p, g;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 g, %6, 0;\n\t"
         "mov.b64 a, {%1, %5};\n\t"
         "mov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi)
+        "@g tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate,
+                                          uint32_t go) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "{\n\t.reg .pred p, g;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 g, %6, 0;\n\t"
         "mov.b64 b, {%2, %5};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi)
+        "@g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go)
         : "memory");
+}
+__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t go) {
+    asm volatile(
+        "{\n\t.reg .pred g;\n\t"
+        "setp.ne.b32 g, %1, 0;\n\t"
+        "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+        "r"(go)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
 
 // Thread-block cluster: all threads of all its CTAs (those that left count as
@@ -349,82 +370,81 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         __syncwarp();
     } else if (warp == 1 || (warp == 2 && (NQ == 1 || nact == 2))) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16_f32(kM, BN, 0, 0);
-            constexpr uint32_t idesc_o = idesc_bf16_f32(kM, D, 0, 1);
-            const int i = NQ == 2 ? warp - 1 : 0;
-            const uint32_t q_lo = desc_lo(smem_addr(sQ + i * L::kQBytes), 16);
-            const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), BN * 128);
-            auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort, kWaitLimit); };
-            // the ring slots of K_t and V_t, and the slot t mod ring, stepped along with the parity of their phase
-            struct Step {
-                int size, slot;
-                uint32_t par;
-                __device__ __forceinline__ void by(int n) {
-                    slot += n;
-                    if (slot >= size) {
-                        slot -= size;
-                        par ^= 1;
-                    }
+        const uint32_t go = elected();
+        constexpr uint32_t idesc_s = idesc_bf16_f32(kM, BN, 0, 0);
+        constexpr uint32_t idesc_o = idesc_bf16_f32(kM, D, 0, 1);
+        const int i = NQ == 2 ? warp - 1 : 0;
+        const uint32_t q_lo = desc_lo(smem_addr(sQ + i * L::kQBytes), 16);
+        const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), BN * 128);
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, abort); };
+        // the ring slots of K_t and V_t, and the slot t mod ring, stepped along with the parity of their phase
+        struct Step {
+            int size, slot;
+            uint32_t par;
+            __device__ __forceinline__ void by(int n) {
+                slot += n;
+                if (slot >= size) {
+                    slot -= size;
+                    par ^= 1;
                 }
-            };
-            Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
-            Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - lead of the next S)
-            // S_t, once K_t is here and the P that sat in S_t's buffer has been read
-            auto do_s = [&](int t) {
-                const int b = t & (NB - 1);
-                if (t >= L::kLead) {
-                    if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
-                    before.by(1);
-                }
-                if (!wait(&aux->full[ks.slot], ks.par)) return false;
-                tc_fence_after();
-                const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int c = kk >> 2, sub = kk & 3;
-                    mma_ss_lo(d_tmem, q_lo + c * (kM * 128 >> 4) + sub * 2, k_lo + c * (BN * 128 >> 4) + sub * 2, idesc_s,
-                              kk > 0);
-                }
-                mma_commit(&aux->s_full[i][b]);
-                if (NQ == 1) mma_commit(&aux->empty[ks.slot]);
-                ks.by(NQ == 1 ? 2 : 1);
-                return true;
-            };
-            // O += P_t V_t, once both are here (NQ = 2: V_t came with K_t)
-            auto do_pv = [&](int t) {
-                const int b = t & (NB - 1);
-                if (NQ == 1 && !wait(&aux->full[vs.slot], vs.par)) return false;
-                if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
-                tc_fence_after();
-                const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
-                const uint32_t p_tmem = tmem + L::s_col(i, b);
-                const int steps = t == T - 1 ? (tail + 15) / 16 : BN / 16;
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * (2048 >> 4), idesc_o, t > 0 || kk > 0);
-                mma_commit(&aux->pv_done[i][done.slot]);
-                if (NQ == 1) mma_commit(&aux->empty[vs.slot]);
-                vs.by(NQ == 1 ? 2 : 1);
-                done.by(1);
-                return true;
-            };
-            bool ok = true;
-            if (NQ == 2 || warp == 1) ok = wait(&aux->q_full[i], 0);
-            if (NQ == 2) {
-                ok = ok && do_s(0);
-                for (int t = 0; t < T && ok; ++t) ok = (t + 1 == T || do_s(t + 1)) && do_pv(t);
-            } else if (warp == 1) {
-                for (int t = 0; t < T && ok; ++t) ok = do_s(t);
-            } else {
-                for (int t = 0; t < T && ok; ++t) ok = do_pv(t);
             }
-            // every product this thread issued completes before the memory is released
-            uint64_t* drain = &aux->drain[warp - 1];
-            mma_commit(drain);
-            volatile int no_abort = 0;
-            mbar_wait(drain, 0, &no_abort, kDrainLimit);
+        };
+        Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
+        Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - lead of the next S)
+        // S_t, once K_t is here and the P that sat in S_t's buffer has been read
+        auto do_s = [&](int t) {
+            const int b = t & (NB - 1);
+            if (t >= L::kLead) {
+                if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
+                before.by(1);
+            }
+            if (!wait(&aux->full[ks.slot], ks.par)) return false;
+            tc_fence_after();
+            const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const int c = kk >> 2, sub = kk & 3;
+                mma_ss_lo(d_tmem, q_lo + c * (kM * 128 >> 4) + sub * 2, k_lo + c * (BN * 128 >> 4) + sub * 2, idesc_s,
+                          kk > 0, go);
+            }
+            commit_if(&aux->s_full[i][b], go);
+            if (NQ == 1) commit_if(&aux->empty[ks.slot], go);
+            ks.by(NQ == 1 ? 2 : 1);
+            return true;
+        };
+        // O += P_t V_t, once both are here (NQ = 2: V_t came with K_t)
+        auto do_pv = [&](int t) {
+            const int b = t & (NB - 1);
+            if (NQ == 1 && !wait(&aux->full[vs.slot], vs.par)) return false;
+            if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
+            tc_fence_after();
+            const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
+            const uint32_t p_tmem = tmem + L::s_col(i, b);
+            const int steps = t == T - 1 ? (tail + 15) / 16 : BN / 16;
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+                if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * (2048 >> 4), idesc_o, t > 0 || kk > 0, go);
+            commit_if(&aux->pv_done[i][done.slot], go);
+            if (NQ == 1) commit_if(&aux->empty[vs.slot], go);
+            vs.by(NQ == 1 ? 2 : 1);
+            done.by(1);
+            return true;
+        };
+        bool ok = true;
+        if (NQ == 2 || warp == 1) ok = wait(&aux->q_full[i], 0);
+        if (NQ == 2) {
+            ok = ok && do_s(0);
+            for (int t = 0; t < T && ok; ++t) ok = (t + 1 == T || do_s(t + 1)) && do_pv(t);
+        } else if (warp == 1) {
+            for (int t = 0; t < T && ok; ++t) ok = do_s(t);
+        } else {
+            for (int t = 0; t < T && ok; ++t) ok = do_pv(t);
         }
+        // every product this thread issued completes before the memory is released
+        uint64_t* drain = &aux->drain[warp - 1];
+        commit_if(drain, go);
+        volatile int no_abort = 0;
+        mbar_wait(drain, 0, &no_abort, kDrainLimit);
         __syncwarp();
     } else if (warp >= 4 && (warp < 8 || nact == 2)) {
         // ------------------------------------------------------------ softmax and epilogue
@@ -708,14 +728,16 @@ int resident_clusters(const spec_attn::CrossVariant& v, int size, int num_sms) {
 }
 
 // States a split takes (a multiple of the tile).
-int choose_split(const spec_attn_cross_problem& p, int max_len, const spec_attn_cross_plan& plan) {
+int choose_split(const spec_attn_cross_problem& p, int max_rows, int max_len, const spec_attn_cross_plan& plan) {
     const spec_attn::CrossVariant deep = spec_attn::cross_variant(p.head_dim, plan.nq, true);
     const spec_attn::CrossVariant shared = spec_attn::cross_variant(p.head_dim, plan.nq, false);
     const int64_t units = (static_cast<int64_t>(max_len) + spec_attn::kBN - 1) / spec_attn::kBN;
     const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
-    // Model (us): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
-    // cluster's barriers; the states come from HBM at best at its rate.
-    const double fixed = 3.0, tile = plan.nq == 2 ? 0.85 : 0.45, cluster = 1.0;
+    // Model (us, measured): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
+    // cluster's barriers and the exchange of its rows; the states come from HBM at best at its rate.
+    const double fixed = 3.0, tile = plan.nq == 2 || p.head_dim == 256 ? 0.8 : 0.43;
+    const double rows = std::min(static_cast<double>(max_rows), static_cast<double>(plan.nq * plan.wt));
+    const double cluster = 1.0 + rows * (p.num_q_heads / p.num_kv_heads) * p.head_dim / 15e3;
     const double hbm = static_cast<double>(p.num_reqs) * max_len * p.num_kv_heads * p.head_dim * 4.0 / 6.5e6;
     double best = 1e300;
     int64_t best_u = units < 1 ? 1 : units;
@@ -788,7 +810,7 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
         const int64_t u = (units + p.force_splits - 1) / p.force_splits;
         plan->keys_per_split = static_cast<int>((u < 1 ? 1 : u) * spec_attn::kBN);
     } else {
-        plan->keys_per_split = choose_split(p, max_len, *plan);
+        plan->keys_per_split = choose_split(p, max_rows, max_len, *plan);
     }
     plan->max_splits = max_len == 0 ? 1 : (max_len - 1) / plan->keys_per_split + 1;
     if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
