@@ -72,11 +72,14 @@ constexpr float kCrossRescale = 8.0f;   // log2 units: O is rescaled when a row'
 constexpr int kBN = 64;                 // states a tile
 
 // DEEP (one tile, d <= 128): the launch has no more CTAs than SMs, and a CTA
-// takes the whole SM; otherwise two CTAs share it, one's start, end and waits
-// under the other's work.  (d = 256 and two tiles always take the whole SM.)
+// takes the whole SM (12 slots and four S buffers; 9 rows x 32/8 heads x 128 over
+// 1500 states for 8 requests: 12.8 us, 14.8 with the half-SM layout); otherwise
+// two CTAs share it, one's start, end and waits under the other's work (64
+// single tokens over 1601 states: 69.9 us, 80.4 with one CTA an SM).  d = 256
+// and two tiles always take the whole SM.
 template <int D, int NQ, bool DEEP>
 struct CrossLayout {
-    static_assert(NQ == 1 || D <= 128, "two O tiles and four S buffers fit 512 columns up to d = 128");
+    static_assert(NQ == 1 || D == 128, "two O tiles and four S buffers fit 512 columns up to d = 128");
     static constexpr int kChunks = D / 64;
     static constexpr int kQBytes = kM * D * 2;             // one query tile
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
@@ -651,7 +654,7 @@ CrossVariant variant_of() {
 }
 CrossVariant cross_variant(int d, int nq, bool deep) {
     if (d == 256) return variant_of<256, 1, true>();
-    if (nq == 2) return d == 64 ? variant_of<64, 2, true>() : variant_of<128, 2, true>();
+    if (nq == 2) return variant_of<128, 2, true>();
     if (d == 64) return deep ? variant_of<64, 1, true>() : variant_of<64, 1, false>();
     return deep ? variant_of<128, 1, true>() : variant_of<128, 1, false>();
 }
@@ -733,22 +736,25 @@ int choose_split(const spec_attn_cross_problem& p, int max_rows, int max_len, co
     const spec_attn::CrossVariant shared = spec_attn::cross_variant(p.head_dim, plan.nq, false);
     const int64_t units = (static_cast<int64_t>(max_len) + spec_attn::kBN - 1) / spec_attn::kBN;
     const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
-    // Model (us, measured): a CTA has a start and an end, a time for each tile of 64 states, and with splits the
-    // cluster's barriers and the exchange of its rows; the states come from HBM at best at its rate.
-    const double fixed = 3.0, tile = plan.nq == 2 || p.head_dim == 256 ? 0.8 : 0.43;
-    const double rows = std::min(static_cast<double>(max_rows), static_cast<double>(plan.nq * plan.wt));
-    const double cluster = 1.0 + rows * (p.num_q_heads / p.num_kv_heads) * p.head_dim / 15e3;
+    // Model (us, measured): a CTA has a start and an end, a time for each tile of 64 states (longer beside another CTA
+    // with many rows), and with splits the cluster's barriers and the exchange of its rows; the states come from HBM
+    // at best at its rate.
+    const double rows = std::min(max_rows, plan.nq * plan.wt) * (p.num_q_heads / p.num_kv_heads);
+    const double fixed = 3.0, cluster = 1.0 + rows * p.head_dim / 6e3;
+    const bool whole = plan.nq == 2 || p.head_dim == 256;
+    const double tile_alone = whole ? 0.8 : 0.43, tile_shared = whole ? 0.8 : (p.head_dim == 64 ? 0.3 : 0.45) * (1.0 + rows / 128.0);
     const double hbm = static_cast<double>(p.num_reqs) * max_len * p.num_kv_heads * p.head_dim * 4.0 / 6.5e6;
     double best = 1e300;
     int64_t best_u = units < 1 ? 1 : units;
     for (int64_t s = 1; s <= units && s <= spec_attn::kMaxSplits; ++s) {
         const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
         if (splits < s) continue;                  // (as an earlier s)
-        const spec_attn::CrossVariant& v = ctas * splits <= plan.num_sms ? deep : shared;
+        const bool alone = ctas * splits <= plan.num_sms;
+        const spec_attn::CrossVariant& v = alone ? deep : shared;
         const int64_t at_once = splits == 1 ? static_cast<int64_t>(plan.num_sms) * v.ctas
                                             : resident_clusters(v, static_cast<int>(splits), plan.num_sms);
         const int64_t waves = (ctas + at_once - 1) / at_once;
-        const double cta = fixed + static_cast<double>(u) * tile + (splits > 1 ? cluster : 0.0);
+        const double cta = fixed + static_cast<double>(u) * (alone ? tile_alone : tile_shared) + (splits > 1 ? cluster : 0.0);
         const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed);
         if (cost < best * 0.98) {
             best = cost;
@@ -795,7 +801,12 @@ int spec_attn_cross_plan_create(const spec_attn_cross_problem* problem, spec_att
     plan->num_sms = sms;
     plan->sm_scale = p.sm_scale > 0.f ? p.sm_scale : 1.0f / std::sqrt(static_cast<float>(p.head_dim));
     plan->wt = 128 / G;
-    plan->nq = (p.head_dim <= 128 && max_rows > plan->wt) ? 2 : 1;
+    // Two query tiles a CTA read K and V once for both, but make half as many CTAs: for d = 128, where one-tile CTAs
+    // would not fit the SMs at once (32/8 heads x 128: 377 instead of 401 us at 4096 x 4096 for two requests, 18.8
+    // instead of 19.6 at 1000 x 1000; below, 17.5 instead of 26 us with one tile at 2 x 200 x 1500).  At d = 64 two
+    // one-tile CTAs an SM are faster throughout (16/8 heads, 4096 x 4096, two requests: 162 instead of 190 us).
+    const int64_t one_tile = (static_cast<int64_t>(max_rows) + plan->wt - 1) / plan->wt * p.num_kv_heads * p.num_reqs;
+    plan->nq = p.head_dim == 128 && max_rows > plan->wt && one_tile > sms ? 2 : 1;
     plan->tiles = static_cast<int>((static_cast<int64_t>(max_rows) + plan->nq * plan->wt - 1) / (plan->nq * plan->wt));
     for (const bool deep : {true, false}) {
         const spec_attn::CrossVariant v = spec_attn::cross_variant(p.head_dim, plan->nq, deep);
