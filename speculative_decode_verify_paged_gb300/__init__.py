@@ -5,7 +5,7 @@ Every step of the computation runs in the library's CUDA kernels; this module
 only marshals arguments: torch tensors are passed as device pointers and the
 current torch CUDA stream is used unless another is given.  The calls around
 the attention (step tables, norm and rotation, cross attention) go through a
-small extension module (``csrc/binding.c``) with the same checks.  There is no CPU
+small extension module (``csrc/binding.cpp``) with the same checks.  There is no CPU
 path: if the library is missing, every call raises.
 
 Names follow the C ABI::
@@ -453,7 +453,7 @@ def _native():
     if _calls is None:
         import importlib.machinery
         import importlib.util
-        import torch
+        import torch  # noqa: F401  (the module uses the libraries that torch loads)
         load_library()
         path = os.path.join(HERE, "_build", "spec_attn_calls.so")
         if not os.path.exists(path):
@@ -462,8 +462,6 @@ def _native():
         loader = importlib.machinery.ExtensionFileLoader("spec_attn_calls", path)
         mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("spec_attn_calls", loader))
         loader.exec_module(mod)
-        mod.setup(torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8, torch.cuda.current_device,
-                  torch._C._cuda_getCurrentRawStream)
         _calls = mod
     return _calls
 

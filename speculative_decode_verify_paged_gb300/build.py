@@ -3,13 +3,16 @@
 Each CUDA translation unit under csrc/ is compiled in parallel into
 _build/*.o, then linked into _build/libspec_attn.so (CUDA runtime linked
 statically, so the library needs only the driver).  The native side of the
-Python binding, csrc/binding.c, becomes the extension module
-_build/spec_attn_calls.so, linked against that library.  No cmake.
+Python binding, csrc/binding.cpp, becomes the extension module
+_build/spec_attn_calls.so, compiled with torch's headers and linked against that
+library.  No cmake.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,7 +26,7 @@ ROOT = os.path.dirname(HERE)
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(BUILD, "libspec_attn.so")
 CALLS = os.path.join(BUILD, "spec_attn_calls.so")
-BINDING = os.path.join(CSRC, "binding.c")
+BINDING = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -61,14 +64,36 @@ def _compile(src, extra):
     return obj, res.stderr
 
 
-def _build_binding():
-    """The extension module: plain C against the running interpreter's headers, finding the library beside it."""
-    tmp = CALLS + f".{os.getpid()}.tmp"
-    cmd = [os.environ.get("CC", "gcc"), "-shared", "-fPIC", "-O2", "-std=c11", "-Wall", "-I", INCLUDE,
-           "-I", sysconfig.get_paths()["include"], BINDING, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN"]
+def _torch_dir() -> str:
+    """Torch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("the Python binding needs torch")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _compile_binding():
+    """The extension module's object: C++ against the headers of the running interpreter and torch."""
+    torch_include = os.path.join(_torch_dir(), "include")
+    obj = os.path.join(BUILD, "binding.o")
+    cmd = [os.environ.get("CXX", "g++"), "-c", "-fPIC", "-O2", "-std=c++17", "-Wall", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", torch_include,
+           "-isystem", os.path.join(torch_include, "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), BINDING, "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"building the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj):
+    """The module finds the library beside it, and torch's libraries where the importing process has loaded them."""
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, CALLS)
 
 
@@ -77,13 +102,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     deps = _deps()
     srcs = sources()
-    # the library is also stale when a source was added or removed since it was linked
+    # the library is also stale when a source was added or removed since it was linked, the module with another torch
     stamp = os.path.join(BUILD, "sources.txt")
-    listing = "\n".join(os.path.basename(s) for s in srcs)
+    listing = "\n".join([os.path.basename(s) for s in srcs] + ["torch " + importlib.metadata.version("torch")])
     same_set = os.path.exists(stamp) and open(stamp).read() == listing
     if not force and not extra_flags and same_set and not _stale(LIB, deps) and not _stale(CALLS, deps):
         return LIB
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, extra_flags), srcs))
     objs = [o for o, _ in results]
     if verbose:
@@ -96,7 +122,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
-    _build_binding()
+    _link_binding(binding.result())
     with open(stamp, "w") as f:
         f.write(listing)
     return LIB

@@ -2,139 +2,127 @@
  * Native side of the Python binding for the calls around the attention (step
  * tables, norm and rotation, cross attention): checks the tensors and makes
  * the C ABI call in one step.  A decode step makes these calls once a layer on
- * kernels of a few microseconds, and the same checks written in Python cost
- * more than the launch (12 tensors: 7.8 of 10.5 us).
+ * kernels of a few microseconds, and the same checks cost more than the launch
+ * when written in Python (12 tensors: 7.8 of 10.5 us) or through the tensors'
+ * Python attributes (2.7 of 6.2); here they are reads of the tensor objects.
  *
- * Tensors are read through their Python attributes (dtype, shape, stride,
- * get_device, is_contiguous, data_ptr), so the module depends on no tensor
- * library's headers.  A bad tensor raises ValueError before anything is
- * launched; the call's spec_attn_status is returned as an int.
+ * A bad tensor raises ValueError before anything is launched; the call's
+ * spec_attn_status is returned as an int.  The library itself does not depend
+ * on torch, only this module does.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
-#include <stdint.h>
+
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdint>
+#include <exception>
 
 #include "spec_attn.h"
 
-static PyObject *n_dtype, *n_shape, *n_stride, *n_get_device, *n_is_contiguous, *n_data_ptr, *n_cuda_stream;
-/* set by setup(): the dtypes, and callables for the current device and its current stream's handle */
-static PyObject *t_bf16, *t_f32, *t_i32, *t_i64, *t_u8, *f_device, *f_stream;
+static PyObject* n_cuda_stream;
 
 enum { kMaxDims = 4 };
+static constexpr at::ScalarType t_bf16 = at::kBFloat16, t_f32 = at::kFloat, t_i32 = at::kInt, t_i64 = at::kLong,
+                                t_u8 = at::kByte;
 
 /* A tensor as a call wants it; shape entries of -1 take the tensor's own size. */
 typedef struct {
     const char* what;
-    PyObject* dtype;
+    at::ScalarType dtype;
     int nd;
     int64_t shape[kMaxDims];
     const int64_t* strides;   /* elements; NULL: contiguous */
 } want_t;
 
-static int sizes(PyObject* tuple, const want_t* w, int64_t* out) {
-    if (!PyTuple_Check(tuple) || PyTuple_GET_SIZE(tuple) != w->nd) {
-        PyErr_Format(PyExc_ValueError, "%s must have %d dimensions, got the shape %R", w->what, w->nd, tuple);
-        return -1;
+/* A checked tensor's address, as whatever pointer the call takes. */
+struct Address {
+    void* p = nullptr;
+    template <class T>
+    operator T*() const {
+        return static_cast<T*>(p);
     }
-    for (int i = 0; i < w->nd; ++i) {
-        out[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(tuple, i));
-        if (out[i] == -1 && PyErr_Occurred()) return -1;
-    }
-    return 0;
-}
+};
 
-/* Address of `t` after its checks, NULL for None.  *dev is the current device, asked for with the first tensor. */
-static int address(PyObject* t, want_t* w, long* dev, void** out) {
-    *out = NULL;
-    if (t == Py_None) return 0;
-    PyObject* o = PyObject_CallMethodNoArgs(t, n_get_device);
-    if (!o) return -1;
-    const long at = PyLong_AsLong(o);
-    Py_DECREF(o);
-    if (at == -1 && PyErr_Occurred()) return -1;
-    if (at < 0) {
+static int check(const at::Tensor& t, want_t* w, long* dev, Address* out) {
+    if (!t.is_cuda()) {
         PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", w->what);
         return -1;
     }
-    if (*dev < 0) {
-        o = PyObject_CallNoArgs(f_device);
-        if (!o) return -1;
-        *dev = PyLong_AsLong(o);
-        Py_DECREF(o);
-        if (*dev < 0) {
-            if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "no current CUDA device");
-            return -1;
-        }
-    }
+    if (*dev < 0) *dev = c10::cuda::current_device();
+    const long at = t.get_device();
     if (at != *dev) {
         PyErr_Format(PyExc_ValueError, "%s must be on the current device, cuda:%ld, got cuda:%ld", w->what, *dev, at);
         return -1;
     }
-    o = PyObject_GetAttr(t, n_dtype);
-    if (!o) return -1;
-    const int same = o == w->dtype;
-    if (!same) PyErr_Format(PyExc_ValueError, "%s must be %S, got %S", w->what, w->dtype, o);
-    Py_DECREF(o);
-    if (!same) return -1;
-    o = PyObject_GetAttr(t, n_shape);
-    if (!o) return -1;
-    int64_t got[kMaxDims];
-    int bad = sizes(o, w, got);
-    for (int i = 0; !bad && i < w->nd; ++i) {
-        if (w->shape[i] < 0) w->shape[i] = got[i];
-        if (w->shape[i] != got[i]) {
-            PyErr_Format(PyExc_ValueError, "%s must have %lld entries in dimension %d, got the shape %R", w->what,
-                         (long long)w->shape[i], i, o);
-            bad = -1;
-        }
+    if (t.scalar_type() != w->dtype) {
+        PyErr_Format(PyExc_ValueError, "%s must be %s, got %s", w->what, c10::toString(w->dtype),
+                     c10::toString(t.scalar_type()));
+        return -1;
     }
-    Py_DECREF(o);
-    if (bad) return -1;
-    if (w->strides) {
-        o = PyObject_CallMethodNoArgs(t, n_stride);
-        if (!o) return -1;
-        bad = sizes(o, w, got);
-        for (int i = 0; !bad && i < w->nd; ++i) {
-            if (w->shape[i] > 1 && got[i] != w->strides[i]) {
-                PyErr_Format(PyExc_ValueError, "%s must have a stride of %lld elements in dimension %d, got %R", w->what,
-                             (long long)w->strides[i], i, o);
-                bad = -1;
-            }
+    const at::IntArrayRef size = t.sizes(), step = t.strides();
+    if (static_cast<int>(size.size()) != w->nd) {
+        PyErr_Format(PyExc_ValueError, "%s must have %d dimensions, got %d", w->what, w->nd, static_cast<int>(size.size()));
+        return -1;
+    }
+    for (int i = 0; i < w->nd; ++i) {
+        if (w->shape[i] < 0) w->shape[i] = size[i];
+        if (w->shape[i] != size[i]) {
+            PyErr_Format(PyExc_ValueError, "%s must have %lld entries in dimension %d, got %lld", w->what,
+                         static_cast<long long>(w->shape[i]), i, static_cast<long long>(size[i]));
+            return -1;
         }
-        Py_DECREF(o);
-        if (bad) return -1;
-    } else {
-        o = PyObject_CallMethodNoArgs(t, n_is_contiguous);
-        if (!o) return -1;
-        const int yes = o == Py_True;
-        Py_DECREF(o);
-        if (!yes) {
-            PyErr_Format(PyExc_ValueError, "%s must be contiguous", w->what);
+        if (w->strides && size[i] > 1 && step[i] != w->strides[i]) {
+            PyErr_Format(PyExc_ValueError, "%s must have a stride of %lld elements in dimension %d, got %lld", w->what,
+                         static_cast<long long>(w->strides[i]), i, static_cast<long long>(step[i]));
             return -1;
         }
     }
-    o = PyObject_CallMethodNoArgs(t, n_data_ptr);
-    if (!o) return -1;
-    *out = PyLong_AsVoidPtr(o);
-    Py_DECREF(o);
-    return (!*out && PyErr_Occurred()) ? -1 : 0;
+    if (!w->strides && !t.is_contiguous()) {
+        PyErr_Format(PyExc_ValueError, "%s must be contiguous", w->what);
+        return -1;
+    }
+    out->p = t.mutable_data_ptr();
+    return 0;
+}
+
+/* Address of `t` after its checks, NULL for None.  *dev is the current device, asked for with the first tensor. */
+static int address(PyObject* t, want_t* w, long* dev, Address* out) {
+    out->p = nullptr;
+    if (t == Py_None) return 0;
+    if (!THPVariable_Check(t)) {
+        PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor", w->what);
+        return -1;
+    }
+    try {
+        return check(THPVariable_Unpack(t), w, dev, out);
+    } catch (const std::exception& e) {   /* (a tensor without storage, a failing driver) */
+        PyErr_Format(PyExc_RuntimeError, "%s: %s", w->what, e.what());
+        return -1;
+    }
 }
 
 /* Handle of `stream` (a torch stream, or None: the current one of the device). */
 static int stream_of(PyObject* stream, long dev, spec_attn_stream_t* out) {
-    PyObject* o;
     if (stream == Py_None) {
-        PyObject* d = PyLong_FromLong(dev < 0 ? 0 : dev);
-        if (!d) return -1;
-        o = PyObject_CallOneArg(f_stream, d);
-        Py_DECREF(d);
-    } else {
-        o = PyObject_GetAttr(stream, n_cuda_stream);
+        try {
+            if (dev < 0) dev = c10::cuda::current_device();
+            *out = reinterpret_cast<spec_attn_stream_t>(
+                c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
+        } catch (const std::exception& e) {
+            PyErr_SetString(PyExc_RuntimeError, e.what());
+            return -1;
+        }
+        return 0;
     }
+    PyObject* o = PyObject_GetAttr(stream, n_cuda_stream);
     if (!o) return -1;
-    *out = (spec_attn_stream_t)PyLong_AsVoidPtr(o);
+    void* p = PyLong_AsVoidPtr(o);
+    *out = reinterpret_cast<spec_attn_stream_t>(p);
     Py_DECREF(o);
-    return (!*out && PyErr_Occurred()) ? -1 : 0;
+    return (!p && PyErr_Occurred()) ? -1 : 0;
 }
 
 /* Integers of a tuple. */
@@ -157,10 +145,10 @@ static int count_args(const char* name, Py_ssize_t got, Py_ssize_t want) {
 }
 
 /* The workspace, one-dimensional bytes. */
-static int workspace_of(PyObject* t, long* dev, void** out, int64_t* bytes) {
+static int workspace_of(PyObject* t, long* dev, Address* out, int64_t* bytes) {
     want_t w = {"workspace", t_u8, 1, {-1}, NULL};
     if (address(t, &w, dev, out)) return -1;
-    *bytes = *out ? w.shape[0] : 0;
+    *bytes = out->p ? w.shape[0] : 0;
     return 0;
 }
 
@@ -171,7 +159,7 @@ static PyObject* build_tables(PyObject* self, PyObject* const* a, Py_ssize_t n) 
     int64_t c[3], bytes;
     if (count_args("build_tables", n, 14) || ints(a[0], 3, c)) return NULL;
     long dev = -1;
-    void *ctx, *win, *prev, *count0, *pages, *table, *seq, *indptr, *count, *pos, *slot, *ws;
+    Address ctx, win, prev, count0, pages, table, seq, indptr, count, pos, slot, ws;
     want_t w = {"ctx_lens", t_i32, 1, {-1}, NULL};
     if (address(a[1], &w, &dev, &ctx)) return NULL;
     const int64_t P = w.shape[0];
@@ -213,7 +201,7 @@ static PyObject* build_tables(PyObject* self, PyObject* const* a, Py_ssize_t n) 
 enum { kHandle, kHq, kHkv, kD, kAxes, kQs, kKs, kVs, kQos, kKos, kKvDtype, kPageSize, kPages, kKvStride, kScStride, kNr };
 
 /* Rows of heads, `stride` elements apart. */
-static int rows_of(PyObject* t, const char* what, int64_t n, int64_t h, int64_t d, int64_t stride, long* dev, void** out,
+static int rows_of(PyObject* t, const char* what, int64_t n, int64_t h, int64_t d, int64_t stride, long* dev, Address* out,
                    int64_t* got_n) {
     const int64_t strides[3] = {stride ? stride : h * d, d, 1};
     want_t w = {what, t_bf16, 3, {n, h, d}, strides};
@@ -226,7 +214,7 @@ typedef struct {
     int64_t c[kNr];
     int64_t n;
     long dev;
-    void *q, *k, *qw, *kw, *pos;
+    Address q, k, qw, kw, pos;
 } nr_call;
 
 /* a: plan, q, k, q_weight, k_weight, positions */
@@ -255,7 +243,7 @@ static PyObject* norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     nr_call r;
     if (count_args("norm_rope", n, 9) || nr_args(a[0], a[1], a[2], a[3], a[4], a[5], &r)) return NULL;
     const int64_t* c = r.c;
-    void *qo, *ko;
+    Address qo, ko;
     spec_attn_stream_t st;
     if (rows_of(a[6], "q_out", r.n, c[kHq], c[kD], c[kQos], &r.dev, &qo, NULL) ||
         rows_of(a[7], "k_out", r.n, c[kHkv], c[kD], c[kKos], &r.dev, &ko, NULL) || stream_of(a[8], r.dev, &st))
@@ -269,8 +257,8 @@ static PyObject* norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* A pool of pages [pages, Hkv, page_size, row], pages `bytes` apart (0: dense). */
-static int pool_of(PyObject* t, const char* what, const int64_t* c, int64_t row, int64_t bytes, int size, PyObject* dtype,
-                   long* dev, void** out) {
+static int pool_of(PyObject* t, const char* what, const int64_t* c, int64_t row, int64_t bytes, int size, at::ScalarType dtype,
+                   long* dev, Address* out) {
     const int64_t dense = c[kHkv] * c[kPageSize] * row;
     const int64_t strides[4] = {bytes ? bytes / size : dense, c[kPageSize] * row, row, 1};
     want_t w = {what, dtype, 4, {c[kPages], c[kHkv], c[kPageSize], row}, strides};
@@ -286,8 +274,8 @@ static PyObject* norm_rope_append(PyObject* self, PyObject* const* a, Py_ssize_t
     const int64_t* c = r.c;
     const int fp4 = c[kKvDtype] == SPEC_ATTN_KV_NVFP4;
     const int64_t row = fp4 ? c[kD] / 2 : c[kD];
-    PyObject* kind = fp4 ? t_u8 : t_bf16;
-    void *v, *slot, *qo, *kp, *vp, *ks, *vs, *ws;
+    const at::ScalarType kind = fp4 ? t_u8 : t_bf16;
+    Address v, slot, qo, kp, vp, ks, vs, ws;
     int64_t bytes;
     spec_attn_stream_t st;
     want_t s = {"slot_map", t_i64, 1, {r.n}, NULL};
@@ -318,7 +306,7 @@ static PyObject* run_cross(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     if (count_args("run_cross", n, 11) || ints(a[0], 8, c)) return NULL;
     const int64_t P = c[1], rows = c[2], hq = c[3], hkv = c[4], d = c[5];
     long dev = -1;
-    void *q, *k, *v, *indptr, *start, *len, *o, *lse, *ws;
+    Address q, k, v, indptr, start, len, o, lse, ws;
     spec_attn_stream_t st;
     want_t wq = {"q", t_bf16, 3, {rows, hq, d}, NULL}, wo = {"o", t_bf16, 3, {rows, hq, d}, NULL};
     want_t wl = {"lse", t_f32, 2, {rows, hq}, NULL}, wi = {"q_indptr", t_i32, 1, {P + 1}, NULL};
@@ -336,30 +324,13 @@ static PyObject* run_cross(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return PyLong_FromLong(status);
 }
 
-/* setup(bfloat16, float32, int32, int64, uint8, current_device, current_raw_stream) */
-static PyObject* setup(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    (void)self;
-    PyObject** to[7] = {&t_bf16, &t_f32, &t_i32, &t_i64, &t_u8, &f_device, &f_stream};
-    if (count_args("setup", n, 7)) return NULL;
-    for (int i = 0; i < 7; ++i) {
-        Py_INCREF(a[i]);
-        Py_XSETREF(*to[i], a[i]);
-    }
-    Py_RETURN_NONE;
-}
-
-#define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
-static PyMethodDef methods[] = {FAST(setup), FAST(build_tables), FAST(norm_rope), FAST(norm_rope_append), FAST(run_cross),
+#define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, NULL}
+static PyMethodDef methods[] = {FAST(build_tables), FAST(norm_rope), FAST(norm_rope_append), FAST(run_cross),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "spec_attn_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit_spec_attn_calls(void) {
-    struct { PyObject** to; const char* name; } names[] = {
-        {&n_dtype, "dtype"}, {&n_shape, "shape"}, {&n_stride, "stride"}, {&n_get_device, "get_device"},
-        {&n_is_contiguous, "is_contiguous"}, {&n_data_ptr, "data_ptr"}, {&n_cuda_stream, "cuda_stream"}};
-    for (size_t i = 0; i < sizeof(names) / sizeof(names[0]); ++i) {
-        *names[i].to = PyUnicode_InternFromString(names[i].name);
-        if (!*names[i].to) return NULL;
-    }
+    n_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+    if (!n_cuda_stream) return NULL;
     return PyModule_Create(&module);
 }
