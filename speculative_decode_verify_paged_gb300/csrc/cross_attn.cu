@@ -10,21 +10,22 @@
 //
 // One CTA = (NQ query tiles of 128 rows) x (one KV head) x (a split of the
 // request's states).  A tile holds wt = 128 / G whole window rows with their G
-// heads, so K and V are read once for the G heads.  NQ = 2 (windows of more
-// than one tile, d <= 128): the two tiles share every K and V tile, one tile's
-// products running under the other tile's softmax.  Each tile's scores have two
-// buffers of 64 columns, so S_{t+1} is made while the softmax works on S_t and the
-// only chain from tile to tile is the softmax itself.  (One buffer of 128
+// heads, so K and V are read once for the G heads.  NQ = 2 (d = 128, launches of
+// many tiles): the two tiles share every K and V tile, one tile's products
+// running under the other tile's softmax.  Scores have two buffers of 64
+// columns a tile or more, so S_{t+1} is made while the softmax works on S_t and
+// the only chain from tile to tile is the softmax itself.  (One buffer of 128
 // columns runs the first product at its full rate, 64 instead of 96 clocks for
-// 128 states and 16 elements, but S_{t+1} then waits for softmax and P V of tile t:
-// 857 TFLOP/s at 4096 x 4096, 32/8 heads x 128.)
+// 128 states and 16 elements, but S_{t+1} then waits for softmax and P V of tile
+// t: 451 us where two of 64 take 376.  A row's scores in halves for two threads:
+// 443 us, the exchange of their maxima costs more than it saves.)
 //
 // Warp roles:
 //   warp 0      the query tiles, then K and V tiles in turn, by TMA into one ring
 //               of slots (64 rows each, 128-byte swizzled, chunk-major).
-//   warps 1, 2  issue the products, one thread each.  NQ = 2: warp 1 + i issues
-//               S_{t+1} and then P_t V_t of tile i.  NQ = 1: warp 1 issues S = Q K^T
-//               and warp 2 O += P V, so that a late K tile holds no P V back.
+//   warps 1, 2  issue the products, one elected thread each.  NQ = 2: warp 1 + i
+//               issues S_{t+1} and then P_t V_t of tile i.  NQ = 1: warp 1 issues
+//               S = Q K^T and warp 2 O += P V, so that a late K tile holds no P V back.
 //   warp 3      owns tensor memory.
 //   warps 4-7 (and 8-11 for the second tile)   softmax, a row a thread, and the
 //               epilogue.  In the last tile they also zero the V rows past the range's
@@ -42,6 +43,17 @@
 // after a cluster barrier every CTA combines a share of the rows, in split
 // order, from its peers' shared memory: no partial goes to global memory and no
 // second kernel follows.
+//
+// Bound.  Long prompts: the tensor cores, 1280 clocks for two tiles and 64 states
+// at d = 128 (S runs at three quarters of its rate at 64 columns, its operands
+// coming from shared memory) of 1350 measured: two requests of 4096 x 4096,
+// 32/8 heads x 128, 376 us (1460 TFLOP/s), 24/4 x 256 580 us (1420), 16/8 x 64
+// 162 us (850, the exponentials' share doubles).  Single tokens and windows of
+// large batches: HBM (64 tokens over 400 to 1601 states, 24/4 x 256: 48 us, 5.5
+// TB/s).  Few short windows: the chain of launch, first tile, some 0.45 us for
+// each further tile of a split (load, maximum, exponentials and store of 64 scores
+// by one thread), staging and combination: 8 windows of 9 rows over 1500 states
+// 12.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>

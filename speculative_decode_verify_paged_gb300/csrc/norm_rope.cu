@@ -34,15 +34,20 @@
 // warp's own.  Where a lane's two pieces are not 128-byte runs across lanes
 // (interleaved pairs, heads rotated in part), the results go back to the slot
 // and leave in the order of memory: 16-byte stores 32 bytes apart cost twice the
-// L2 requests.  The next row's positions and slot are asked for a row ahead.  (With the loads in registers, two or four
-// heads at a time, each warp waited out a memory round trip a batch: 16384 rows
-// x 40 heads x 128 took 58.7 us, 8192 x 32 x 256 into the cache 52.7 us.)
+// L2 requests.  The next row's positions and slot are asked for a row ahead.
+// (With the loads in registers, two or four heads at a time, each warp waited
+// out a memory round trip a batch: 16384 rows x 40 heads x 128 took 58.7 us,
+// now 55.5; 8192 x 32 x 256 into the cache 52.7, now 45.4.  Rings of 4, 8 or 16
+// iterations and three CTAs an SM were no faster.)
 // CTAs stay resident and step over the rows, so the frequencies are copied from
 // the kernel parameters to shared memory once per CTA, before the programmatic
 // wait.
 //
-// Bound: HBM (2 bytes read and 2 written an element) for long inputs; launch
-// and two dependent memory round trips for a window.
+// Bound: HBM (2 bytes read and 2 written an element) for long inputs, 6.0 and
+// 5.9 TB/s of algorithmic bytes in the two cases above (87 to 89 % of a copy);
+// launch and two dependent memory round trips for a window (3.0 us for one row
+// and for 72 into the cache); for an NVFP4 cache the quantiser's arithmetic
+// (4097 rows of 24/4 heads x 256: 26.4 us, bytes alone 18).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

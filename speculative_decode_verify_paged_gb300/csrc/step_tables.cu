@@ -19,12 +19,18 @@
 // Work split: each CTA makes the three sums itself (the lengths are a few KB
 // and come from L2) and then takes its share of rows, taken pages and returned
 // pages by a binary search in its shared-memory copy.  One kernel, no
-// grid-wide wait.  Where seq_lens or free_count overwrite an input, the CTA
-// that finishes last (a ticket in the workspace) writes them, after every CTA
-// has read.
+// grid-wide wait.  Rows are dealt from the first CTA on and pages from the last,
+// so that the two chains of dependent loads run in different CTAs (512
+// requests: 6.4 us with both in turn, 4.3 like this).  A thread takes one row:
+// four adjacent ones, with wider stores, are four searches in turn where
+// windows are short (8.8 us).  Where seq_lens or free_count overwrite an
+// input, the CTA that finishes last (a ticket in the workspace) writes them,
+// after every CTA has read.
 //
-// Bound: the chain of dependent memory round trips (lengths, table entry), not
-// bytes, up to some 100K rows.
+// Bound: the chain of dependent memory round trips (lengths, sums, table entry,
+// stack entry) behind the launch, not bytes: 8 requests with 72 rows 2.7 us, 512
+// requests with 512 to 4608 rows 3.4 to 4.3, 61 prompts with 262144 rows 5.1 (3.2 MB
+// written).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -34,8 +40,9 @@
 namespace spec_attn {
 namespace {
 
-constexpr int kTabThreads = 512;
+constexpr int kTabThreads = 1024;         // at most
 constexpr int kTabWarps = kTabThreads / 32;
+constexpr int kTabAdjacent = 8;
 
 struct Sums {
     long long w, n, t;   // window rows, new pages, returned pages
@@ -90,28 +97,41 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     __shared__ long long s_held[kTabWarps];
     __shared__ unsigned int s_bad[kTabWarps];
     __shared__ int s_last;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, warps = threads >> 5;
     pdl_wait_primary();
     pdl_launch_dependents();
 
-    // ---- the three sums: thread t takes requests [t * per, (t + 1) * per)
-    const int per = (P + kTabThreads - 1) / kTabThreads;
-    const int r0 = min(tid * per, P), r1 = min(r0 + per, P);
+    // ---- the three sums.  A thread takes `per` requests: adjacent ones, summed in its registers, or (many) every 32nd
+    // of its warp's, read side by side but scanned over the warp again for each (16384 requests: 28 us, 45 with
+    // adjacent ones; 512: 4.2 us adjacent, 4.9 side by side)
+    const int per = (P + threads - 1) / threads;
+    const bool adjacent = per <= kTabAdjacent;
+    const int r0 = adjacent ? tid * per : warp * 32 * per + lane, step = adjacent ? 1 : 32;
     const int F = *p.prev_free_count;
     unsigned int bad = 0;
+    auto counts = [&](int r, long long& held) -> Sums {
+        if (r >= P) return {0, 0, 0};
+        const TabReq q = tab_request(p, r, bad);
+        held += q.held;
+        return {q.w, max(0, q.need - q.held), max(0, q.held - q.need)};
+    };
+    auto scan = [&](const Sums& mine) {   // inclusive, over the warp
+        Sums inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Sums up = {__shfl_up_sync(kFullMask, inc.w, o), __shfl_up_sync(kFullMask, inc.n, o),
+                             __shfl_up_sync(kFullMask, inc.t, o)};
+            if (lane >= o) inc = add(inc, up);
+        }
+        return inc;
+    };
     Sums mine = {0, 0, 0};
     long long held = 0;
-    for (int r = r0; r < r1; ++r) {
-        const TabReq q = tab_request(p, r, bad);
-        mine = add(mine, {q.w, max(0, q.need - q.held), max(0, q.held - q.need)});
-        held += q.held;
-    }
-    Sums inc = mine;
+#pragma unroll 4
+    for (int k = 0; k < per; ++k) mine = add(mine, counts(r0 + step * k, held));
+    const Sums inc = scan(mine);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const Sums up = {__shfl_up_sync(kFullMask, inc.w, o), __shfl_up_sync(kFullMask, inc.n, o),
-                         __shfl_up_sync(kFullMask, inc.t, o)};
-        if (lane >= o) inc = add(inc, up);
         held += __shfl_xor_sync(kFullMask, held, o);
         bad |= __shfl_xor_sync(kFullMask, bad, o);
     }
@@ -124,7 +144,7 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     Sums base = {0, 0, 0}, total = {0, 0, 0};
     held = 0;
     bad = 0;
-    for (int k = 0; k < kTabWarps; ++k) {
+    for (int k = 0; k < warps; ++k) {
         if (k < warp) base = add(base, s_warp[k]);
         total = add(total, s_warp[k]);
         held += s_held[k];
@@ -138,13 +158,26 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     const int F2 = ok ? F + R - N : F;
     if (ok) {
         // (every sum fits 32 bits: rows <= max_rows, pages <= num_pages)
-        Sums at = add(base, {inc.w - mine.w, inc.n - mine.n, inc.t - mine.t});
-        for (int r = r0; r < r1; ++r) {
+        auto put = [&](int r, const Sums& at) {
+            if (r >= P) return;
             s_row[r] = (int)at.w;
             s_new[r] = (int)at.n;
             s_ret[r] = (int)at.t;
-            const TabReq q = tab_request(p, r, bad);
-            at = add(at, {q.w, max(0, q.need - q.held), max(0, q.held - q.need)});
+        };
+        if (adjacent) {
+            Sums at = add(base, {inc.w - mine.w, inc.n - mine.n, inc.t - mine.t});
+            for (int k = 0; k < per; ++k) {
+                put(r0 + k, at);
+                if (k + 1 < per) at = add(at, counts(r0 + k, held));
+            }
+        } else {
+            Sums at = base;
+            for (int k = 0; k < per; ++k) {
+                const Sums one = counts(r0 + 32 * k, held), all = scan(one);
+                put(r0 + 32 * k, add(at, {all.w - one.w, all.n - one.n, all.t - one.t}));
+                at = add(at, {__shfl_sync(kFullMask, all.w, 31), __shfl_sync(kFullMask, all.n, 31),
+                              __shfl_sync(kFullMask, all.t, 31)});
+            }
         }
         if (tid == 0) {
             s_row[P] = rows;
@@ -157,7 +190,9 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     __syncthreads();
 
     // (unsigned: an index may pass 2^31 on its last step)
-    const unsigned g0 = blockIdx.x * kTabThreads + tid, gn = gridDim.x * kTabThreads;
+    const unsigned g0 = blockIdx.x * threads + tid, gn = gridDim.x * threads;
+    // pages are dealt from the last CTA on: those there have no rows, and the two chains of loads run side by side
+    const unsigned p0 = (gridDim.x - 1 - blockIdx.x) * threads + tid;
     unsigned int sick = 0;
     auto entry = [&](int r, int j) -> int32_t* { return p.block_table + (size_t)r * p.bt_stride + j; };
     auto returned = [&](int i) {   // the i-th page given back
@@ -189,11 +224,11 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     }
     if (ok) {
         // ---- pages handed out, and what is left of the returned ones on the stack
-        for (unsigned k = g0; k < (unsigned)N; k += gn) {
+        for (unsigned k = p0; k < (unsigned)N; k += gn) {
             const int r = owner(s_new, P, (int)k);
             *entry(r, tab_request(p, r, sick).held + ((int)k - s_new[r])) = taken((int)k);
         }
-        for (unsigned i = g0; i < (unsigned)max(0, F2 - F); i += gn) {
+        for (unsigned i = p0; i < (unsigned)max(0, F2 - F); i += gn) {
             const int page = returned((int)i);
             if (page < 0 || page >= p.num_pages) sick |= kDevBadPage;
             p.free_pages[F + i] = page;
@@ -215,8 +250,8 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
         last = s_last != 0;
     }
     if (last) {
-        const unsigned first = p.in_place ? tid : g0, step = p.in_place ? kTabThreads : gn;
-        for (unsigned r = first; r < (unsigned)P; r += step)
+        const unsigned first = p.in_place ? tid : g0, stride = p.in_place ? threads : gn;
+        for (unsigned r = first; r < (unsigned)P; r += stride)
             p.seq_lens[r] = ok ? p.ctx_lens[r] + p.window_lens[r] : p.prev_seq_lens[r];
         if (first == 0) *p.free_count = F2;
     }
@@ -231,14 +266,15 @@ cudaError_t tables_launch(const TablesParams& p, cudaStream_t stream) {
                                                    static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    // a thread a row, at most two CTAs for each of the 152 SMs
-    const long long work = p.max_rows > p.num_reqs ? p.max_rows : (long long)p.num_reqs + 1;
-    long long ctas = (work + kTabThreads - 1) / kTabThreads;
-    if (ctas > 304) ctas = 304;
-    if (ctas < 1) ctas = 1;
+    // (each CTA sums all requests: more threads for many, less to synchronise for few)
+    const int threads = p.num_reqs <= 256 * kTabAdjacent ? 256 : kTabThreads;
+    // a thread a row and one for each page that the rows may take, as many as the 152 SMs hold
+    const long long pages = (p.max_rows >> p.page_shift) + (long long)p.num_reqs + 1;
+    const long long ctas = ((long long)p.max_rows + threads - 1) / threads + (pages + threads - 1) / threads;
+    const long long most = 152 * 1024 / threads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-    cfg.blockDim = dim3(kTabThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
