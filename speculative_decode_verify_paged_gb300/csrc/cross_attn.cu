@@ -31,8 +31,8 @@
 //               epilogue.  In the last tile they also zero the V rows past the range's
 //               end (what lies there may be anything, and 0 x NaN is NaN).
 //
-// TMEM columns: O tiles [0, NQ d), then two S buffers of 64 columns a tile, P
-// (bf16 pairs) in the first half of its S buffer.
+// TMEM columns: O tiles [0, NQ d), then two or four S buffers of 64 columns a
+// tile, P (bf16 pairs) in the first half of its S buffer.
 //
 // Every wait is bounded; on time-out the CTA sets the device-status bit, drains
 // its copies and products, frees its tensor memory and leaves.
@@ -40,12 +40,12 @@
 // Splits: where the tiles alone would leave SMs idle, each request's states are
 // cut into up to 8 ranges, whose CTAs form a cluster.  Each leaves its
 // normalised rows in fp32 with their log-sum-exp in its own shared memory, and
-// after a cluster barrier every CTA combines a share of the rows, in split
+// after a cluster barrier every CTA combines a share of the rows, in a fixed
 // order, from its peers' shared memory: no partial goes to global memory and no
 // second kernel follows.
 //
 // Bound.  Long prompts: the tensor cores, 1280 clocks for two tiles and 64 states
-// at d = 128 (S runs at three quarters of its rate at 64 columns, its operands
+// at d = 128 (S runs at two thirds of its rate at 64 columns, its operands
 // coming from shared memory) of 1350 measured: two requests of 4096 x 4096,
 // 32/8 heads x 128, 376 us (1460 TFLOP/s), 24/4 x 256 580 us (1420), 16/8 x 64
 // 162 us (850, the exponentials' share doubles).  Single tokens and windows of

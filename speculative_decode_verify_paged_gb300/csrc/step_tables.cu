@@ -21,7 +21,8 @@
 // pages by a binary search in its shared-memory copy.  One kernel, no
 // grid-wide wait.  Rows are dealt from the first CTA on and pages from the last,
 // so that the two chains of dependent loads run in different CTAs (512
-// requests: 6.4 us with both in turn, 4.3 like this).  A thread takes one row:
+// requests: 6.4 us with both in turn, 5.0 like this, 4.3 with 256 threads a CTA
+// instead of 512).  A thread takes one row:
 // four adjacent ones, with wider stores, are four searches in turn where
 // windows are short (8.8 us).  Where seq_lens or free_count overwrite an
 // input, the CTA that finishes last (a ticket in the workspace) writes them,
