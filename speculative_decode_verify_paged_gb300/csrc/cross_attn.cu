@@ -556,7 +556,8 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
         tc_fence_after();
         if (ok) {
             float* row = stage + (i * p.wt * G + m) * L::kRowFloats;   // (rows past the tile's wt * G are not written)
-            const float inv = 1.f / l_sum;
+            // (scores of minus infinity throughout: no weight, which the other splits' rows outweigh)
+            const float inv = nsplits > 1 && l_sum == 0.f ? 0.f : 1.f / l_sum;
             if (live) {
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
@@ -633,7 +634,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const float w = fast_exp2(ls[k] - mx);
+                    const float w = ls[k] == -INFINITY ? 0.f : fast_exp2(ls[k] - mx);
                     a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
                     a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);
                     sum += w;

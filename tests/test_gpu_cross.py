@@ -135,6 +135,34 @@ def test_growing_scores_move_the_reference(hq, hkv, d, rows):
     c.check()
 
 
+@pytest.mark.parametrize("splits", [1, 2, 4])
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 64, 9), (8, 2, 128, 40), (6, 2, 256, 5)])
+def test_infinite_scores(hq, hkv, d, rows, splits):
+    """States whose scores are minus infinity weigh nothing, whole splits of them included; where all are, the softmax
+    is 0 / 0 and the log-sum-exp minus infinity; one score of plus infinity makes its rows NaN."""
+    c = Case([rows, rows, rows], [300, 200, 130], hq, hkv, d, force_splits=splits, seed=30)
+    c.q.abs_().add_(0.5)
+    c.q[sum(c.rows):] = float("nan")
+    s0, s1, s2 = c.starts
+    c.k[s0:s0 + 170] = -math.inf
+    c.k[s1:s1 + 200] = -math.inf
+    c.k[s2 + 77] = math.inf
+    c.run()
+    lse = c.lse[rows:2 * rows]
+    assert bool((lse == -math.inf).all()) and bool(c.o[rows:2 * rows].isnan().all())
+    assert bool(c.o[2 * rows:3 * rows].isnan().all())
+    k, v = (t[s0 + 170:s0 + 300].double().cpu().repeat_interleave(hq // hkv, 1) for t in (c.k, c.v))
+    x = torch.einsum("whd,shd->hws", c.q[:rows].double().cpu(), k) * c.sm_scale
+    want = torch.einsum("hws,shd->whd", torch.softmax(x, -1), v)
+    A = torch.einsum("hws,shd->whd", torch.softmax(x, -1), v.abs())
+    e = (2.0 ** -20 * (8 + x.abs().amax(-1))).t()
+    E = 2.0 ** -18 * torch.einsum("whd,shd->hws", c.q[:rows].double().cpu(), k.abs()).amax(-1).t() * c.sm_scale
+    tol = 2.0 ** -8 * (1 + 2.0 ** -6) * (want.abs() + A) + 2 * (e + E)[..., None] * A
+    assert bool(((c.o[:rows].double().cpu() - want).abs() <= tol).all())
+    assert bool(((c.lse[:rows].double().cpu() - torch.logsumexp(x, -1).t()).abs() <= e + E).all())
+    assert sa.spec_attn_check_device_status(c.ws) == 0
+
+
 def test_shared_and_overlapping_ranges():
     c = Case([4, 4, 30], [300, 300, 200], 8, 2, 128, starts=[5, 5, 100], seed=3)
     c.run()
