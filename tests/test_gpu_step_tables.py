@@ -131,6 +131,20 @@ def test_tables_match_the_simulation(case, in_place):
         s.check(simulate(ctx, win, prev, free, table, ps, rows), free)
 
 
+@pytest.mark.parametrize("P", [255, 256, 257, 2047, 2048, 2049, 8192, 8193])
+def test_request_counts_at_the_edges_of_the_split(P):
+    """Around a thread's shares of the requests: one, several adjacent ones, or every 32nd."""
+    ps, rng = 16, random.Random(P)
+    ctx, win, prev = draw(rng, P, ps, 60, 5)
+    stride = -(-(max(c + w for c, w in zip(ctx, win)) + max(prev) + 1) // ps)
+    num_pages = P * stride
+    table, free = place(rng, prev, ps, stride, num_pages)
+    rows = sum(win) + 3
+    s = State(ctx, win, prev, free, table, num_pages, ps, rows, P % 2 == 0)
+    s.run()
+    s.check(simulate(ctx, win, prev, free, table, ps, rows), free)
+
+
 def test_returned_pages_serve_the_same_step():
     """An empty stack: the pages of requests that end go straight to one that joins."""
     ctx, win, prev = [0, 0, 5, 0], [0, 75, 1, 0], [48, 0, 16, 33]
