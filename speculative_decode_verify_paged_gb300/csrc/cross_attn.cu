@@ -48,13 +48,13 @@
 // at d = 128 (S runs at two thirds of its rate at 64 columns, its operands
 // coming from shared memory) of 1350 measured: two requests of 4096 x 4096,
 // 32/8 heads x 128, 376 us (1460 TFLOP/s), 24/4 x 256 580 us (1420), 16/8 x 64
-// 162 us (850, the exponentials' share doubles).  At d = 256 the copies: TMA brings
-// 42 bytes a clock into an SM, 1560 clocks for a tile's 64 KB (products 1280).  Single tokens and windows of
-// large batches: HBM (64 tokens over 400 to 1601 states, 24/4 x 256: 48 us, 5.5
-// TB/s).  Few short windows: the chain of launch, first tile, some 0.45 us for
-// each further tile of a split (load, maximum, exponentials and store of 64 scores
-// by one thread), staging and combination: 8 windows of 9 rows over 1500 states
-// 12.5 us.
+// 162 us (850, the exponentials' share doubles).  At d = 256 the copies: TMA
+// brings 42 bytes a clock into an SM, 1560 clocks for a tile's 64 KB (products
+// 1280).  Single tokens and windows of large batches: HBM (64 tokens over 400 to
+// 1601 states, 24/4 x 256: 48 us, 5.5 TB/s).  Few short windows: the chain of
+// launch, first tile, some 0.45 us for each further tile of a split (load, maximum,
+// exponentials and store of 64 scores by one thread), staging and combination:
+// 8 windows of 9 rows over 1500 states 12.6 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
