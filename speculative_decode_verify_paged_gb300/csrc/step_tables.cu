@@ -258,13 +258,19 @@ __global__ void __launch_bounds__(kTabThreads) tables_kernel(const TablesParams 
     }
 }
 
+// The three sums of each request, and their totals.
+constexpr size_t tab_smem_bytes(int reqs) { return 3 * (static_cast<size_t>(reqs) + 1) * sizeof(int32_t); }
+static_assert(tab_smem_bytes(SPEC_ATTN_TABLES_MAX_REQS) + 4096 <= 232448, "shared memory of a CTA, static part included");
+
 }  // namespace
 
 cudaError_t tables_launch(const TablesParams& p, cudaStream_t stream) {
-    const size_t smem = 3 * ((size_t)p.num_reqs + 1) * sizeof(int32_t);
+    const size_t smem = tab_smem_bytes(p.num_reqs);
     if (smem > 46 * 1024) {   // (2 KB are static)
+        // The limit belongs to the kernel, not to this launch: one constant for every size, so that no call lowers it
+        // under another thread's launch or under a node of a graph.
         const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+                                                   static_cast<int>(tab_smem_bytes(SPEC_ATTN_TABLES_MAX_REQS)));
         if (e != cudaSuccess) return e;
     }
     // (each CTA sums all requests: more threads for many, less to synchronise for few)

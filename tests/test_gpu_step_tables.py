@@ -1,7 +1,11 @@
 """The step tables built on the GPU against a plain simulation of the rules in
 Python (lists and loops): every output equal, whole buffers compared, so that
 what a call must leave alone is checked as well."""
+import ctypes
+import os
 import random
+import subprocess
+import threading
 
 import pytest
 import torch
@@ -260,3 +264,73 @@ def test_another_stream_and_the_largest_batch():
     s.run(stream=st)
     st.synchronize()
     s.check(simulate(ctx, win, prev, free, table, ps, rows), free)
+
+
+def _large(P, in_place=False):
+    """A step of P short requests, and its answer."""
+    rng = random.Random(P)
+    ctx, win, prev = draw(rng, P, 16, 60, 4)
+    table, free = place(rng, prev, 16, 12, P * 12)
+    rows = sum(win) + 3
+    return State(ctx, win, prev, free, table, P * 12, 16, rows, in_place), simulate(ctx, win, prev, free, table, 16, rows), free
+
+
+def test_two_threads_with_different_request_counts(tmp_path):
+    """Both above 3924 requests, where a launch asks for more shared memory than a kernel has by itself: neither call
+    takes it from the other's launch.  (Each on a stream of its own, with its own buffers and workspace; the calls are
+    made from C, where no interpreter lock keeps them apart.)"""
+    src, exe = tmp_path / "many.c", tmp_path / "many.so"
+    src.write_text("""
+        #include "spec_attn.h"
+        typedef int (*tables_fn)(const spec_attn_tables_problem*, const int32_t*, const int32_t*, const int32_t*,
+                                 const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int32_t*, int64_t*,
+                                 void*, size_t, spec_attn_stream_t);
+        int many(tables_fn f, int n, const spec_attn_tables_problem* p, void** a, spec_attn_stream_t s) {
+            int failed = 0;
+            for (int i = 0; i < n; ++i)
+                failed += f(p, a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7], a[8], a[9], a[10], a[11], 256, s) != 0;
+            return failed;
+        }
+    """)
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run(["gcc", "-shared", "-fPIC", "-O2", "-I", include, str(src), "-o", str(exe)], check=True)
+    many = ctypes.CDLL(str(exe)).many
+    many.argtypes = [ctypes.c_void_p, ctypes.c_int] + [ctypes.c_void_p] * 3
+    tables = ctypes.cast(sa.load_library().spec_attn_build_tables, ctypes.c_void_p)
+    steps = [_large(P) for P in (4000, 16384)]
+    for s, _, _ in steps:
+        s.run()                  # (the first call, with its loading of the kernel)
+    torch.cuda.synchronize()
+    streams, failed = [torch.cuda.Stream() for _ in steps], [None, None]
+
+    def loop(i):
+        torch.cuda.set_device(0)
+        s = steps[i][0]
+        prob = sa.spec_attn_tables_problem(s.ctx.numel(), s.pos.numel(), s.ps, s.free.numel(), s.table.shape[1], 1 << 20,
+                                           1 << 30)
+        at = (ctypes.c_void_p * 12)(*[t.data_ptr() for t in (s.ctx, s.win, s.prev, s.prev_count, s.free, s.table, s.seq,
+                                                             s.indptr, s.count, s.pos, s.slot, s.ws)])
+        failed[i] = many(tables, 3000, ctypes.addressof(prob), ctypes.addressof(at), streams[i].cuda_stream)
+    threads = [threading.Thread(target=loop, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert failed == [0, 0]
+    for s, want, free in steps:
+        s.check(want, free)
+
+
+def test_one_graph_with_two_request_counts():
+    """A call with fewer requests between the capture of a larger one and the graph's first replay."""
+    steps = [_large(P) for P in (16384, 4000)]
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        for s, _, _ in steps:
+            s.run(stream=stream)
+    graph.replay()
+    torch.cuda.synchronize()
+    for s, want, free in steps:
+        s.check(want, free)
