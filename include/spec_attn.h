@@ -587,7 +587,9 @@ int spec_attn_norm_rope_append(const spec_attn_norm_rope_plan* plan, int32_t num
  * kv_start[r] on, all of them:
  *   s_j = sm_scale * <q, k_j>,  O = sum_j softmax(s)_j v_j,  LSE natural log
  * with fp32 accumulation, O bf16, LSE fp32.  kv_len[r] = 0 gives O = 0 and
- * LSE = -infinity.  K and V are dense rows [total_kv_rows, Hkv, head_dim] bf16
+ * LSE = -infinity.  Scores of -infinity weigh nothing; a row of nothing else, or
+ * with a score of +infinity, has O = NaN and LSE = -infinity or +infinity; a NaN
+ * score makes both NaN.  K and V are dense rows [total_kv_rows, Hkv, head_dim] bf16
  * (not the paged cache: an encoder's states are written once and do not
  * grow), kv_row_stride elements apart, so that a fused projection's [rows, 2,
  * Hkv, head_dim] is taken as it is; packed states, a padded batch and states

@@ -502,7 +502,9 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 const bool need = mx > m_ref + kCrossRescale;
                 const float ref = need ? mx : m_ref;
                 const float alpha = need ? fast_exp2(m_ref - ref) : 1.f;   // (0 at the first tile)
-                const float nref = ref == -INFINITY ? 0.f : -ref;
+                // (an infinite reference is not subtracted: inf - inf would hide in the sum what the scores were.  Plus
+                // infinity makes the sum and with it the log-sum-exp infinite, and O, times 1 / inf, NaN.)
+                const float nref = fabsf(ref) == INFINITY ? 0.f : -ref;
                 const uint64_t nref2 = pack2(nref, nref);
                 uint32_t pk[BN / 2];
                 uint64_t ps[2] = {0, 0};   // two fp32 zeros each
@@ -635,7 +637,7 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    const float w = ls[k] == -INFINITY ? 0.f : fast_exp2(ls[k] - mx);
+                    const float w = ls[k] == -INFINITY ? 0.f : ls[k] == mx ? 1.f : fast_exp2(ls[k] - mx);   // (mx may be inf)
                     a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
                     a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);
                     sum += w;

@@ -163,6 +163,31 @@ def test_infinite_scores(hq, hkv, d, rows, splits):
     assert sa.spec_attn_check_device_status(c.ws) == 0
 
 
+@pytest.mark.parametrize("splits", [1, 2, 3, 8])
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 64, 9), (8, 2, 128, 40), (8, 2, 128, 400), (6, 2, 256, 5)])
+def test_log_sum_exp_of_infinite_scores(hq, hkv, d, rows, splits):
+    """ln sum exp as torch.logsumexp has it: one score of plus infinity, in the first tile or a later one, beside minus
+    infinities or not, gives plus infinity; a NaN score anywhere gives NaN.  O is NaN in all of them."""
+    c = Case([rows] * 5, [520] * 5, hq, hkv, d, force_splits=splits, seed=31)
+    c.q.abs_().add_(0.5)
+    c.q[sum(c.rows):] = float("nan")
+    first, late, both, nan_after, nan_alone = c.starts
+    c.k[first + 3] = math.inf
+    c.k[late + 400] = math.inf
+    c.k[both:both + 300] = -math.inf
+    c.k[both + 301] = math.inf
+    c.k[both + 519] = math.inf
+    c.k[nan_after + 60] = math.inf
+    c.k[nan_after + 450] = math.nan
+    c.k[nan_alone + 77] = math.nan
+    c.run()
+    torch.cuda.synchronize()
+    assert sa.spec_attn_check_device_status(c.ws) == 0
+    n = 3 * rows
+    assert bool((c.lse[:n] == math.inf).all()) and bool(c.lse[n:5 * rows].isnan().all())
+    assert bool(c.o[:5 * rows].isnan().all())
+
+
 def test_shared_and_overlapping_ranges():
     c = Case([4, 4, 30], [300, 300, 200], 8, 2, 128, starts=[5, 5, 100], seed=3)
     c.run()
