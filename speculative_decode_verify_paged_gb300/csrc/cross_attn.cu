@@ -630,13 +630,13 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                 }
                 float mx = ls[0], sum = 0.f;
 #pragma unroll
-                for (int k = 1; k < N; ++k) {
-                    if (k >= nsplits) ls[k] = -INFINITY;
-                    mx = fmaxf(mx, ls[k]);
-                }
+                for (int k = 1; k < N; ++k)
+                    if (k < nsplits) mx = fmaxf(mx, ls[k]);
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
+                    // (not past the splits there are: a weight of 0 does not take out a row that holds infinity)
+                    if (k >= nsplits) break;
                     const float w = ls[k] == -INFINITY ? 0.f : ls[k] == mx ? 1.f : fast_exp2(ls[k] - mx);   // (mx may be inf)
                     a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
                     a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);

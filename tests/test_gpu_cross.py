@@ -188,6 +188,29 @@ def test_log_sum_exp_of_infinite_scores(hq, hkv, d, rows, splits):
     assert bool(c.o[:5 * rows].isnan().all())
 
 
+@pytest.mark.parametrize("splits", [1, 2, 3, 5, 6, 7, 8])
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 64, 9), (8, 2, 128, 40), (6, 2, 256, 5)])
+def test_infinite_values(hq, hkv, d, rows, splits):
+    """An infinite element of one state makes that element of its rows infinite, by the formula, and leaves the others
+    as they are, whichever split the state falls to and whichever CTA combines the row."""
+    c = Case([rows, rows], [600, 600], hq, hkv, d, force_splits=splits, seed=32)
+    clean = c.v.clone()
+    c.run()
+    want = c.o.clone(), c.lse.clone()
+    for at in (5, 200, 333, 480, 599):
+        c.v.copy_(clean)
+        c.v[c.starts[0] + at, 1, 0::3] = math.inf
+        c.v[c.starts[0] + at, 1, 1::3] = -math.inf
+        c.o.fill_(MARK), c.lse.fill_(MARK)
+        c.run()
+        heads = slice(hq // 2, hq)
+        assert bool((c.o[:rows, heads, 0::3] == math.inf).all()), at
+        assert bool((c.o[:rows, heads, 1::3] == -math.inf).all()), at
+        c.o[:rows, heads, 0::3], c.o[:rows, heads, 1::3] = want[0][:rows, heads, 0::3], want[0][:rows, heads, 1::3]
+        assert torch.equal(c.o, want[0]) and torch.equal(c.lse, want[1]), at
+    assert sa.spec_attn_check_device_status(c.ws) == 0
+
+
 def test_shared_and_overlapping_ranges():
     c = Case([4, 4, 30], [300, 300, 200], 8, 2, 128, starts=[5, 5, 100], seed=3)
     c.run()
