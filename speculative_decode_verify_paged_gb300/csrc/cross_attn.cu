@@ -628,16 +628,19 @@ cross_attn_kernel(const CrossParams p, const __grid_constant__ CUtensorMap tmq, 
                     ls[k] = ld_peer(lse_at[k] + m * 4);
                     x[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 4) * 4);
                 }
+                // (N is the least of 2, 4 and 8 that holds the splits: those past the middle may not be there, and a
+                // weight of 0 would not take out a row that holds infinity)
+                auto here = [&](int k) { return k <= N / 2 || k < nsplits; };
                 float mx = ls[0], sum = 0.f;
 #pragma unroll
                 for (int k = 1; k < N; ++k)
-                    if (k < nsplits) mx = fmaxf(mx, ls[k]);
+                    if (here(k)) mx = fmaxf(mx, ls[k]);
+                const float ref = fabsf(mx) == INFINITY ? 0.f : mx;   // (as in the softmax)
                 float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int k = 0; k < N; ++k) {
-                    // (not past the splits there are: a weight of 0 does not take out a row that holds infinity)
-                    if (k >= nsplits) break;
-                    const float w = ls[k] == -INFINITY ? 0.f : ls[k] == mx ? 1.f : fast_exp2(ls[k] - mx);   // (mx may be inf)
+                    if (!here(k)) break;
+                    const float w = fast_exp2(ls[k] - ref);
                     a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
                     a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);
                     sum += w;
