@@ -553,9 +553,10 @@ int spec_attn_norm_rope_plan_destroy(spec_attn_norm_rope_plan* plan);
  * q [num_rows, Hq, d], k [num_rows, Hkv, d] -> q_out, k_out of the same shapes,
  * rows at the plan's strides, all 16-byte aligned.  q_weight, k_weight [d] fp32
  * or NULL (no norm of q, of k); positions [num_axes, num_rows] int32 (any
- * value).  q_out may be q, and k_out k, at equal strides; otherwise outputs
- * overlap no input.  Asynchronous on `stream`, allocation-free, graph
- * capturable.
+ * value).  q_out may be q, and k_out k, at equal strides; otherwise an output
+ * shares no byte with an input or another output (SPEC_ATTN_E_INVALID_ARG; rows
+ * that lie between each other, as views of one fused projection do, are
+ * apart).  Asynchronous on `stream`, allocation-free, graph capturable.
  */
 int spec_attn_norm_rope(const spec_attn_norm_rope_plan* plan, int32_t num_rows, const void* q, const void* k,
                         const float* q_weight, const float* k_weight, const int32_t* positions, void* q_out,
@@ -572,7 +573,10 @@ int spec_attn_norm_rope(const spec_attn_norm_rope_plan* plan, int32_t num_rows, 
  * for it.  A slot at or past num_pages * page_size sets
  * SPEC_ATTN_DEV_BAD_PAGE and skips the row.  Rows must have distinct slots.
  * Pools, scales and decode scales as spec_attn_append_kv; workspace: 256 bytes
- * holding the device-status word.
+ * holding the device-status word.  q_out may be q at equal strides; otherwise
+ * q_out, pools, scales and workspace share no byte with an input or with each
+ * other (SPEC_ATTN_E_INVALID_ARG; pages of K and V may alternate in one
+ * allocation).
  */
 int spec_attn_norm_rope_append(const spec_attn_norm_rope_plan* plan, int32_t num_rows, const void* q,
                                const void* k, const void* v, const float* q_weight, const float* k_weight,

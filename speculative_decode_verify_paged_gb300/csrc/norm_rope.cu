@@ -59,6 +59,7 @@
 #include "../../include/spec_attn.h"
 #include "common.cuh"
 #include "nvfp4_quant.cuh"
+#include "overlap.h"
 #include "sm100.cuh"
 
 namespace spec_attn {
@@ -570,6 +571,13 @@ int prepare_call(const spec_attn_norm_rope_plan* plan, int32_t num_rows, const v
     return SPEC_ATTN_OK;
 }
 
+// `n` rows of `heads` heads, `stride` elements apart.
+spec_attn::ByteRows rows_of(const void* p, int heads, int d, long long stride, int n) {
+    return {p, 2ull * heads * d, 2ull * stride, static_cast<uint64_t>(n)};
+}
+// An input that is also the output in its place is looked at as that output.
+const void* unless_in_place(const void* in, const void* out) { return in == out ? nullptr : in; }
+
 }  // namespace
 
 extern "C" {
@@ -666,6 +674,16 @@ int spec_attn_norm_rope(const spec_attn_norm_rope_plan* plan, int32_t num_rows, 
     if ((q_out == q && q && c.q_out_row_stride != c.q_row_stride) ||
         (k_out == k && k && c.k_out_row_stride != c.k_row_stride))
         return SPEC_ATTN_E_INVALID_ARG;
+    using spec_attn::bytes_at;
+    const uint64_t w4 = 4ull * p.head_dim;
+    const spec_attn::ByteRows out[] = {rows_of(q_out, p.num_q_heads, p.head_dim, c.q_out_row_stride, num_rows),
+                                       rows_of(k_out, p.num_kv_heads, p.head_dim, c.k_out_row_stride, num_rows)};
+    const spec_attn::ByteRows in[] = {
+        rows_of(unless_in_place(q, q_out), p.num_q_heads, p.head_dim, c.q_row_stride, num_rows),
+        rows_of(unless_in_place(k, k_out), p.num_kv_heads, p.head_dim, c.k_row_stride, num_rows),
+        bytes_at(q_weight, w4), bytes_at(k_weight, w4),
+        bytes_at(positions, p.rot_dim ? 4ull * p.num_axes * num_rows : 0)};
+    if (spec_attn::outputs_overlap(out, in)) return SPEC_ATTN_E_INVALID_ARG;
     c.k_out = static_cast<uint16_t*>(k_out);
     const cudaError_t e = spec_attn::norm_rope_launch(c, p.head_dim, false, 0, plan->num_sms,
                                                       reinterpret_cast<cudaStream_t>(stream));
@@ -694,6 +712,25 @@ int spec_attn_norm_rope_append(const spec_attn_norm_rope_plan* plan, int32_t num
             return SPEC_ATTN_E_INVALID_ARG;
     }
     if (workspace_bytes < 256) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
+    using spec_attn::bytes_at;
+    const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
+    const uint64_t w4 = 4ull * p.head_dim, slots = static_cast<uint64_t>(p.num_kv_heads) * p.page_size;
+    const uint64_t page = slots * (fp4 ? p.head_dim / 2 : 2 * p.head_dim), scales = fp4 ? slots * (p.head_dim / 16) : 0;
+    const uint64_t pages = static_cast<uint64_t>(p.num_pages);
+    const spec_attn::ByteRows out[] = {
+        rows_of(q_out, p.num_q_heads, p.head_dim, c.q_out_row_stride, num_rows),
+        {k_pool, page, static_cast<uint64_t>(c.kv_page_stride), pages},
+        {v_pool, page, static_cast<uint64_t>(c.kv_page_stride), pages},
+        {k_scales, scales, static_cast<uint64_t>(c.scale_page_stride), pages},
+        {v_scales, scales, static_cast<uint64_t>(c.scale_page_stride), pages},
+        bytes_at(workspace, 256)};
+    const spec_attn::ByteRows in[] = {
+        rows_of(unless_in_place(q, q_out), p.num_q_heads, p.head_dim, c.q_row_stride, num_rows),
+        rows_of(k, p.num_kv_heads, p.head_dim, c.k_row_stride, num_rows),
+        rows_of(v, p.num_kv_heads, p.head_dim, c.v_row_stride, num_rows),
+        bytes_at(q_weight, w4), bytes_at(k_weight, w4),
+        bytes_at(positions, p.rot_dim ? 4ull * p.num_axes * num_rows : 0), bytes_at(slot_map, 8ull * num_rows)};
+    if (spec_attn::outputs_overlap(out, in)) return SPEC_ATTN_E_INVALID_ARG;
     c.v = static_cast<const uint16_t*>(v);
     c.slot_map = reinterpret_cast<const long long*>(slot_map);
     c.k_pool = static_cast<unsigned char*>(k_pool);

@@ -413,3 +413,62 @@ def test_quantised_values_of_every_range(seed, gscale):
                            q_indptr=torch.arange(n // 16 + 1, dtype=torch.int32) * 16)
     for got, want in zip(pools, ref):
         assert np.array_equal(_bytes(got), want.view(np.uint8).reshape(-1))
+
+
+def test_overlapping_buffers_are_refused():
+    """An output that shares bytes with an input it is not in the place of, or with another output."""
+    n, hq, hkv, d, ps, pages = 6, 4, 4, 64, 16, 2
+    c = Case(n, hq, hkv, d, seed=16, page_size=ps, num_pages=pages)
+    c.run()
+    want = c.q_out.clone(), c.k_out.clone()
+    buf = torch.full((2 * n + 2, hq, d), 5.0, dtype=torch.bfloat16, device="cuda")
+
+    def norm_rope(**over):
+        a = {**dict(q=c.q, k=c.k, qw=c.qw, kw=c.kw, pos=c.pos, q_out=buf[:n], k_out=buf[n:2 * n]), **over}
+        sa.spec_attn_norm_rope(c.plan, *[a[x] for x in ("q", "k", "qw", "kw", "pos", "q_out", "k_out")])
+
+    as_pos = buf.view(torch.int32).flatten()[:n].view(1, n)
+    for over in (dict(q=buf[1:n + 1]), dict(k=buf[:n]), dict(k=buf[n + 1:2 * n + 1]), dict(k_out=buf[n - 1:2 * n - 1]),
+                 dict(q=buf[n:2 * n]), dict(qw=buf.view(torch.float32).flatten()[:d]), dict(pos=as_pos),
+                 dict(q=buf[:n], k_out=buf[:n])):
+        with pytest.raises(sa.SpecAttnError) as e:
+            norm_rope(**over)
+        assert e.value.status == sa.SPEC_ATTN_E_INVALID_ARG
+    pools = _cache(pages, hkv, ps, d, W.KV_BF16, False)
+    slot, ws = torch.arange(n, device="cuda"), torch.zeros(256, dtype=torch.uint8, device="cuda")
+
+    def append(**over):
+        a = {**dict(q=c.q, k=c.k, v=c.v, qw=c.qw, kw=c.kw, pos=c.pos, slot=slot, q_out=buf[:n], k_pool=pools[0],
+                    v_pool=pools[1], ws=ws), **over}
+        sa.spec_attn_norm_rope_append(c.plan, *a.values())
+
+    as_rows = pools[0].view(-1)[5 * d:5 * d + n * hkv * d].view(n, hkv, d)
+    for over in (dict(v_pool=pools[0]), dict(k=as_rows), dict(v=as_rows), dict(q_out=as_rows), dict(v=buf[:n]),
+                 dict(k=buf[1:n + 1]), dict(slot=buf.view(torch.int64).flatten()[:n]),
+                 dict(ws=buf.view(torch.uint8).flatten()[:256])):
+        with pytest.raises(sa.SpecAttnError) as e:
+            append(**over)
+        assert e.value.status == sa.SPEC_ATTN_E_INVALID_ARG
+    torch.cuda.synchronize()
+    assert bool((buf == 5.0).all()) and all(bool((p == 9).all()) for p in pools)
+    norm_rope()
+    assert torch.equal(buf[:n], want[0]) and torch.equal(buf[n:2 * n], want[1]) and bool((buf[2 * n:] == 5.0).all())
+
+
+def test_outputs_between_the_rows_of_their_inputs():
+    """Rows of one buffer that lie between each other at two strides are apart: outputs in the gaps of the inputs' rows,
+    and every second row of a wider stride."""
+    n, hq, hkv, d = 9, 2, 1, 64
+    a = Case(n, hq, hkv, d, seed=17)
+    a.run()
+    wide = torch.full((n, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    q, k, q_out = wide[:, :128].unflatten(1, (hq, d)), wide[:, 128:192].unflatten(1, (hkv, d)), wide[:, 256:384].unflatten(1, (hq, d))
+    long = torch.full((2 * n, 512), 3.0, dtype=torch.bfloat16, device="cuda")
+    k_out = long[::2, 64:128].unflatten(1, (hkv, d))
+    q.copy_(a.q), k.copy_(a.k)
+    plan = sa.spec_attn_norm_rope_plan_create(num_q_heads=hq, num_kv_heads=hkv, head_dim=d, inv_freq=a.freq, eps=1e-6,
+                                              q_row_stride=512, k_row_stride=512, q_out_row_stride=512,
+                                              k_out_row_stride=1024)
+    sa.spec_attn_norm_rope(plan, q, k, a.qw, a.kw, a.pos, q_out, k_out)
+    assert torch.equal(q_out, a.q_out) and torch.equal(k_out, a.k_out) and torch.equal(q, a.q) and torch.equal(k, a.k)
+    assert bool((wide[:, 384:] == 3.0).all()) and bool((long[1::2] == 3.0).all())
