@@ -630,8 +630,9 @@ int spec_attn_cross_plan_destroy(spec_attn_cross_plan* plan);
 /*
  * q [total_q_rows, Hq, d], o likewise, k and v at the plan's row stride, all
  * bf16 and 16-byte aligned; q_indptr [P+1], kv_start [P], kv_len [P] int32;
- * lse [total_q_rows, Hq] fp32 or NULL; outputs overlap no input.  workspace:
- * 256 bytes, 256-byte aligned, holding the device-status word (zeroed once).
+ * lse [total_q_rows, Hq] fp32 or NULL; workspace: 256 bytes, 256-byte aligned,
+ * holding the device-status word (zeroed once).  o, lse and workspace share no
+ * byte with an input or with each other (SPEC_ATTN_E_INVALID_ARG).
  * Asynchronous on `stream`, allocation-free, graph capturable.
  */
 int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const void* k, const void* v,

@@ -67,6 +67,7 @@
 
 #include "../../include/spec_attn.h"
 #include "common.cuh"
+#include "overlap.h"
 #include "sm100.cuh"
 #include "tc_common.cuh"
 
@@ -873,6 +874,13 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
     if (p.total_kv_rows > 0 && (!k || !v || !cross_aligned(k, 16) || !cross_aligned(v, 16)))
         return SPEC_ATTN_E_INVALID_ARG;
     if (workspace_bytes < 256) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
+    const uint64_t heads = static_cast<uint64_t>(p.total_q_rows) * p.num_q_heads, reqs4 = 4ull * p.num_reqs;
+    const uint64_t state = 2ull * p.num_kv_heads * p.head_dim, step = 2ull * p.kv_row_stride;
+    const uint64_t states = static_cast<uint64_t>(p.total_kv_rows);
+    const ByteRows out[] = {bytes_at(o, 2 * heads * p.head_dim), bytes_at(lse, 4 * heads), bytes_at(workspace, 256)};
+    const ByteRows in[] = {bytes_at(q, 2 * heads * p.head_dim), {k, state, step, states}, {v, state, step, states},
+                           bytes_at(q_indptr, reqs4 + 4), bytes_at(kv_start, reqs4), bytes_at(kv_len, reqs4)};
+    if (outputs_overlap(out, in)) return SPEC_ATTN_E_INVALID_ARG;
     int dev = -1;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return record_cuda_error(e);

@@ -364,3 +364,46 @@ def test_refused_calls_write_nothing():
     assert e.value.status == sa.SPEC_ATTN_E_WORKSPACE_TOO_SMALL
     torch.cuda.synchronize()
     assert bool((c.o == MARK).all())
+
+
+def test_overlapping_buffers_are_refused():
+    """An output that shares bytes with an input or another output; rows beside the states in one buffer are apart."""
+    hq, hkv, d, n, S = 4, 2, 64, 6, 100
+    c = Case([n], [S], hq, hkv, d, starts=[0], gap=0, pad_rows=0, seed=14)
+    c.run()
+    want = c.o.clone(), c.lse.clone()
+    buf = torch.full((S, 8, hkv, d), 5.0, dtype=torch.bfloat16, device="cuda")
+    kv = buf[:, 2:4]
+    k, v = kv[:, 0], kv[:, 1]
+    k.copy_(c.k), v.copy_(c.v)
+    before = buf.clone()
+    plan = sa.spec_attn_cross_plan_create(num_reqs=1, total_q_rows=n, max_q_rows=n, num_q_heads=hq, num_kv_heads=hkv,
+                                          head_dim=d, total_kv_rows=S, max_kv_len=S, kv_row_stride=8 * hkv * d)
+    names = ("q", "k", "v", "indptr", "kv_start", "kv_len", "o", "lse", "ws")
+
+    def run(**over):
+        a = {**{x: getattr(c, x) for x in names}, **dict(k=k, v=v), **over}
+        sa.spec_attn_run_cross(plan, *[a[x] for x in names])
+
+    flat = buf.view(-1)
+    rows = lambda at: flat[at:at + n * hq * d].view(n, hq, d)  # noqa: E731
+    both = torch.zeros(n * hq * d + 16, dtype=torch.bfloat16, device="cuda")
+    for over in (dict(o=rows(0)), dict(o=c.q), dict(q=both[8:8 + n * hq * d].view(n, hq, d), o=both[:-16].view(n, hq, d)),
+                 dict(lse=flat[:2 * n * hq].view(torch.float32).view(n, hq), o=rows(0)),
+                 dict(lse=c.q.view(torch.float32).flatten()[:n * hq].view(n, hq)),
+                 dict(ws=c.o.view(torch.uint8).flatten()[:256]), dict(kv_len=c.lse.view(torch.int32).flatten()[:1])):
+        with pytest.raises(sa.SpecAttnError) as e:
+            run(**over)
+        assert e.value.status == sa.SPEC_ATTN_E_INVALID_ARG
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before)
+    gap = flat[4 * hkv * d:8 * hkv * d]                  # 512 elements behind the first state: two query rows' worth
+    assert gap.numel() == 2 * hq * d
+    two = sa.spec_attn_cross_plan_create(num_reqs=1, total_q_rows=2, max_q_rows=n, num_q_heads=hq, num_kv_heads=hkv,
+                                         head_dim=d, total_kv_rows=S, max_kv_len=S, kv_row_stride=8 * hkv * d)
+    o, lse = gap.view(2, hq, d), torch.zeros(2, hq, device="cuda")
+    indptr = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    sa.spec_attn_run_cross(two, c.q[:2], k, v, indptr, c.kv_start, c.kv_len, o, lse, c.ws)
+    assert torch.equal(o, want[0][:2]) and torch.equal(lse, want[1][:2])
+    before[0, 4:8] = buf[0, 4:8]
+    assert torch.equal(buf, before)
