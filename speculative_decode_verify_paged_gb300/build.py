@@ -2,10 +2,11 @@
 
 Each CUDA translation unit under csrc/ is compiled in parallel into
 _build/*.o, then linked into _build/libspec_attn.so (CUDA runtime linked
-statically, so the library needs only the driver).  The native side of the
-Python binding, csrc/binding.cpp, becomes the extension module
-_build/spec_attn_calls.so, compiled with torch's headers and linked against that
-library.  No cmake.
+statically, so the library needs only the driver, and nvcc alone builds it).
+Where torch is installed, the native side of the Python binding,
+csrc/binding.cpp, then becomes the extension module _build/spec_attn_calls.so,
+compiled with torch's headers and linked against that library; it has a stamp
+of its own, and its failure leaves the library built.  No cmake.
 """
 from __future__ import annotations
 
@@ -44,8 +45,19 @@ def sources():
 
 def _deps():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  glob.glob(os.path.join(CSRC, "*.h")) + [BINDING] + glob.glob(os.path.join(INCLUDE, "*.h")) +
+                  glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
                   [os.path.abspath(__file__)])
+
+
+def _binding_deps():
+    return [BINDING] + sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [os.path.abspath(__file__)]
+
+
+def _same(stamp, text):
+    if not os.path.exists(stamp):
+        return False
+    with open(stamp) as f:
+        return f.read() == text
 
 
 def _stale(target, deps):
@@ -64,17 +76,21 @@ def _compile(src, extra):
     return obj, res.stderr
 
 
-def _torch_dir() -> str:
-    """Torch's folder, found without importing it."""
+def _torch():
+    """(folder, version) of torch, found without importing it; None where it is not installed."""
     spec = importlib.util.find_spec("torch")
-    if spec is None:
-        raise RuntimeError("the Python binding needs torch")
-    return list(spec.submodule_search_locations)[0]
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:      # (a source tree on the path)
+        version = "unknown"
+    return list(spec.submodule_search_locations)[0], version
 
 
-def _compile_binding():
+def _compile_binding(torch_dir):
     """The extension module's object: C++ against the headers of the running interpreter and torch."""
-    torch_include = os.path.join(_torch_dir(), "include")
+    torch_include = os.path.join(torch_dir, "include")
     obj = os.path.join(BUILD, "binding.o")
     cmd = [os.environ.get("CXX", "g++"), "-c", "-fPIC", "-O2", "-std=c++17", "-Wall", "-I", INCLUDE,
            "-I", sysconfig.get_paths()["include"], "-isystem", torch_include,
@@ -86,11 +102,11 @@ def _compile_binding():
     return obj
 
 
-def _link_binding(obj):
+def _link_binding(obj, torch_dir):
     """The module finds the library beside it, and torch's libraries where the importing process has loaded them."""
     tmp = CALLS + f".{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX", "g++"), "-shared", obj, "-o", tmp, LIB, "-Wl,-rpath,$ORIGIN",
-           "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+           "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"linking the binding failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
@@ -98,33 +114,45 @@ def _link_binding(obj):
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every CUDA source and link the shared library; return its path."""
+    """Compile every CUDA source and link the shared library, then the binding's module where torch is installed; return
+    the library's path."""
     os.makedirs(BUILD, exist_ok=True)
-    deps = _deps()
     srcs = sources()
     # the library is also stale when a source was added or removed since it was linked, the module with another torch
-    stamp = os.path.join(BUILD, "sources.txt")
-    listing = "\n".join([os.path.basename(s) for s in srcs] + ["torch " + importlib.metadata.version("torch")])
-    same_set = os.path.exists(stamp) and open(stamp).read() == listing
-    if not force and not extra_flags and same_set and not _stale(LIB, deps) and not _stale(CALLS, deps):
+    stamp, listing = os.path.join(BUILD, "sources.txt"), "\n".join(os.path.basename(s) for s in srcs)
+    lib_due = bool(force or extra_flags or not _same(stamp, listing) or _stale(LIB, _deps()))
+    torch = _torch()
+    calls_stamp, calls_made_with = os.path.join(BUILD, "calls.txt"), torch and "torch " + torch[1]
+    calls_due = torch is not None and bool(force or extra_flags or not _same(calls_stamp, calls_made_with) or
+                                           _stale(CALLS, _binding_deps()))
+    if not lib_due and not calls_due:
         return LIB
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 4))) as ex:
-        binding = ex.submit(_compile_binding)
-        results = list(ex.map(lambda s: _compile(s, extra_flags), srcs))
-    objs = [o for o, _ in results]
-    if verbose:
-        for _, log in results:
-            if log:
-                sys.stderr.write(log)
-    tmp = LIB + f".{os.getpid()}.tmp"
-    cmd = [nvcc()] + ARCH + ["-shared", "-cudart", "static", "-Xlinker", "-soname=libspec_attn.so", "-o", tmp] + objs
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB)
-    _link_binding(binding.result())
-    with open(stamp, "w") as f:
-        f.write(listing)
+        binding = ex.submit(_compile_binding, torch[0]) if calls_due else None
+        results = list(ex.map(lambda s: _compile(s, extra_flags), srcs)) if lib_due else []
+    if lib_due:
+        if verbose:
+            for _, log in results:
+                if log:
+                    sys.stderr.write(log)
+        tmp = LIB + f".{os.getpid()}.tmp"
+        cmd = ([nvcc()] + ARCH + ["-shared", "-cudart", "static", "-Xlinker", "-soname=libspec_attn.so", "-o", tmp] +
+               [o for o, _ in results])
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, LIB)
+        with open(stamp, "w") as f:
+            f.write(listing)
+    if calls_due:
+        try:
+            _link_binding(binding.result(), torch[0])
+        except Exception:
+            if os.path.exists(CALLS):      # (an older one, or another torch's, would be imported in its place)
+                os.remove(CALLS)
+            raise
+        with open(calls_stamp, "w") as f:
+            f.write(calls_made_with)
     return LIB
 
 
