@@ -47,8 +47,12 @@
 // Bound.  Long prompts: the tensor cores, 1280 clocks for two tiles and 64 states
 // at d = 128 (S runs at two thirds of its rate at 64 columns, its operands
 // coming from shared memory) of 1350 measured: two requests of 4096 x 4096,
-// 32/8 heads x 128, 376 us (1460 TFLOP/s), 24/4 x 256 580 us (1420), 16/8 x 64
-// 162 us (850, the exponentials' share doubles).  At d = 256 the copies: TMA
+// 32/8 heads x 128, 376 us (1460 TFLOP/s), 24/4 x 256 580 us (1420).  At d = 64
+// no unit is full (16/8 heads, the same rows: 162 us, 850 TFLOP/s; of a launch the
+// tensor pipe is busy 58 %, the issue slots 50, the exponentials' pipe 35): each
+// score takes half the products that it takes at d = 128, and with two query
+// tiles an SM the chain from scores over maximum, exponentials and P to the next
+// product shows.  At d = 256 the copies: TMA
 // brings 42 bytes a clock into an SM, 1560 clocks for a tile's 64 KB (products
 // 1280).  Single tokens and windows of large batches: HBM (64 tokens over 400 to
 // 1601 states, 24/4 x 256: 48 us, 5.5 TB/s).  Few short windows: the chain of

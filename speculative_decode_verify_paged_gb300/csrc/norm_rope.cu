@@ -46,8 +46,12 @@
 // Bound: HBM (2 bytes read and 2 written an element) for long inputs, 6.0 and
 // 5.9 TB/s of algorithmic bytes in the two cases above (87 to 89 % of a copy);
 // launch and two dependent memory round trips for a window (3.0 us for one row
-// and for 72 into the cache); for an NVFP4 cache the quantiser's arithmetic
-// (4097 rows of 24/4 heads x 256: 26.4 us, bytes alone 18).
+// and for 72 into the cache, 3.5 into an NVFP4 cache).  Into an NVFP4 cache 4097
+// rows of 24/4 heads x 256 take 26.3 us, bytes alone 18 (bf16: 24.0 and 20); no
+// unit is full: issue slots 59 % of the cycles that an SM is active, integer pipe
+// 35, FMA 32, shared memory 60, HBM 33 % of the launch.  The 16 warps of an SM
+// wait for their own last instruction, for shared memory and, twice as often as
+// with a bf16 cache, for instructions to arrive; SMs are active 83 % of the time.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
