@@ -42,11 +42,16 @@ static __device__ __noinline__ float quotient(float x, float y) { return __fdiv_
 // 0 : E2M1(x / den), every product and quotient in binary32 to nearest even.
 //
 // The 16 quotients share their divisor.  With r = 1 / den to nearest, q = x r
-// is within an ulp of x / den, its residual x - q den is exact in one fused
-// multiply-add, and q + r (x - q den) in another is the quotient rounded to
+// is close to x / den, its residual x - q den is exact in one fused multiply-add
+// or nearly so, and q + r (x - q den) in another is the quotient rounded to
 // nearest (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990) while nothing overflows or loses bits below
 // the normal range: three instructions for each element instead of a division.
+// The theorem asks for a q within an ulp, and here it is within 1.5; but only a
+// quotient within an ulp or two of a rounding border of E2M1 could change its
+// code, x has 8 significant bits, and for every such x and every divisor in
+// reach of a border the result is the division's (checked in rational
+// arithmetic, tests/test_nvfp4_quotients_host.py).
 // The theorem excludes a divisor whose significand is all ones.  Such a den, one
 // outside 2^-60 .. 2^60, and a block whose largest quotient passes 2^20 take the
 // division itself; elements below 2^-40 den are far from every rounding border.
