@@ -275,7 +275,8 @@ def _prepare_move(case, seed):
     if own:
         import speculative_decode_verify_paged_gb300 as sa
         s["plan"] = sa.spec_attn_norm_rope_plan_create(num_q_heads=0, num_kv_heads=hkv, head_dim=d, rot_dim=0, inv_freq=[],
-                                                       page_size=ps, num_pages=pages, kv_dtype=int(case["kv"] == "nvfp4"))
+                                                       page_size=ps, num_pages=pages, kv_dtype=int(case["kv"] == "nvfp4"),
+                                                       q_row_stride=s["q"].stride(0), q_out_row_stride=s["q"].stride(0))
         s["lists"] = [[p.get(name) for p in s["pools"]] for name in ("k_pool", "v_pool", "k_scales", "v_scales")]
     return s
 
