@@ -639,6 +639,173 @@ int spec_attn_run_cross(const spec_attn_cross_plan* plan, const void* q, const v
                         const int32_t* q_indptr, const int32_t* kv_start, const int32_t* kv_len, void* o,
                         float* lse, void* workspace, size_t workspace_bytes, spec_attn_stream_t stream);
 
+/*
+ * Attention of windows of any width over the paged cache under wider masks than
+ * spec_attn_run's: drafted trees, where each row sees its ancestors among the
+ * window's keys, and a sliding window whose first keys stay visible (sinks), for
+ * chains (one token, a verify window, a chunk of a prompt) and trees alike.  The
+ * pages of spec_attn_run restate one drafted chain a request; these are the same
+ * step with more of it kept.
+ *
+ * As for spec_attn_run, request r's W_r = q_indptr[r+1] - q_indptr[r] rows are its
+ * last W_r keys, already in the cache, and ctx_r = seq_len[r] - W_r.  Row i has
+ * position pos_i: ctx_r + i for a chain (tree = 0); for a tree (tree = 1) the
+ * greater of ctx_r and positions[row], read only with window_left > 0.  It sees
+ *   context keys j < ctx_r:   all; with window_left = n > 0 those with
+ *                             j > pos_i - n or j < sink_keys
+ *   the window's key ctx_r + j, chain:  j <= i (and in the window or a sink, as above)
+ *                               tree:   bit j of the row's mask, alone
+ * row_mask [total_q_rows, mask_row_words] int32: bit j of a row is bit j mod 32 of
+ * its word j / 32; bits from W_r on are ignored.  spec_attn_build_tree makes masks and
+ * positions from parent pointers.  A row that sees nothing has O = 0 and LSE =
+ * -infinity, like one whose scores are all -infinity.  A score of +infinity makes
+ * O = NaN and LSE = +infinity, a NaN score both NaN.
+ *
+ * With a window, the keys from sink_keys to max(0, ctx_r - n + 1) are seen by no
+ * row: pages that hold only such keys are not read and their table entries may be
+ * anything, so a streaming cache may free them.  K and V of keys that no row of the
+ * request sees by these bounds, and of slots past seq_len, may be anything; V of the
+ * keys within them has to be finite (a row's weight 0 does not take out an infinity
+ * or a NaN that other rows see), K may be anything where a row does not see it.
+ *
+ * Pools, scales, lengths, tables, layouts and device checks are as for
+ * spec_attn_run; a request that fails a check is skipped, its rows left as they were,
+ * like rows of no request.
+ */
+typedef struct spec_attn_masked_problem {
+    int32_t num_reqs;            /* P, 0 .. 65535 */
+    int32_t total_q_rows;        /* rows of Q and O, at most 2^30 */
+    int32_t max_w;               /* upper bound on a request's rows, >= 1 */
+    int32_t num_q_heads;         /* Hq */
+    int32_t num_kv_heads;        /* Hkv, at most 65535; Hq % Hkv == 0, Hq / Hkv <= 16 */
+    int32_t head_dim;            /* 64, 128 or 256 */
+    int32_t page_size;           /* 16, 32 or 64 */
+    int32_t num_pages;           /* pages in each pool; >= 1 when num_reqs > 0 */
+    int32_t block_table_stride;  /* entries per block-table row, stride x page_size <= 2^31 - 1 */
+    int32_t kv_dtype;            /* spec_attn_kv_dtype */
+    float sm_scale;              /* 0 selects 1/sqrt(head_dim) */
+    int32_t tree;                /* 1: the window's keys by row_mask; 0: a chain */
+    int32_t window_left;         /* sliding window in keys, the row's own among them; 0: none */
+    int32_t sink_keys;           /* first keys that stay visible behind the window, >= 0 */
+    int32_t mask_row_words;      /* words from a row of row_mask to the next; 0: ceil(max_w / 32) */
+    int32_t force_splits;        /* 0: the library's choice; n > 0: cut the longest span n ways */
+    int64_t max_seq_len;         /* upper bound on every seq_len, at most 2^31 - 1 */
+    int64_t kv_page_stride;      /* page strides in bytes, as spec_attn_problem */
+    int64_t scale_page_stride;
+} spec_attn_masked_problem;
+
+typedef struct spec_attn_masked_plan spec_attn_masked_plan;   /* opaque */
+
+/* Host only; the current device is the one the plan targets.
+ * *workspace_bytes (nullable) receives what spec_attn_run_masked needs. */
+int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_attn_masked_plan** out,
+                                 size_t* workspace_bytes);
+int spec_attn_masked_plan_destroy(spec_attn_masked_plan* plan);
+
+/*
+ * Arguments as spec_attn_run; row_mask for trees only (NULL for chains), positions
+ * [total_q_rows] int32 for trees with a window only (NULL otherwise).  lse may be
+ * NULL.  o, lse and workspace share no byte with an input or with each other
+ * (SPEC_ATTN_E_INVALID_ARG).  Asynchronous on `stream`, allocation-free, graph
+ * capturable.
+ */
+int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const void* k_pool, const void* v_pool,
+                         const void* k_scales, const void* v_scales, float k_gscale, float v_gscale,
+                         const int32_t* block_table, const int32_t* seq_lens, const int32_t* q_indptr,
+                         const int32_t* row_mask, const int32_t* positions, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, spec_attn_stream_t stream);
+
+/*
+ * Drafted trees.  A request's window is a tree of W_r nodes in an order that puts
+ * parents before children: parents[row] is the parent's place in the window, or -1
+ * for a root.  Node 0 is the seed token, the last one already accepted.  A parent
+ * below -1 or not before its child sets SPEC_ATTN_DEV_BAD_TREE and counts as -1.
+ *
+ * spec_attn_build_tree writes, for the rows of every request,
+ *   positions[row] = ctx_r + depth (a root's depth is 0), and
+ *   row_mask[row]: the node and its ancestors -- with window_left = n > 0 only those
+ *   fewer than n levels above the node, or at a position below sink_keys --
+ * in mask_row_words words a row (0: ceil(max_w / 32)), unused bits 0.  Rows of no
+ * request get position 0 and an empty mask.  ctx_r = seq_lens[r] - W_r.
+ *
+ * spec_attn_accept_tree walks each tree from node 0: the next node is the lowest
+ * child whose draft token is the target token of its parent (the token that the
+ * model takes after that node).
+ *   path [P, path_stride]: the nodes, node 0 first, -1 behind the last
+ *   accept_lens[r]: their number, at most path_stride (0 for a request without rows)
+ *   next_tokens[r]: the target token of the last (-1 without rows)
+ *   ctx_lens[r] = ctx_r + accept_lens[r], the ctx_lens of the next step's
+ *                 spec_attn_build_tables (whose prev_seq_lens are these seq_lens)
+ * ctx_lens may be seq_lens.  draft_tokens [total_rows], target_tokens [total_rows] and
+ * next_tokens [P] int64.
+ *
+ * A window below 0, above max_w or past total_rows sets SPEC_ATTN_DEV_BAD_WINDOW, a
+ * seq_len below its window SPEC_ATTN_DEV_BAD_SEQ_LEN; such a request's rows are left
+ * as they were, its path is empty, accept_lens 0, next_tokens -1 and ctx_lens its
+ * seq_len.  Outputs share no byte with an input (ctx_lens apart) or with each other
+ * (SPEC_ATTN_E_INVALID_ARG).  workspace: 256 bytes holding the device-status word.  Asynchronous on
+ * `stream`, one kernel, allocation-free, graph capturable.
+ */
+#define SPEC_ATTN_TREE_MAX_W 1024
+#define SPEC_ATTN_DEV_BAD_TREE      0x40u /* a parent that is no earlier node; a path that does not ascend */
+typedef struct spec_attn_tree_problem {
+    int32_t num_reqs;            /* P, 0 .. 65535 */
+    int32_t total_rows;          /* entries of parents (a padded batch may have more than q_indptr[P]) */
+    int32_t max_w;               /* upper bound on a tree's nodes, 1 .. SPEC_ATTN_TREE_MAX_W */
+    int32_t mask_row_words;      /* spec_attn_build_tree: at least ceil(max_w / 32), or 0 */
+    int32_t window_left;         /* spec_attn_build_tree, >= 0 */
+    int32_t sink_keys;           /* spec_attn_build_tree, >= 0 */
+    int32_t path_stride;         /* spec_attn_accept_tree: entries of a row of path, >= 1 */
+    int32_t reserved;            /* 0 */
+} spec_attn_tree_problem;
+
+int spec_attn_build_tree(const spec_attn_tree_problem* problem, const int32_t* parents, const int32_t* seq_lens,
+                         const int32_t* q_indptr, int32_t* positions, int32_t* row_mask, void* workspace,
+                         size_t workspace_bytes, spec_attn_stream_t stream);
+int spec_attn_accept_tree(const spec_attn_tree_problem* problem, const int32_t* parents, const int64_t* draft_tokens,
+                          const int64_t* target_tokens, const int32_t* seq_lens, const int32_t* q_indptr, int32_t* path,
+                          int32_t* accept_lens, int64_t* next_tokens, int32_t* ctx_lens, void* workspace,
+                          size_t workspace_bytes, spec_attn_stream_t stream);
+
+/*
+ * Move the accepted nodes' keys and values together, in the caches of several
+ * layers at once: for i < accept_lens[r], key ctx_r + path[r][i] of request r goes to
+ * key ctx_r + i, for every KV head (NVFP4 caches: codes and scales, byte for byte).
+ * Afterwards the request's first ctx_r + accept_lens[r] keys are its accepted text; a
+ * chain needs no such call.  Nothing else is written.
+ *
+ * h_k_pools, h_v_pools, h_k_scales, h_v_scales: host arrays of num_layers device
+ * pointers, read before the call returns (the scales' NULL for bf16).  All layers
+ * have the same shapes, strides and block table; no pool shares a byte with another
+ * (not checked between layers) or with the index arrays.
+ *
+ * Device checks: those of spec_attn_append_kv; a path of request r that does not
+ * ascend from 0 or more within the window, or an accept_lens[r] below 0 or above
+ * path_stride or W_r, sets SPEC_ATTN_DEV_BAD_TREE.  Such a request is skipped whole; a
+ * bad page skips its keys' moves.
+ */
+typedef struct spec_attn_move_problem {
+    int32_t num_reqs;            /* P, 0 .. 65535 */
+    int32_t num_layers;          /* >= 0 */
+    int32_t num_kv_heads;        /* Hkv, 1 .. 65535 */
+    int32_t head_dim;            /* 64, 128 or 256 */
+    int32_t page_size;           /* 16, 32 or 64 */
+    int32_t num_pages;           /* pages of each pool */
+    int32_t block_table_stride;
+    int32_t kv_dtype;            /* spec_attn_kv_dtype */
+    int32_t path_stride;         /* entries of a row of path, >= 1 */
+    int32_t reserved;            /* 0 */
+    int64_t max_seq_len;         /* at most 2^31 - 1 */
+    int64_t kv_page_stride;      /* page strides in bytes, as spec_attn_problem */
+    int64_t scale_page_stride;
+} spec_attn_move_problem;
+
+int spec_attn_move_kv(const spec_attn_move_problem* problem, void* const* h_k_pools, void* const* h_v_pools,
+                      void* const* h_k_scales, void* const* h_v_scales, const int32_t* block_table,
+                      const int32_t* seq_lens, const int32_t* q_indptr, const int32_t* path,
+                      const int32_t* accept_lens, void* workspace, size_t workspace_bytes,
+                      spec_attn_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

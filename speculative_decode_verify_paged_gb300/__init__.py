@@ -47,6 +47,8 @@ SPEC_ATTN_DEV_BAD_WINDOW = 0x4
 SPEC_ATTN_DEV_WAIT_TIMEOUT = 0x8
 SPEC_ATTN_DEV_OUT_OF_PAGES = 0x10
 SPEC_ATTN_DEV_BAD_FREE_LIST = 0x20
+SPEC_ATTN_DEV_BAD_TREE = 0x40
+SPEC_ATTN_TREE_MAX_W = 1024
 
 # every symbol include/spec_attn.h declares
 EXPORTED_SYMBOLS = (
@@ -58,7 +60,8 @@ EXPORTED_SYMBOLS = (
     "spec_attn_run_append", "spec_attn_run_dense_block", "spec_attn_build_tables",
     "spec_attn_norm_rope_plan_create", "spec_attn_norm_rope_plan_destroy", "spec_attn_norm_rope",
     "spec_attn_norm_rope_append", "spec_attn_cross_plan_create", "spec_attn_cross_plan_destroy",
-    "spec_attn_run_cross",
+    "spec_attn_run_cross", "spec_attn_masked_plan_create", "spec_attn_masked_plan_destroy", "spec_attn_run_masked",
+    "spec_attn_build_tree", "spec_attn_accept_tree", "spec_attn_move_kv",
 )
 
 
@@ -121,6 +124,36 @@ class spec_attn_cross_problem(ctypes.Structure):
         ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
         ("total_kv_rows", ctypes.c_int32), ("max_kv_len", ctypes.c_int32), ("sm_scale", ctypes.c_float),
         ("force_splits", ctypes.c_int32), ("kv_row_stride", ctypes.c_int64),
+    ]
+
+
+class spec_attn_masked_problem(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("total_q_rows", ctypes.c_int32), ("max_w", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32), ("block_table_stride", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32), ("sm_scale", ctypes.c_float), ("tree", ctypes.c_int32),
+        ("window_left", ctypes.c_int32), ("sink_keys", ctypes.c_int32), ("mask_row_words", ctypes.c_int32),
+        ("force_splits", ctypes.c_int32), ("max_seq_len", ctypes.c_int64), ("kv_page_stride", ctypes.c_int64),
+        ("scale_page_stride", ctypes.c_int64),
+    ]
+
+
+class spec_attn_tree_problem(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("total_rows", ctypes.c_int32), ("max_w", ctypes.c_int32),
+        ("mask_row_words", ctypes.c_int32), ("window_left", ctypes.c_int32), ("sink_keys", ctypes.c_int32),
+        ("path_stride", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class spec_attn_move_problem(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32), ("num_layers", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+        ("block_table_stride", ctypes.c_int32), ("kv_dtype", ctypes.c_int32), ("path_stride", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("max_seq_len", ctypes.c_int64), ("kv_page_stride", ctypes.c_int64),
+        ("scale_page_stride", ctypes.c_int64),
     ]
 
 
@@ -194,6 +227,19 @@ def load_library(path: Optional[str] = None):
         lib.spec_attn_cross_plan_destroy.argtypes = [vp]
         lib.spec_attn_run_cross.restype = i32
         lib.spec_attn_run_cross.argtypes = [vp] * 10 + [sz, vp]
+        lib.spec_attn_masked_plan_create.restype = i32
+        lib.spec_attn_masked_plan_create.argtypes = [ctypes.POINTER(spec_attn_masked_problem), ctypes.POINTER(vp),
+                                                     ctypes.POINTER(sz)]
+        lib.spec_attn_masked_plan_destroy.restype = i32
+        lib.spec_attn_masked_plan_destroy.argtypes = [vp]
+        lib.spec_attn_run_masked.restype = i32
+        lib.spec_attn_run_masked.argtypes = [vp] * 6 + [ctypes.c_float, ctypes.c_float] + [vp] * 8 + [sz, vp]
+        lib.spec_attn_build_tree.restype = i32
+        lib.spec_attn_build_tree.argtypes = [ctypes.POINTER(spec_attn_tree_problem)] + [vp] * 6 + [sz, vp]
+        lib.spec_attn_accept_tree.restype = i32
+        lib.spec_attn_accept_tree.argtypes = [ctypes.POINTER(spec_attn_tree_problem)] + [vp] * 10 + [sz, vp]
+        lib.spec_attn_move_kv.restype = i32
+        lib.spec_attn_move_kv.argtypes = [ctypes.POINTER(spec_attn_move_problem)] + [vp] * 10 + [sz, vp]
         if path is None:
             _lib = lib
         return lib
@@ -599,6 +645,82 @@ def spec_attn_run_cross(plan: CrossPlan, q, k, v, q_indptr, kv_start, kv_len, o,
     (asynchronous).  ``lse`` may be None."""
     _check((_calls or _native()).run_cross(plan.spec, q, k, v, q_indptr, kv_start, kv_len, o, lse, workspace, stream),
            "spec_attn_run_cross")
+
+
+# --------------------------------------------------------------------------- #
+# Drafted trees, and windows with sinks
+# --------------------------------------------------------------------------- #
+class MaskedPlan:
+    """Owns a spec_attn_masked_plan* (destroyed with this object)."""
+
+    def __init__(self, handle, workspace_bytes, problem):
+        self._lib = load_library()
+        self.handle = handle
+        self.workspace_bytes = int(workspace_bytes)
+        self.problem = problem
+        p = problem
+        # (in the order the native call reads them)
+        self.spec = (handle.value, p.num_reqs, p.total_q_rows, p.num_q_heads, p.num_kv_heads, p.head_dim, p.num_pages,
+                     p.page_size, p.block_table_stride, p.kv_dtype, p.kv_page_stride, p.scale_page_stride, p.tree,
+                     p.mask_row_words or -(-p.max_w // 32))
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h is not None:
+            try:
+                self._lib.spec_attn_masked_plan_destroy(h)
+            except Exception:
+                pass
+
+
+def spec_attn_masked_plan_create(*, num_reqs, total_q_rows, max_w, num_q_heads, num_kv_heads, head_dim, num_pages,
+                                 block_table_stride, max_seq_len, kv_dtype=0, page_size=16, sm_scale=0.0, tree=0,
+                                 window_left=0, sink_keys=0, mask_row_words=0, force_splits=0, kv_page_stride=0,
+                                 scale_page_stride=0) -> MaskedPlan:
+    prob = spec_attn_masked_problem(num_reqs, total_q_rows, max_w, num_q_heads, num_kv_heads, head_dim, page_size,
+                                    num_pages, block_table_stride, kv_dtype, float(sm_scale), int(tree), window_left,
+                                    sink_keys, mask_row_words, force_splits, int(max_seq_len), int(kv_page_stride),
+                                    int(scale_page_stride))
+    handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
+    _check(load_library().spec_attn_masked_plan_create(ctypes.byref(prob), ctypes.byref(handle), ctypes.byref(ws)),
+           "spec_attn_masked_plan_create")
+    return MaskedPlan(handle, ws.value, prob)
+
+
+def spec_attn_run_masked(plan: MaskedPlan, q, k_pool, v_pool, block_table, seq_lens, q_indptr, row_mask, positions, o,
+                         lse, workspace, k_scales=None, v_scales=None, k_gscale=1.0, v_gscale=1.0, stream=None):
+    """Attention over the paged cache under tree masks, or under a sliding
+    window with sinks (asynchronous).  ``row_mask`` [rows, words] int32 for
+    trees, ``positions`` [rows] int32 for trees with a window; else None."""
+    _check((_calls or _native()).run_masked(plan.spec, q, k_pool, v_pool, k_scales, v_scales, k_gscale, v_gscale,
+                                            block_table, seq_lens, q_indptr, row_mask, positions, o, lse, workspace,
+                                            stream), "spec_attn_run_masked")
+
+
+def spec_attn_build_tree(parents, seq_lens, q_indptr, positions, row_mask, workspace, *, max_w, window_left=0,
+                         sink_keys=0, stream=None):
+    """Positions [rows] and ancestor masks [rows, words] int32 of every
+    request's tree from its nodes' parents (asynchronous)."""
+    _check((_calls or _native()).build_tree((max_w, window_left, sink_keys), parents, seq_lens, q_indptr, positions,
+                                            row_mask, workspace, stream), "spec_attn_build_tree")
+
+
+def spec_attn_accept_tree(parents, draft_tokens, target_tokens, seq_lens, q_indptr, path, accept_lens, next_tokens,
+                          ctx_lens, workspace, *, max_w, stream=None):
+    """The accepted path of every request's tree (asynchronous).  Tokens int64;
+    ctx_lens may be seq_lens."""
+    _check((_calls or _native()).accept_tree((max_w,), parents, draft_tokens, target_tokens, seq_lens, q_indptr, path,
+                                             accept_lens, next_tokens, ctx_lens, workspace, stream),
+           "spec_attn_accept_tree")
+
+
+def spec_attn_move_kv(k_pools, v_pools, block_table, seq_lens, q_indptr, path, accept_lens, workspace, *, max_seq_len,
+                      k_scales=None, v_scales=None, stream=None):
+    """Move the accepted nodes' keys and values into place in every layer's
+    cache (asynchronous).  Pools and scales: lists of one tensor [pages, Hkv,
+    page_size, row] a layer; layers share shapes and strides."""
+    _check((_calls or _native()).move_kv((max_seq_len,), k_pools, v_pools, k_scales, v_scales, block_table, seq_lens,
+                                         q_indptr, path, accept_lens, workspace, stream), "spec_attn_move_kv")
 
 
 # --------------------------------------------------------------------------- #

@@ -1,6 +1,6 @@
 /*
  * Native side of the Python binding for the calls around the attention (step
- * tables, norm and rotation, cross attention): checks the tensors and makes
+ * tables, norm and rotation, cross attention, trees): checks the tensors and makes
  * the C ABI call in one step.  A decode step makes these calls once a layer on
  * kernels of a few microseconds, and the same checks cost more than the launch
  * when written in Python (12 tensors: 7.8 of 10.5 us) or through the tensors'
@@ -19,6 +19,7 @@
 
 #include <cstdint>
 #include <exception>
+#include <vector>
 
 #include "spec_attn.h"
 
@@ -324,8 +325,213 @@ static PyObject* run_cross(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     return PyLong_FromLong(status);
 }
 
+/* What a masked plan tells: handle, P, query rows, Hq, Hkv, d, pages, page size, table stride, KV dtype, page strides in
+ * bytes (0: dense), whether the windows are trees, words of a mask row. */
+enum { mHandle, mP, mRows, mHq, mHkv, mD, mPages, mPageSize, mTable, mKvDtype, mKvStride, mScStride, mTree, mWords, mN };
+
+/* Pools and scales, with the layout pool_of reads. */
+static int caches_of(PyObject* const* a, const int64_t* m, long* dev, Address* kp, Address* vp, Address* ks, Address* vs) {
+    int64_t c[kNr] = {};
+    c[kHkv] = m[mHkv];
+    c[kPageSize] = m[mPageSize];
+    c[kPages] = m[mPages];
+    const int fp4 = m[mKvDtype] == SPEC_ATTN_KV_NVFP4;
+    const int64_t row = fp4 ? m[mD] / 2 : m[mD];
+    const at::ScalarType kind = fp4 ? t_u8 : t_bf16;
+    return pool_of(a[0], "k_pool", c, row, m[mKvStride], fp4 ? 1 : 2, kind, dev, kp) ||
+           pool_of(a[1], "v_pool", c, row, m[mKvStride], fp4 ? 1 : 2, kind, dev, vp) ||
+           pool_of(a[2], "k_scales", c, m[mD] / 16, m[mScStride], 1, t_u8, dev, ks) ||
+           pool_of(a[3], "v_scales", c, m[mD] / 16, m[mScStride], 1, t_u8, dev, vs);
+}
+
+/* run_masked(plan, q, k_pool, v_pool, k_scales, v_scales, k_gscale, v_gscale, block_table, seq_lens, q_indptr, row_mask,
+ * positions, o, lse, workspace, stream) */
+static PyObject* run_masked(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    int64_t m[mN], bytes;
+    if (count_args("run_masked", n, 17) || ints(a[0], mN, m)) return NULL;
+    long dev = -1;
+    Address q, kp, vp, ks, vs, table, seq, indptr, mask, pos, o, lse, ws;
+    spec_attn_stream_t st;
+    want_t wq = {"q", t_bf16, 3, {m[mRows], m[mHq], m[mD]}, NULL}, wo = {"o", t_bf16, 3, {m[mRows], m[mHq], m[mD]}, NULL};
+    want_t wl = {"lse", t_f32, 2, {m[mRows], m[mHq]}, NULL}, wt = {"block_table", t_i32, 2, {m[mP], m[mTable]}, NULL};
+    want_t wn = {"seq_lens", t_i32, 1, {m[mP]}, NULL}, wi = {"q_indptr", t_i32, 1, {m[mP] + 1}, NULL};
+    want_t wm = {"row_mask", t_i32, 2, {m[mRows], m[mWords]}, NULL}, wp = {"positions", t_i32, 1, {m[mRows]}, NULL};
+    if (address(a[1], &wq, &dev, &q) || caches_of(a + 2, m, &dev, &kp, &vp, &ks, &vs)) return NULL;
+    const double kg = PyFloat_AsDouble(a[6]), vg = PyFloat_AsDouble(a[7]);
+    if (PyErr_Occurred()) return NULL;
+    if (address(a[8], &wt, &dev, &table) || address(a[9], &wn, &dev, &seq) || address(a[10], &wi, &dev, &indptr) ||
+        address(a[11], &wm, &dev, &mask) || address(a[12], &wp, &dev, &pos) || address(a[13], &wo, &dev, &o) ||
+        address(a[14], &wl, &dev, &lse) || workspace_of(a[15], &dev, &ws, &bytes) || stream_of(a[16], dev, &st))
+        return NULL;
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = spec_attn_run_masked((const spec_attn_masked_plan*)(intptr_t)m[mHandle], q, kp, vp, ks, vs, (float)kg,
+                                  (float)vg, table, seq, indptr, mask, pos, o, lse, ws, (size_t)bytes, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
+}
+
+/* The tensors both tree calls take: parents [rows], seq_lens [P], q_indptr [P + 1]. */
+static int tree_of(PyObject* const* a, PyObject* seqs, PyObject* ptr, long* dev, Address* parents, Address* seq,
+                   Address* indptr, int64_t* rows, int64_t* reqs) {
+    want_t wp = {"parents", t_i32, 1, {-1}, NULL}, wn = {"seq_lens", t_i32, 1, {-1}, NULL};
+    if (address(a[0], &wp, dev, parents) || address(seqs, &wn, dev, seq)) return -1;
+    want_t wi = {"q_indptr", t_i32, 1, {wn.shape[0] + 1}, NULL};
+    if (address(ptr, &wi, dev, indptr)) return -1;
+    *rows = wp.shape[0];
+    *reqs = wn.shape[0];
+    return 0;
+}
+
+static int fits(int64_t v) { return v >= INT32_MIN && v <= INT32_MAX; }
+
+/* build_tree((max_w, window_left, sink_keys), parents, seq_lens, q_indptr, positions, row_mask, workspace, stream) */
+static PyObject* build_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    int64_t c[3], bytes, rows, P;
+    if (count_args("build_tree", n, 8) || ints(a[0], 3, c)) return NULL;
+    long dev = -1;
+    Address parents, seq, indptr, pos, mask, ws;
+    spec_attn_stream_t st;
+    if (tree_of(a + 1, a[2], a[3], &dev, &parents, &seq, &indptr, &rows, &P)) return NULL;
+    want_t wp = {"positions", t_i32, 1, {rows}, NULL}, wm = {"row_mask", t_i32, 2, {rows, -1}, NULL};
+    if (address(a[4], &wp, &dev, &pos) || address(a[5], &wm, &dev, &mask) || workspace_of(a[6], &dev, &ws, &bytes) ||
+        stream_of(a[7], dev, &st))
+        return NULL;
+    if (P < 0 || rows < 0 || wm.shape[1] < 1) return PyLong_FromLong(SPEC_ATTN_E_INVALID_ARG);
+    if (!fits(P) || !fits(rows) || !fits(wm.shape[1]) || !fits(c[0]) || !fits(c[1]) || !fits(c[2]))
+        return PyLong_FromLong(SPEC_ATTN_E_UNSUPPORTED);
+    const spec_attn_tree_problem p = {(int32_t)P, (int32_t)rows, (int32_t)c[0], (int32_t)wm.shape[1], (int32_t)c[1],
+                                      (int32_t)c[2], 1, 0};
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = spec_attn_build_tree(&p, parents, seq, indptr, pos, mask, ws, (size_t)bytes, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
+}
+
+/* accept_tree((max_w,), parents, draft_tokens, target_tokens, seq_lens, q_indptr, path, accept_lens, next_tokens, ctx_lens,
+ * workspace, stream) */
+static PyObject* accept_tree(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    int64_t c[1], bytes, rows, P;
+    if (count_args("accept_tree", n, 12) || ints(a[0], 1, c)) return NULL;
+    long dev = -1;
+    Address parents, draft, target, seq, indptr, path, accepted, next, ctx, ws;
+    spec_attn_stream_t st;
+    if (tree_of(a + 1, a[4], a[5], &dev, &parents, &seq, &indptr, &rows, &P)) return NULL;
+    want_t wd = {"draft_tokens", t_i64, 1, {rows}, NULL}, wt = {"target_tokens", t_i64, 1, {rows}, NULL};
+    want_t wp = {"path", t_i32, 2, {P, -1}, NULL}, wa = {"accept_lens", t_i32, 1, {P}, NULL};
+    want_t wn = {"next_tokens", t_i64, 1, {P}, NULL}, wc = {"ctx_lens", t_i32, 1, {P}, NULL};
+    if (address(a[2], &wd, &dev, &draft) || address(a[3], &wt, &dev, &target) || address(a[6], &wp, &dev, &path) ||
+        address(a[7], &wa, &dev, &accepted) || address(a[8], &wn, &dev, &next) || address(a[9], &wc, &dev, &ctx) ||
+        workspace_of(a[10], &dev, &ws, &bytes) || stream_of(a[11], dev, &st))
+        return NULL;
+    if (P < 0 || rows < 0 || wp.shape[1] < 1) return PyLong_FromLong(SPEC_ATTN_E_INVALID_ARG);
+    if (!fits(P) || !fits(rows) || !fits(wp.shape[1]) || !fits(c[0])) return PyLong_FromLong(SPEC_ATTN_E_UNSUPPORTED);
+    const spec_attn_tree_problem p = {(int32_t)P, (int32_t)rows, (int32_t)c[0], 0, 0, 0, (int32_t)wp.shape[1], 0};
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = spec_attn_accept_tree(&p, parents, draft, target, seq, indptr, path, accepted, next, ctx, ws, (size_t)bytes,
+                                   st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
+}
+
+/* move_kv((max_seq_len,), k_pools, v_pools, k_scales, v_scales, block_table, seq_lens, q_indptr, path, accept_lens,
+ * workspace, stream): pools are lists of tensors, the scales' None for bf16.  The first layer's pools give the shapes. */
+static PyObject* move_kv(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    int64_t c[1], bytes;
+    if (count_args("move_kv", n, 12) || ints(a[0], 1, c)) return NULL;
+    for (int i = 1; i < 5; ++i)
+        if (!(PyList_Check(a[i]) || (i > 2 && a[i] == Py_None))) {
+            PyErr_SetString(PyExc_TypeError, "pools and scales are lists of tensors, one for each layer");
+            return NULL;
+        }
+    const Py_ssize_t layers = PyList_GET_SIZE(a[1]);
+    const int fp4 = a[3] != Py_None;
+    for (int i = 2; i < (fp4 ? 5 : 3); ++i)
+        if (!PyList_Check(a[i]) || PyList_GET_SIZE(a[i]) != layers) {
+            PyErr_SetString(PyExc_ValueError, "pools and scales must have the same number of layers");
+            return NULL;
+        }
+    if (!fp4 && a[4] != Py_None) {
+        PyErr_SetString(PyExc_ValueError, "k_scales and v_scales go together");
+        return NULL;
+    }
+    spec_attn_move_problem p = {};
+    long dev = -1;
+    Address table, seq, indptr, path, accepted, ws;
+    spec_attn_stream_t st;
+    want_t wn = {"seq_lens", t_i32, 1, {-1}, NULL};
+    if (address(a[6], &wn, &dev, &seq)) return NULL;
+    const int64_t P = wn.shape[0];
+    want_t wi = {"q_indptr", t_i32, 1, {P + 1}, NULL}, wt = {"block_table", t_i32, 2, {P, -1}, NULL};
+    want_t wp = {"path", t_i32, 2, {P, -1}, NULL}, wa = {"accept_lens", t_i32, 1, {P}, NULL};
+    if (address(a[5], &wt, &dev, &table) || address(a[7], &wi, &dev, &indptr) || address(a[8], &wp, &dev, &path) ||
+        address(a[9], &wa, &dev, &accepted) || workspace_of(a[10], &dev, &ws, &bytes) || stream_of(a[11], dev, &st))
+        return NULL;
+    int64_t m[mN] = {};
+    m[mKvDtype] = fp4;
+    if (layers > 0) {   /* shapes and strides of the first layer's K */
+        PyObject* k0 = PyList_GET_ITEM(a[1], 0);
+        PyObject* s0 = fp4 ? PyList_GET_ITEM(a[3], 0) : Py_None;
+        if (!THPVariable_Check(k0) || THPVariable_Unpack(k0).dim() != 4 ||
+            (fp4 && (!THPVariable_Check(s0) || THPVariable_Unpack(s0).dim() != 4))) {
+            PyErr_SetString(PyExc_ValueError, "pools and scales must be CUDA tensors [pages, Hkv, page_size, row]");
+            return NULL;
+        }
+        const at::Tensor& k = THPVariable_Unpack(k0);
+        m[mPages] = k.size(0);
+        m[mHkv] = k.size(1);
+        m[mPageSize] = k.size(2);
+        m[mD] = fp4 ? k.size(3) * 2 : k.size(3);
+        if (k.size(0) > 1) m[mKvStride] = k.stride(0) * (fp4 ? 1 : 2);
+        if (fp4 && k.size(0) > 1) m[mScStride] = THPVariable_Unpack(s0).stride(0);
+    }
+    std::vector<void*> at[4];
+    try {
+        for (auto& v : at) v.resize(static_cast<size_t>(layers));
+    } catch (const std::exception&) {
+        return PyErr_NoMemory();
+    }
+    for (Py_ssize_t l = 0; l < layers; ++l) {
+        PyObject* const pools[4] = {PyList_GET_ITEM(a[1], l), PyList_GET_ITEM(a[2], l),
+                                    fp4 ? PyList_GET_ITEM(a[3], l) : Py_None, fp4 ? PyList_GET_ITEM(a[4], l) : Py_None};
+        Address x[4];
+        if (caches_of(pools, m, &dev, &x[0], &x[1], &x[2], &x[3])) return NULL;
+        for (int i = 0; i < 4; ++i) at[i][static_cast<size_t>(l)] = x[i].p;
+    }
+    if (P < 0 || wt.shape[1] < 0 || wp.shape[1] < 0) return PyLong_FromLong(SPEC_ATTN_E_INVALID_ARG);
+    if (layers == 0) return PyLong_FromLong(SPEC_ATTN_OK);
+    if (!fits(P) || !fits(layers) || !fits(m[mHkv]) || !fits(m[mD]) || !fits(m[mPageSize]) || !fits(m[mPages]) ||
+        !fits(wt.shape[1]) || !fits(wp.shape[1]))
+        return PyLong_FromLong(SPEC_ATTN_E_UNSUPPORTED);
+    p.num_reqs = (int32_t)P;
+    p.num_layers = (int32_t)layers;
+    p.num_kv_heads = (int32_t)m[mHkv];
+    p.head_dim = (int32_t)m[mD];
+    p.page_size = (int32_t)m[mPageSize];
+    p.num_pages = (int32_t)m[mPages];
+    p.block_table_stride = (int32_t)wt.shape[1];
+    p.kv_dtype = fp4;
+    p.path_stride = (int32_t)wp.shape[1];
+    p.max_seq_len = c[0];
+    p.kv_page_stride = m[mKvStride];
+    p.scale_page_stride = m[mScStride];
+    int status;
+    Py_BEGIN_ALLOW_THREADS
+    status = spec_attn_move_kv(&p, at[0].data(), at[1].data(), at[2].data(), at[3].data(), table, seq, indptr, path,
+                               accepted, ws, (size_t)bytes, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
+}
+
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {FAST(build_tables), FAST(norm_rope), FAST(norm_rope_append), FAST(run_cross),
+                                FAST(run_masked), FAST(build_tree), FAST(accept_tree), FAST(move_kv),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "spec_attn_calls", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
