@@ -150,60 +150,6 @@ struct CrossAux {
 };
 static_assert(sizeof(CrossAux) <= 2048, "aux region");
 
-// Bounded wait of a whole warp; the clock is read only when the phase is still open.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (__all_sync(kFullMask, mbar_try_wait(bar, parity))) return true;
-    return warp_wait(bar, parity, abort);
-}
-
-// A shared-memory matrix descriptor is its high word, the same for every tile of
-// one kind, and a low word that a constant step moves along the tile: the
-// issuing thread adds to one register instead of building 64 bits each time.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes) {
-    return ((saddr >> 4) & 0x3FFFu) | ((lbo_bytes >> 4) << 16);   // (in a cluster the address has the rank above bit 23)
-}
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups 1024 B apart, version 1, 128-byte swizzle
-// Products and commits are issued by the one thread whose `go` is set, under a
-// predicate: the whole warp runs the issuing loop and its waits.  (With the loop
-// in a branch of one thread, each wait cost the next product 200 clocks: 8 + 4
-// instructions with a wait before each kind took 1053 clocks, and 621 like this.)
-__device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate,
-                                          uint32_t go) {
-    asm volatile(
-        "{\n\t.reg .pred p, g;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 g, %6, 0;\n\t"
-        "mov.b64 a, {%1, %5};\n\t"
-        "mov.b64 b, {%2, %5};\n\t"
-        "@g tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go)
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate,
-                                          uint32_t go) {
-    asm volatile(
-        "{\n\t.reg .pred p, g;\n\t.reg .b64 b;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "setp.ne.b32 g, %6, 0;\n\t"
-        "mov.b64 b, {%2, %5};\n\t"
-        "@g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go)
-        : "memory");
-}
-__device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t go) {
-    asm volatile(
-        "{\n\t.reg .pred g;\n\t"
-        "setp.ne.b32 g, %1, 0;\n\t"
-        "@g tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
-        "r"(go)
-        : "memory");
-}
-__device__ __forceinline__ uint32_t elected() {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r;
-}
-
 // Thread-block cluster: all threads of all its CTAs (those that left count as
 // arrived), and shared memory of the CTA of a given rank.
 __device__ __forceinline__ void cluster_sync() {

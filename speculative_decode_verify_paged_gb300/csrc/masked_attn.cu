@@ -1,5 +1,51 @@
 // Attention over the paged cache under tree masks and under a sliding window with
-// sinks (spec_attn_run_masked), windows of any width.
+// sinks (spec_attn_run_masked), windows of any width, bf16 or NVFP4 caches, on
+// 5th-generation tensor cores.
+//
+//   s_j = sm_scale <q, k_j>,  O = sum_j softmax(s)_j v_j,  LSE = ln sum_j exp(s_j)
+//
+// over the keys a row sees, in one sweep with a running maximum and sum per row
+// (base 2, fp32; the weights are rounded to 16 bits for the second product, the sum
+// adds them unrounded).
+//
+// One CTA = (NQ query tiles of 128 rows) x (one KV head) x (a split of the keys).  A
+// tile holds 128 / G whole window rows with their G heads, so K and V are read once
+// for the G heads; NQ = 2 (d = 128) shares every K and V tile between two query tiles,
+// one's products under the other's softmax.
+//
+// Keys.  The pages a CTA's rows can see are at most two runs: the sinks' and those
+// from its first row's window on.  They are walked as one list of pages, 64 keys a
+// tile; pages between the runs are never touched, and only the tile with the seam
+// has keys of both.  A row's mask of a tile is 64 bits made from its bounds (lowest
+// key of its window, sinks, its own key) and, where the tile reaches into a tree's
+// window, two words of its mask row, fetched before the scores are waited for.
+// Tiles that every row of a warp sees whole skip it.  V rows that no row of the CTA may
+// see are zeroed in shared memory (what lies there may be anything, and 0 x NaN is
+// NaN); masked scores are replaced, so K may hold anything there.
+//
+// Warp roles:
+//   warp 0      the query tiles, then K and V tiles in turn, by TMA into one ring of
+//               slots: a box of 64 elements x one page's keys each, 128-byte swizzle.
+//               NVFP4: codes and scales into a raw ring.
+//   warps 1, 2  issue the products, one elected thread each.  NQ = 2: warp 1 + i
+//               issues S_{t+1} and then P_t V_t of tile i.  NQ = 1: warp 1 issues
+//               S = Q K^T and warp 2 O += P V.
+//   warp 3      owns tensor memory.
+//   warps 4-7 (and 8-11 for the second tile)   softmax, a row a thread, and epilogue.
+//   NVFP4: warps 8-11 decode K and 12-15 V into fp16 operand tiles of the same ring;
+//               query rows and weights are fp16 too.
+//
+// Tensor memory: O tiles [0, NQ d), two or four S buffers of 64 columns a tile, P in the
+// first half of its S buffer, and where there is room (one tile, the SM to itself) the
+// query tile, which frees its shared memory and doubles the first product's rate.
+//
+// Splits leave normalised rows as fp16 of the row's largest element (off by at most
+// 2^-12 of it) with their log-sum-exps; a second kernel joins them in split order.
+//
+// Every wait is bounded; on time-out the CTA sets the device-status bit, drains its
+// copies and products, frees its tensor memory and leaves.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -10,16 +56,23 @@
 #include "../../include/spec_attn.h"
 #include "common.cuh"
 #include "overlap.h"
+#include "sm100.cuh"
+#include "tc_common.cuh"
 
 namespace spec_attn {
 namespace {
 
+using namespace sm100;
+using namespace tcc;
+
+constexpr int kM = 128;
+constexpr int kBN = 64;                 // keys a tile
+constexpr int kMaxRing = 14;
+constexpr int kMaxRaw = 8;
+constexpr int kMaxSorted = 256;         // requests put in order by one CTA's threads
+constexpr float kRescale = 8.0f;        // log2 units: O is rescaled when a row's maximum grows by more
+
 struct MaskedParams {
-    const uint16_t* q;
-    const unsigned char* k_pool;
-    const unsigned char* v_pool;
-    const uint8_t* k_scales;
-    const uint8_t* v_scales;
     const int32_t* block_table;
     const int32_t* seq_lens;
     const int32_t* q_indptr;
@@ -28,77 +81,854 @@ struct MaskedParams {
     uint16_t* o;
     float* lse;
     unsigned int* status;
-    int num_reqs, total_rows, max_w, num_q_heads, num_kv_heads, group;
+    float2* ws_ls;              // partials: per split and (row, head): (log2 of the sum, largest |element|)
+    uint16_t* ws_o;             //   and the row's elements over it, fp16
+    int total_rows, max_w, num_q_heads, num_kv_heads, group;
     int page_shift;             // log2(page_size)
     int num_pages, bt_stride, tree, window, sinks, mask_words;
-    long long max_seq_len, kv_page_stride, scale_page_stride;
+    int wt;                     // window rows of a query tile: 128 / group
+    int cta_rows;               // window rows of a CTA: wt, or twice that
+    int tiles;                  // CTAs' shares of the widest window
+    int tiles_per_split;        // key tiles
+    int max_splits;
+    int longest_first;          // requests to put in order of length (0: as they come)
+    long long max_seq_len;
     float score_scale_log2;     // sm_scale * log2(e) [* k_gscale]
     float out_scale;            // 1 or v_gscale
 };
 
-// A warp for each (window row, query head): the row's keys one after another.
-template <int D, bool FP4>
-__global__ void __launch_bounds__(128) masked_attn_kernel(const MaskedParams p) {
-    constexpr int E = D / 32;   // elements a lane
+// The pages that window rows [lo, lo + cta_rows) of a request can see, as one list: the sinks' pages, then those from
+// `first` on.
+struct Span {
+    int hi;              // keys from here on are seen by no row
+    int base;            // first key of the first row's window
+    int first;           // its page
+    int sink_pages;
+    int pages;
+    int tiles;
+};
+__device__ __forceinline__ Span span_of(const MaskedParams& p, const ReqInfo& ri, int lo) {
+    Span s;
+    const int per_tile = 64 >> p.page_shift;
+    s.hi = p.tree ? ri.len : ri.ctx + min(ri.w, lo + p.cta_rows);
+    s.base = p.window ? max(0, ri.ctx + (p.tree ? 0 : lo) - p.window + 1) : 0;
+    s.first = s.base >> p.page_shift;
+    s.sink_pages = p.window ? min(p.sinks ? ((p.sinks - 1) >> p.page_shift) + 1 : 0, s.first) : 0;
+    s.pages = s.sink_pages + ((s.hi - 1) >> p.page_shift) + 1 - s.first;
+    s.tiles = (s.pages + per_tile - 1) / per_tile;
+    return s;
+}
+
+// The keys of a tile's columns: key a + c for columns c < seam, key b + c from there on.
+struct Columns {
+    int a, b, seam;
+    uint64_t low;        // columns before the seam
+};
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+__device__ __forceinline__ Columns columns_of(const Span& s, int page_shift, int tile) {
+    Columns c;
+    const int v = tile << (6 - page_shift);                // the tile's first page in the list
+    if (v >= s.sink_pages) {
+        c.a = c.seam = 0;
+        c.b = (v - s.sink_pages + s.first) << page_shift;
+    } else {
+        c.a = v << page_shift;
+        c.seam = min(64, (s.sink_pages - v) << page_shift);
+        c.b = (s.first << page_shift) - c.seam;
+    }
+    c.low = low_bits(c.seam);
+    return c;
+}
+// columns whose key is below x
+__device__ __forceinline__ uint64_t below(const Columns& c, int x) {
+    const uint64_t b = low_bits(x - c.b);
+    return c.seam == 0 ? b : (low_bits(x - c.a) & c.low) | (b & ~c.low);
+}
+// columns that some row of the CTA may see
+__device__ __forceinline__ uint64_t live_columns(const MaskedParams& p, const Span& s, const Columns& c) {
+    uint64_t m = below(c, s.hi);
+    if (p.window) m &= ~below(c, s.base) | below(c, p.sinks);
+    return m;
+}
+
+// NVFP4 raw slot: the codes and scales of a tile's 16-key units, K then V.  Every copy lands on a 128-byte boundary, so
+// a unit's scales (d bytes) take at least 128.
+template <int D>
+struct MaskedRaw {
+    static constexpr int kCodes = 16 * D / 2;
+    static constexpr int kScaleBox = D;
+    static constexpr int kScales = kScaleBox < 128 ? 128 : kScaleBox;
+    static constexpr int kKS = 4 * kCodes;                 // offsets inside a slot
+    static constexpr int kVC = kKS + 4 * kScales;
+    static constexpr int kVS = kVC + 4 * kCodes;
+    static constexpr int kSlot = 8 * (kCodes + kScales);
+};
+
+// DEEP (d <= 128, one query tile, bf16): the launch has no more CTAs than SMs, and a CTA takes the whole SM; otherwise two
+// CTAs share it, one's start, end and waits under the other's work.  d = 256, two tiles and NVFP4 always take the whole SM.
+template <int D, bool FP4, int NQ, bool DEEP>
+struct MaskedLayout {
+    static_assert(NQ == 1 || (D == 128 && DEEP && !FP4), "two O tiles and four S buffers fit 512 columns at d = 128");
+    static_assert(DEEP || (!FP4 && D <= 128), "half an SM");
+    static constexpr int kChunks = D / 64;
+    static constexpr int kQBytes = kM * D * 2;             // one query tile
+    static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
+    static constexpr int kAux = 2048;
+    static constexpr int kCtas = DEEP ? 1 : 2;
+    static constexpr bool kQT = NQ == 1 && DEEP;           // the query tile in tensor memory
+    // S buffers of a tile (a power of two); with four, S_{t+1} does not wait for P V of tile t - 1
+    static constexpr int kBufShift = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
+    static constexpr int kBufs = 1 << kBufShift;
+    static constexpr int kQCol = NQ * (D + kBufs * kBN);
+    static constexpr int kNeed = kQCol + (kQT ? D / 2 : 0);
+    static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;   // allocated: a power of two
+    static_assert(kNeed <= 512 && kCols * kCtas <= 512, "tensor memory");
+    // first column of buffer b of tile i
+    __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (kBufs * i + b) * kBN; }
+    // The ring.  NQ = 1: a slot a tile, K_t and V_t in turn, each let go as soon as it has been read.  NQ = 2: a slot holds
+    // K_t and V_t, filled and let go together.  A query tile bound for tensor memory lands in the last two slots.
+    static constexpr int kSlotBytes = NQ * kTileBytes;
+    static constexpr int kQSmem = kQT ? 0 : NQ * kQBytes;
+    static constexpr int kMax = DEEP ? 232448 : 232448 / 2 - 1024;   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
+    static constexpr int kFit = (kMax - 1024 - kAux - kQSmem) / kSlotBytes;
+    static constexpr int kRing = FP4 ? (D == 256 ? 4 : 6) : kFit > kMaxRing ? kMaxRing : kFit;
+    static_assert(kRing >= 4, "tiles ahead of the ones in use");
+    static constexpr int kRawFit = (kMax - 1024 - kAux - kRing * kTileBytes) / MaskedRaw<D>::kSlot;
+    static constexpr int kRaw = !FP4 ? 0 : kRawFit > kMaxRaw ? kMaxRaw : kRawFit;
+    static constexpr int kTail = kRing * kSlotBytes + kRaw * MaskedRaw<D>::kSlot;   // ring and raw ring, adjacent
+    static constexpr int kSmem = 1024 + kAux + kQSmem + kTail;
+    // S may lead P V by as many tiles as it has buffers.  An odd ring puts K_t where V of tile t - (ring + 1) / 2 was, and
+    // that V has to be gone before its slot's next phase is waited for.
+    static constexpr int kLead = (NQ == 2 || kBufs <= (kRing + 1) / 2) ? kBufs : (kRing + 1) / 2;
+    // P V barriers in use: one a slot (NQ = 2), or one an S buffer and at least four
+    static constexpr int kPv = NQ == 2 ? kRing : 4;
+    // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), their log2 sums and largest elements
+    static constexpr int kRowFloats = D + 4;
+    static_assert(NQ * kM * (kRowFloats + 2) * 4 <= kQSmem + kTail, "epilogue staging");
+    static constexpr int kThreads = FP4 ? 512 : 128 + NQ * 128;
+};
+
+struct MaskedAux {
+    uint64_t full[kMaxRing];
+    uint64_t empty[kMaxRing];           // NQ = 1
+    uint64_t pv_done[2][kMaxRing];      // P_t V_t of tile i done: O, P_t's buffer and (NQ = 2) the slot; by t mod kPv
+    uint64_t q_full[2];
+    uint64_t q_ready;                   // the query tile is in tensor memory (four softmax warps)
+    uint64_t s_full[2][4];              // [tile][buffer] scores written
+    uint64_t p_full[2][4];              // P written over them (four softmax warps)
+    uint64_t raw_full[kMaxRaw];
+    uint64_t raw_empty[kMaxRaw];        // eight decoding warps
+    uint64_t drain[2];
+    uint32_t tmem_base;
+    int abort;
+    int request;                        // longest-first order: the CTA's request
+    int lens[kMaxSorted];
+};
+static_assert(sizeof(MaskedAux) <= 2048, "aux region");
+
+
+// One decoding warpgroup's work on a tile: the K or V codes of the raw slot into the fp16 operand tile, chunk-major,
+// 128-byte swizzle; columns that no row may see as zeros.  A unit is one key's 64 elements (32 code bytes, 4 scales, one
+// 128-byte row); eight consecutive keys run side by side, so that the row stores hit distinct banks.
+template <int D>
+__device__ __forceinline__ void decode_tile(const unsigned char* codes, const unsigned char* scales, unsigned char* tile,
+                                            uint64_t live, int dt) {
+    using R = MaskedRaw<D>;
+    constexpr int CPK = D / 64;
+    for (int u = dt; u < kBN * CPK; u += 128) {
+        const int j = (u / (8 * CPK)) * 8 + (u & 7), c = (u >> 3) % CPK;
+        const int unit = j >> 4, sl = j & 15;
+        uint4 outp[8];
+        if ((live >> j) & 1) {
+            const unsigned char* kr = codes + unit * R::kCodes + sl * (D / 2);
+            const uint4 w0 = *reinterpret_cast<const uint4*>(kr + raw_code_chunk<D>(sl, 2 * c) * 16);
+            const uint4 w1 = *reinterpret_cast<const uint4*>(kr + raw_code_chunk<D>(sl, 2 * c + 1) * 16);
+            const uint32_t sc4 = *reinterpret_cast<const uint32_t*>(scales + unit * R::kScales + sl * (D / 16) + c * 4);
+            const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t s2 = e4m3_pair_f16x2((sc4 >> (8 * (q >> 1))) & 0xFFu);
+                e2m1x8_f16(words[q], s2, outp[q].x, outp[q].y, outp[q].z, outp[q].w);
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) outp[q] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        unsigned char* row = tile + c * (kBN * 128) + j * 128;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(row + ((q ^ (j & 7)) << 4)) = outp[q];
+    }
+}
+
+template <int D, bool FP4, int NQ, bool DEEP>
+__global__ void __launch_bounds__(MaskedLayout<D, FP4, NQ, DEEP>::kThreads, MaskedLayout<D, FP4, NQ, DEEP>::kCtas)
+masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant__ CUtensorMap tmq,
+                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                   const __grid_constant__ CUtensorMap tmks, const __grid_constant__ CUtensorMap tmvs) {
+    using L = MaskedLayout<D, FP4, NQ, DEEP>;
+    using R = MaskedRaw<D>;
+    constexpr int PV = L::kPv, RING = L::kRing, SH = L::kBufShift, NB = L::kBufs;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int split = blockIdx.x % p.max_splits;
+    const int tile = p.tiles - 1 - blockIdx.x / p.max_splits;     // (a chain's last rows see the most keys)
+    const int kvh = blockIdx.y;
+    int r = blockIdx.z;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                           ~static_cast<uintptr_t>(1023));
+    MaskedAux* aux = reinterpret_cast<MaskedAux*>(smem);
+    unsigned char* ring = smem + L::kAux + L::kQSmem;
+    unsigned char* raw = ring + RING * L::kSlotBytes;
+    unsigned char* sQ = L::kQT ? ring + (RING - 2) * L::kTileBytes : smem + L::kAux;
+    volatile int* abort = &aux->abort;
+
+    if (tid == 0) {
+        for (int s = 0; s < RING; ++s) {
+            mbar_init(&aux->full[s], FP4 ? 4 : 1);
+            mbar_init(&aux->empty[s], 1);
+        }
+        for (int s = 0; s < L::kRaw; ++s) {
+            mbar_init(&aux->raw_full[s], 1);
+            mbar_init(&aux->raw_empty[s], 8);
+        }
+        for (int i = 0; i < NQ; ++i) {
+            for (int s = 0; s < PV; ++s) mbar_init(&aux->pv_done[i][s], 1);
+            mbar_init(&aux->q_full[i], 1);
+            for (int b = 0; b < NB; ++b) {
+                mbar_init(&aux->s_full[i][b], 1);
+                mbar_init(&aux->p_full[i][b], 4);
+            }
+        }
+        mbar_init(&aux->q_ready, 4);
+        mbar_init(&aux->drain[0], 1);
+        mbar_init(&aux->drain[1], 1);
+        aux->abort = 0;
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
+        tma_prefetch_desc(&tmq);
+        tma_prefetch_desc(&tmk);
+        tma_prefetch_desc(&tmv);
+        if (FP4) {
+            tma_prefetch_desc(&tmks);
+            tma_prefetch_desc(&tmvs);
+        }
+    }
+    if (warp == 3) tmem_alloc(&aux->tmem_base, L::kCols);
+    // up to here the CTA touched only its own resources, while the previous kernel drains
+    pdl_wait_primary();
+    if (p.longest_first) {
+        // More CTAs than the GPU holds: the requests with the most keys go first, so that the last CTAs to start are
+        // short ones.  Each CTA ranks the lengths itself (ties by index).
+        const int limit = p.window ? p.window : INT_MAX;
+        if (tid < p.longest_first) aux->lens[tid] = min(p.seq_lens[tid], limit);
+        __syncthreads();
+        if (tid < p.longest_first) {
+            const int mine = aux->lens[tid];
+            int rank = 0;
+            for (int j = 0; j < p.longest_first; ++j) rank += aux->lens[j] > mine || (aux->lens[j] == mine && j < tid);
+            if (rank == blockIdx.z) aux->request = tid;
+        }
+        __syncthreads();
+        r = aux->request;
+    }
+    ReqInfo ri;
+    const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
+    bool active = load_request(p.seq_lens, p.q_indptr, r, p.max_w, p.total_rows, p.max_seq_len,
+                               p.bt_stride << p.page_shift, kBN, reporter ? p.status : nullptr, ri);
+    const int lo = tile * p.cta_rows;                      // first window row of the CTA
+    active = active && lo < ri.w;
+    Span span = {};
+    int nsplits = 0;
+    if (active) {
+        span = span_of(p, ri, lo);
+        nsplits = (span.tiles + p.tiles_per_split - 1) / p.tiles_per_split;
+        active = split < nsplits;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // The next kernel's CTAs set up as these leave their SMs.  (Not before this CTA has its tensor memory: theirs would
+    // hold it while they wait for this grid.)
+    pdl_launch_dependents();
+    const uint32_t tmem = aux->tmem_base;
+    if (!active) {                                         // uniform across the CTA
+        if (warp == 3) tmem_dealloc(tmem, L::kCols);
+        return;
+    }
+    const int G = p.group;
+    const int nact = (NQ == 2 && lo + p.wt < ri.w) ? 2 : 1;
+    const int rows = min(ri.w - lo, p.cta_rows) * G;       // query rows of the CTA, wt * G of them in its first tile
+    const int t0 = split * p.tiles_per_split;              // its key tiles
+    const int T = min(p.tiles_per_split, span.tiles - t0);
+    // products of P V take whole 16-key steps: those of the request's last tile end with its keys
+    int last_steps = kBN / 16;
+    if (t0 + T == span.tiles) {
+        const Columns c = columns_of(span, p.page_shift, t0 + T - 1);
+        last_steps = (64 - __clzll(static_cast<long long>(live_columns(p, span, c))) + 15) / 16;
+    }
+    // row m of the CTA: its place in O and LSE
+    auto place = [&](int m) { return (size_t)(ri.row0 + lo + m / G) * p.num_q_heads + kvh * G + m % G; };
+    float* stage = reinterpret_cast<float*>(smem + L::kAux);   // (epilogue)
+    float* stage_lse = stage + NQ * kM * L::kRowFloats;
+    float* stage_max = stage_lse + NQ * kM;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        int issued = 0;
+        if (lane == 0) {
+            const uint32_t qbytes = static_cast<uint32_t>(L::kChunks * 128 * G * p.wt);
+            for (int i = 0; i < nact; ++i) {
+                mbar_arrive_expect_tx(&aux->q_full[i], qbytes);
+                for (int c = 0; c < L::kChunks; ++c)
+                    tma_load_3d(sQ + i * L::kQBytes + c * (kM * 128), &tmq, c * 64, kvh * G, ri.row0 + lo + i * p.wt,
+                                &aux->q_full[i]);
+            }
+        }
+        __syncwarp();
+        // the split's pages, 32 at a time in the lanes' registers, the next 32 on their way
+        const int shift = p.page_shift, per_tile = 64 >> shift;
+        const int v0 = t0 * per_tile, pages = min(span.pages - v0, T * per_tile);
+        const int32_t* table = p.block_table + (size_t)r * p.bt_stride;
+        auto fetch = [&](int k) {
+            if (k >= pages) return 0;
+            const int v = v0 + k;
+            return ld_volatile_i32(table + (v < span.sink_pages ? v : v - span.sink_pages + span.first));
+        };
+        auto checked = [&](int page) {
+            if (page >= 0 && page < p.num_pages) return page;
+            atomicOr(p.status, kDevBadPage);
+            return 0;
+        };
+        int cur = checked(fetch(lane)), next = fetch(32 + lane), batch = 0;
+        auto turn = [&](int k) {                           // k: first page of the tile
+            if (k >> 5 == batch) return;
+            batch = k >> 5;
+            cur = checked(next);
+            next = fetch(32 * (batch + 1) + lane);
+        };
+        if constexpr (FP4) {
+            for (int t = 0; t < T; ++t) {
+                const int slot = t % L::kRaw, k = t * per_tile;
+                if (t >= L::kRaw && !wait_warp(&aux->raw_empty[slot], ((t / L::kRaw) - 1) & 1, abort)) break;
+                turn(k);
+                const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
+                uint64_t* bar = &aux->raw_full[slot];
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * 2 * (R::kCodes + R::kScaleBox)));
+                const int pp = (lane >> 2) & 3, kind = lane & 3, sub = pp & ((1 << (shift - 4)) - 1);
+                const int page = __shfl_sync(kFullMask, cur, (k & 31) + (pp >> (shift - 4)));
+                __syncwarp();
+                if (lane < 4 * units) {
+                    unsigned char* dst = raw + slot * R::kSlot;
+                    if (kind == 0) tma_load_4d(dst + pp * R::kCodes, &tmk, 0, sub * 16, kvh, page, bar);
+                    else if (kind == 1) tma_load_4d(dst + R::kVC + pp * R::kCodes, &tmv, 0, sub * 16, kvh, page, bar);
+                    else if (kind == 2) tma_load_3d(dst + R::kKS + pp * R::kScales, &tmks, sub * D, kvh, page, bar);
+                    else tma_load_3d(dst + R::kVS + pp * R::kScales, &tmvs, sub * D, kvh, page, bar);
+                }
+                __syncwarp();
+                issued = t + 1;
+            }
+        } else {
+            for (int n = 0; n < (NQ == 2 ? T : 2 * T); ++n) {
+                const int slot = n % RING, k = (NQ == 2 ? n : n >> 1) * per_tile;
+                const uint32_t gone = ((n / RING) - 1) & 1;
+                if (n >= RING) {
+                    if (NQ == 1 && !wait_warp(&aux->empty[slot], gone, abort)) break;
+                    if (NQ == 2 && !(wait_warp(&aux->pv_done[0][slot], gone, abort) &&
+                                     (nact == 1 || wait_warp(&aux->pv_done[1][slot], gone, abort))))
+                        break;
+                }
+                // (the query tile has to leave the last two slots first)
+                if (L::kQT && n == RING - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
+                turn(k);
+                const int np = min(per_tile, pages - k);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(NQ * np * L::kChunks * (128 << shift)));
+                // a box a lane: page pp of the tile, 64-element chunk c; NQ = 2: K by the first half of the warp, V by the other
+                const int pp = (lane & 15) / L::kChunks, c = lane % L::kChunks;
+                const int page = __shfl_sync(kFullMask, cur, (k & 31) + min(pp, per_tile - 1));
+                const bool is_v = NQ == 2 ? lane >= 16 : (n & 1) != 0;
+                __syncwarp();
+                if (pp < np && (NQ == 2 || lane < 16))
+                    tma_load_4d(ring + slot * L::kSlotBytes + (NQ == 2 && is_v ? L::kTileBytes : 0) + c * (kBN * 128) +
+                                    pp * (128 << shift),
+                                is_v ? &tmv : &tmk, c * 64, 0, kvh, page, &aux->full[slot]);
+                __syncwarp();
+                issued = n + 1;
+            }
+        }
+        if (*abort && lane == 0) {
+            if (FP4) drain_copies<FP4 ? L::kRaw : 1>(aux->raw_full, issued);
+            else drain_copies<RING>(aux->full, issued);
+            volatile int no_abort = 0;
+            for (int i = 0; i < nact; ++i) mbar_wait(&aux->q_full[i], 0, &no_abort, kDrainLimit);
+        }
+        __syncwarp();
+    } else if (warp == 1 || (warp == 2 && (NQ == 1 || nact == 2))) {
+        // ------------------------------------------------------------ products
+        const uint32_t go = elected();
+        constexpr uint32_t idesc_s = FP4 ? idesc_f16_f32(kM, kBN, 0, 0) : idesc_bf16_f32(kM, kBN, 0, 0);
+        constexpr uint32_t idesc_o = FP4 ? idesc_f16_f32(kM, D, 0, 1) : idesc_bf16_f32(kM, D, 0, 1);
+        const int i = NQ == 2 ? warp - 1 : 0;
+        const uint32_t q_lo = desc_lo(smem_addr(sQ + i * L::kQBytes), 16);
+        const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), kBN * 128);
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, abort); };
+        // the ring slots of K_t and V_t, and the slot t mod kPv, stepped along with the parity of their phase
+        struct Step {
+            int size, slot;
+            uint32_t par;
+            __device__ __forceinline__ void by(int n) {
+                slot += n;
+                if (slot >= size) {
+                    slot -= size;
+                    par ^= 1;
+                }
+            }
+        };
+        Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
+        Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - lead of the next S)
+        // S_t, once K_t is here and the P that sat in S_t's buffer has been read
+        auto do_s = [&](int t) {
+            const int b = t & (NB - 1);
+            if (t >= L::kLead) {
+                if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
+                before.by(1);
+            }
+            if (!wait(&aux->full[ks.slot], ks.par)) return false;
+            tc_fence_after();
+            const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t k_at = k_lo + (kk >> 2) * (kBN * 128 >> 4) + (kk & 3) * 2;
+                if (L::kQT) mma_ts_lo(d_tmem, tmem + L::kQCol + kk * 8, k_at, idesc_s, kk > 0, go);
+                else mma_ss_lo(d_tmem, q_lo + (kk >> 2) * (kM * 128 >> 4) + (kk & 3) * 2, k_at, idesc_s, kk > 0, go);
+            }
+            commit_if(&aux->s_full[i][b], go);
+            if (NQ == 1) commit_if(&aux->empty[ks.slot], go);
+            ks.by(NQ == 1 ? 2 : 1);
+            return true;
+        };
+        // O += P_t V_t, once both are here (NQ = 2: V_t came with K_t)
+        auto do_pv = [&](int t) {
+            const int b = t & (NB - 1);
+            if (NQ == 1 && !wait(&aux->full[vs.slot], vs.par)) return false;
+            if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
+            tc_fence_after();
+            const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
+            const uint32_t p_tmem = tmem + L::s_col(i, b);
+            const int steps = t == T - 1 ? last_steps : kBN / 16;
+#pragma unroll
+            for (int kk = 0; kk < kBN / 16; ++kk)
+                if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * (2048 >> 4), idesc_o, t > 0 || kk > 0, go);
+            commit_if(&aux->pv_done[i][done.slot], go);
+            if (NQ == 1) commit_if(&aux->empty[vs.slot], go);
+            vs.by(NQ == 1 ? 2 : 1);
+            done.by(1);
+            return true;
+        };
+        bool ok = true;
+        if (NQ == 2 || warp == 1) ok = wait(L::kQT ? &aux->q_ready : &aux->q_full[i], 0);
+        tc_fence_after();
+        if (NQ == 2) {
+            ok = ok && do_s(0);
+            for (int t = 0; t < T && ok; ++t) ok = (t + 1 == T || do_s(t + 1)) && do_pv(t);
+        } else if (warp == 1) {
+            for (int t = 0; t < T && ok; ++t) ok = do_s(t);
+        } else {
+            for (int t = 0; t < T && ok; ++t) ok = do_pv(t);
+        }
+        // every product this thread issued completes before the memory is released
+        uint64_t* drain = &aux->drain[warp - 1];
+        commit_if(drain, go);
+        volatile int no_abort = 0;
+        mbar_wait(drain, 0, &no_abort, kDrainLimit);
+        __syncwarp();
+    } else if (FP4 && warp >= 8) {
+        // ------------------------------------------------------------ NVFP4: K (warps 8-11) and V (12-15) into operand tiles
+        const bool is_v = warp >= 12;
+        for (int t = 0; t < T; ++t) {
+            const int n = 2 * t + is_v, slot = n % RING, rs = t % max(1, L::kRaw);
+            const uint64_t live = live_columns(p, span, columns_of(span, p.page_shift, t0 + t));
+            if (!wait_warp(&aux->raw_full[rs], (t / max(1, L::kRaw)) & 1, abort)) break;
+            if (n >= RING && !wait_warp(&aux->empty[slot], ((n / RING) - 1) & 1, abort)) break;
+            // (the query tile has to leave the last two slots first)
+            if (n >= RING - 2 && n < RING && !wait_warp(&aux->q_ready, 0, abort)) break;
+            const unsigned char* src = raw + rs * R::kSlot;
+            decode_tile<D>(src + (is_v ? R::kVC : 0), src + (is_v ? R::kVS : R::kKS), ring + slot * L::kTileBytes, live,
+                           tid & 127);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&aux->full[slot]);
+                mbar_arrive(&aux->raw_empty[rs]);
+            }
+        }
+    } else if (warp >= 4 && (warp < 8 || nact == 2)) {
+        // ------------------------------------------------------------ softmax and epilogue
+        const int i = warp >= 8 ? 1 : 0;                   // tile
+        const int m = (warp & 3) * 32 + lane;              // row of the tile
+        const uint32_t lane_tmem = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const int wrow = lo + i * p.wt + m / G;            // window row
+        const bool valid = m < p.wt * G && wrow < ri.w;
+        // a warp without rows leaves its scores as they are: they weigh on no other row
+        const bool live = __any_sync(kFullMask, valid);
+        bool ok = true;
+        if (L::kQT) {
+            // the query row into tensor memory, two elements a column; NVFP4: as fp16 (saturating; exact for magnitudes of
+            // 2^-14 to 65504).  Rows that are none are zeros.
+            if ((ok = wait_warp(&aux->q_full[0], 0, abort))) {
+                const uint32_t row = smem_addr(sQ) + m * 128;
+#pragma unroll 1
+                for (int c = 0; c < L::kChunks; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                        if (valid) v = ld_shared_v4(row + c * (kM * 128) + ((q ^ (m & 7)) << 4));
+                        w[4 * q + 0] = FP4 ? bf16x2_to_f16x2_sat(v.x) : v.x;
+                        w[4 * q + 1] = FP4 ? bf16x2_to_f16x2_sat(v.y) : v.y;
+                        w[4 * q + 2] = FP4 ? bf16x2_to_f16x2_sat(v.z) : v.z;
+                        w[4 * q + 3] = FP4 ? bf16x2_to_f16x2_sat(v.w) : v.w;
+                    }
+                    __syncwarp();
+                    tmem_st32u(lane_tmem + L::kQCol + c * 32, w);
+                }
+                tmem_wait_st();
+                fence_proxy_async_smem();                  // (the slots are written by copies next)
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->q_ready);
+            }
+        }
+        // the row's bounds: context keys from `from` (or below the sinks) to `to`
+        int to = INT_MAX, from = 0;
+        const uint32_t* mask_row = nullptr;
+        if (valid) {
+            const int row = ri.row0 + wrow;
+            int pos = ri.ctx + wrow;
+            if (p.tree) {
+                pos = p.window ? max(ri.ctx, p.positions[row]) : ri.ctx;
+                mask_row = p.row_mask + (size_t)row * p.mask_words;
+            }
+            to = p.tree ? ri.ctx : pos + 1;
+            if (p.window) from = max(0, pos - p.window + 1);
+            if (p.tree) from = min(from, ri.ctx);
+        }
+        // keys that every row of the warp sees
+        const int all_from = __reduce_max_sync(kFullMask, from), all_to = __reduce_min_sync(kFullMask, to);
+        const float sc = p.score_scale_log2;
+        float m_ref = -INFINITY, l_sum = 0.f;
+        const uint64_t sc2 = pack2(sc, sc);
+        for (int t = 0; t < T && ok; ++t) {
+            const int b = t & (NB - 1);
+            const Columns col = columns_of(span, p.page_shift, t0 + t);
+            uint64_t sees = ~0ull;
+            if (col.seam != 0 || col.b < all_from || col.b > all_to - kBN) {
+                if (valid) {
+                    sees = below(col, to);
+                    if (p.window) sees &= ~below(col, from) | below(col, p.sinks);
+                    const int off = col.b - ri.ctx;        // the window's key at column 0, or how many context keys precede it
+                    if (p.tree && off > -kBN) {
+                        const int o = max(off, 0), at = o >> 5, n = p.mask_words;
+                        const uint32_t w0 = at < n ? mask_row[at] : 0u, w1 = at + 1 < n ? mask_row[at + 1] : 0u;
+                        const uint32_t w2 = at + 2 < n ? mask_row[at + 2] : 0u;
+                        uint64_t bits = static_cast<uint64_t>(__funnelshift_r(w1, w2, o & 31)) << 32 |
+                                        __funnelshift_r(w0, w1, o & 31);
+                        if (off < 0) bits <<= -off;
+                        sees |= bits & ~col.low & below(col, ri.len);
+                    }
+                }
+            }
+            const bool masked = !__all_sync(kFullMask, sees == ~0ull);
+            if (!(ok = wait_warp(&aux->s_full[i][b], (t >> SH) & 1, abort))) break;
+            tc_fence_after();
+            const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
+            if (live) {
+                __syncwarp();
+                float sv[kBN];
+                tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sv));
+                tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+                tmem_wait_ld();
+                if (masked) {
+                    const uint32_t s0 = static_cast<uint32_t>(sees), s1 = static_cast<uint32_t>(sees >> 32);
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        sv[c] = s0 >> c & 1 ? sv[c] : -INFINITY;
+                        sv[32 + c] = s1 >> c & 1 ? sv[32 + c] : -INFINITY;
+                    }
+                }
+                float mx4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+                for (int c = 4; c < kBN; c += 8) {   // (three-way maxima)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx4[k] = fmaxf(fmaxf(mx4[k], sv[c + k]), c + 4 < kBN ? sv[c + 4 + k] : mx4[k]);
+                }
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sc;
+                // the reference moves at the first key seen, and when the maximum outgrows it
+                const bool need = mx > m_ref + kRescale;
+                const float ref = need ? mx : m_ref;
+                const float alpha = need ? fast_exp2(m_ref - ref) : 1.f;   // (0 at the first)
+                // (an infinite reference is not subtracted: inf - inf would hide in the sum what the scores were.  Plus
+                // infinity makes the sum and with it the log-sum-exp infinite, and O, times 1 / inf, NaN.)
+                const float nref = fabsf(ref) == INFINITY ? 0.f : -ref;
+                const uint64_t nref2 = pack2(nref, nref);
+                uint32_t pk[kBN / 2];
+                uint64_t ps[2] = {0, 0};   // two fp32 zeros each
+#pragma unroll
+                for (int c = 0; c < kBN; c += 2) {
+                    const float2 x = unpack2(fma2(pack2(sv[c], sv[c + 1]), sc2, nref2));
+                    const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
+                    ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], pack2(p0, p1));
+                    if constexpr (FP4) {
+                        pk[c >> 1] = pack_half2(p0, p1);
+                    } else {
+                        const __nv_bfloat162 h2 = __floats2bfloat162_rn(p0, p1);
+                        pk[c >> 1] = *reinterpret_cast<const uint32_t*>(&h2);
+                    }
+                }
+                const float2 psum = unpack2(add2(ps[0], ps[1]));
+                l_sum = l_sum * alpha + (psum.x + psum.y);
+                m_ref = ref;
+                if (t > 0 && __any_sync(kFullMask, valid && need)) {
+                    // every earlier P V has to be in
+                    if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % PV], ((t - 1) / PV) & 1, abort))) break;
+                    tc_fence_after();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        float ov[32];
+                        tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                        tmem_st32(lane_tmem + i * D + ch * 32, ov);
+                    }
+                }
+                tmem_st32u(s_tmem, pk);
+                tmem_wait_st();
+            }
+            if (!FP4 && (col.seam != 0 || col.b < span.base || col.b > span.hi - kBN)) {
+                // V rows that no row of the CTA may see.  (The slot's earlier tile was consumed before these scores could
+                // be made, so the parity names this phase.  Both tiles' warps write the same zeros.)
+                const int steps = t == T - 1 ? last_steps : kBN / 16;
+                const uint64_t dead = ~live_columns(p, span, col) & low_bits(steps * 16);
+                if (dead) {
+                    constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
+                    const int n = NQ == 2 ? t : 2 * t + 1;
+                    if (!(ok = wait_warp(&aux->full[n % RING], (n / RING) & 1, abort))) break;
+                    const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
+                    for (int u = m; u < kBN * C8; u += 128)
+                        if ((dead >> (u / C8)) & 1)
+                            st_shared_v4(v_addr + ((u % C8) >> 3) * (kBN * 128) + (u / C8) * 128 + (u & 7) * 16,
+                                         make_uint4(0u, 0u, 0u, 0u));
+                    fence_proxy_async_smem();
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
+        }
+        // both tiles' products are done: the query tiles and the ring are free
+        for (int j = 0; j < NQ; ++j)
+            if (ok && j < nact) ok = wait_warp(&aux->pv_done[j][(T - 1) % PV], ((T - 1) / PV) & 1, abort);
+        tc_fence_after();
+        if (ok) {
+            const int sr = i * p.wt * G + m;               // (rows past the tile's wt * G are not written)
+            float* row = stage + sr * L::kRowFloats;
+            const float inv = l_sum == 0.f ? 0.f : p.out_scale / l_sum;
+            float most = 0.f;
+            if (live) {
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float ov[32];
+                    tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                    tmem_wait_ld();
+                    if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 x = make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
+                            most = fmaxf(fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+                            *reinterpret_cast<float4*>(row + ch * 32 + e) = x;
+                        }
+                    }
+                    __syncwarp();   // the next load takes the whole warp at once
+                }
+            }
+            if (valid) {
+                stage_lse[sr] = m_ref + log2f(l_sum);
+                stage_max[sr] = most;
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kCols);
+    }
+    if (*abort) {
+        if (tid == 0) atomicOr(p.status, kDevWaitTimeout);
+        return;
+    }
+    // ---------------------------------------------------------------- rows out
+    constexpr int C8 = D / 8;
+    const size_t part = (size_t)split * p.total_rows * p.num_q_heads;
+    for (int u = tid; u < rows * C8; u += L::kThreads) {
+        const int m = u / C8, c = u % C8;
+        const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
+        const float4 a = src[0], b = src[1];
+        const size_t at = place(m);
+        if (nsplits == 1) {
+            auto pair = [](float x, float y) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+                return *reinterpret_cast<const uint32_t*>(&h);
+            };
+            st_global_v4(p.o + at * D + c * 8, make_uint4(pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)));
+            if (c == 0 && p.lse) p.lse[at] = stage_lse[m] * kLn2;
+        } else {
+            const float most = stage_max[m], s = most > 0.f ? 1.f / most : 0.f;
+            st_global_v4(p.ws_o + (part + at) * D + c * 8,
+                         make_uint4(pack_half2(a.x * s, a.y * s), pack_half2(a.z * s, a.w * s),
+                                    pack_half2(b.x * s, b.y * s), pack_half2(b.z * s, b.w * s)));
+            if (c == 0) p.ws_ls[part + at] = make_float2(stage_lse[m], most);
+        }
+    }
+}
+
+// Joins the splits' rows: O = sum_s 2^(lse_s - lse) O_s, in split order.  A thread an 8-element piece of a (row, head).
+template <int D>
+__global__ void __launch_bounds__(256) masked_join_kernel(const __grid_constant__ MaskedParams p) {
+    constexpr int C8 = D / 8, kBatch = 8;
     pdl_wait_primary();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int m = blockIdx.x * 4 + warp, kvh = blockIdx.y, r = blockIdx.z;
     ReqInfo ri;
-    if (!load_request(p.seq_lens, p.q_indptr, r, p.max_w, p.total_rows, p.max_seq_len, p.bt_stride << p.page_shift, 64,
-                      threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0 ? p.status : nullptr, ri))
+    if (!load_request(p.seq_lens, p.q_indptr, blockIdx.y, p.max_w, p.total_rows, p.max_seq_len,
+                      p.bt_stride << p.page_shift, kBN, nullptr, ri))
         return;
-    const int i = m / p.group;
-    if (i >= ri.w) return;
-    const size_t at = (size_t)(ri.row0 + i) * p.num_q_heads + kvh * p.group + m % p.group;
-    float q[E], acc[E];
-    for (int e = 0; e < E; ++e) {
-        q[e] = bf16_bits_to_float(p.q[at * D + lane * E + e]);
-        acc[e] = 0.f;
+    const long long u = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int wrow = static_cast<int>(u / (p.num_q_heads * C8));
+    if (wrow >= ri.w) return;
+    const Span s = span_of(p, ri, wrow / p.cta_rows * p.cta_rows);
+    const int n = (s.tiles + p.tiles_per_split - 1) / p.tiles_per_split;
+    if (n == 1) return;
+    const size_t at = (size_t)ri.row0 * p.num_q_heads + u / C8, step = (size_t)p.total_rows * p.num_q_heads;
+    const int c = static_cast<int>(u % C8);
+    float acc[8] = {}, mx = -INFINITY, sum = 0.f;
+    for (int s0 = 0; s0 < n; s0 += kBatch) {
+        float2 ls[kBatch];
+        uint4 x[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (s0 + k >= n) break;
+            ls[k] = p.ws_ls[at + (s0 + k) * step];
+            x[k] = *reinterpret_cast<const uint4*>(p.ws_o + (at + (s0 + k) * step) * D + c * 8);
+        }
+        float m2 = mx;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+            if (s0 + k < n) m2 = fmaxf(m2, ls[k].x);
+        const float ref = fabsf(m2) == INFINITY ? 0.f : m2;   // (as in the softmax)
+        const float a = m2 > mx ? fast_exp2(mx - ref) : 1.f;
+        sum *= a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= a;
+        mx = m2;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (s0 + k >= n) break;
+            const float w = fast_exp2(ls[k].x - ref), ws = w * ls[k].y;
+            sum += w;
+            const uint32_t h[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack_half2(h[e]);
+                acc[2 * e] = fmaf(ws, f.x, acc[2 * e]);
+                acc[2 * e + 1] = fmaf(ws, f.y, acc[2 * e + 1]);
+            }
+        }
     }
-    int pos = ri.ctx + i;
-    if (p.tree) pos = p.window ? max(ri.ctx, p.positions[ri.row0 + i]) : ri.ctx;
-    // first key of the window, beside the sinks (a tree's own keys are the mask's alone)
-    int first = p.window ? max(0, pos - p.window + 1) : 0;
-    if (p.tree) first = min(first, ri.ctx);
-    const int end = p.tree ? ri.len : pos + 1;
-    float mx = -INFINITY, l = 0.f;
-    auto value = [&](const unsigned char* pool, const uint8_t* scales, int page, int slot, int e) {
-        const size_t row = (size_t)kvh << p.page_shift | slot;
-        if (!FP4) return bf16_bits_to_float(reinterpret_cast<const uint16_t*>(pool + page * p.kv_page_stride)[row * D + e]);
-        const uint32_t c = (pool + page * p.kv_page_stride)[row * (D / 2) + e / 2];
-        return e2m1_to_float(e & 1 ? c >> 4 : c & 15) *
-               e4m3_to_float((scales + page * p.scale_page_stride)[row * (D / 16) + e / 16]);
-    };
-    for (int j = 0; j < end; ++j) {
-        if (j >= p.sinks && j < first) {
-            j = first;
-            if (j >= end) break;
-        }
-        if (p.tree && j >= ri.ctx) {
-            const int b = j - ri.ctx;
-            if (!(p.row_mask[(size_t)(ri.row0 + i) * p.mask_words + (b >> 5)] >> (b & 31) & 1)) continue;
-        }
-        int page = p.block_table[(size_t)r * p.bt_stride + (j >> p.page_shift)];
-        if (page < 0 || page >= p.num_pages) {
-            if (lane == 0) atomicOr(p.status, kDevBadPage);
-            page = 0;
-        }
-        const int slot = j & ((1 << p.page_shift) - 1);
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s = fmaf(q[e], value(p.k_pool, p.k_scales, page, slot, lane * E + e), s);
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(kFullMask, s, o);
-        s *= p.score_scale_log2;
-        const float mn = fmaxf(mx, s), ref = fabsf(mn) == INFINITY ? 0.f : mn;
-        const float a = mn > mx ? exp2f(mx - ref) : 1.f, w = exp2f(s - ref);
-        mx = mn;
-        l = l * a + w;
-        for (int e = 0; e < E; ++e)
-            acc[e] = fmaf(w, value(p.v_pool, p.v_scales, page, slot, lane * E + e), acc[e] * a);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+        out[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    const float inv = l == 0.f ? 0.f : p.out_scale / l;
-    for (int e = 0; e < E; ++e) p.o[at * D + lane * E + e] = float_to_bf16_bits(acc[e] * inv);
-    if (p.lse && lane == 0) p.lse[at] = (mx + log2f(l)) * kLn2;
+    st_global_v4(p.o + at * D + c * 8, make_uint4(out[0], out[1], out[2], out[3]));
+    if (c == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
+}
+
+using MaskedKernel = void (*)(const MaskedParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                              const CUtensorMap);
+using JoinKernel = void (*)(const MaskedParams);
+
+// What a launch of (d, cache type, query tiles a CTA) needs.
+struct MaskedVariant {
+    MaskedKernel kernel;
+    int threads, smem, ctas;   // ctas: on one SM
+};
+template <int D, bool FP4, int NQ, bool DEEP>
+MaskedVariant variant_of() {
+    using L = MaskedLayout<D, FP4, NQ, DEEP>;
+    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas};
+}
+MaskedVariant masked_variant(int d, bool fp4, int nq, bool deep) {
+    if (fp4) return d == 64 ? variant_of<64, true, 1, true>() : d == 128 ? variant_of<128, true, 1, true>() : variant_of<256, true, 1, true>();
+    if (d == 256) return variant_of<256, false, 1, true>();
+    if (nq == 2) return variant_of<128, false, 2, true>();
+    if (d == 64) return deep ? variant_of<64, false, 1, true>() : variant_of<64, false, 1, false>();
+    return deep ? variant_of<128, false, 1, true>() : variant_of<128, false, 1, false>();
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 masked_encode_fn() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
+                                                         &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr) : nullptr;
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* at, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    auto fn = masked_encode_fn();
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn && fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(at), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Q [rows, Hq, d] bf16 as (element, head, row); box = 64 elements x G heads x wt rows.
+bool encode_q(CUtensorMap* map, const void* q, int rows, int hq, int d, int group, int wt) {
+    const cuuint64_t dims[] = {(cuuint64_t)d, (cuuint64_t)hq, (cuuint64_t)rows};
+    const cuuint64_t strides[] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * hq};
+    const cuuint32_t box[] = {64, (cuuint32_t)group, (cuuint32_t)wt};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// A pool as (element, slot, head, page).  bf16: box = 64 elements x one page's slots; NVFP4 codes: a 16-key unit, swizzled
+// 128/64/32 bytes for d = 256/128/64 (the row is d/2 bytes).
+bool encode_pool(CUtensorMap* map, const void* pool, bool fp4, const spec_attn_masked_problem& p) {
+    const cuuint64_t row = fp4 ? p.head_dim / 2 : p.head_dim * 2, ps = (cuuint64_t)p.page_size;
+    const cuuint64_t dims[] = {(cuuint64_t)(fp4 ? p.head_dim / 2 : p.head_dim), ps, (cuuint64_t)p.num_kv_heads,
+                               (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[] = {row, row * ps, (cuuint64_t)p.kv_page_stride};
+    const cuuint32_t box[] = {(cuuint32_t)(fp4 ? p.head_dim / 2 : 64), (cuuint32_t)(fp4 ? 16 : p.page_size), 1, 1};
+    const CUtensorMapSwizzle sw = !fp4 || p.head_dim == 256 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : p.head_dim == 128       ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                            : CU_TENSOR_MAP_SWIZZLE_32B;
+    return encode(map, fp4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, sw);
+}
+// A scale pool as (a head's scales, head, page); box = the d scales of a 16-key unit.
+bool encode_scales(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p) {
+    const cuuint64_t row = (cuuint64_t)p.page_size * p.head_dim / 16;
+    const cuuint64_t dims[] = {row, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[] = {row, (cuuint64_t)p.scale_page_stride};
+    const cuuint32_t box[] = {(cuuint32_t)p.head_dim, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 bool masked_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -109,8 +939,54 @@ bool masked_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t
 struct spec_attn_masked_plan {
     spec_attn_masked_problem prob;
     int device;
+    int num_sms;
+    int nq;
+    int wt;
+    int tiles;
+    int tiles_per_split;
+    int max_splits;
     float sm_scale;
+    size_t workspace_bytes;
+    spec_attn::MaskedVariant variant;
 };
+
+namespace {
+
+// Key tiles a split takes.
+int choose_tiles(const spec_attn_masked_problem& p, int64_t units, int rows, const spec_attn_masked_plan& plan) {
+    const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
+    const spec_attn::MaskedVariant deep = spec_attn::masked_variant(p.head_dim, fp4, plan.nq, true);
+    const spec_attn::MaskedVariant shared = spec_attn::masked_variant(p.head_dim, fp4, plan.nq, false);
+    const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
+    // Model (us): a CTA has a start and an end and a time for each tile of 64 keys (longer beside another CTA with many
+    // rows), splits the join behind them; the keys come from HBM at best at its rate.
+    const int group = p.num_q_heads / p.num_kv_heads;
+    const double cta_rows = std::min(rows, plan.nq * plan.wt) * group;
+    const double fixed = 3.0;
+    const bool whole = plan.nq == 2 || p.head_dim == 256 || fp4;
+    const double tile_alone = whole ? 0.8 : 0.43, tile_shared = whole ? 0.8 : (p.head_dim == 64 ? 0.3 : 0.45) * (1.0 + cta_rows / 128.0);
+    const double row_bytes = fp4 ? p.head_dim * 1.125 : p.head_dim * 4.0;
+    const double hbm = static_cast<double>(p.num_reqs) * units * 64 * p.num_kv_heads * row_bytes / 6.5e6;
+    double best = 1e300;
+    int64_t best_u = units < 1 ? 1 : units;
+    for (int64_t s = 1; s <= units && s <= 128; ++s) {
+        const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
+        if (splits < s) continue;                  // (as an earlier s)
+        const bool alone = ctas * splits <= plan.num_sms;
+        const spec_attn::MaskedVariant& v = alone ? deep : shared;
+        const int64_t waves = (ctas * splits + static_cast<int64_t>(plan.num_sms) * v.ctas - 1) / (static_cast<int64_t>(plan.num_sms) * v.ctas);
+        const double cta = fixed + static_cast<double>(u) * (alone ? tile_alone : tile_shared);
+        const double join = splits > 1 ? 2.5 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * p.head_dim * 4.0 / 5e6 : 0.0;
+        const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed) + join;
+        if (cost < best * 0.98) {
+            best = cost;
+            best_u = u;
+        }
+    }
+    return static_cast<int>(best_u);
+}
+
+}  // namespace
 
 extern "C" {
 
@@ -142,8 +1018,9 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
     auto bad_stride = [](int64_t stride, int64_t dense) { return stride != 0 && (stride < dense || stride % 16 != 0); };
     if (bad_stride(p.kv_page_stride, page) || (fp4 && bad_stride(p.scale_page_stride, scale_page)))
         return SPEC_ATTN_E_INVALID_ARG;
-    int dev = 0;
-    const cudaError_t e = cudaGetDevice(&dev);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return spec_attn::record_cuda_error(e);
     spec_attn_masked_plan* plan = new (std::nothrow) spec_attn_masked_plan();
     if (!plan) return SPEC_ATTN_E_INVALID_ARG;
@@ -152,8 +1029,45 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
     if (p.scale_page_stride == 0) plan->prob.scale_page_stride = scale_page;
     if (p.mask_row_words == 0) plan->prob.mask_row_words = words;
     plan->device = dev;
+    plan->num_sms = sms;
     plan->sm_scale = p.sm_scale > 0.f ? p.sm_scale : 1.0f / std::sqrt(static_cast<float>(p.head_dim));
-    if (workspace_bytes) *workspace_bytes = 256;
+    // bounds beyond the rows and pages there are (INT32_MAX for "any") size nothing
+    const int rows = std::max(1, std::min(p.max_w, p.total_q_rows));
+    const int64_t max_len = std::max<int64_t>(1, std::min(p.max_seq_len, static_cast<int64_t>(p.block_table_stride) * p.page_size));
+    plan->wt = 128 / (p.num_q_heads / p.num_kv_heads);
+    // Two query tiles a CTA read K and V once for both, but make half as many CTAs.
+    const int64_t one_tile = (static_cast<int64_t>(rows) + plan->wt - 1) / plan->wt * p.num_kv_heads * p.num_reqs;
+    plan->nq = p.head_dim == 128 && !fp4 && rows > plan->wt && one_tile > sms ? 2 : 1;
+    const int cta_rows = plan->nq * plan->wt;
+    plan->tiles = (rows - 1) / cta_rows + 1;
+    // most key tiles of a CTA (as span_of counts them)
+    int64_t pages = (max_len + p.page_size - 1) / p.page_size;
+    if (p.window_left > 0) {
+        const int64_t reach = static_cast<int64_t>(p.window_left) - 1 + (p.tree ? rows : std::min(rows, cta_rows));
+        pages = std::min(pages, (static_cast<int64_t>(p.sink_keys) + p.page_size - 1) / p.page_size + reach / p.page_size + 2);
+    }
+    const int64_t units = (pages * p.page_size + spec_attn::kBN - 1) / spec_attn::kBN;
+    for (const bool deep : {true, false}) {
+        const spec_attn::MaskedVariant v = spec_attn::masked_variant(p.head_dim, fp4, plan->nq, deep);
+        e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+        if (e != cudaSuccess) {
+            delete plan;
+            return spec_attn::record_cuda_error(e);
+        }
+    }
+    plan->tiles_per_split = p.force_splits > 0 ? static_cast<int>((units + p.force_splits - 1) / p.force_splits)
+                                               : choose_tiles(p, units, rows, *plan);
+    plan->max_splits = static_cast<int>((units - 1) / plan->tiles_per_split) + 1;
+    if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
+        delete plan;
+        return SPEC_ATTN_E_UNSUPPORTED;
+    }
+    plan->variant = spec_attn::masked_variant(
+        p.head_dim, fp4, plan->nq, static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms);
+    // partials: the pairs of every split, then their elements (a multiple of 256 bytes each)
+    const size_t pairs = static_cast<size_t>(plan->max_splits) * p.total_q_rows * p.num_q_heads;
+    plan->workspace_bytes = 256 + (plan->max_splits > 1 ? (pairs * 8 + 255) / 256 * 256 + pairs * p.head_dim * 2 : 0);
+    if (workspace_bytes) *workspace_bytes = plan->workspace_bytes;
     *out = plan;
     return SPEC_ATTN_OK;
 }
@@ -173,7 +1087,7 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     const spec_attn_masked_problem& p = plan->prob;
     const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
     if (!workspace || !masked_aligned(workspace, 256)) return SPEC_ATTN_E_INVALID_ARG;
-    if (workspace_bytes < 256) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
+    if (workspace_bytes < plan->workspace_bytes) return SPEC_ATTN_E_WORKSPACE_TOO_SMALL;
     if (p.num_reqs == 0 || p.total_q_rows == 0) return SPEC_ATTN_OK;
     if (!q || !o || !k_pool || !v_pool || (fp4 && (!k_scales || !v_scales)) || !seq_lens || !q_indptr ||
         (p.block_table_stride > 0 && !block_table) || (p.tree && !row_mask) || (p.tree && p.window_left > 0 && !positions))
@@ -188,7 +1102,7 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     const uint64_t keys = static_cast<uint64_t>(p.num_kv_heads) * p.page_size, pages = static_cast<uint64_t>(p.num_pages);
     const uint64_t page = keys * (fp4 ? p.head_dim / 2 : p.head_dim * 2), scale_page = fp4 ? keys * (p.head_dim / 16) : 0;
     const uint64_t step = static_cast<uint64_t>(p.kv_page_stride), scale_step = static_cast<uint64_t>(p.scale_page_stride);
-    const ByteRows out[] = {bytes_at(o, 2 * heads * p.head_dim), bytes_at(lse, 4 * heads), bytes_at(workspace, 256)};
+    const ByteRows out[] = {bytes_at(o, 2 * heads * p.head_dim), bytes_at(lse, 4 * heads), bytes_at(workspace, plan->workspace_bytes)};
     const ByteRows in[] = {bytes_at(q, 2 * heads * p.head_dim), {k_pool, page, step, pages}, {v_pool, page, step, pages},
                            {k_scales, scale_page, scale_step, pages}, {v_scales, scale_page, scale_step, pages},
                            bytes_at(block_table, reqs4 * p.block_table_stride), bytes_at(seq_lens, reqs4),
@@ -201,11 +1115,6 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     if (dev != plan->device) return SPEC_ATTN_E_INVALID_ARG;
 
     MaskedParams m = {};
-    m.q = static_cast<const uint16_t*>(q);
-    m.k_pool = static_cast<const unsigned char*>(k_pool);
-    m.v_pool = static_cast<const unsigned char*>(v_pool);
-    m.k_scales = static_cast<const uint8_t*>(k_scales);
-    m.v_scales = static_cast<const uint8_t*>(v_scales);
     m.block_table = block_table;
     m.seq_lens = seq_lens;
     m.q_indptr = q_indptr;
@@ -214,7 +1123,9 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     m.o = static_cast<uint16_t*>(o);
     m.lse = lse;
     m.status = static_cast<unsigned int*>(workspace);
-    m.num_reqs = p.num_reqs;
+    const size_t pairs = static_cast<size_t>(plan->max_splits) * rows * p.num_q_heads;
+    m.ws_ls = reinterpret_cast<float2*>(static_cast<unsigned char*>(workspace) + 256);
+    m.ws_o = reinterpret_cast<uint16_t*>(static_cast<unsigned char*>(workspace) + 256 + (pairs * 8 + 255) / 256 * 256);
     m.total_rows = p.total_q_rows;
     m.max_w = p.max_w;
     m.num_q_heads = p.num_q_heads;
@@ -227,28 +1138,58 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     m.window = p.window_left;
     m.sinks = p.sink_keys;
     m.mask_words = p.mask_row_words;
+    m.wt = plan->wt;
+    m.cta_rows = plan->nq * plan->wt;
+    m.tiles = plan->tiles;
+    m.tiles_per_split = plan->tiles_per_split;
+    m.max_splits = plan->max_splits;
+    // (one request, or all CTAs at once: nothing to order)
+    const int64_t ctas = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs;
+    m.longest_first = p.num_reqs > 1 && p.num_reqs <= kMaxSorted &&
+                              ctas > static_cast<int64_t>(plan->num_sms) * plan->variant.ctas
+                          ? p.num_reqs
+                          : 0;
     m.max_seq_len = p.max_seq_len;
-    m.kv_page_stride = p.kv_page_stride;
-    m.scale_page_stride = p.scale_page_stride;
     m.score_scale_log2 = plan->sm_scale * 1.4426950408889634f * (fp4 ? k_gscale : 1.f);
     m.out_scale = fp4 ? v_gscale : 1.f;
-    void (*kernel)(const MaskedParams) = nullptr;
-    if (p.head_dim == 64) kernel = fp4 ? &masked_attn_kernel<64, true> : &masked_attn_kernel<64, false>;
-    if (p.head_dim == 128) kernel = fp4 ? &masked_attn_kernel<128, true> : &masked_attn_kernel<128, false>;
-    if (p.head_dim == 256) kernel = fp4 ? &masked_attn_kernel<256, true> : &masked_attn_kernel<256, false>;
-    const int64_t per_req = static_cast<int64_t>(std::min(p.max_w, p.total_q_rows)) * m.group;
+
+    CUtensorMap maps[5] = {};
+    auto encode_all = [&] {
+        return encode_q(&maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim, m.group, plan->wt) &&
+               encode_pool(&maps[1], k_pool, fp4, p) && encode_pool(&maps[2], v_pool, fp4, p) &&
+               (!fp4 || (encode_scales(&maps[3], k_scales, p) && encode_scales(&maps[4], v_scales, p)));
+    };
+    if (!encode_all()) {
+        // a thread's first CUDA call has no context to encode in yet: bind the device's and try once more
+        e = cudaSetDevice(dev);
+        if (e != cudaSuccess) return record_cuda_error(e);
+        if (!encode_all()) return SPEC_ATTN_E_INVALID_ARG;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((per_req + 3) / 4), static_cast<unsigned>(p.num_kv_heads),
+    cfg.gridDim = dim3(static_cast<unsigned>(plan->tiles * plan->max_splits), static_cast<unsigned>(p.num_kv_heads),
                        static_cast<unsigned>(p.num_reqs));
-    cfg.blockDim = dim3(128);
+    cfg.blockDim = dim3(static_cast<unsigned>(plan->variant.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(plan->variant.smem);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, m);
-    return e == cudaSuccess ? SPEC_ATTN_OK : record_cuda_error(e);
+    e = cudaLaunchKernelEx(&cfg, plan->variant.kernel, m, maps[0], maps[1], maps[2], maps[3], maps[4]);
+    if (e != cudaSuccess) return record_cuda_error(e);
+    if (plan->max_splits > 1) {
+        const JoinKernel join = p.head_dim == 64    ? &masked_join_kernel<64>
+                                : p.head_dim == 128 ? &masked_join_kernel<128>
+                                                    : &masked_join_kernel<256>;
+        const int64_t pieces = static_cast<int64_t>(std::min(p.max_w, p.total_q_rows)) * p.num_q_heads * (p.head_dim / 8);
+        cfg.gridDim = dim3(static_cast<unsigned>((pieces + 255) / 256), static_cast<unsigned>(p.num_reqs));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, join, m);
+        if (e != cudaSuccess) return record_cuda_error(e);
+    }
+    return SPEC_ATTN_OK;
 }
 
 }  // extern "C"
