@@ -175,6 +175,14 @@ struct MaskedLayout {
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
     static constexpr int kAux = 2048;
     static constexpr int kCtas = DEEP ? 1 : 2;
+    // Layout of a bf16 tile.  Boxes of one 16-key unit with all its chunks (4 KB at d = 128, 8 KB at d = 256) keep the copy
+    // engine's few boxes in flight large: unit-major, [unit][chunk][16 keys][128 bytes].  V is read that way as it is.
+    // K's 8-key groups then have no one stride from unit to unit, so S is made by two products of 32 columns, of the
+    // first and of the second 8 keys of each unit; with two query tiles, whose first product is slow at 32 columns, K
+    // comes chunk by chunk instead, [chunk][64 keys][128 bytes], as decoded tiles are.
+    static constexpr bool kUnitK = !FP4 && NQ == 1 && D > 64;
+    static constexpr bool kUnitV = !FP4;
+    static constexpr int kUnit = 16 * D * 2;
     static constexpr bool kQT = NQ == 1 && DEEP;           // the query tile in tensor memory
     // S buffers of a tile (a power of two); with four, S_{t+1} does not wait for P V of tile t - 1
     static constexpr int kBufShift = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
@@ -441,18 +449,21 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 // (the query tile has to leave the last two slots first)
                 if (L::kQT && n == RING - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
                 turn(k);
-                const int np = min(per_tile, pages - k);
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(NQ * np * L::kChunks * (128 << shift)));
-                // a box a lane: page pp of the tile, 64-element chunk c; NQ = 2: K by the first half of the warp, V by the other
-                const int pp = (lane & 15) / L::kChunks, c = lane % L::kChunks;
-                const int page = __shfl_sync(kFullMask, cur, (k & 31) + min(pp, per_tile - 1));
+                const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
+                if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(NQ * units * L::kUnit));
+                // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K; NQ = 2: K by the
+                // first half of the warp, V by the other
                 const bool is_v = NQ == 2 ? lane >= 16 : (n & 1) != 0;
+                const bool whole = is_v || L::kUnitK;
+                const int pp = whole ? lane & 15 : (lane & 15) / L::kChunks, c = lane % L::kChunks;
+                const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16;
+                const int page = __shfl_sync(kFullMask, cur, (k & 31) + (min(pp, 3) >> (shift - 4)));
                 __syncwarp();
-                if (pp < np && (NQ == 2 || lane < 16))
-                    tma_load_4d(ring + slot * L::kSlotBytes + (NQ == 2 && is_v ? L::kTileBytes : 0) + c * (kBN * 128) +
-                                    pp * (128 << shift),
-                                is_v ? &tmv : &tmk, c * 64, 0, kvh, page, &aux->full[slot]);
+                if (pp < units && (NQ == 2 || lane < 16)) {
+                    unsigned char* dst = ring + slot * L::kSlotBytes + (NQ == 2 && is_v ? L::kTileBytes : 0);
+                    if (whole) tma_load_5d(dst + pp * L::kUnit, is_v ? &tmv : &tmk, 0, sub, 0, kvh, page, &aux->full[slot]);
+                    else tma_load_4d(dst + c * (kBN * 128) + pp * 2048, &tmk, c * 64, sub, kvh, page, &aux->full[slot]);
+                }
                 __syncwarp();
                 issued = n + 1;
             }
@@ -467,11 +478,15 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     } else if (warp == 1 || (warp == 2 && (NQ == 1 || nact == 2))) {
         // ------------------------------------------------------------ products
         const uint32_t go = elected();
-        constexpr uint32_t idesc_s = FP4 ? idesc_f16_f32(kM, kBN, 0, 0) : idesc_bf16_f32(kM, kBN, 0, 0);
+        constexpr int kN = L::kUnitK ? kBN / 2 : kBN;      // columns of a product of S
+        constexpr uint32_t idesc_s = FP4 ? idesc_f16_f32(kM, kN, 0, 0) : idesc_bf16_f32(kM, kN, 0, 0);
+        constexpr uint32_t k_hi = L::kUnitK ? (L::kUnit >> 4 | (kDescHi & ~0x3FFFu)) : kDescHi;   // (8-key groups a unit apart)
+        constexpr int kChunkStep = (L::kUnitK ? 2048 : kBN * 128) >> 4;
+        constexpr int kVStep = (L::kUnitV ? L::kUnit : 2048) >> 4;                     // 16 keys of V further
         constexpr uint32_t idesc_o = FP4 ? idesc_f16_f32(kM, D, 0, 1) : idesc_bf16_f32(kM, D, 0, 1);
         const int i = NQ == 2 ? warp - 1 : 0;
         const uint32_t q_lo = desc_lo(smem_addr(sQ + i * L::kQBytes), 16);
-        const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), kBN * 128);
+        const uint32_t k_lo0 = desc_lo(smem_addr(ring), 16), v_lo0 = desc_lo(smem_addr(ring), L::kUnitV ? 2048 : kBN * 128);
         auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, abort); };
         // the ring slots of K_t and V_t, and the slot t mod kPv, stepped along with the parity of their phase
         struct Step {
@@ -499,9 +514,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t k_at = k_lo + (kk >> 2) * (kBN * 128 >> 4) + (kk & 3) * 2;
-                if (L::kQT) mma_ts_lo(d_tmem, tmem + L::kQCol + kk * 8, k_at, idesc_s, kk > 0, go);
-                else mma_ss_lo(d_tmem, q_lo + (kk >> 2) * (kM * 128 >> 4) + (kk & 3) * 2, k_at, idesc_s, kk > 0, go);
+#pragma unroll
+                for (int h = 0; h < kBN / kN; ++h) {
+                    const uint32_t k_at = k_lo + (kk >> 2) * kChunkStep + (kk & 3) * 2 + h * (1024 >> 4), to = d_tmem + h * kN;
+                    if (L::kQT) mma_ts_lo(to, tmem + L::kQCol + kk * 8, k_at, idesc_s, kk > 0, go, k_hi);
+                    else mma_ss_lo(to, q_lo + (kk >> 2) * (kM * 128 >> 4) + (kk & 3) * 2, k_at, idesc_s, kk > 0, go, k_hi);
+                }
             }
             commit_if(&aux->s_full[i][b], go);
             if (NQ == 1) commit_if(&aux->empty[ks.slot], go);
@@ -519,7 +537,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             const int steps = t == T - 1 ? last_steps : kBN / 16;
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-                if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * (2048 >> 4), idesc_o, t > 0 || kk > 0, go);
+                if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * kVStep, idesc_o, t > 0 || kk > 0, go);
             commit_if(&aux->pv_done[i][done.slot], go);
             if (NQ == 1) commit_if(&aux->empty[vs.slot], go);
             vs.by(NQ == 1 ? 2 : 1);
@@ -645,10 +663,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
             if (live) {
                 __syncwarp();
-                float sv[kBN];
-                tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sv));
-                tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
+                float sx[kBN], sv[kBN];
+                tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sx));
+                tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sx + 32));
                 tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < kBN; ++c) sv[c] = sx[L::kUnitK ? (c >> 4) * 8 + (c & 7) + (c >> 3 & 1) * 32 : c];
                 if (masked) {
                     const uint32_t s0 = static_cast<uint32_t>(sees), s1 = static_cast<uint32_t>(sees >> 32);
 #pragma unroll
@@ -720,7 +740,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                     const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
                     for (int u = m; u < kBN * C8; u += 128)
                         if ((dead >> (u / C8)) & 1)
-                            st_shared_v4(v_addr + ((u % C8) >> 3) * (kBN * 128) + (u / C8) * 128 + (u & 7) * 16,
+                            st_shared_v4(v_addr + (u / C8 >> 4) * L::kUnit + ((u % C8) >> 3) * 2048 + (u / C8 & 15) * 128 + (u & 7) * 16,
                                          make_uint4(0u, 0u, 0u, 0u));
                     fence_proxy_async_smem();
                 }
@@ -867,11 +887,12 @@ using JoinKernel = void (*)(const MaskedParams);
 struct MaskedVariant {
     MaskedKernel kernel;
     int threads, smem, ctas;   // ctas: on one SM
+    bool whole_k;              // K comes in units with all their chunks
 };
 template <int D, bool FP4, int NQ, bool DEEP>
 MaskedVariant variant_of() {
     using L = MaskedLayout<D, FP4, NQ, DEEP>;
-    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas};
+    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kUnitK};
 }
 MaskedVariant masked_variant(int d, bool fp4, int nq, bool deep) {
     if (fp4) return d == 64 ? variant_of<64, true, 1, true>() : d == 128 ? variant_of<128, true, 1, true>() : variant_of<256, true, 1, true>();
@@ -896,7 +917,7 @@ PFN_cuTensorMapEncodeTiled_v12000 masked_encode_fn() {
 bool encode(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* at, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
     auto fn = masked_encode_fn();
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     return fn && fn(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(at), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -909,14 +930,22 @@ bool encode_q(CUtensorMap* map, const void* q, int rows, int hq, int d, int grou
     const cuuint32_t box[] = {64, (cuuint32_t)group, (cuuint32_t)wt};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// A pool as (element, slot, head, page).  bf16: box = 64 elements x one page's slots; NVFP4 codes: a 16-key unit, swizzled
+// A bf16 pool as (64 elements, slot, 64-element chunk, head, page); box = 16 keys of a head with all their chunks.
+bool encode_units(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p) {
+    const cuuint64_t row = (cuuint64_t)p.head_dim * 2, ps = (cuuint64_t)p.page_size, chunks = (cuuint64_t)p.head_dim / 64;
+    const cuuint64_t dims[] = {64, ps, chunks, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[] = {row, 128, row * ps, (cuuint64_t)p.kv_page_stride};
+    const cuuint32_t box[] = {64, 16, (cuuint32_t)chunks, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// A pool as (element, slot, head, page); box = 16 keys of a head, bf16: 64 elements of them, NVFP4: their codes, swizzled
 // 128/64/32 bytes for d = 256/128/64 (the row is d/2 bytes).
 bool encode_pool(CUtensorMap* map, const void* pool, bool fp4, const spec_attn_masked_problem& p) {
     const cuuint64_t row = fp4 ? p.head_dim / 2 : p.head_dim * 2, ps = (cuuint64_t)p.page_size;
     const cuuint64_t dims[] = {(cuuint64_t)(fp4 ? p.head_dim / 2 : p.head_dim), ps, (cuuint64_t)p.num_kv_heads,
                                (cuuint64_t)p.num_pages};
     const cuuint64_t strides[] = {row, row * ps, (cuuint64_t)p.kv_page_stride};
-    const cuuint32_t box[] = {(cuuint32_t)(fp4 ? p.head_dim / 2 : 64), (cuuint32_t)(fp4 ? 16 : p.page_size), 1, 1};
+    const cuuint32_t box[] = {(cuuint32_t)(fp4 ? p.head_dim / 2 : 64), 16, 1, 1};
     const CUtensorMapSwizzle sw = !fp4 || p.head_dim == 256 ? CU_TENSOR_MAP_SWIZZLE_128B
                                   : p.head_dim == 128       ? CU_TENSOR_MAP_SWIZZLE_64B
                                                             : CU_TENSOR_MAP_SWIZZLE_32B;
@@ -1156,7 +1185,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     CUtensorMap maps[5] = {};
     auto encode_all = [&] {
         return encode_q(&maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim, m.group, plan->wt) &&
-               encode_pool(&maps[1], k_pool, fp4, p) && encode_pool(&maps[2], v_pool, fp4, p) &&
+               (fp4 || !plan->variant.whole_k ? encode_pool(&maps[1], k_pool, fp4, p) : encode_units(&maps[1], k_pool, p)) &&
+               (fp4 ? encode_pool(&maps[2], v_pool, fp4, p) : encode_units(&maps[2], v_pool, p)) &&
                (!fp4 || (encode_scales(&maps[3], k_scales, p) && encode_scales(&maps[4], v_scales, p)));
     };
     if (!encode_all()) {

@@ -59,27 +59,28 @@ constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row 
 // predicate: the whole warp runs the issuing loop and its waits.  (With the loop
 // in a branch of one thread, each wait cost the next product 200 clocks: 8 + 4
 // instructions with a wait before each kind took 1053 clocks, and 621 like this.)
+// `b_hi`: the high word of B's descriptor.
 __device__ __forceinline__ void mma_ss_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate,
-                                          uint32_t go) {
+                                          uint32_t go, uint32_t b_hi = kDescHi) {
     asm volatile(
         "{\n\t.reg .pred p, g;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 g, %6, 0;\n\t"
         "mov.b64 a, {%1, %5};\n\t"
-        "mov.b64 b, {%2, %5};\n\t"
+        "mov.b64 b, {%2, %7};\n\t"
         "@g tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go)
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go), "r"(b_hi)
         : "memory");
 }
 __device__ __forceinline__ void mma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate,
-                                          uint32_t go) {
+                                          uint32_t go, uint32_t b_hi = kDescHi) {
     asm volatile(
         "{\n\t.reg .pred p, g;\n\t.reg .b64 b;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
         "setp.ne.b32 g, %6, 0;\n\t"
         "mov.b64 b, {%2, %5};\n\t"
         "@g tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(kDescHi), "r"(go)
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1 : 0), "r"(b_hi), "r"(go)
         : "memory");
 }
 __device__ __forceinline__ void commit_if(uint64_t* bar, uint32_t go) {
