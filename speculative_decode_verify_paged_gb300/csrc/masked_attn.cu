@@ -24,13 +24,13 @@
 // NaN); masked scores are replaced, so K may hold anything there.
 //
 // Warp roles:
-//   warp 0      the query tiles, then K and V tiles in turn, by TMA into one ring of
-//               slots: a box of 64 elements x one page's keys each, 128-byte swizzle.
-//               NVFP4: codes and scales into a raw ring.
+//   warp 0      the query tiles, then the K tiles, by TMA into one ring of slots with
+//               the V tiles of warp 3, 128-byte swizzle.  NVFP4: codes and scales into a
+//               raw ring.
 //   warps 1, 2  issue the products, one elected thread each.  NQ = 2: warp 1 + i
 //               issues S_{t+1} and then P_t V_t of tile i.  NQ = 1: warp 1 issues
 //               S = Q K^T and warp 2 O += P V.
-//   warp 3      owns tensor memory.
+//   warp 3      owns tensor memory; the V tiles.
 //   warps 4-7 (and 8-11 for the second tile)   softmax, a row a thread, and epilogue.
 //   NVFP4: warps 8-11 decode K and 12-15 V into fp16 operand tiles of the same ring;
 //               query rows and weights are fp16 too.
@@ -292,11 +292,11 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < RING; ++s) {
-            mbar_init(&aux->full[s], FP4 ? 4 : 1);
+            mbar_init(&aux->full[s], FP4 ? 4 : NQ);
             mbar_init(&aux->empty[s], 1);
         }
         for (int s = 0; s < L::kRaw; ++s) {
-            mbar_init(&aux->raw_full[s], 1);
+            mbar_init(&aux->raw_full[s], 2);
             mbar_init(&aux->raw_empty[s], 8);
         }
         for (int i = 0; i < NQ; ++i) {
@@ -380,10 +380,11 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     float* stage_lse = stage + NQ * kM * L::kRowFloats;
     float* stage_max = stage_lse + NQ * kM;
 
-    if (warp == 0) {
-        // ------------------------------------------------------------ copies
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------ copies: K by warp 0, V by warp 3
+        const bool is_v = warp == 3;
         int issued = 0;
-        if (lane == 0) {
+        if (warp == 0 && lane == 0) {
             const uint32_t qbytes = static_cast<uint32_t>(L::kChunks * 128 * G * p.wt);
             for (int i = 0; i < nact; ++i) {
                 mbar_arrive_expect_tx(&aux->q_full[i], qbytes);
@@ -421,24 +422,21 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 turn(k);
                 const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
                 uint64_t* bar = &aux->raw_full[slot];
-                if (lane == 0)
-                    mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * 2 * (R::kCodes + R::kScaleBox)));
-                const int pp = (lane >> 2) & 3, kind = lane & 3, sub = pp & ((1 << (shift - 4)) - 1);
+                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * (R::kCodes + R::kScaleBox)));
+                const int pp = (lane >> 1) & 3, sub = pp & ((1 << (shift - 4)) - 1);
                 const int page = __shfl_sync(kFullMask, cur, (k & 31) + (pp >> (shift - 4)));
                 __syncwarp();
-                if (lane < 4 * units) {
-                    unsigned char* dst = raw + slot * R::kSlot;
-                    if (kind == 0) tma_load_4d(dst + pp * R::kCodes, &tmk, 0, sub * 16, kvh, page, bar);
-                    else if (kind == 1) tma_load_4d(dst + R::kVC + pp * R::kCodes, &tmv, 0, sub * 16, kvh, page, bar);
-                    else if (kind == 2) tma_load_3d(dst + R::kKS + pp * R::kScales, &tmks, sub * D, kvh, page, bar);
-                    else tma_load_3d(dst + R::kVS + pp * R::kScales, &tmvs, sub * D, kvh, page, bar);
+                if (lane < 2 * units) {
+                    unsigned char* dst = raw + slot * R::kSlot + (is_v ? R::kVC : 0);
+                    if (lane & 1) tma_load_3d(dst + R::kKS + pp * R::kScales, is_v ? &tmvs : &tmks, sub * D, kvh, page, bar);
+                    else tma_load_4d(dst + pp * R::kCodes, is_v ? &tmv : &tmk, 0, sub * 16, kvh, page, bar);
                 }
                 __syncwarp();
                 issued = t + 1;
             }
         } else {
-            for (int n = 0; n < (NQ == 2 ? T : 2 * T); ++n) {
-                const int slot = n % RING, k = (NQ == 2 ? n : n >> 1) * per_tile;
+            for (int t = 0; t < T; ++t) {
+                const int n = NQ == 2 ? t : 2 * t + is_v, slot = n % RING, k = t * per_tile;
                 const uint32_t gone = ((n / RING) - 1) & 1;
                 if (n >= RING) {
                     if (NQ == 1 && !wait_warp(&aux->empty[slot], gone, abort)) break;
@@ -447,31 +445,33 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                         break;
                 }
                 // (the query tile has to leave the last two slots first)
-                if (L::kQT && n == RING - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
+                if (L::kQT && n >= RING - 2 && n < RING && !wait_warp(&aux->q_ready, 0, abort)) break;
                 turn(k);
                 const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
-                if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(NQ * units * L::kUnit));
-                // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K; NQ = 2: K by the
-                // first half of the warp, V by the other
-                const bool is_v = NQ == 2 ? lane >= 16 : (n & 1) != 0;
+                if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(units * L::kUnit));
+                // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K
                 const bool whole = is_v || L::kUnitK;
-                const int pp = whole ? lane & 15 : (lane & 15) / L::kChunks, c = lane % L::kChunks;
+                const int pp = whole ? lane : lane / L::kChunks, c = lane % L::kChunks;
                 const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16;
                 const int page = __shfl_sync(kFullMask, cur, (k & 31) + (min(pp, 3) >> (shift - 4)));
                 __syncwarp();
-                if (pp < units && (NQ == 2 || lane < 16)) {
+                if (pp < units) {
                     unsigned char* dst = ring + slot * L::kSlotBytes + (NQ == 2 && is_v ? L::kTileBytes : 0);
                     if (whole) tma_load_5d(dst + pp * L::kUnit, is_v ? &tmv : &tmk, 0, sub, 0, kvh, page, &aux->full[slot]);
                     else tma_load_4d(dst + c * (kBN * 128) + pp * 2048, &tmk, c * 64, sub, kvh, page, &aux->full[slot]);
                 }
                 __syncwarp();
-                issued = n + 1;
+                issued = t + 1;
             }
         }
         if (*abort && lane == 0) {
-            if (FP4) drain_copies<FP4 ? L::kRaw : 1>(aux->raw_full, issued);
-            else drain_copies<RING>(aux->full, issued);
+            // every copy in flight lands before the CTA's shared memory goes away
             volatile int no_abort = 0;
+            constexpr int kAhead = FP4 ? L::kRaw : RING;
+            for (int t = max(0, issued - kAhead); t < issued; ++t) {
+                const int n = FP4 || NQ == 2 ? t : 2 * t + is_v;
+                mbar_wait(FP4 ? &aux->raw_full[n % kAhead] : &aux->full[n % kAhead], (n / kAhead) & 1, &no_abort, kDrainLimit);
+            }
             for (int i = 0; i < nact; ++i) mbar_wait(&aux->q_full[i], 0, &no_abort, kDrainLimit);
         }
         __syncwarp();
