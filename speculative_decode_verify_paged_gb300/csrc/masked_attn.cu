@@ -180,7 +180,8 @@ struct MaskedLayout {
     // K's 8-key groups then have no one stride from unit to unit, so S is made by two products of 32 columns, of the
     // first and of the second 8 keys of each unit; with two query tiles, whose first product is slow at 32 columns, K
     // comes chunk by chunk instead, [chunk][64 keys][128 bytes], as decoded tiles are.
-    static constexpr bool kUnitK = !FP4 && NQ == 1 && D > 64;
+    static constexpr bool kUnitK = !FP4 && NQ == 1 && D == 128;
+    static constexpr bool kEightK = !FP4 && D == 256;
     static constexpr bool kUnitV = !FP4;
     static constexpr int kUnit = 16 * D * 2;
     static constexpr bool kQT = NQ == 1 && DEEP;           // the query tile in tensor memory
@@ -450,14 +451,15 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
                 if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(units * L::kUnit));
                 // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K
-                const bool whole = is_v || L::kUnitK;
-                const int pp = whole ? lane : lane / L::kChunks, c = lane % L::kChunks;
-                const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16;
+                const bool whole = is_v || L::kUnitK || L::kEightK;
+                const int halves = !is_v && L::kEightK ? 1 : 0;
+                const int box = whole ? lane : lane / L::kChunks, c = lane % L::kChunks, pp = box >> halves;
+                const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16 + (box & halves) * 8;
                 const int page = __shfl_sync(kFullMask, cur, (k & 31) + (min(pp, 3) >> (shift - 4)));
                 __syncwarp();
                 if (pp < units) {
                     unsigned char* dst = ring + slot * L::kSlotBytes + (NQ == 2 && is_v ? L::kTileBytes : 0);
-                    if (whole) tma_load_5d(dst + pp * L::kUnit, is_v ? &tmv : &tmk, 0, sub, 0, kvh, page, &aux->full[slot]);
+                    if (whole) tma_load_5d(dst + box * (L::kUnit >> halves), is_v ? &tmv : &tmk, 0, sub, 0, kvh, page, &aux->full[slot]);
                     else tma_load_4d(dst + c * (kBN * 128) + pp * 2048, &tmk, c * 64, sub, kvh, page, &aux->full[slot]);
                 }
                 __syncwarp();
@@ -480,8 +482,9 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         const uint32_t go = elected();
         constexpr int kN = L::kUnitK ? kBN / 2 : kBN;      // columns of a product of S
         constexpr uint32_t idesc_s = FP4 ? idesc_f16_f32(kM, kN, 0, 0) : idesc_bf16_f32(kM, kN, 0, 0);
-        constexpr uint32_t k_hi = L::kUnitK ? (L::kUnit >> 4 | (kDescHi & ~0x3FFFu)) : kDescHi;   // (8-key groups a unit apart)
-        constexpr int kChunkStep = (L::kUnitK ? 2048 : kBN * 128) >> 4;
+        constexpr int kGroup = L::kUnitK ? L::kUnit : L::kEightK ? L::kUnit / 2 : 1024;   // from an 8-key group of K to the next
+        constexpr uint32_t k_hi = kGroup >> 4 | (kDescHi & ~0x3FFFu);
+        constexpr int kChunkStep = (L::kUnitK ? 2048 : L::kEightK ? 1024 : kBN * 128) >> 4;
         constexpr int kVStep = (L::kUnitV ? L::kUnit : 2048) >> 4;                     // 16 keys of V further
         constexpr uint32_t idesc_o = FP4 ? idesc_f16_f32(kM, D, 0, 1) : idesc_bf16_f32(kM, D, 0, 1);
         const int i = NQ == 2 ? warp - 1 : 0;
@@ -887,12 +890,12 @@ using JoinKernel = void (*)(const MaskedParams);
 struct MaskedVariant {
     MaskedKernel kernel;
     int threads, smem, ctas;   // ctas: on one SM
-    bool whole_k;              // K comes in units with all their chunks
+    int whole_k;               // keys of a copy of K with all its chunks, 0: chunk by chunk
 };
 template <int D, bool FP4, int NQ, bool DEEP>
 MaskedVariant variant_of() {
     using L = MaskedLayout<D, FP4, NQ, DEEP>;
-    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kUnitK};
+    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kUnitK ? 16 : L::kEightK ? 8 : 0};
 }
 MaskedVariant masked_variant(int d, bool fp4, int nq, bool deep) {
     if (fp4) return d == 64 ? variant_of<64, true, 1, true>() : d == 128 ? variant_of<128, true, 1, true>() : variant_of<256, true, 1, true>();
@@ -931,11 +934,11 @@ bool encode_q(CUtensorMap* map, const void* q, int rows, int hq, int d, int grou
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // A bf16 pool as (64 elements, slot, 64-element chunk, head, page); box = 16 keys of a head with all their chunks.
-bool encode_units(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p) {
+bool encode_units(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p, int keys) {
     const cuuint64_t row = (cuuint64_t)p.head_dim * 2, ps = (cuuint64_t)p.page_size, chunks = (cuuint64_t)p.head_dim / 64;
     const cuuint64_t dims[] = {64, ps, chunks, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
     const cuuint64_t strides[] = {row, 128, row * ps, (cuuint64_t)p.kv_page_stride};
-    const cuuint32_t box[] = {64, 16, (cuuint32_t)chunks, 1, 1};
+    const cuuint32_t box[] = {64, (cuuint32_t)keys, (cuuint32_t)chunks, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // A pool as (element, slot, head, page); box = 16 keys of a head, bf16: 64 elements of them, NVFP4: their codes, swizzled
@@ -1185,8 +1188,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     CUtensorMap maps[5] = {};
     auto encode_all = [&] {
         return encode_q(&maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim, m.group, plan->wt) &&
-               (fp4 || !plan->variant.whole_k ? encode_pool(&maps[1], k_pool, fp4, p) : encode_units(&maps[1], k_pool, p)) &&
-               (fp4 ? encode_pool(&maps[2], v_pool, fp4, p) : encode_units(&maps[2], v_pool, p)) &&
+               (fp4 || !plan->variant.whole_k ? encode_pool(&maps[1], k_pool, fp4, p) : encode_units(&maps[1], k_pool, p, plan->variant.whole_k)) &&
+               (fp4 ? encode_pool(&maps[2], v_pool, fp4, p) : encode_units(&maps[2], v_pool, p, 16)) &&
                (!fp4 || (encode_scales(&maps[3], k_scales, p) && encode_scales(&maps[4], v_scales, p)));
     };
     if (!encode_all()) {
