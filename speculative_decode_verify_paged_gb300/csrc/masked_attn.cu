@@ -194,21 +194,24 @@ struct MaskedLayout {
     static_assert(kNeed <= 512 && kCols * kCtas <= 512, "tensor memory");
     // first column of buffer b of tile i
     __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (kBufs * i + b) * kBN; }
-    // The ring.  NQ = 1: a slot a tile, K_t and V_t in turn, each let go as soon as it has been read.  NQ = 2: a slot holds
-    // K_t and V_t, filled and let go together.  A query tile bound for tensor memory lands in the last two slots.
+    // The ring.  NQ = 1: a slot a tile, each let go as soon as it has been read, the first kRingK slots for K and the rest
+    // for V (their producers run apart: a slot that both filled in turn could be a phase further than the one that waits
+    // for it can tell).  NQ = 2: a slot holds K_t and V_t, filled and let go together.  A query tile bound for tensor memory
+    // lands in the last two V slots.
     static constexpr int kSlotBytes = NQ * kTileBytes;
     static constexpr int kQSmem = kQT ? 0 : NQ * kQBytes;
     static constexpr int kMax = DEEP ? 232448 : 232448 / 2 - 1024;   // 227 KB a CTA, 228 KB an SM (1 KB of each CTA reserved)
     static constexpr int kFit = (kMax - 1024 - kAux - kQSmem) / kSlotBytes;
     static constexpr int kRing = FP4 ? (D == 256 ? 4 : 6) : kFit > kMaxRing ? kMaxRing : kFit;
     static_assert(kRing >= 4, "tiles ahead of the ones in use");
+    static constexpr int kRingK = NQ == 2 ? kRing : (kRing + 1) / 2, kRingV = NQ == 2 ? kRing : kRing / 2;
+    __host__ __device__ static constexpr int k_slot(int t) { return t % kRingK; }
+    __host__ __device__ static constexpr int v_slot(int t) { return NQ == 2 ? t % kRing : kRingK + t % kRingV; }
     static constexpr int kRawFit = (kMax - 1024 - kAux - kRing * kTileBytes) / MaskedRaw<D>::kSlot;
     static constexpr int kRaw = !FP4 ? 0 : kRawFit > kMaxRaw ? kMaxRaw : kRawFit;
     static constexpr int kTail = kRing * kSlotBytes + kRaw * MaskedRaw<D>::kSlot;   // ring and raw ring, adjacent
     static constexpr int kSmem = 1024 + kAux + kQSmem + kTail;
-    // S may lead P V by as many tiles as it has buffers.  An odd ring puts K_t where V of tile t - (ring + 1) / 2 was, and
-    // that V has to be gone before its slot's next phase is waited for.
-    static constexpr int kLead = (NQ == 2 || kBufs <= (kRing + 1) / 2) ? kBufs : (kRing + 1) / 2;
+    static constexpr int kLead = kBufs;                    // tiles by which S leads P V at most
     // P V barriers in use: one a slot (NQ = 2), or one an S buffer and at least four
     static constexpr int kPv = NQ == 2 ? kRing : 4;
     // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), their log2 sums and largest elements
@@ -437,16 +440,16 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             }
         } else {
             for (int t = 0; t < T; ++t) {
-                const int n = NQ == 2 ? t : 2 * t + is_v, slot = n % RING, k = t * per_tile;
-                const uint32_t gone = ((n / RING) - 1) & 1;
-                if (n >= RING) {
+                const int slot = is_v ? L::v_slot(t) : L::k_slot(t), lap = t / (is_v ? L::kRingV : L::kRingK), k = t * per_tile;
+                const uint32_t gone = (lap - 1) & 1;
+                if (lap > 0) {
                     if (NQ == 1 && !wait_warp(&aux->empty[slot], gone, abort)) break;
                     if (NQ == 2 && !(wait_warp(&aux->pv_done[0][slot], gone, abort) &&
                                      (nact == 1 || wait_warp(&aux->pv_done[1][slot], gone, abort))))
                         break;
                 }
                 // (the query tile has to leave the last two slots first)
-                if (L::kQT && n >= RING - 2 && n < RING && !wait_warp(&aux->q_ready, 0, abort)) break;
+                if (L::kQT && is_v && t == L::kRingV - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
                 turn(k);
                 const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
                 if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(units * L::kUnit));
@@ -469,11 +472,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         if (*abort && lane == 0) {
             // every copy in flight lands before the CTA's shared memory goes away
             volatile int no_abort = 0;
-            constexpr int kAhead = FP4 ? L::kRaw : RING;
-            for (int t = max(0, issued - kAhead); t < issued; ++t) {
-                const int n = FP4 || NQ == 2 ? t : 2 * t + is_v;
-                mbar_wait(FP4 ? &aux->raw_full[n % kAhead] : &aux->full[n % kAhead], (n / kAhead) & 1, &no_abort, kDrainLimit);
-            }
+            const int ahead = FP4 ? L::kRaw : is_v ? L::kRingV : L::kRingK;
+            for (int t = max(0, issued - ahead); t < issued; ++t)
+                mbar_wait(FP4 ? &aux->raw_full[t % ahead] : &aux->full[is_v ? L::v_slot(t) : L::k_slot(t)], (t / ahead) & 1,
+                          &no_abort, kDrainLimit);
             for (int i = 0; i < nact; ++i) mbar_wait(&aux->q_full[i], 0, &no_abort, kDrainLimit);
         }
         __syncwarp();
@@ -493,24 +495,23 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, abort); };
         // the ring slots of K_t and V_t, and the slot t mod kPv, stepped along with the parity of their phase
         struct Step {
-            int size, slot;
+            int first, end, slot;
             uint32_t par;
-            __device__ __forceinline__ void by(int n) {
-                slot += n;
-                if (slot >= size) {
-                    slot -= size;
+            __device__ __forceinline__ void next() {
+                if (++slot == end) {
+                    slot = first;
                     par ^= 1;
                 }
             }
         };
-        Step ks = {RING, 0, 0}, vs = {RING, NQ == 1 ? 1 : 0, 0};
-        Step done = {PV, 0, 0}, before = {PV, 0, 0};   // (before: t - lead of the next S)
+        Step ks = {0, L::kRingK, 0, 0}, vs = {L::v_slot(0), L::v_slot(0) + L::kRingV, L::v_slot(0), 0};
+        Step done = {0, PV, 0, 0}, before = {0, PV, 0, 0};   // (before: t - lead of the next S)
         // S_t, once K_t is here and the P that sat in S_t's buffer has been read
         auto do_s = [&](int t) {
             const int b = t & (NB - 1);
             if (t >= L::kLead) {
                 if (!wait(&aux->pv_done[i][before.slot], before.par)) return false;
-                before.by(1);
+                before.next();
             }
             if (!wait(&aux->full[ks.slot], ks.par)) return false;
             tc_fence_after();
@@ -526,7 +527,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             }
             commit_if(&aux->s_full[i][b], go);
             if (NQ == 1) commit_if(&aux->empty[ks.slot], go);
-            ks.by(NQ == 1 ? 2 : 1);
+            ks.next();
             return true;
         };
         // O += P_t V_t, once both are here (NQ = 2: V_t came with K_t)
@@ -543,8 +544,8 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * kVStep, idesc_o, t > 0 || kk > 0, go);
             commit_if(&aux->pv_done[i][done.slot], go);
             if (NQ == 1) commit_if(&aux->empty[vs.slot], go);
-            vs.by(NQ == 1 ? 2 : 1);
-            done.by(1);
+            vs.next();
+            done.next();
             return true;
         };
         bool ok = true;
@@ -568,12 +569,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         // ------------------------------------------------------------ NVFP4: K (warps 8-11) and V (12-15) into operand tiles
         const bool is_v = warp >= 12;
         for (int t = 0; t < T; ++t) {
-            const int n = 2 * t + is_v, slot = n % RING, rs = t % max(1, L::kRaw);
+            const int slot = is_v ? L::v_slot(t) : L::k_slot(t), lap = t / (is_v ? L::kRingV : L::kRingK), rs = t % max(1, L::kRaw);
             const uint64_t live = live_columns(p, span, columns_of(span, p.page_shift, t0 + t));
             if (!wait_warp(&aux->raw_full[rs], (t / max(1, L::kRaw)) & 1, abort)) break;
-            if (n >= RING && !wait_warp(&aux->empty[slot], ((n / RING) - 1) & 1, abort)) break;
+            if (lap > 0 && !wait_warp(&aux->empty[slot], (lap - 1) & 1, abort)) break;
             // (the query tile has to leave the last two slots first)
-            if (n >= RING - 2 && n < RING && !wait_warp(&aux->q_ready, 0, abort)) break;
+            if (is_v && t == L::kRingV - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
             const unsigned char* src = raw + rs * R::kSlot;
             decode_tile<D>(src + (is_v ? R::kVC : 0), src + (is_v ? R::kVS : R::kKS), ring + slot * L::kTileBytes, live,
                            tid & 127);
@@ -732,15 +733,20 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 tmem_wait_st();
             }
             if (!FP4 && (col.seam != 0 || col.b < span.base || col.b > span.hi - kBN)) {
-                // V rows that no row of the CTA may see.  (The slot's earlier tile was consumed before these scores could
-                // be made, so the parity names this phase.  Both tiles' warps write the same zeros.)
+                // V rows that no row of the CTA may see.  Once the slot's earlier tile has been used the parity names this
+                // phase.  (Both tiles' warps write the same zeros.)
                 const int steps = t == T - 1 ? last_steps : kBN / 16;
                 const uint64_t dead = ~live_columns(p, span, col) & low_bits(steps * 16);
                 if (dead) {
                     constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
-                    const int n = NQ == 2 ? t : 2 * t + 1;
-                    if (!(ok = wait_warp(&aux->full[n % RING], (n / RING) & 1, abort))) break;
-                    const uint32_t v_addr = smem_addr(ring + (n % RING) * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
+                    // (P V of tile t - lead is in, or S_t could not have been made: earlier ones need no wait, whose parity
+                    // could be a phase behind)
+                    const int slot = L::v_slot(t), used = t - L::kRingV;
+                    if (L::kRingV < L::kLead && used >= 0 &&
+                        !(ok = wait_warp(&aux->pv_done[i][used % PV], (used / PV) & 1, abort)))
+                        break;
+                    if (!(ok = wait_warp(&aux->full[slot], (t / L::kRingV) & 1, abort))) break;
+                    const uint32_t v_addr = smem_addr(ring + slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
                     for (int u = m; u < kBN * C8; u += 128)
                         if ((dead >> (u / C8)) & 1)
                             st_shared_v4(v_addr + (u / C8 >> 4) * L::kUnit + ((u % C8) >> 3) * 2048 + (u / C8 & 15) * 128 + (u & 7) * 16,
