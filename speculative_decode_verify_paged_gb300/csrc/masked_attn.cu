@@ -144,6 +144,17 @@ __device__ __forceinline__ uint64_t below(const Columns& c, int x) {
     const uint64_t b = low_bits(x - c.b);
     return c.seam == 0 ? b : (low_bits(x - c.a) & c.low) | (b & ~c.low);
 }
+// The tiles [lo, hi) of the list that lie within the keys [from, to), behind the seam.  (Made once: the columns of every
+// tile and their comparison took 290 of a tile's 1150 clocks.)
+struct Tiles {
+    int lo, hi;
+    __device__ __forceinline__ bool has(int t) const { return t >= lo && t < hi; }
+};
+__device__ __forceinline__ Tiles tiles_within(const Span& s, int page_shift, int from, int to) {
+    const int origin = (s.first - s.sink_pages) << page_shift;     // tile t starts at key origin + 64 t
+    const int seam = (s.sink_pages + (64 >> page_shift) - 1) >> (6 - page_shift);
+    return {max(seam, (max(from - origin, 0) + kBN - 1) / kBN), to - origin < kBN ? 0 : (to - origin) / kBN};
+}
 // columns that some row of the CTA may see
 __device__ __forceinline__ uint64_t live_columns(const MaskedParams& p, const Span& s, const Columns& c) {
     uint64_t m = below(c, s.hi);
@@ -184,16 +195,21 @@ struct MaskedLayout {
     static constexpr bool kEightK = !FP4 && D == 256;
     static constexpr bool kUnitV = !FP4;
     static constexpr int kUnit = 16 * D * 2;
+    // Key streams: two softmax warpgroups take the query tile's key tiles in turn, each with an O tile and a running
+    // maximum and sum of its own, and their rows are joined at the end.  A lone group is bound by its chain of latencies
+    // (barrier, scores, maximum, exponentials, weights, barrier: 950 clocks a tile, of them 350 exponentials).
+    static constexpr int kStreams = NQ == 1 && DEEP && !FP4 && D == 64 ? 2 : 1;
+    static constexpr int kGroups = NQ * kStreams;          // softmax warpgroups, and O tiles
     static constexpr bool kQT = NQ == 1 && DEEP;           // the query tile in tensor memory
     // S buffers of a tile (a power of two); with four, S_{t+1} does not wait for P V of tile t - 1
     static constexpr int kBufShift = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
     static constexpr int kBufs = 1 << kBufShift;
-    static constexpr int kQCol = NQ * (D + kBufs * kBN);
+    static constexpr int kQCol = kGroups * D + NQ * kBufs * kBN;
     static constexpr int kNeed = kQCol + (kQT ? D / 2 : 0);
     static constexpr uint32_t kCols = kNeed <= 256 ? 256u : 512u;   // allocated: a power of two
     static_assert(kNeed <= 512 && kCols * kCtas <= 512, "tensor memory");
-    // first column of buffer b of tile i
-    __host__ __device__ static constexpr int s_col(int i, int b) { return NQ * D + (kBufs * i + b) * kBN; }
+    // first column of buffer b of query tile i
+    __host__ __device__ static constexpr int s_col(int i, int b) { return kGroups * D + (kBufs * i + b) * kBN; }
     // The ring.  NQ = 1: a slot a tile, each let go as soon as it has been read, the first kRingK slots for K and the rest
     // for V (their producers run apart: a slot that both filled in turn could be a phase further than the one that waits
     // for it can tell).  NQ = 2: a slot holds K_t and V_t, filled and let go together.  A query tile bound for tensor memory
@@ -216,8 +232,8 @@ struct MaskedLayout {
     static constexpr int kPv = NQ == 2 ? kRing : 4;
     // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), their log2 sums and largest elements
     static constexpr int kRowFloats = D + 4;
-    static_assert(NQ * kM * (kRowFloats + 2) * 4 <= kQSmem + kTail, "epilogue staging");
-    static constexpr int kThreads = FP4 ? 512 : 128 + NQ * 128;
+    static_assert(kGroups * kM * (kRowFloats + 2) * 4 <= kQSmem + kTail, "epilogue staging");
+    static constexpr int kThreads = FP4 ? 512 : 128 + kGroups * 128;
 };
 
 struct MaskedAux {
@@ -279,7 +295,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                    const __grid_constant__ CUtensorMap tmks, const __grid_constant__ CUtensorMap tmvs) {
     using L = MaskedLayout<D, FP4, NQ, DEEP>;
     using R = MaskedRaw<D>;
-    constexpr int PV = L::kPv, RING = L::kRing, SH = L::kBufShift, NB = L::kBufs;
+    constexpr int PV = L::kPv, RING = L::kRing, SH = L::kBufShift, NB = L::kBufs, KS = L::kStreams;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = blockIdx.x % p.max_splits;
     const int tile = p.tiles - 1 - blockIdx.x / p.max_splits;     // (a chain's last rows see the most keys)
@@ -381,8 +397,8 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     // row m of the CTA: its place in O and LSE
     auto place = [&](int m) { return (size_t)(ri.row0 + lo + m / G) * p.num_q_heads + kvh * G + m % G; };
     float* stage = reinterpret_cast<float*>(smem + L::kAux);   // (epilogue)
-    float* stage_lse = stage + NQ * kM * L::kRowFloats;
-    float* stage_max = stage_lse + NQ * kM;
+    float* stage_lse = stage + L::kGroups * kM * L::kRowFloats;
+    float* stage_max = stage_lse + L::kGroups * kM;
 
     if (warp == 0 || warp == 3) {
         // ------------------------------------------------------------ copies: K by warp 0, V by warp 3
@@ -453,7 +469,8 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 turn(k);
                 const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
                 if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(units * L::kUnit));
-                // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K
+                // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K.  (About 85 clocks a box,
+                // from either warp, whatever its size; all from one warp in turn are no faster, nor are prefetches to L2.)
                 const bool whole = is_v || L::kUnitK || L::kEightK;
                 const int halves = !is_v && L::kEightK ? 1 : 0;
                 const int box = whole ? lane : lane / L::kChunks, c = lane % L::kChunks, pp = box >> halves;
@@ -537,11 +554,11 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
             tc_fence_after();
             const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
-            const uint32_t p_tmem = tmem + L::s_col(i, b);
+            const uint32_t p_tmem = tmem + L::s_col(i, b), o_tmem = tmem + (KS == 2 ? t & 1 : i) * D;
             const int steps = t == T - 1 ? last_steps : kBN / 16;
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
-                if (kk < steps) mma_ts_lo(tmem + i * D, p_tmem + kk * 8, v_lo + kk * kVStep, idesc_o, t > 0 || kk > 0, go);
+                if (kk < steps) mma_ts_lo(o_tmem, p_tmem + kk * 8, v_lo + kk * kVStep, idesc_o, t >= KS || kk > 0, go);
             commit_if(&aux->pv_done[i][done.slot], go);
             if (NQ == 1) commit_if(&aux->empty[vs.slot], go);
             vs.next();
@@ -568,9 +585,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     } else if (FP4 && warp >= 8) {
         // ------------------------------------------------------------ NVFP4: K (warps 8-11) and V (12-15) into operand tiles
         const bool is_v = warp >= 12;
+        const Tiles whole = tiles_within(span, p.page_shift, span.base, span.hi);
         for (int t = 0; t < T; ++t) {
             const int slot = is_v ? L::v_slot(t) : L::k_slot(t), lap = t / (is_v ? L::kRingV : L::kRingK), rs = t % max(1, L::kRaw);
-            const uint64_t live = live_columns(p, span, columns_of(span, p.page_shift, t0 + t));
+            const uint64_t live = whole.has(t0 + t) ? ~0ull : live_columns(p, span, columns_of(span, p.page_shift, t0 + t));
             if (!wait_warp(&aux->raw_full[rs], (t / max(1, L::kRaw)) & 1, abort)) break;
             if (lap > 0 && !wait_warp(&aux->empty[slot], (lap - 1) & 1, abort)) break;
             // (the query tile has to leave the last two slots first)
@@ -585,9 +603,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 mbar_arrive(&aux->raw_empty[rs]);
             }
         }
-    } else if (warp >= 4 && (warp < 8 || nact == 2)) {
+    } else if (warp >= 4 && (warp < 8 || nact == 2 || KS == 2)) {
         // ------------------------------------------------------------ softmax and epilogue
-        const int i = warp >= 8 ? 1 : 0;                   // tile
+        const int g = warp >= 8 ? 1 : 0;                   // group: a query tile's, or a key stream's
+        const int i = NQ == 2 ? g : 0;                     // query tile
         const int m = (warp & 3) * 32 + lane;              // row of the tile
         const uint32_t lane_tmem = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const int wrow = lo + i * p.wt + m / G;            // window row
@@ -595,7 +614,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         // a warp without rows leaves its scores as they are: they weigh on no other row
         const bool live = __any_sync(kFullMask, valid);
         bool ok = true;
-        if (L::kQT) {
+        if (L::kQT && g == 0) {
             // the query row into tensor memory, two elements a column; NVFP4: as fp16 (saturating; exact for magnitudes of
             // 2^-14 to 65504).  Rows that are none are zeros.
             if ((ok = wait_warp(&aux->q_full[0], 0, abort))) {
@@ -636,16 +655,17 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             if (p.window) from = max(0, pos - p.window + 1);
             if (p.tree) from = min(from, ri.ctx);
         }
-        // keys that every row of the warp sees
-        const int all_from = __reduce_max_sync(kFullMask, from), all_to = __reduce_min_sync(kFullMask, to);
+        // tiles that every row of the warp sees whole
+        const Tiles whole = tiles_within(span, p.page_shift, max(span.base, __reduce_max_sync(kFullMask, from)),
+                                         min(span.hi, __reduce_min_sync(kFullMask, to)));
         const float sc = p.score_scale_log2;
         float m_ref = -INFINITY, l_sum = 0.f;
         const uint64_t sc2 = pack2(sc, sc);
-        for (int t = 0; t < T && ok; ++t) {
+        for (int t = KS == 2 ? g : 0; t < T && ok; t += KS) {
             const int b = t & (NB - 1);
-            const Columns col = columns_of(span, p.page_shift, t0 + t);
-            uint64_t sees = ~0ull;
-            if (col.seam != 0 || col.b < all_from || col.b > all_to - kBN) {
+            uint64_t sees = ~0ull, dead = 0;
+            if (!whole.has(t0 + t)) {
+                const Columns col = columns_of(span, p.page_shift, t0 + t);
                 if (valid) {
                     sees = below(col, to);
                     if (p.window) sees &= ~below(col, from) | below(col, p.sinks);
@@ -660,11 +680,11 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                         sees |= bits & ~col.low & below(col, ri.len);
                     }
                 }
+                if (!FP4) dead = ~live_columns(p, span, col) & low_bits((t == T - 1 ? last_steps : kBN / 16) * 16);
             }
-            const bool masked = !__all_sync(kFullMask, sees == ~0ull);
+            const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
             if (!(ok = wait_warp(&aux->s_full[i][b], (t >> SH) & 1, abort))) break;
             tc_fence_after();
-            const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
             if (live) {
                 __syncwarp();
                 float sx[kBN], sv[kBN];
@@ -673,7 +693,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < kBN; ++c) sv[c] = sx[L::kUnitK ? (c >> 4) * 8 + (c & 7) + (c >> 3 & 1) * 32 : c];
-                if (masked) {
+                if (!__all_sync(kFullMask, sees == ~0ull)) {
                     const uint32_t s0 = static_cast<uint32_t>(sees), s1 = static_cast<uint32_t>(sees >> 32);
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
@@ -714,56 +734,54 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 const float2 psum = unpack2(add2(ps[0], ps[1]));
                 l_sum = l_sum * alpha + (psum.x + psum.y);
                 m_ref = ref;
-                if (t > 0 && __any_sync(kFullMask, valid && need)) {
-                    // every earlier P V has to be in
-                    if (!(ok = wait_warp(&aux->pv_done[i][(t - 1) % PV], ((t - 1) / PV) & 1, abort))) break;
+                if (t >= KS && __any_sync(kFullMask, valid && need)) {
+                    // every earlier P V of the O tile has to be in
+                    if (!(ok = wait_warp(&aux->pv_done[i][(t - KS) % PV], ((t - KS) / PV) & 1, abort))) break;
                     tc_fence_after();
                     __syncwarp();
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
                         float ov[32];
-                        tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                        tmem_ld32(lane_tmem + g * D + ch * 32, ov);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                        tmem_st32(lane_tmem + i * D + ch * 32, ov);
+                        tmem_st32(lane_tmem + g * D + ch * 32, ov);
                     }
                 }
                 tmem_st32u(s_tmem, pk);
-                tmem_wait_st();
             }
-            if (!FP4 && (col.seam != 0 || col.b < span.base || col.b > span.hi - kBN)) {
+            if (!FP4 && dead) {
                 // V rows that no row of the CTA may see.  Once the slot's earlier tile has been used the parity names this
-                // phase.  (Both tiles' warps write the same zeros.)
-                const int steps = t == T - 1 ? last_steps : kBN / 16;
-                const uint64_t dead = ~live_columns(p, span, col) & low_bits(steps * 16);
-                if (dead) {
-                    constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
-                    // (P V of tile t - lead is in, or S_t could not have been made: earlier ones need no wait, whose parity
-                    // could be a phase behind)
-                    const int slot = L::v_slot(t), used = t - L::kRingV;
-                    if (L::kRingV < L::kLead && used >= 0 &&
-                        !(ok = wait_warp(&aux->pv_done[i][used % PV], (used / PV) & 1, abort)))
-                        break;
-                    if (!(ok = wait_warp(&aux->full[slot], (t / L::kRingV) & 1, abort))) break;
-                    const uint32_t v_addr = smem_addr(ring + slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
-                    for (int u = m; u < kBN * C8; u += 128)
-                        if ((dead >> (u / C8)) & 1)
-                            st_shared_v4(v_addr + (u / C8 >> 4) * L::kUnit + ((u % C8) >> 3) * 2048 + (u / C8 & 15) * 128 + (u & 7) * 16,
-                                         make_uint4(0u, 0u, 0u, 0u));
-                    fence_proxy_async_smem();
-                }
+                // phase.  (P V of tile t - lead is in, or S_t could not have been made: earlier ones need no wait, whose
+                // parity could be a phase behind.  Both tiles' warps write the same zeros.)
+                constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
+                const int slot = L::v_slot(t), used = t - L::kRingV;
+                if (L::kRingV < L::kLead && used >= 0 &&
+                    !(ok = wait_warp(&aux->pv_done[i][used % PV], (used / PV) & 1, abort)))
+                    break;
+                if (!(ok = wait_warp(&aux->full[slot], (t / L::kRingV) & 1, abort))) break;
+                const uint32_t v_addr = smem_addr(ring + slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
+                for (int u = m; u < kBN * C8; u += 128)
+                    if ((dead >> (u / C8)) & 1)
+                        st_shared_v4(v_addr + (u / C8 >> 4) * L::kUnit + ((u % C8) >> 3) * 2048 + (u / C8 & 15) * 128 + (u & 7) * 16,
+                                     make_uint4(0u, 0u, 0u, 0u));
+                fence_proxy_async_smem();
             }
+            if (live) tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
         }
-        // both tiles' products are done: the query tiles and the ring are free
+        // every product is done: the query tiles and the ring are free.  (A stream that does not have the last tile waits
+        // for its own first: P V is done in order, so that the last one's parity names its phase.)
+        if (KS == 2 && ok && T >= 2 && (T - 1 - g) % 2 != 0)
+            ok = wait_warp(&aux->pv_done[i][(T - 2) % PV], ((T - 2) / PV) & 1, abort);
         for (int j = 0; j < NQ; ++j)
             if (ok && j < nact) ok = wait_warp(&aux->pv_done[j][(T - 1) % PV], ((T - 1) / PV) & 1, abort);
         tc_fence_after();
         if (ok) {
-            const int sr = i * p.wt * G + m;               // (rows past the tile's wt * G are not written)
+            const int sr = (KS == 2 ? g * kM : i * p.wt * G) + m;   // (rows past the tile's wt * G are not written)
             float* row = stage + sr * L::kRowFloats;
             const float inv = l_sum == 0.f ? 0.f : p.out_scale / l_sum;
             float most = 0.f;
@@ -771,8 +789,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
                     float ov[32];
-                    tmem_ld32(lane_tmem + i * D + ch * 32, ov);
+                    tmem_ld32(lane_tmem + g * D + ch * 32, ov);
                     tmem_wait_ld();
+                    if (KS == 2 && g >= T) {               // (a stream without tiles: its O tile was never written)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+                    }
                     if (valid) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
@@ -806,7 +828,20 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     for (int u = tid; u < rows * C8; u += L::kThreads) {
         const int m = u / C8, c = u % C8;
         const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
-        const float4 a = src[0], b = src[1];
+        float4 a = src[0], b = src[1];
+        float lse = stage_lse[m], most = stage_max[m];     // (joined rows: at least their largest element)
+        if (KS == 2) {
+            const float4* other = src + kM * L::kRowFloats / 4;
+            const float4 a1 = other[0], b1 = other[1];
+            const float l1 = stage_lse[kM + m], mx = fmaxf(lse, l1), ref = fabsf(mx) == INFINITY ? 0.f : mx;
+            const float e0 = fast_exp2(lse - ref), e1 = fast_exp2(l1 - ref), sum = e0 + e1;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum, w0 = e0 * inv, w1 = e1 * inv;
+            auto mix = [&](float x, float y) { return fmaf(w0, x, w1 * y); };
+            a = make_float4(mix(a.x, a1.x), mix(a.y, a1.y), mix(a.z, a1.z), mix(a.w, a1.w));
+            b = make_float4(mix(b.x, b1.x), mix(b.y, b1.y), mix(b.z, b1.z), mix(b.w, b1.w));
+            lse = mx + log2f(sum);
+            most = fmaxf(most, stage_max[kM + m]);
+        }
         const size_t at = place(m);
         if (nsplits == 1) {
             auto pair = [](float x, float y) {
@@ -814,13 +849,13 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 return *reinterpret_cast<const uint32_t*>(&h);
             };
             st_global_v4(p.o + at * D + c * 8, make_uint4(pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)));
-            if (c == 0 && p.lse) p.lse[at] = stage_lse[m] * kLn2;
+            if (c == 0 && p.lse) p.lse[at] = lse * kLn2;
         } else {
-            const float most = stage_max[m], s = most > 0.f ? 1.f / most : 0.f;
+            const float s = most > 0.f ? 1.f / most : 0.f;
             st_global_v4(p.ws_o + (part + at) * D + c * 8,
                          make_uint4(pack_half2(a.x * s, a.y * s), pack_half2(a.z * s, a.w * s),
                                     pack_half2(b.x * s, b.y * s), pack_half2(b.z * s, b.w * s)));
-            if (c == 0) p.ws_ls[part + at] = make_float2(stage_lse[m], most);
+            if (c == 0) p.ws_ls[part + at] = make_float2(lse, most);
         }
     }
 }
