@@ -39,8 +39,11 @@
 // first half of its S buffer, and where there is room (one tile, the SM to itself) the
 // query tile, which frees its shared memory and doubles the first product's rate.
 //
-// Splits leave normalised rows as fp16 of the row's largest element (off by at most
-// 2^-12 of it) with their log-sum-exps; a second kernel joins them in split order.
+// Splits.  Up to 8 of them form a cluster: each leaves its normalised rows in fp32 with
+// their log-sum-exps in its own shared memory, and after a cluster barrier every CTA
+// combines a share of the rows from its peers' shared memory.  More leave their rows
+// in the workspace as fp16 of the row's largest element (off by at most 2^-12 of it),
+// and a second kernel joins them.  Both in an order that the split fixes.
 //
 // Every wait is bounded; on time-out the CTA sets the device-status bit, drains its
 // copies and products, frees its tensor memory and leaves.
@@ -52,6 +55,7 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "../../include/spec_attn.h"
 #include "common.cuh"
@@ -70,6 +74,7 @@ constexpr int kBN = 64;                 // keys a tile
 constexpr int kMaxRing = 14;
 constexpr int kMaxRaw = 8;
 constexpr int kMaxSorted = 256;         // requests put in order by one CTA's threads
+constexpr int kMaxCluster = 8;          // CTAs of a cluster that any GPU schedules
 constexpr float kRescale = 8.0f;        // log2 units: O is rescaled when a row's maximum grows by more
 
 struct MaskedParams {
@@ -91,6 +96,7 @@ struct MaskedParams {
     int tiles;                  // CTAs' shares of the widest window
     int tiles_per_split;        // key tiles
     int max_splits;
+    int cluster;                // the splits of a CTA's rows form a cluster
     int longest_first;          // requests to put in order of length (0: as they come)
     long long max_seq_len;
     float score_scale_log2;     // sm_scale * log2(e) [* k_gscale]
@@ -818,46 +824,105 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         tc_fence_after();
         tmem_dealloc(tmem, L::kCols);
     }
-    if (*abort) {
-        if (tid == 0) atomicOr(p.status, kDevWaitTimeout);
-        return;
-    }
+    if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
     // ---------------------------------------------------------------- rows out
-    constexpr int C8 = D / 8;
-    const size_t part = (size_t)split * p.total_rows * p.num_q_heads;
-    for (int u = tid; u < rows * C8; u += L::kThreads) {
-        const int m = u / C8, c = u % C8;
-        const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
-        float4 a = src[0], b = src[1];
-        float lse = stage_lse[m], most = stage_max[m];     // (joined rows: at least their largest element)
-        if (KS == 2) {
-            const float4* other = src + kM * L::kRowFloats / 4;
-            const float4 a1 = other[0], b1 = other[1];
-            const float l1 = stage_lse[kM + m], mx = fmaxf(lse, l1), ref = fabsf(mx) == INFINITY ? 0.f : mx;
-            const float e0 = fast_exp2(lse - ref), e1 = fast_exp2(l1 - ref), sum = e0 + e1;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum, w0 = e0 * inv, w1 = e1 * inv;
-            auto mix = [&](float x, float y) { return fmaf(w0, x, w1 * y); };
-            a = make_float4(mix(a.x, a1.x), mix(a.y, a1.y), mix(a.z, a1.z), mix(a.w, a1.w));
-            b = make_float4(mix(b.x, b1.x), mix(b.y, b1.y), mix(b.z, b1.z), mix(b.w, b1.w));
-            lse = mx + log2f(sum);
-            most = fmaxf(most, stage_max[kM + m]);
-        }
-        const size_t at = place(m);
-        if (nsplits == 1) {
-            auto pair = [](float x, float y) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-                return *reinterpret_cast<const uint32_t*>(&h);
-            };
-            st_global_v4(p.o + at * D + c * 8, make_uint4(pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)));
-            if (c == 0 && p.lse) p.lse[at] = lse * kLn2;
-        } else {
-            const float s = most > 0.f ? 1.f / most : 0.f;
-            st_global_v4(p.ws_o + (part + at) * D + c * 8,
-                         make_uint4(pack_half2(a.x * s, a.y * s), pack_half2(a.z * s, a.w * s),
-                                    pack_half2(b.x * s, b.y * s), pack_half2(b.z * s, b.w * s)));
-            if (c == 0) p.ws_ls[part + at] = make_float2(lse, most);
+    auto pair = [](float x, float y) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    const bool clustered = p.cluster && nsplits > 1;
+    if (!*abort && !(clustered && KS == 1)) {
+        constexpr int C8 = D / 8;
+        const size_t part = (size_t)split * p.total_rows * p.num_q_heads;
+        for (int u = tid; u < rows * C8; u += L::kThreads) {
+            const int m = u / C8, c = u % C8;
+            float4* src = reinterpret_cast<float4*>(stage + m * L::kRowFloats + c * 8);
+            float4 a = src[0], b = src[1];
+            float lse = stage_lse[m];
+            if (KS == 2) {
+                const float4* other = src + kM * L::kRowFloats / 4;
+                const float4 a1 = other[0], b1 = other[1];
+                const float l1 = stage_lse[kM + m], mx = fmaxf(lse, l1), ref = fabsf(mx) == INFINITY ? 0.f : mx;
+                const float e0 = fast_exp2(lse - ref), e1 = fast_exp2(l1 - ref), sum = e0 + e1;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum, w0 = e0 * inv, w1 = e1 * inv;
+                auto mix = [&](float x, float y) { return fmaf(w0, x, w1 * y); };
+                a = make_float4(mix(a.x, a1.x), mix(a.y, a1.y), mix(a.z, a1.z), mix(a.w, a1.w));
+                b = make_float4(mix(b.x, b1.x), mix(b.y, b1.y), mix(b.z, b1.z), mix(b.w, b1.w));
+                lse = mx + log2f(sum);
+                if (clustered) {                           // (the rows stay here for the cluster, their sums where most was)
+                    src[0] = a;
+                    src[1] = b;
+                    if (c == 0) stage_max[m] = lse;
+                    continue;
+                }
+            }
+            const size_t at = place(m);
+            if (nsplits == 1) {
+                st_global_v4(p.o + at * D + c * 8, make_uint4(pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)));
+                if (c == 0 && p.lse) p.lse[at] = lse * kLn2;
+            } else {
+                // (two streams' joined row: its largest element or more)
+                const float most = KS == 2 ? fmaxf(stage_max[m], stage_max[kM + m]) : stage_max[m];
+                const float s = most > 0.f ? 1.f / most : 0.f;
+                st_global_v4(p.ws_o + (part + at) * D + c * 8,
+                             make_uint4(pack_half2(a.x * s, a.y * s), pack_half2(a.z * s, a.w * s),
+                                        pack_half2(b.x * s, b.y * s), pack_half2(b.z * s, b.w * s)));
+                if (c == 0) p.ws_ls[part + at] = make_float2(lse, most);
+            }
         }
     }
+    if (!clustered) return;
+    __syncwarp();
+    cluster_sync();                                        // every split's rows are in its shared memory
+    if (!*abort) {
+        auto combine = [&](auto most) {
+            constexpr int N = decltype(most)::value, C4 = D / 4;
+            // Every load of a unit is on its way before the first is used, and each CTA begins with its own rows.
+            uint32_t rows_at[N], lse_at[N];
+            const float* sums = KS == 2 ? stage_max : stage_lse;
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int rank = split + k < nsplits ? split + k : split + k - nsplits;
+                rows_at[k] = peer_addr(smem_addr(stage), k < nsplits ? rank : split);
+                lse_at[k] = peer_addr(smem_addr(sums), k < nsplits ? rank : split);
+            }
+            for (int u = split * L::kThreads + tid; u < rows * C4; u += nsplits * L::kThreads) {
+                const int m = u / C4, c = u % C4;
+                float ls[N];
+                float4 x[N];
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    ls[k] = ld_peer(lse_at[k] + m * 4);
+                    x[k] = ld_peer_v4(rows_at[k] + (m * L::kRowFloats + c * 4) * 4);
+                }
+                // (N is the least of 2, 4 and 8 that holds the splits: those past the middle may not be there)
+                auto here = [&](int k) { return k <= N / 2 || k < nsplits; };
+                float mx = ls[0], sum = 0.f;
+#pragma unroll
+                for (int k = 1; k < N; ++k)
+                    if (here(k)) mx = fmaxf(mx, ls[k]);
+                const float ref = fabsf(mx) == INFINITY ? 0.f : mx;   // (as in the softmax)
+                float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    if (!here(k)) break;
+                    const float w = fast_exp2(ls[k] - ref);
+                    a.x = fmaf(w, x[k].x, a.x); a.y = fmaf(w, x[k].y, a.y);
+                    a.z = fmaf(w, x[k].z, a.z); a.w = fmaf(w, x[k].w, a.w);
+                    sum += w;
+                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                *reinterpret_cast<uint2*>(p.o + place(m) * D + c * 4) =
+                    make_uint2(pair(a.x * inv, a.y * inv), pair(a.z * inv, a.w * inv));
+                if (c == 0 && p.lse) p.lse[place(m)] = (mx + log2f(sum)) * kLn2;
+            }
+        };
+        if (nsplits <= 2) combine(std::integral_constant<int, 2>());
+        else if (nsplits <= 4) combine(std::integral_constant<int, 4>());
+        else combine(std::integral_constant<int, kMaxCluster>());
+    }
+    __syncwarp();
+    cluster_sync();                                        // no CTA leaves while its rows are being read
 }
 
 // Joins the splits' rows: O = sum_s 2^(lse_s - lse) O_s, in split order.  A thread an 8-element piece of a (row, head).
@@ -1025,6 +1090,27 @@ struct spec_attn_masked_plan {
 
 namespace {
 
+// Clusters of `size` CTAs that the GPU holds at once (a cluster stays within one group of SMs).
+int64_t resident_clusters(const spec_attn::MaskedVariant& v, int size, int num_sms) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(static_cast<unsigned>(v.threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(v.smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, v.kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = std::max(1, num_sms / size);
+    }
+    return static_cast<int64_t>(n) * v.ctas;   // (counted at one CTA an SM for kernels with tensor memory)
+}
+
 // Key tiles a split takes.
 int choose_tiles(const spec_attn_masked_problem& p, int64_t units, int rows, const spec_attn_masked_plan& plan) {
     const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
@@ -1035,9 +1121,9 @@ int choose_tiles(const spec_attn_masked_problem& p, int64_t units, int rows, con
     // rows), splits the join behind them; the keys come from HBM at best at its rate.
     const int group = p.num_q_heads / p.num_kv_heads;
     const double cta_rows = std::min(rows, plan.nq * plan.wt) * group;
-    const double fixed = 3.0;
+    const double fixed = 3.0, cluster = 1.0 + cta_rows * p.head_dim / 6e3;
     const bool whole = plan.nq == 2 || p.head_dim == 256 || fp4;
-    const double tile_alone = whole ? 0.8 : 0.43, tile_shared = whole ? 0.8 : (p.head_dim == 64 ? 0.3 : 0.45) * (1.0 + cta_rows / 128.0);
+    const double tile_alone = whole ? 0.8 : 0.45, tile_shared = whole ? 0.8 : (p.head_dim == 64 ? 0.3 : 0.45) * (1.0 + cta_rows / 128.0);
     const double row_bytes = fp4 ? p.head_dim * 1.125 : p.head_dim * 4.0;
     const double hbm = static_cast<double>(p.num_reqs) * units * 64 * p.num_kv_heads * row_bytes / 6.5e6;
     double best = 1e300;
@@ -1047,9 +1133,16 @@ int choose_tiles(const spec_attn_masked_problem& p, int64_t units, int rows, con
         if (splits < s) continue;                  // (as an earlier s)
         const bool alone = ctas * splits <= plan.num_sms;
         const spec_attn::MaskedVariant& v = alone ? deep : shared;
-        const int64_t waves = (ctas * splits + static_cast<int64_t>(plan.num_sms) * v.ctas - 1) / (static_cast<int64_t>(plan.num_sms) * v.ctas);
+        const int64_t slots = static_cast<int64_t>(plan.num_sms) * v.ctas;
+        const int64_t at_once = splits == 1 || splits > spec_attn::kMaxCluster
+                                    ? std::max<int64_t>(1, slots / splits)
+                                    : resident_clusters(v, static_cast<int>(splits), plan.num_sms);
+        const int64_t waves = (ctas + at_once - 1) / at_once;
         const double cta = fixed + static_cast<double>(u) * (alone ? tile_alone : tile_shared);
-        const double join = splits > 1 ? 2.5 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * p.head_dim * 4.0 / 5e6 : 0.0;
+        const double join = splits == 1 ? 0.0
+                            : splits <= spec_attn::kMaxCluster
+                                ? cluster
+                                : 2.5 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * p.head_dim * 4.0 / 5e6;
         const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed) + join;
         if (cost < best * 0.98) {
             best = cost;
@@ -1139,7 +1232,7 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
         p.head_dim, fp4, plan->nq, static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms);
     // partials: the pairs of every split, then their elements (a multiple of 256 bytes each)
     const size_t pairs = static_cast<size_t>(plan->max_splits) * p.total_q_rows * p.num_q_heads;
-    plan->workspace_bytes = 256 + (plan->max_splits > 1 ? (pairs * 8 + 255) / 256 * 256 + pairs * p.head_dim * 2 : 0);
+    plan->workspace_bytes = 256 + (plan->max_splits > spec_attn::kMaxCluster ? (pairs * 8 + 255) / 256 * 256 + pairs * p.head_dim * 2 : 0);
     if (workspace_bytes) *workspace_bytes = plan->workspace_bytes;
     *out = plan;
     return SPEC_ATTN_OK;
@@ -1216,6 +1309,7 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     m.tiles = plan->tiles;
     m.tiles_per_split = plan->tiles_per_split;
     m.max_splits = plan->max_splits;
+    m.cluster = plan->max_splits > 1 && plan->max_splits <= kMaxCluster;
     // (one request, or all CTAs at once: nothing to order)
     const int64_t ctas = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs;
     m.longest_first = p.num_reqs > 1 && p.num_reqs <= kMaxSorted &&
@@ -1245,21 +1339,25 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     cfg.blockDim = dim3(static_cast<unsigned>(plan->variant.threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(plan->variant.smem);
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan->max_splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = m.cluster ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, plan->variant.kernel, m, maps[0], maps[1], maps[2], maps[3], maps[4]);
     if (e != cudaSuccess) return record_cuda_error(e);
-    if (plan->max_splits > 1) {
+    if (plan->max_splits > kMaxCluster) {
         const JoinKernel join = p.head_dim == 64    ? &masked_join_kernel<64>
                                 : p.head_dim == 128 ? &masked_join_kernel<128>
                                                     : &masked_join_kernel<256>;
         const int64_t pieces = static_cast<int64_t>(std::min(p.max_w, p.total_q_rows)) * p.num_q_heads * (p.head_dim / 8);
         cfg.gridDim = dim3(static_cast<unsigned>((pieces + 255) / 256), static_cast<unsigned>(p.num_reqs));
         cfg.blockDim = dim3(256);
-        cfg.dynamicSmemBytes = 0;
+        cfg.dynamicSmemBytes = 0;   // (numAttrs is 1 here: the splits were no cluster)
         e = cudaLaunchKernelEx(&cfg, join, m);
         if (e != cudaSuccess) return record_cuda_error(e);
     }

@@ -97,6 +97,30 @@ __device__ __forceinline__ uint32_t elected() {
     return r;
 }
 
+// Thread-block cluster: all threads of all its CTAs (those that left count as
+// arrived), and shared memory of the CTA of a given rank.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+    uint32_t d;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(saddr), "r"(rank));
+    return d;
+}
+__device__ __forceinline__ float4 ld_peer_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float ld_peer(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
 // Position of 16-byte code chunk ch (of D / 32) within key sl's row of a page's
 // codes in the raw ring.  The TMA copies them with the 128/64/32-byte swizzle
 // of d = 256/128/64 (16-byte chunk index XOR address bits 7..9), which places
