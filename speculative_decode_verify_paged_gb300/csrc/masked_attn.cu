@@ -98,6 +98,9 @@ struct MaskedParams {
     int max_splits;
     int cluster;                // the splits of a CTA's rows form a cluster
     int longest_first;          // requests to put in order of length (0: as they come)
+    const uint8_t* k_scales;    // NVFP4
+    const uint8_t* v_scales;
+    long long scale_page_stride;
     long long max_seq_len;
     float score_scale_log2;     // sm_scale * log2(e) [* k_gscale]
     float out_scale;            // 1 or v_gscale
@@ -168,13 +171,12 @@ __device__ __forceinline__ uint64_t live_columns(const MaskedParams& p, const Sp
     return m;
 }
 
-// NVFP4 raw slot: the codes and scales of a tile's 16-key units, K then V.  Every copy lands on a 128-byte boundary, so
-// a unit's scales (d bytes) take at least 128.
+// NVFP4 raw slot: the codes and scales of a tile's 16-key units, K then V.  Codes land on 128-byte boundaries, so a unit's
+// scales (d bytes) take at least 128.
 template <int D>
 struct MaskedRaw {
     static constexpr int kCodes = 16 * D / 2;
-    static constexpr int kScaleBox = D;
-    static constexpr int kScales = kScaleBox < 128 ? 128 : kScaleBox;
+    static constexpr int kScales = D < 128 ? 128 : D;
     static constexpr int kKS = 4 * kCodes;                 // offsets inside a slot
     static constexpr int kVC = kKS + 4 * kScales;
     static constexpr int kVS = kVC + 4 * kCodes;
@@ -230,7 +232,7 @@ struct MaskedLayout {
     __host__ __device__ static constexpr int k_slot(int t) { return t % kRingK; }
     __host__ __device__ static constexpr int v_slot(int t) { return NQ == 2 ? t % kRing : kRingK + t % kRingV; }
     static constexpr int kRawFit = (kMax - 1024 - kAux - kRing * kTileBytes) / MaskedRaw<D>::kSlot;
-    static constexpr int kRaw = !FP4 ? 0 : kRawFit > kMaxRaw ? kMaxRaw : kRawFit;
+    static constexpr int kRaw = !FP4 ? 0 : kRawFit > kMaxRaw ? kMaxRaw : kRawFit & ~1;   // (even: a slot is one pair's of decoders)
     static constexpr int kTail = kRing * kSlotBytes + kRaw * MaskedRaw<D>::kSlot;   // ring and raw ring, adjacent
     static constexpr int kSmem = 1024 + kAux + kQSmem + kTail;
     static constexpr int kLead = kBufs;                    // tiles by which S leads P V at most
@@ -251,7 +253,7 @@ struct MaskedAux {
     uint64_t s_full[2][4];              // [tile][buffer] scores written
     uint64_t p_full[2][4];              // P written over them (four softmax warps)
     uint64_t raw_full[kMaxRaw];
-    uint64_t raw_empty[kMaxRaw];        // eight decoding warps
+    uint64_t raw_empty[kMaxRaw];        // four decoding warps
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -261,15 +263,25 @@ struct MaskedAux {
 static_assert(sizeof(MaskedAux) <= 2048, "aux region");
 
 
-// One decoding warpgroup's work on a tile: the K or V codes of the raw slot into the fp16 operand tile, chunk-major,
-// 128-byte swizzle; columns that no row may see as zeros.  A unit is one key's 64 elements (32 code bytes, 4 scales, one
-// 128-byte row); eight consecutive keys run side by side, so that the row stores hit distinct banks.
+// 16 bytes to shared memory, and an arrival on `bar` once this thread's copies so far are there (counted in its initial
+// count).
+__device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Two decoding warps' work on a tile: the K or V codes of the raw slot into the fp16 operand tile, chunk-major, 128-byte
+// swizzle; columns that no row may see as zeros.  A unit is one key's 64 elements (32 code bytes, 4 scales, one 128-byte
+// row); eight consecutive keys run side by side, so that the row stores hit distinct banks.
 template <int D>
 __device__ __forceinline__ void decode_tile(const unsigned char* codes, const unsigned char* scales, unsigned char* tile,
                                             uint64_t live, int dt) {
     using R = MaskedRaw<D>;
     constexpr int CPK = D / 64;
-    for (int u = dt; u < kBN * CPK; u += 128) {
+    for (int u = dt; u < kBN * CPK; u += 64) {
         const int j = (u / (8 * CPK)) * 8 + (u & 7), c = (u >> 3) % CPK;
         const int unit = j >> 4, sl = j & 15;
         uint4 outp[8];
@@ -297,8 +309,7 @@ __device__ __forceinline__ void decode_tile(const unsigned char* codes, const un
 template <int D, bool FP4, int NQ, bool DEEP>
 __global__ void __launch_bounds__(MaskedLayout<D, FP4, NQ, DEEP>::kThreads, MaskedLayout<D, FP4, NQ, DEEP>::kCtas)
 masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant__ CUtensorMap tmq,
-                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                   const __grid_constant__ CUtensorMap tmks, const __grid_constant__ CUtensorMap tmvs) {
+                   const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
     using L = MaskedLayout<D, FP4, NQ, DEEP>;
     using R = MaskedRaw<D>;
     constexpr int PV = L::kPv, RING = L::kRing, SH = L::kBufShift, NB = L::kBufs, KS = L::kStreams;
@@ -318,12 +329,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < RING; ++s) {
-            mbar_init(&aux->full[s], FP4 ? 4 : NQ);
+            mbar_init(&aux->full[s], FP4 ? 2 : NQ);
             mbar_init(&aux->empty[s], 1);
         }
         for (int s = 0; s < L::kRaw; ++s) {
-            mbar_init(&aux->raw_full[s], 2);
-            mbar_init(&aux->raw_empty[s], 8);
+            mbar_init(&aux->raw_full[s], 2 + 64);          // codes by either producer, scales by all their lanes
+            mbar_init(&aux->raw_empty[s], 4);
         }
         for (int i = 0; i < NQ; ++i) {
             for (int s = 0; s < PV; ++s) mbar_init(&aux->pv_done[i][s], 1);
@@ -342,10 +353,6 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         tma_prefetch_desc(&tmq);
         tma_prefetch_desc(&tmk);
         tma_prefetch_desc(&tmv);
-        if (FP4) {
-            tma_prefetch_desc(&tmks);
-            tma_prefetch_desc(&tmvs);
-        }
     }
     if (warp == 3) tmem_alloc(&aux->tmem_base, L::kCols);
     // up to here the CTA touched only its own resources, while the previous kernel drains
@@ -448,15 +455,25 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 turn(k);
                 const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
                 uint64_t* bar = &aux->raw_full[slot];
-                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * (R::kCodes + R::kScaleBox)));
-                const int pp = (lane >> 1) & 3, sub = pp & ((1 << (shift - 4)) - 1);
+                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * R::kCodes));
+                unsigned char* dst = raw + slot * R::kSlot + (is_v ? R::kVC : 0);
+                // The scales, d bytes a unit, by plain asynchronous copies: the copy engine takes some 85 clocks a box whatever
+                // its size, and 16 of them a tile were what bound it (d 64 and 128: 0.70 us a tile).
+                constexpr int kPieces = D / 16;            // of a unit
+#pragma unroll
+                for (int x = 0; x < (4 * kPieces + 31) / 32; ++x) {
+                    const int piece = x * 32 + lane, u = piece / kPieces, sub = u & ((1 << (shift - 4)) - 1);
+                    const int page = __shfl_sync(kFullMask, cur, (k & 31) + (min(u, 3) >> (shift - 4)));
+                    if (u < units)
+                        cp_async_16(dst + R::kKS + u * R::kScales + piece % kPieces * 16,
+                                    (is_v ? p.v_scales : p.k_scales) + page * p.scale_page_stride +
+                                        ((((long long)kvh << shift) + sub * 16) * (D / 16) + piece % kPieces * 16));
+                }
+                cp_async_arrive(bar);
+                const int pp = lane & 3, sub = pp & ((1 << (shift - 4)) - 1);
                 const int page = __shfl_sync(kFullMask, cur, (k & 31) + (pp >> (shift - 4)));
                 __syncwarp();
-                if (lane < 2 * units) {
-                    unsigned char* dst = raw + slot * R::kSlot + (is_v ? R::kVC : 0);
-                    if (lane & 1) tma_load_3d(dst + R::kKS + pp * R::kScales, is_v ? &tmvs : &tmks, sub * D, kvh, page, bar);
-                    else tma_load_4d(dst + pp * R::kCodes, is_v ? &tmv : &tmk, 0, sub * 16, kvh, page, bar);
-                }
+                if (lane < units) tma_load_4d(dst + pp * R::kCodes, is_v ? &tmv : &tmk, 0, sub * 16, kvh, page, bar);
                 __syncwarp();
                 issued = t + 1;
             }
@@ -492,6 +509,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 issued = t + 1;
             }
         }
+        if (FP4) cp_async_wait_all();
         if (*abort && lane == 0) {
             // every copy in flight lands before the CTA's shared memory goes away
             volatile int no_abort = 0;
@@ -589,19 +607,20 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         mbar_wait(drain, 0, &no_abort, kDrainLimit);
         __syncwarp();
     } else if (FP4 && warp >= 8) {
-        // ------------------------------------------------------------ NVFP4: K (warps 8-11) and V (12-15) into operand tiles
+        // ------------------------------------------------------------ NVFP4: K (warps 8-11) and V (12-15) into operand tiles,
+        // two warps a tile, the pairs in turn: what a tile takes a warp is mostly waits, stores and the fence behind them
         const bool is_v = warp >= 12;
         const Tiles whole = tiles_within(span, p.page_shift, span.base, span.hi);
-        for (int t = 0; t < T; ++t) {
+        for (int t = warp >> 1 & 1; t < T; t += 2) {
             const int slot = is_v ? L::v_slot(t) : L::k_slot(t), lap = t / (is_v ? L::kRingV : L::kRingK), rs = t % max(1, L::kRaw);
             const uint64_t live = whole.has(t0 + t) ? ~0ull : live_columns(p, span, columns_of(span, p.page_shift, t0 + t));
             if (!wait_warp(&aux->raw_full[rs], (t / max(1, L::kRaw)) & 1, abort)) break;
             if (lap > 0 && !wait_warp(&aux->empty[slot], (lap - 1) & 1, abort)) break;
             // (the query tile has to leave the last two slots first)
-            if (is_v && t == L::kRingV - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
+            if (is_v && t >= L::kRingV - 2 && t < L::kRingV && !wait_warp(&aux->q_ready, 0, abort)) break;
             const unsigned char* src = raw + rs * R::kSlot;
             decode_tile<D>(src + (is_v ? R::kVC : 0), src + (is_v ? R::kVS : R::kKS), ring + slot * L::kTileBytes, live,
-                           tid & 127);
+                           tid & 63);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -988,8 +1007,7 @@ __global__ void __launch_bounds__(256) masked_join_kernel(const __grid_constant_
     if (c == 0 && p.lse) p.lse[at] = (mx + log2f(sum)) * kLn2;
 }
 
-using MaskedKernel = void (*)(const MaskedParams, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
-                              const CUtensorMap);
+using MaskedKernel = void (*)(const MaskedParams, const CUtensorMap, const CUtensorMap, const CUtensorMap);
 using JoinKernel = void (*)(const MaskedParams);
 
 // What a launch of (d, cache type, query tiles a CTA) needs.
@@ -1060,15 +1078,6 @@ bool encode_pool(CUtensorMap* map, const void* pool, bool fp4, const spec_attn_m
                                                             : CU_TENSOR_MAP_SWIZZLE_32B;
     return encode(map, fp4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, sw);
 }
-// A scale pool as (a head's scales, head, page); box = the d scales of a 16-key unit.
-bool encode_scales(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p) {
-    const cuuint64_t row = (cuuint64_t)p.page_size * p.head_dim / 16;
-    const cuuint64_t dims[] = {row, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
-    const cuuint64_t strides[] = {row, (cuuint64_t)p.scale_page_stride};
-    const cuuint32_t box[] = {(cuuint32_t)p.head_dim, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
-}
-
 bool masked_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
@@ -1316,16 +1325,18 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
                               ctas > static_cast<int64_t>(plan->num_sms) * plan->variant.ctas
                           ? p.num_reqs
                           : 0;
+    m.k_scales = static_cast<const uint8_t*>(k_scales);
+    m.v_scales = static_cast<const uint8_t*>(v_scales);
+    m.scale_page_stride = p.scale_page_stride;
     m.max_seq_len = p.max_seq_len;
     m.score_scale_log2 = plan->sm_scale * 1.4426950408889634f * (fp4 ? k_gscale : 1.f);
     m.out_scale = fp4 ? v_gscale : 1.f;
 
-    CUtensorMap maps[5] = {};
+    CUtensorMap maps[3] = {};
     auto encode_all = [&] {
         return encode_q(&maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim, m.group, plan->wt) &&
                (fp4 || !plan->variant.whole_k ? encode_pool(&maps[1], k_pool, fp4, p) : encode_units(&maps[1], k_pool, p, plan->variant.whole_k)) &&
-               (fp4 ? encode_pool(&maps[2], v_pool, fp4, p) : encode_units(&maps[2], v_pool, p, 16)) &&
-               (!fp4 || (encode_scales(&maps[3], k_scales, p) && encode_scales(&maps[4], v_scales, p)));
+               (fp4 ? encode_pool(&maps[2], v_pool, fp4, p) : encode_units(&maps[2], v_pool, p, 16));
     };
     if (!encode_all()) {
         // a thread's first CUDA call has no context to encode in yet: bind the device's and try once more
@@ -1348,7 +1359,7 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = m.cluster ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, plan->variant.kernel, m, maps[0], maps[1], maps[2], maps[3], maps[4]);
+    e = cudaLaunchKernelEx(&cfg, plan->variant.kernel, m, maps[0], maps[1], maps[2]);
     if (e != cudaSuccess) return record_cuda_error(e);
     if (plan->max_splits > kMaxCluster) {
         const JoinKernel join = p.head_dim == 64    ? &masked_join_kernel<64>
