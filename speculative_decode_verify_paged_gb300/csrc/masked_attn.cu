@@ -194,21 +194,21 @@ struct MaskedLayout {
     static constexpr int kTileBytes = kBN * D * 2;         // one K or V tile
     static constexpr int kAux = 2048;
     static constexpr int kCtas = DEEP ? 1 : 2;
+    // Key streams: two softmax warpgroups take the query tile's key tiles in turn, each with an O tile and a running
+    // maximum and sum of its own, and their rows are joined at the end.  A lone group is bound by its chain of latencies
+    // (barrier, scores, maximum, exponentials, weights, barrier: 950 clocks a tile, of them 350 exponentials).
+    static constexpr int kStreams = NQ == 1 && DEEP && !FP4 && D <= 128 ? 2 : 1;
+    static constexpr int kGroups = NQ * kStreams;          // softmax warpgroups, and O tiles
     // Layout of a bf16 tile.  Boxes of one 16-key unit with all its chunks (4 KB at d = 128, 8 KB at d = 256) keep the copy
     // engine's few boxes in flight large: unit-major, [unit][chunk][16 keys][128 bytes].  V is read that way as it is.
     // K's 8-key groups then have no one stride from unit to unit, so S is made by two products of 32 columns, of the
     // first and of the second 8 keys of each unit; with two query tiles, whose first product is slow at 32 columns, K
     // comes chunk by chunk instead, [chunk][64 keys][128 bytes], as decoded tiles are.
-    static constexpr bool kUnitK = !FP4 && NQ == 1 && D == 128;
-    static constexpr bool kEightK = !FP4 && D == 256;
+    static constexpr bool kUnitK = !FP4 && NQ == 1 && D == 128 && kStreams == 1;
+    static constexpr bool kEightK = !FP4 && NQ == 1 && (D == 256 || (D == 128 && kStreams == 2));
     static constexpr bool kUnitV = !FP4;
     static constexpr int kUnit = 16 * D * 2;
-    // Key streams: two softmax warpgroups take the query tile's key tiles in turn, each with an O tile and a running
-    // maximum and sum of its own, and their rows are joined at the end.  A lone group is bound by its chain of latencies
-    // (barrier, scores, maximum, exponentials, weights, barrier: 950 clocks a tile, of them 350 exponentials).
-    static constexpr int kStreams = NQ == 1 && DEEP && !FP4 && D == 64 ? 2 : 1;
-    static constexpr int kGroups = NQ * kStreams;          // softmax warpgroups, and O tiles
-    static constexpr bool kQT = NQ == 1 && DEEP;           // the query tile in tensor memory
+    static constexpr bool kQT = NQ == 1 && DEEP && (kStreams == 1 || D == 64);   // the query tile in tensor memory
     // S buffers of a tile (a power of two); with four, S_{t+1} does not wait for P V of tile t - 1
     static constexpr int kBufShift = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
     static constexpr int kBufs = 1 << kBufShift;
@@ -478,10 +478,21 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 issued = t + 1;
             }
         } else {
-            for (int t = 0; t < T; ++t) {
-                const int slot = is_v ? L::v_slot(t) : L::k_slot(t), lap = t / (is_v ? L::kRingV : L::kRingK), k = t * per_tile;
-                const uint32_t gone = (lap - 1) & 1;
-                if (lap > 0) {
+            // A box a lane: unit pp of V, or (unit-major) of K, whole or in halves, else 64-element chunk c of K.  (About 90
+            // clocks a box and 200 a tile, whatever the sizes; the whole warp issuing them one by one is no faster, and
+            // prefetches to L2 are slower.)
+            const bool whole = is_v || L::kUnitK || L::kEightK;
+            const int halves = !is_v && L::kEightK ? 1 : 0, boxes = whole ? 4 << halves : 4 * L::kChunks;
+            const int c = lane % L::kChunks, pp = whole ? lane >> halves : lane / L::kChunks;
+            const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16 + (lane & halves) * 8, turn_of = min(pp, 3) >> (shift - 4);
+            const int first = is_v ? L::v_slot(0) : 0, end = first + (is_v ? L::kRingV : L::kRingK);
+            unsigned char* const to = ring + (NQ == 2 && is_v ? L::kTileBytes : 0) +
+                                      (whole ? lane * (L::kUnit >> halves) : c * (kBN * 128) + pp * 2048);
+            const CUtensorMap* const map = is_v ? &tmv : &tmk;
+            int slot = first, k = 0;
+            uint32_t gone = 1;                             // parity of the phase that lets the slot go (none in the first lap)
+            for (int t = 0; t < T; ++t, k += per_tile) {
+                if (t >= end - first) {
                     if (NQ == 1 && !wait_warp(&aux->empty[slot], gone, abort)) break;
                     if (NQ == 2 && !(wait_warp(&aux->pv_done[0][slot], gone, abort) &&
                                      (nact == 1 || wait_warp(&aux->pv_done[1][slot], gone, abort))))
@@ -490,23 +501,22 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 // (the query tile has to leave the last two slots first)
                 if (L::kQT && is_v && t == L::kRingV - 2 && !wait_warp(&aux->q_ready, 0, abort)) break;
                 turn(k);
-                const int units = min(4, min(per_tile, pages - k) << (shift - 4));   // of 16 keys
-                if (lane == 0) mbar_arrive_expect_tx(&aux->full[slot], static_cast<uint32_t>(units * L::kUnit));
-                // a box a lane: unit pp, of V or (unit-major) of K whole, else 64-element chunk c of K.  (About 85 clocks a box,
-                // from either warp, whatever its size; all from one warp in turn are no faster, nor are prefetches to L2.)
-                const bool whole = is_v || L::kUnitK || L::kEightK;
-                const int halves = !is_v && L::kEightK ? 1 : 0;
-                const int box = whole ? lane : lane / L::kChunks, c = lane % L::kChunks, pp = box >> halves;
-                const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16 + (box & halves) * 8;
-                const int page = __shfl_sync(kFullMask, cur, (k & 31) + (min(pp, 3) >> (shift - 4)));
-                __syncwarp();
-                if (pp < units) {
-                    unsigned char* dst = ring + slot * L::kSlotBytes + (NQ == 2 && is_v ? L::kTileBytes : 0);
-                    if (whole) tma_load_5d(dst + box * (L::kUnit >> halves), is_v ? &tmv : &tmk, 0, sub, 0, kvh, page, &aux->full[slot]);
-                    else tma_load_4d(dst + c * (kBN * 128) + pp * 2048, &tmk, c * 64, sub, kvh, page, &aux->full[slot]);
+                const int page = __shfl_sync(kFullMask, cur, (k & 31) + turn_of);
+                const int units = k + per_tile <= pages ? 4 : (pages - k) << (shift - 4);   // of 16 keys
+                uint64_t* const bar = &aux->full[slot];
+                // (the bytes may come before they are expected: the phase stays open until this arrival)
+                if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * L::kUnit));
+                if (lane < boxes && pp < units) {
+                    unsigned char* const dst = to + slot * L::kSlotBytes;
+                    if (whole) tma_load_5d(dst, map, 0, sub, 0, kvh, page, bar);
+                    else tma_load_4d(dst, map, c * 64, sub, kvh, page, bar);
                 }
                 __syncwarp();
                 issued = t + 1;
+                if (++slot == end) {
+                    slot = first;
+                    gone ^= 1;
+                }
             }
         }
         if (FP4) cp_async_wait_all();
@@ -1120,45 +1130,45 @@ int64_t resident_clusters(const spec_attn::MaskedVariant& v, int size, int num_s
     return static_cast<int64_t>(n) * v.ctas;   // (counted at one CTA an SM for kernels with tensor memory)
 }
 
-// Key tiles a split takes.
-int choose_tiles(const spec_attn_masked_problem& p, int64_t units, int rows, const spec_attn_masked_plan& plan) {
+struct MaskedChoice {
+    double cost;
+    int tiles_per_split;
+};
+
+// Key tiles a split takes with nq query tiles a CTA, of `units` at most, and the call's time by a model (us, fitted to
+// measurements): a CTA has a start and an end that grow with its rows, and a time for each tile of 64 keys (longer beside
+// another CTA with many rows); splits add their combination, in the cluster or by a second kernel; the keys come from HBM at
+// best at its rate.
+MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, int rows, int nq, int num_sms) {
     const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
-    const spec_attn::MaskedVariant deep = spec_attn::masked_variant(p.head_dim, fp4, plan.nq, true);
-    const spec_attn::MaskedVariant shared = spec_attn::masked_variant(p.head_dim, fp4, plan.nq, false);
-    const int64_t ctas = static_cast<int64_t>(plan.tiles) * p.num_kv_heads * p.num_reqs;
-    // Model (us): a CTA has a start and an end and a time for each tile of 64 keys (longer beside another CTA with many
-    // rows), splits the join behind them; the keys come from HBM at best at its rate.
-    const int group = p.num_q_heads / p.num_kv_heads;
-    const double cta_rows = std::min(rows, plan.nq * plan.wt) * group;
-    const double fixed = 3.0, cluster = 1.0 + cta_rows * p.head_dim / 6e3;
-    const bool whole = plan.nq == 2 || p.head_dim == 256 || fp4;
-    const double tile_alone = whole ? 0.8 : 0.45, tile_shared = whole ? 0.8 : (p.head_dim == 64 ? 0.3 : 0.45) * (1.0 + cta_rows / 128.0);
-    const double row_bytes = fp4 ? p.head_dim * 1.125 : p.head_dim * 4.0;
-    const double hbm = static_cast<double>(p.num_reqs) * units * 64 * p.num_kv_heads * row_bytes / 6.5e6;
-    double best = 1e300;
-    int64_t best_u = units < 1 ? 1 : units;
+    const spec_attn::MaskedVariant deep = spec_attn::masked_variant(p.head_dim, fp4, nq, true);
+    const spec_attn::MaskedVariant shared = spec_attn::masked_variant(p.head_dim, fp4, nq, false);
+    const int group = p.num_q_heads / p.num_kv_heads, wt = nq * (128 / group), d = p.head_dim;
+    const int64_t ctas = static_cast<int64_t>((rows - 1) / wt + 1) * p.num_kv_heads * p.num_reqs;
+    const double cta_rows = std::min(rows, wt) * group, part = cta_rows * d / 16384.0;
+    const double fixed = nq == 2 ? 9.0 : 4.3 + (fp4 ? 1.8 : 1.2) * part, cluster = 1.1 + 1.1 * part;
+    const double tile_alone = nq == 2 ? 0.75 : fp4 ? (d == 64 ? 0.55 : d == 128 ? 0.64 : 0.91) : d == 64 ? 0.44 : d == 128 ? 0.50 : 0.81;
+    const double tile_shared = nq == 2 || fp4 || d == 256 ? tile_alone : (d == 64 ? 0.33 : 0.44) * (1.0 + cta_rows / 128.0);
+    const double hbm = static_cast<double>(p.num_reqs) * units * 64 * p.num_kv_heads * (fp4 ? d * 1.125 : d * 4.0) / 6.2e6;
+    MaskedChoice best = {1e300, static_cast<int>(units)};
     for (int64_t s = 1; s <= units && s <= 128; ++s) {
         const int64_t u = (units + s - 1) / s, splits = (units + u - 1) / u;
         if (splits < s) continue;                  // (as an earlier s)
-        const bool alone = ctas * splits <= plan.num_sms;
+        const bool alone = ctas * splits <= num_sms;
         const spec_attn::MaskedVariant& v = alone ? deep : shared;
-        const int64_t slots = static_cast<int64_t>(plan.num_sms) * v.ctas;
-        const int64_t at_once = splits == 1 || splits > spec_attn::kMaxCluster
-                                    ? std::max<int64_t>(1, slots / splits)
-                                    : resident_clusters(v, static_cast<int>(splits), plan.num_sms);
+        const int64_t slots = static_cast<int64_t>(num_sms) * v.ctas;
+        const int64_t at_once = splits == 1                        ? slots
+                                : splits <= spec_attn::kMaxCluster ? resident_clusters(v, static_cast<int>(splits), num_sms)
+                                                                   : std::max<int64_t>(1, slots / splits);
         const int64_t waves = (ctas + at_once - 1) / at_once;
         const double cta = fixed + static_cast<double>(u) * (alone ? tile_alone : tile_shared);
-        const double join = splits == 1 ? 0.0
-                            : splits <= spec_attn::kMaxCluster
-                                ? cluster
-                                : 2.5 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * p.head_dim * 4.0 / 5e6;
+        const double join = splits == 1                        ? 0.0
+                            : splits <= spec_attn::kMaxCluster ? cluster
+                                                               : 2.6 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * d * 4.0 / 1e7;
         const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed) + join;
-        if (cost < best * 0.98) {
-            best = cost;
-            best_u = u;
-        }
+        if (cost < best.cost * 0.98) best = {cost, static_cast<int>(u)};
     }
-    return static_cast<int>(best_u);
+    return best;
 }
 
 }  // namespace
@@ -1210,28 +1220,38 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
     const int rows = std::max(1, std::min(p.max_w, p.total_q_rows));
     const int64_t max_len = std::max<int64_t>(1, std::min(p.max_seq_len, static_cast<int64_t>(p.block_table_stride) * p.page_size));
     plan->wt = 128 / (p.num_q_heads / p.num_kv_heads);
-    // Two query tiles a CTA read K and V once for both, but make half as many CTAs.
-    const int64_t one_tile = (static_cast<int64_t>(rows) + plan->wt - 1) / plan->wt * p.num_kv_heads * p.num_reqs;
-    plan->nq = p.head_dim == 128 && !fp4 && rows > plan->wt && one_tile > sms ? 2 : 1;
-    const int cta_rows = plan->nq * plan->wt;
-    plan->tiles = (rows - 1) / cta_rows + 1;
-    // most key tiles of a CTA (as span_of counts them)
-    int64_t pages = (max_len + p.page_size - 1) / p.page_size;
-    if (p.window_left > 0) {
-        const int64_t reach = static_cast<int64_t>(p.window_left) - 1 + (p.tree ? rows : std::min(rows, cta_rows));
-        pages = std::min(pages, (static_cast<int64_t>(p.sink_keys) + p.page_size - 1) / p.page_size + reach / p.page_size + 2);
-    }
-    const int64_t units = (pages * p.page_size + spec_attn::kBN - 1) / spec_attn::kBN;
-    for (const bool deep : {true, false}) {
-        const spec_attn::MaskedVariant v = spec_attn::masked_variant(p.head_dim, fp4, plan->nq, deep);
-        e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
-        if (e != cudaSuccess) {
-            delete plan;
-            return spec_attn::record_cuda_error(e);
+    // most key tiles of a CTA of `reach` window rows (as span_of counts them)
+    auto most_tiles = [&](int cta_rows) {
+        int64_t pages = (max_len + p.page_size - 1) / p.page_size;
+        if (p.window_left > 0) {
+            const int64_t reach = static_cast<int64_t>(p.window_left) - 1 + (p.tree ? rows : std::min(rows, cta_rows));
+            pages = std::min(pages, (static_cast<int64_t>(p.sink_keys) + p.page_size - 1) / p.page_size + reach / p.page_size + 2);
+        }
+        return (pages * p.page_size + spec_attn::kBN - 1) / spec_attn::kBN;
+    };
+    // Two query tiles a CTA (d = 128, bf16) read K and V once for both, but make half as many CTAs: the model decides.
+    spec_attn::MaskedVariant v;
+    MaskedChoice best = {1e300, 1};
+    plan->nq = 1;
+    for (int nq = 1; nq <= (p.head_dim == 128 && !fp4 && rows > plan->wt ? 2 : 1); ++nq) {
+        for (const bool deep : {true, false}) {
+            v = spec_attn::masked_variant(p.head_dim, fp4, nq, deep);
+            e = cudaFuncSetAttribute(v.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+            if (e != cudaSuccess) {
+                delete plan;
+                return spec_attn::record_cuda_error(e);
+            }
+        }
+        const MaskedChoice c = choose_split(p, most_tiles(nq * plan->wt), rows, nq, sms);
+        if (c.cost < best.cost) {
+            best = c;
+            plan->nq = nq;
         }
     }
-    plan->tiles_per_split = p.force_splits > 0 ? static_cast<int>((units + p.force_splits - 1) / p.force_splits)
-                                               : choose_tiles(p, units, rows, *plan);
+    const int cta_rows = plan->nq * plan->wt;
+    const int64_t units = most_tiles(cta_rows);
+    plan->tiles = (rows - 1) / cta_rows + 1;
+    plan->tiles_per_split = p.force_splits > 0 ? static_cast<int>((units + p.force_splits - 1) / p.force_splits) : best.tiles_per_split;
     plan->max_splits = static_cast<int>((units - 1) / plan->tiles_per_split) + 1;
     if (static_cast<int64_t>(plan->tiles) * plan->max_splits > INT32_MAX) {
         delete plan;
