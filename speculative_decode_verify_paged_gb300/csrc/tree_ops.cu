@@ -2,10 +2,11 @@
 // path of each (spec_attn_accept_tree), and the move of its keys and values into
 // place (spec_attn_move_kv).
 //
-// Tables.  A thread a node walks up its parents in shared memory; ancestors have
-// lower places, so the words of its mask come out from high to low and each is
-// written once, without a copy in shared memory.  depth steps a node: a tree of 64
-// nodes has some 8 levels, the largest chain 1024.
+// Tables.  A thread a node walks up its parents in shared memory, depth steps: a tree
+// of 64 nodes has some 8 levels, the largest chain 1024.  Up to 256 nodes the words of
+// its mask are registers (NW of them; with one word at a time, written as the walk
+// leaves it, 256 trees of 255 nodes took 4.8 us, 3.1 like this); beyond, ancestors
+// having lower places, the words come out from high to low, each written once.
 //
 // Accepted path.  Whether a child would be taken depends on its own parent only, so
 // every node tests itself at once and the lowest child that passes is kept for each
@@ -43,6 +44,7 @@ struct TreeParams {
     int32_t* ctx_lens;
     unsigned int* status;
     int num_reqs, total_rows, max_w, words, window, sinks, path_stride;
+    int whole;                   // row_mask is aligned for 16-byte stores
 };
 
 struct TreeReq {
@@ -74,6 +76,7 @@ __device__ __forceinline__ int tree_parent(const TreeParams& p, int row0, int i)
     return -1;
 }
 
+template <int NW>
 __global__ void build_tree_kernel(const TreeParams p) {
     extern __shared__ int parent[];
     pdl_wait_primary();
@@ -92,17 +95,38 @@ __global__ void build_tree_kernel(const TreeParams p) {
     const int ctx = q.len - q.w;
     for (int i = tid; i < q.w; i += threads) {
         int depth = 0;
-        for (int j = parent[i]; j >= 0; j = parent[j]) ++depth;
-        p.positions[q.row0 + i] = ctx + depth;
-        uint32_t* words = p.row_mask + (long long)(q.row0 + i) * p.words;
-        int at = p.words - 1;        // the word being made; those above are written
-        uint32_t word = 0;
-        int d = depth;
-        for (int j = i; j >= 0; j = parent[j], --d) {
-            for (; at > j >> 5; --at, word = 0) words[at] = word;
-            if (p.window == 0 || depth - d < p.window || ctx + d < p.sinks) word |= 1u << (j & 31);
+        if (p.window > 0)            // (which ancestors count depends on the node's own depth)
+            for (int j = parent[i]; j >= 0; j = parent[j]) ++depth;
+        uint32_t* out = p.row_mask + (long long)(q.row0 + i) * p.words;
+        int above = 0;               // levels from the node up to j
+        auto counts = [&] { return p.window == 0 || above < p.window || ctx + depth - above < p.sinks; };
+        if constexpr (NW > 0) {
+            uint32_t words[NW] = {};
+            for (int j = i; j >= 0; j = parent[j], ++above) {
+                const uint32_t bit = counts() ? 1u << (j & 31) : 0u;
+#pragma unroll
+                for (int k = 0; k < NW; ++k) words[k] |= j >> 5 == k ? bit : 0u;
+            }
+            if (p.words == NW && p.whole) {
+#pragma unroll
+                for (int k = 0; k < NW; k += 4)
+                    *reinterpret_cast<uint4*>(out + k) = make_uint4(words[k], words[k + 1], words[k + 2], words[k + 3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < NW; ++k)
+                    if (k < p.words) out[k] = words[k];
+                for (int k = NW; k < p.words; ++k) out[k] = 0;
+            }
+        } else {
+            int at = p.words - 1;    // the word being made; those above are written
+            uint32_t word = 0;
+            for (int j = i; j >= 0; j = parent[j], ++above) {
+                for (; at > j >> 5; --at, word = 0) out[at] = word;
+                if (counts()) word |= 1u << (j & 31);
+            }
+            for (; at >= 0; --at, word = 0) out[at] = word;
         }
-        for (; at >= 0; --at, word = 0) words[at] = word;
+        p.positions[q.row0 + i] = ctx + above - 1;
     }
 }
 
@@ -313,7 +337,11 @@ int spec_attn_build_tree(const spec_attn_tree_problem* problem, const int32_t* p
     t.words = words;
     t.window = p.window_left;
     t.sinks = p.sink_keys;
-    const cudaError_t e = launch(build_tree_kernel, dim3(p.num_reqs ? static_cast<unsigned>(p.num_reqs) : 1u), tree_threads(p.max_w),
+    t.whole = aligned(row_mask, 16);
+    void (*const kernel)(const TreeParams) = p.max_w <= 128   ? &build_tree_kernel<4>
+                                             : p.max_w <= 256 ? &build_tree_kernel<8>
+                                                              : &build_tree_kernel<0>;
+    const cudaError_t e = launch(kernel, dim3(p.num_reqs ? static_cast<unsigned>(p.num_reqs) : 1u), tree_threads(p.max_w),
                                  4 * static_cast<size_t>(p.max_w), reinterpret_cast<cudaStream_t>(stream), t);
     return e == cudaSuccess ? SPEC_ATTN_OK : record_cuda_error(e);
 }
