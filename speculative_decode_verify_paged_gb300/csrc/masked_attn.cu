@@ -372,6 +372,15 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         __syncthreads();
         r = aux->request;
     }
+    // Without a window a split's first table entries sit at a known place: the producers fetch them in the same round trip as
+    // the request's window and length (entries past its pages are not used).
+    const int32_t* const table = p.block_table + (size_t)r * p.bt_stride;
+    const int v0 = split * p.tiles_per_split << (6 - p.page_shift);   // the split's first page in the list
+    int early0 = 0, early1 = 0;
+    if (!p.window && (warp == 0 || warp == 3)) {
+        if (v0 + lane < p.bt_stride) early0 = ld_volatile_i32(table + v0 + lane);
+        if (v0 + 32 + lane < p.bt_stride) early1 = ld_volatile_i32(table + v0 + 32 + lane);
+    }
     ReqInfo ri;
     const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
     bool active = load_request(p.seq_lens, p.q_indptr, r, p.max_w, p.total_rows, p.max_seq_len,
@@ -408,7 +417,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         last_steps = (64 - __clzll(static_cast<long long>(live_columns(p, span, c))) + 15) / 16;
     }
     // row m of the CTA: its place in O and LSE
-    auto place = [&](int m) { return (size_t)(ri.row0 + lo + m / G) * p.num_q_heads + kvh * G + m % G; };
+    // (m / G by its rounded-up reciprocal in 2^-16, exact below 2^12 for G <= 16)
+    const unsigned by_g = (65536u + G - 1) / G;
+    auto place = [&](unsigned m) {
+        const unsigned w = m * by_g >> 16;
+        return (size_t)(ri.row0 + lo + w) * p.num_q_heads + kvh * G + (m - w * G);
+    };
     float* stage = reinterpret_cast<float*>(smem + L::kAux);   // (epilogue)
     float* stage_lse = stage + L::kGroups * kM * L::kRowFloats;
     float* stage_max = stage_lse + L::kGroups * kM;
@@ -417,6 +431,20 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         // ------------------------------------------------------------ copies: K by warp 0, V by warp 3
         const bool is_v = warp == 3;
         int issued = 0;
+        // the split's pages, 32 at a time in the lanes' registers, the next 32 on their way
+        const int shift = p.page_shift, per_tile = 64 >> shift;
+        const int pages = min(span.pages - v0, T * per_tile);
+        auto fetch = [&](int k) {
+            if (k >= pages) return 0;
+            const int v = v0 + k;
+            return ld_volatile_i32(table + (v < span.sink_pages ? v : v - span.sink_pages + span.first));
+        };
+        auto checked = [&](int k, int page) {
+            if (k >= pages || (page >= 0 && page < p.num_pages)) return k < pages ? page : 0;
+            atomicOr(p.status, kDevBadPage);
+            return 0;
+        };
+        int cur = p.window ? fetch(lane) : early0, next = p.window ? fetch(32 + lane) : early1, batch = 0;
         if (warp == 0 && lane == 0) {
             const uint32_t qbytes = static_cast<uint32_t>(L::kChunks * 128 * G * p.wt);
             for (int i = 0; i < nact; ++i) {
@@ -427,25 +455,11 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             }
         }
         __syncwarp();
-        // the split's pages, 32 at a time in the lanes' registers, the next 32 on their way
-        const int shift = p.page_shift, per_tile = 64 >> shift;
-        const int v0 = t0 * per_tile, pages = min(span.pages - v0, T * per_tile);
-        const int32_t* table = p.block_table + (size_t)r * p.bt_stride;
-        auto fetch = [&](int k) {
-            if (k >= pages) return 0;
-            const int v = v0 + k;
-            return ld_volatile_i32(table + (v < span.sink_pages ? v : v - span.sink_pages + span.first));
-        };
-        auto checked = [&](int page) {
-            if (page >= 0 && page < p.num_pages) return page;
-            atomicOr(p.status, kDevBadPage);
-            return 0;
-        };
-        int cur = checked(fetch(lane)), next = fetch(32 + lane), batch = 0;
+        cur = checked(lane, cur);
         auto turn = [&](int k) {                           // k: first page of the tile
             if (k >> 5 == batch) return;
             batch = k >> 5;
-            cur = checked(next);
+            cur = checked(32 * batch + lane, next);
             next = fetch(32 * (batch + 1) + lane);
         };
         if constexpr (FP4) {
@@ -822,17 +836,18 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             float most = 0.f;
             if (live) {
 #pragma unroll 1
-                for (int ch = 0; ch < D / 32; ++ch) {
-                    float ov[32];
-                    tmem_ld32(lane_tmem + g * D + ch * 32, ov);
+                for (int ch = 0; ch < D / 32; ch += 2) {
+                    float ov[64];
+                    tmem_ld32(lane_tmem + g * D + ch * 32, *reinterpret_cast<float(*)[32]>(ov));
+                    tmem_ld32(lane_tmem + g * D + ch * 32 + 32, *reinterpret_cast<float(*)[32]>(ov + 32));
                     tmem_wait_ld();
                     if (KS == 2 && g >= T) {               // (a stream without tiles: its O tile was never written)
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = 0.f;
+                        for (int e = 0; e < 64; ++e) ov[e] = 0.f;
                     }
                     if (valid) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
+                        for (int e = 0; e < 64; e += 4) {
                             const float4 x = make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
                             most = fmaxf(fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
                             *reinterpret_cast<float4*>(row + ch * 32 + e) = x;
@@ -861,42 +876,57 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     };
     const bool clustered = p.cluster && nsplits > 1;
     if (!*abort && !(clustered && KS == 1)) {
-        constexpr int C8 = D / 8;
+        constexpr int C8 = D / 8, kAtOnce = 4;             // pieces of 8 elements; a thread's loads before its first store
         const size_t part = (size_t)split * p.total_rows * p.num_q_heads;
-        for (int u = tid; u < rows * C8; u += L::kThreads) {
-            const int m = u / C8, c = u % C8;
-            float4* src = reinterpret_cast<float4*>(stage + m * L::kRowFloats + c * 8);
-            float4 a = src[0], b = src[1];
-            float lse = stage_lse[m];
-            if (KS == 2) {
-                const float4* other = src + kM * L::kRowFloats / 4;
-                const float4 a1 = other[0], b1 = other[1];
-                const float l1 = stage_lse[kM + m], mx = fmaxf(lse, l1), ref = fabsf(mx) == INFINITY ? 0.f : mx;
-                const float e0 = fast_exp2(lse - ref), e1 = fast_exp2(l1 - ref), sum = e0 + e1;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum, w0 = e0 * inv, w1 = e1 * inv;
-                auto mix = [&](float x, float y) { return fmaf(w0, x, w1 * y); };
-                a = make_float4(mix(a.x, a1.x), mix(a.y, a1.y), mix(a.z, a1.z), mix(a.w, a1.w));
-                b = make_float4(mix(b.x, b1.x), mix(b.y, b1.y), mix(b.z, b1.z), mix(b.w, b1.w));
-                lse = mx + log2f(sum);
-                if (clustered) {                           // (the rows stay here for the cluster, their sums where most was)
-                    src[0] = a;
-                    src[1] = b;
-                    if (c == 0) stage_max[m] = lse;
-                    continue;
+        const int pieces = rows * C8;
+        for (int u0 = tid; u0 < pieces; u0 += kAtOnce * L::kThreads) {
+            float4 a[kAtOnce], b[kAtOnce];
+            float lse[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int u = u0 + k * L::kThreads, m = u / C8, c = u % C8;
+                if (u >= pieces) break;
+                const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
+                a[k] = src[0];
+                b[k] = src[1];
+                lse[k] = stage_lse[m];
+                if (KS == 2) {
+                    const float4* other = src + kM * L::kRowFloats / 4;
+                    const float4 a1 = other[0], b1 = other[1];
+                    const float l1 = stage_lse[kM + m], mx = fmaxf(lse[k], l1), ref = fabsf(mx) == INFINITY ? 0.f : mx;
+                    const float e0 = fast_exp2(lse[k] - ref), e1 = fast_exp2(l1 - ref), sum = e0 + e1;
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum, w0 = e0 * inv, w1 = e1 * inv;
+                    auto mix = [&](float x, float y) { return fmaf(w0, x, w1 * y); };
+                    a[k] = make_float4(mix(a[k].x, a1.x), mix(a[k].y, a1.y), mix(a[k].z, a1.z), mix(a[k].w, a1.w));
+                    b[k] = make_float4(mix(b[k].x, b1.x), mix(b[k].y, b1.y), mix(b[k].z, b1.z), mix(b[k].w, b1.w));
+                    lse[k] = mx + log2f(sum);
                 }
             }
-            const size_t at = place(m);
-            if (nsplits == 1) {
-                st_global_v4(p.o + at * D + c * 8, make_uint4(pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)));
-                if (c == 0 && p.lse) p.lse[at] = lse * kLn2;
-            } else {
-                // (two streams' joined row: its largest element or more)
-                const float most = KS == 2 ? fmaxf(stage_max[m], stage_max[kM + m]) : stage_max[m];
-                const float s = most > 0.f ? 1.f / most : 0.f;
-                st_global_v4(p.ws_o + (part + at) * D + c * 8,
-                             make_uint4(pack_half2(a.x * s, a.y * s), pack_half2(a.z * s, a.w * s),
-                                        pack_half2(b.x * s, b.y * s), pack_half2(b.z * s, b.w * s)));
-                if (c == 0) p.ws_ls[part + at] = make_float2(lse, most);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int u = u0 + k * L::kThreads, m = u / C8, c = u % C8;
+                if (u >= pieces) break;
+                if (clustered) {                           // (the rows stay here for the cluster, their sums where most was)
+                    float4* to = reinterpret_cast<float4*>(stage + m * L::kRowFloats + c * 8);
+                    to[0] = a[k];
+                    to[1] = b[k];
+                    if (c == 0) stage_max[m] = lse[k];
+                    continue;
+                }
+                const size_t at = place(m);
+                if (nsplits == 1) {
+                    st_global_v4(p.o + at * D + c * 8, make_uint4(pair(a[k].x, a[k].y), pair(a[k].z, a[k].w),
+                                                                  pair(b[k].x, b[k].y), pair(b[k].z, b[k].w)));
+                    if (c == 0 && p.lse) p.lse[at] = lse[k] * kLn2;
+                } else {
+                    // (two streams' joined row: its largest element or more)
+                    const float most = KS == 2 ? fmaxf(stage_max[m], stage_max[kM + m]) : stage_max[m];
+                    const float s = most > 0.f ? 1.f / most : 0.f;
+                    st_global_v4(p.ws_o + (part + at) * D + c * 8,
+                                 make_uint4(pack_half2(a[k].x * s, a[k].y * s), pack_half2(a[k].z * s, a[k].w * s),
+                                            pack_half2(b[k].x * s, b[k].y * s), pack_half2(b[k].z * s, b[k].w * s)));
+                    if (c == 0) p.ws_ls[part + at] = make_float2(lse[k], most);
+                }
             }
         }
     }
