@@ -199,13 +199,12 @@ struct MaskedLayout {
     // (barrier, scores, maximum, exponentials, weights, barrier: 950 clocks a tile, of them 350 exponentials).
     static constexpr int kStreams = NQ == 1 && DEEP && !FP4 && D <= 128 ? 2 : 1;
     static constexpr int kGroups = NQ * kStreams;          // softmax warpgroups, and O tiles
-    // Layout of a bf16 tile.  Boxes of one 16-key unit with all its chunks (4 KB at d = 128, 8 KB at d = 256) keep the copy
-    // engine's few boxes in flight large: unit-major, [unit][chunk][16 keys][128 bytes].  V is read that way as it is.
-    // K's 8-key groups then have no one stride from unit to unit, so S is made by two products of 32 columns, of the
-    // first and of the second 8 keys of each unit; with two query tiles, whose first product is slow at 32 columns, K
-    // comes chunk by chunk instead, [chunk][64 keys][128 bytes], as decoded tiles are.
-    static constexpr bool kUnitK = !FP4 && NQ == 1 && D == 128 && kStreams == 1;
-    static constexpr bool kEightK = !FP4 && NQ == 1 && (D == 256 || (D == 128 && kStreams == 2));
+    // Layout of a bf16 tile: unit-major, a unit 16 keys, [unit][chunk][16 keys][128 bytes], so that a copy takes a whole unit
+    // of V (4 KB at d = 128).  K comes 8 keys a copy, [8 keys' group][chunk][8][128 bytes]: its groups then have one stride
+    // and S is a product of 64 columns.  (K in units of 16, S in two products of 32 columns: four copies less a tile, but
+    // 1080 clocks of products instead of 640, and 64 single tokens under a window of 4096 took 165 us, not 156.  At d = 64
+    // a unit is both.)  Decoded tiles are chunk-major, [chunk][64 keys][128 bytes].
+    static constexpr bool kEightK = !FP4 && D >= 128;
     static constexpr bool kUnitV = !FP4;
     static constexpr int kUnit = 16 * D * 2;
     static constexpr bool kQT = NQ == 1 && DEEP && (kStreams == 1 || D == 64);   // the query tile in tensor memory
@@ -492,16 +491,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 issued = t + 1;
             }
         } else {
-            // A box a lane: unit pp of V, or (unit-major) of K, whole or in halves, else 64-element chunk c of K.  (About 90
-            // clocks a box and 200 a tile, whatever the sizes; the whole warp issuing them one by one is no faster, and
-            // prefetches to L2 are slower.)
-            const bool whole = is_v || L::kUnitK || L::kEightK;
-            const int halves = !is_v && L::kEightK ? 1 : 0, boxes = whole ? 4 << halves : 4 * L::kChunks;
-            const int c = lane % L::kChunks, pp = whole ? lane >> halves : lane / L::kChunks;
+            // A copy a lane: unit pp of V, the same or half of it of K.  (About 90 clocks a copy and 200 a tile, whatever the
+            // sizes; the whole warp issuing them one by one is no faster, and prefetches to L2 are slower.)
+            const int halves = !is_v && L::kEightK ? 1 : 0, copies = 4 << halves, pp = lane >> halves;
             const int sub = (pp & ((1 << (shift - 4)) - 1)) * 16 + (lane & halves) * 8, turn_of = min(pp, 3) >> (shift - 4);
             const int first = is_v ? L::v_slot(0) : 0, end = first + (is_v ? L::kRingV : L::kRingK);
-            unsigned char* const to = ring + (NQ == 2 && is_v ? L::kTileBytes : 0) +
-                                      (whole ? lane * (L::kUnit >> halves) : c * (kBN * 128) + pp * 2048);
+            unsigned char* const to = ring + (NQ == 2 && is_v ? L::kTileBytes : 0) + lane * (L::kUnit >> halves);
             const CUtensorMap* const map = is_v ? &tmv : &tmk;
             int slot = first, k = 0;
             uint32_t gone = 1;                             // parity of the phase that lets the slot go (none in the first lap)
@@ -520,11 +515,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 uint64_t* const bar = &aux->full[slot];
                 // (the bytes may come before they are expected: the phase stays open until this arrival)
                 if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(units * L::kUnit));
-                if (lane < boxes && pp < units) {
-                    unsigned char* const dst = to + slot * L::kSlotBytes;
-                    if (whole) tma_load_5d(dst, map, 0, sub, 0, kvh, page, bar);
-                    else tma_load_4d(dst, map, c * 64, sub, kvh, page, bar);
-                }
+                if (lane < copies && pp < units) tma_load_5d(to + slot * L::kSlotBytes, map, 0, sub, 0, kvh, page, bar);
                 __syncwarp();
                 issued = t + 1;
                 if (++slot == end) {
@@ -547,11 +538,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     } else if (warp == 1 || (warp == 2 && (NQ == 1 || nact == 2))) {
         // ------------------------------------------------------------ products
         const uint32_t go = elected();
-        constexpr int kN = L::kUnitK ? kBN / 2 : kBN;      // columns of a product of S
-        constexpr uint32_t idesc_s = FP4 ? idesc_f16_f32(kM, kN, 0, 0) : idesc_bf16_f32(kM, kN, 0, 0);
-        constexpr int kGroup = L::kUnitK ? L::kUnit : L::kEightK ? L::kUnit / 2 : 1024;   // from an 8-key group of K to the next
+        constexpr uint32_t idesc_s = FP4 ? idesc_f16_f32(kM, kBN, 0, 0) : idesc_bf16_f32(kM, kBN, 0, 0);
+        constexpr int kGroup = L::kEightK ? L::kUnit / 2 : 1024;                       // from 8 keys of K to the next
         constexpr uint32_t k_hi = kGroup >> 4 | (kDescHi & ~0x3FFFu);
-        constexpr int kChunkStep = (L::kUnitK ? 2048 : L::kEightK ? 1024 : kBN * 128) >> 4;
+        constexpr int kChunkStep = (L::kEightK ? 1024 : kBN * 128) >> 4;
         constexpr int kVStep = (L::kUnitV ? L::kUnit : 2048) >> 4;                     // 16 keys of V further
         constexpr uint32_t idesc_o = FP4 ? idesc_f16_f32(kM, D, 0, 1) : idesc_bf16_f32(kM, D, 0, 1);
         const int i = NQ == 2 ? warp - 1 : 0;
@@ -583,12 +573,9 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             const uint32_t k_lo = k_lo0 + ks.slot * (L::kSlotBytes >> 4), d_tmem = tmem + L::s_col(i, b);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-#pragma unroll
-                for (int h = 0; h < kBN / kN; ++h) {
-                    const uint32_t k_at = k_lo + (kk >> 2) * kChunkStep + (kk & 3) * 2 + h * (1024 >> 4), to = d_tmem + h * kN;
-                    if (L::kQT) mma_ts_lo(to, tmem + L::kQCol + kk * 8, k_at, idesc_s, kk > 0, go, k_hi);
-                    else mma_ss_lo(to, q_lo + (kk >> 2) * (kM * 128 >> 4) + (kk & 3) * 2, k_at, idesc_s, kk > 0, go, k_hi);
-                }
+                const uint32_t k_at = k_lo + (kk >> 2) * kChunkStep + (kk & 3) * 2;
+                if (L::kQT) mma_ts_lo(d_tmem, tmem + L::kQCol + kk * 8, k_at, idesc_s, kk > 0, go, k_hi);
+                else mma_ss_lo(d_tmem, q_lo + (kk >> 2) * (kM * 128 >> 4) + (kk & 3) * 2, k_at, idesc_s, kk > 0, go, k_hi);
             }
             commit_if(&aux->s_full[i][b], go);
             if (NQ == 1) commit_if(&aux->empty[ks.slot], go);
@@ -736,12 +723,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             tc_fence_after();
             if (live) {
                 __syncwarp();
-                float sx[kBN], sv[kBN];
-                tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sx));
-                tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sx + 32));
+                float sv[kBN];
+                tmem_ld32(s_tmem, *reinterpret_cast<float(*)[32]>(sv));
+                tmem_ld32(s_tmem + 32, *reinterpret_cast<float(*)[32]>(sv + 32));
                 tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < kBN; ++c) sv[c] = sx[L::kUnitK ? (c >> 4) * 8 + (c & 7) + (c >> 3 & 1) * 32 : c];
                 if (!__all_sync(kFullMask, sees == ~0ull)) {
                     const uint32_t s0 = static_cast<uint32_t>(sees), s1 = static_cast<uint32_t>(sees >> 32);
 #pragma unroll
@@ -1054,12 +1039,12 @@ using JoinKernel = void (*)(const MaskedParams);
 struct MaskedVariant {
     MaskedKernel kernel;
     int threads, smem, ctas;   // ctas: on one SM
-    int whole_k;               // keys of a copy of K with all its chunks, 0: chunk by chunk
+    int keys_k;                // keys of a copy of K (bf16)
 };
 template <int D, bool FP4, int NQ, bool DEEP>
 MaskedVariant variant_of() {
     using L = MaskedLayout<D, FP4, NQ, DEEP>;
-    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kUnitK ? 16 : L::kEightK ? 8 : 0};
+    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kEightK ? 8 : 16};
 }
 MaskedVariant masked_variant(int d, bool fp4, int nq, bool deep) {
     if (fp4) return d == 64 ? variant_of<64, true, 1, true>() : d == 128 ? variant_of<128, true, 1, true>() : variant_of<256, true, 1, true>();
@@ -1097,7 +1082,7 @@ bool encode_q(CUtensorMap* map, const void* q, int rows, int hq, int d, int grou
     const cuuint32_t box[] = {64, (cuuint32_t)group, (cuuint32_t)wt};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// A bf16 pool as (64 elements, slot, 64-element chunk, head, page); box = 16 keys of a head with all their chunks.
+// A bf16 pool as (64 elements, slot, 64-element chunk, head, page); box = `keys` keys of a head with all their chunks.
 bool encode_units(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p, int keys) {
     const cuuint64_t row = (cuuint64_t)p.head_dim * 2, ps = (cuuint64_t)p.page_size, chunks = (cuuint64_t)p.head_dim / 64;
     const cuuint64_t dims[] = {64, ps, chunks, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
@@ -1105,19 +1090,19 @@ bool encode_units(CUtensorMap* map, const void* pool, const spec_attn_masked_pro
     const cuuint32_t box[] = {64, (cuuint32_t)keys, (cuuint32_t)chunks, 1, 1};
     return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, pool, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// A pool as (element, slot, head, page); box = 16 keys of a head, bf16: 64 elements of them, NVFP4: their codes, swizzled
-// 128/64/32 bytes for d = 256/128/64 (the row is d/2 bytes).
-bool encode_pool(CUtensorMap* map, const void* pool, bool fp4, const spec_attn_masked_problem& p) {
-    const cuuint64_t row = fp4 ? p.head_dim / 2 : p.head_dim * 2, ps = (cuuint64_t)p.page_size;
-    const cuuint64_t dims[] = {(cuuint64_t)(fp4 ? p.head_dim / 2 : p.head_dim), ps, (cuuint64_t)p.num_kv_heads,
-                               (cuuint64_t)p.num_pages};
+// An NVFP4 code pool as (byte, slot, head, page); box = a head's codes of 16 keys, swizzled 128/64/32 bytes for d = 256/128/64
+// (the row is d/2 bytes).
+bool encode_codes(CUtensorMap* map, const void* pool, const spec_attn_masked_problem& p) {
+    const cuuint64_t row = (cuuint64_t)p.head_dim / 2, ps = (cuuint64_t)p.page_size;
+    const cuuint64_t dims[] = {row, ps, (cuuint64_t)p.num_kv_heads, (cuuint64_t)p.num_pages};
     const cuuint64_t strides[] = {row, row * ps, (cuuint64_t)p.kv_page_stride};
-    const cuuint32_t box[] = {(cuuint32_t)(fp4 ? p.head_dim / 2 : 64), 16, 1, 1};
-    const CUtensorMapSwizzle sw = !fp4 || p.head_dim == 256 ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : p.head_dim == 128       ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                            : CU_TENSOR_MAP_SWIZZLE_32B;
-    return encode(map, fp4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool, dims, strides, box, sw);
+    const cuuint32_t box[] = {(cuuint32_t)row, 16, 1, 1};
+    const CUtensorMapSwizzle sw = p.head_dim == 256   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : p.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                      : CU_TENSOR_MAP_SWIZZLE_32B;
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool, dims, strides, box, sw);
 }
+
 bool masked_aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 }  // namespace
@@ -1165,20 +1150,22 @@ struct MaskedChoice {
     int tiles_per_split;
 };
 
-// Key tiles a split takes with nq query tiles a CTA, of `units` at most, and the call's time by a model (us, fitted to
-// measurements): a CTA has a start and an end that grow with its rows, and a time for each tile of 64 keys (longer beside
+// Key tiles a split takes with nq query tiles a CTA, of `units` at most (and `mean` of it over the CTAs: a prompt's rows see
+// half its own keys), and the call's time by a model (us, fitted to measurements): a CTA has a start and an end that grow with its rows, and a time for each tile of 64 keys (longer beside
 // another CTA with many rows); splits add their combination, in the cluster or by a second kernel; the keys come from HBM at
 // best at its rate.
-MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, int rows, int nq, int num_sms) {
+MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, double mean, int rows, int nq, int num_sms) {
     const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
     const spec_attn::MaskedVariant deep = spec_attn::masked_variant(p.head_dim, fp4, nq, true);
     const spec_attn::MaskedVariant shared = spec_attn::masked_variant(p.head_dim, fp4, nq, false);
     const int group = p.num_q_heads / p.num_kv_heads, wt = nq * (128 / group), d = p.head_dim;
     const int64_t ctas = static_cast<int64_t>((rows - 1) / wt + 1) * p.num_kv_heads * p.num_reqs;
     const double cta_rows = std::min(rows, wt) * group, part = cta_rows * d / 16384.0;
-    const double fixed = nq == 2 ? 9.0 : 4.3 + (fp4 ? 1.8 : 1.2) * part, cluster = 1.1 + 1.1 * part;
-    const double tile_alone = nq == 2 ? 0.75 : fp4 ? (d == 64 ? 0.55 : d == 128 ? 0.64 : 0.91) : d == 64 ? 0.44 : d == 128 ? 0.50 : 0.81;
-    const double tile_shared = nq == 2 || fp4 || d == 256 ? tile_alone : (d == 64 ? 0.33 : 0.44) * (1.0 + cta_rows / 128.0);
+    const bool whole = nq == 2 || fp4 || d == 256;
+    const double fixed_alone = nq == 2 ? 12.0 : 4.3 + (fp4 ? 2.4 : 2.0) * part, cluster = 1.1 + 1.1 * part;
+    const double fixed_shared = whole ? fixed_alone : fixed_alone + 3.5 * part * part;
+    const double tile_alone = nq == 2 ? 0.71 : fp4 ? (d == 64 ? 0.55 : d == 128 ? 0.64 : 0.91) : d == 64 ? 0.44 : d == 128 ? 0.46 + 0.12 * part : 0.81;
+    const double tile_shared = whole ? tile_alone : (d == 64 ? 0.33 : 0.42) * (1.0 + cta_rows / 128.0);
     const double hbm = static_cast<double>(p.num_reqs) * units * 64 * p.num_kv_heads * (fp4 ? d * 1.125 : d * 4.0) / 6.2e6;
     MaskedChoice best = {1e300, static_cast<int>(units)};
     for (int64_t s = 1; s <= units && s <= 128; ++s) {
@@ -1190,12 +1177,13 @@ MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, int 
         const int64_t at_once = splits == 1                        ? slots
                                 : splits <= spec_attn::kMaxCluster ? resident_clusters(v, static_cast<int>(splits), num_sms)
                                                                    : std::max<int64_t>(1, slots / splits);
-        const int64_t waves = (ctas + at_once - 1) / at_once;
-        const double cta = fixed + static_cast<double>(u) * (alone ? tile_alone : tile_shared);
+        const double waves = std::ceil(static_cast<double>(ctas) * (splits > 1 ? mean : 1.0) / static_cast<double>(at_once));
+        const double tiles = static_cast<double>(u) * (splits == 1 && waves > 1.0 ? mean : 1.0);
+        const double cta = alone ? fixed_alone + tiles * tile_alone : fixed_shared + tiles * tile_shared;
         const double join = splits == 1                        ? 0.0
                             : splits <= spec_attn::kMaxCluster ? cluster
                                                                : 2.6 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * d * 4.0 / 1e7;
-        const double cost = std::max(static_cast<double>(waves) * cta, hbm + fixed) + join;
+        const double cost = std::max(waves * cta, hbm + fixed_alone) + join;
         if (cost < best.cost * 0.98) best = {cost, static_cast<int>(u)};
     }
     return best;
@@ -1259,6 +1247,7 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
         }
         return (pages * p.page_size + spec_attn::kBN - 1) / spec_attn::kBN;
     };
+    const double mean = p.tree || p.window_left > 0 ? 1.0 : 1.0 - 0.5 * std::min(1.0, static_cast<double>(rows) / max_len);
     // Two query tiles a CTA (d = 128, bf16) read K and V once for both, but make half as many CTAs: the model decides.
     spec_attn::MaskedVariant v;
     MaskedChoice best = {1e300, 1};
@@ -1272,7 +1261,7 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
                 return spec_attn::record_cuda_error(e);
             }
         }
-        const MaskedChoice c = choose_split(p, most_tiles(nq * plan->wt), rows, nq, sms);
+        const MaskedChoice c = choose_split(p, most_tiles(nq * plan->wt), mean, rows, nq, sms);
         if (c.cost < best.cost) {
             best = c;
             plan->nq = nq;
@@ -1385,8 +1374,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     CUtensorMap maps[3] = {};
     auto encode_all = [&] {
         return encode_q(&maps[0], q, p.total_q_rows, p.num_q_heads, p.head_dim, m.group, plan->wt) &&
-               (fp4 || !plan->variant.whole_k ? encode_pool(&maps[1], k_pool, fp4, p) : encode_units(&maps[1], k_pool, p, plan->variant.whole_k)) &&
-               (fp4 ? encode_pool(&maps[2], v_pool, fp4, p) : encode_units(&maps[2], v_pool, p, 16));
+               (fp4 ? encode_codes(&maps[1], k_pool, p) : encode_units(&maps[1], k_pool, p, plan->variant.keys_k)) &&
+               (fp4 ? encode_codes(&maps[2], v_pool, p) : encode_units(&maps[2], v_pool, p, 16));
     };
     if (!encode_all()) {
         // a thread's first CUDA call has no context to encode in yet: bind the device's and try once more
