@@ -703,10 +703,12 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
 int spec_attn_masked_plan_destroy(spec_attn_masked_plan* plan);
 
 /*
- * Arguments as spec_attn_run; row_mask for trees only (NULL for chains), positions
- * [total_q_rows] int32 for trees with a window only (NULL otherwise).  lse may be
- * NULL.  o, lse and workspace share no byte with an input or with each other
- * (SPEC_ATTN_E_INVALID_ARG).  Asynchronous on `stream`, allocation-free, graph
+ * Arguments as spec_attn_run, the NVFP4 global scales positive and finite; row_mask
+ * for trees only (NULL for chains), positions [total_q_rows] int32 for trees with a
+ * window only (NULL otherwise).  lse may be NULL.  o, lse and workspace share no byte
+ * with an input or with each other (SPEC_ATTN_E_INVALID_ARG).  Up to 8 splits need
+ * 256 bytes of workspace, the device-status word; more leave partial rows in it, and
+ * runs that may overlap on the GPU then need workspaces of their own.  Asynchronous on `stream`, allocation-free, graph
  * capturable.
  */
 int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const void* k_pool, const void* v_pool,

@@ -235,6 +235,7 @@ struct MaskedLayout {
     static constexpr int kTail = kRing * kSlotBytes + kRaw * MaskedRaw<D>::kSlot;   // ring and raw ring, adjacent
     static constexpr int kSmem = 1024 + kAux + kQSmem + kTail;
     static constexpr int kLead = kBufs;                    // tiles by which S leads P V at most
+    static_assert(FP4 || kRingV >= kLead, "V of tile t - kRingV was here when S_t is made");
     // P V barriers in use: one a slot (NQ = 2), or one an S buffer and at least four
     static constexpr int kPv = NQ == 2 ? kRing : 4;
     // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), their log2 sums and largest elements
@@ -786,14 +787,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 tmem_st32u(s_tmem, pk);
             }
             if (!FP4 && dead) {
-                // V rows that no row of the CTA may see.  Once the slot's earlier tile has been used the parity names this
-                // phase.  (P V of tile t - lead is in, or S_t could not have been made: earlier ones need no wait, whose
-                // parity could be a phase behind.  Both tiles' warps write the same zeros.)
+                // V rows that no row of the CTA may see.  (P V of tile t - lead is done, or S_t could not have been made, and with
+                // it the slot's earlier tile was here: the parity names this phase.  Both tiles' warps write the same zeros.)
                 constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
-                const int slot = L::v_slot(t), used = t - L::kRingV;
-                if (L::kRingV < L::kLead && used >= 0 &&
-                    !(ok = wait_warp(&aux->pv_done[i][used % PV], (used / PV) & 1, abort)))
-                    break;
+                const int slot = L::v_slot(t);
                 if (!(ok = wait_warp(&aux->full[slot], (t / L::kRingV) & 1, abort))) break;
                 const uint32_t v_addr = smem_addr(ring + slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
                 for (int u = m; u < kBN * C8; u += 128)
@@ -1305,6 +1302,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     if (p.num_reqs == 0 || p.total_q_rows == 0) return SPEC_ATTN_OK;
     if (!q || !o || !k_pool || !v_pool || (fp4 && (!k_scales || !v_scales)) || !seq_lens || !q_indptr ||
         (p.block_table_stride > 0 && !block_table) || (p.tree && !row_mask) || (p.tree && p.window_left > 0 && !positions))
+        return SPEC_ATTN_E_INVALID_ARG;
+    if (fp4 && (!(k_gscale > 0.f) || !(v_gscale > 0.f) || std::isinf(k_gscale) || std::isinf(v_gscale)))
         return SPEC_ATTN_E_INVALID_ARG;
     for (const void* x : {q, k_pool, v_pool, static_cast<const void*>(o), fp4 ? k_scales : nullptr, fp4 ? v_scales : nullptr})
         if (!masked_aligned(x, 16)) return SPEC_ATTN_E_INVALID_ARG;

@@ -577,3 +577,29 @@ def test_plans_are_refused_with_their_status(over, status):
     with pytest.raises(sa.SpecAttnError) as e:
         sa.spec_attn_masked_plan_create(**{**prob, **over})
     assert e.value.status == status
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, math.inf, math.nan])
+def test_bad_global_scales_are_refused(scale):
+    c = Case([4], [100], 8, 2, 64, tree=True, kv="nvfp4", seed=13)
+    for scales in ((scale, 0.7), (0.3, scale)):
+        c.gscale = scales
+        with pytest.raises(sa.SpecAttnError) as e:
+            c.run()
+        assert e.value.status == sa.SPEC_ATTN_E_INVALID_ARG
+    torch.cuda.synchronize()
+    assert bool((c.o == MARK).all())
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("hq,hkv,d,rows,ctx", [(32, 8, 128, [64] * 10, 700), (32, 8, 128, [128] * 4, 900), (8, 1, 64, [40] * 170, 90),
+                                               (24, 4, 256, [21] * 45, 150), (16, 1, 128, [300, 2, 90, 40] * 6, 400)])
+def test_every_shape_of_launch(hq, hkv, d, rows, ctx, kv):
+    """Two query tiles a CTA, CTAs that share an SM, more CTAs than fit: the plans that larger batches get."""
+    rng = random.Random(d + len(rows))
+    c = Case(rows, [rng.randint(ctx // 2, ctx) for _ in rows], hq, hkv, d, tree=True, kv=kv, seed=d)
+    c.run()
+    c.check()
+    c = Case(rows, [rng.randint(ctx // 2, ctx) for _ in rows], hq, hkv, d, window=200, sinks=7, kv=kv, ps=32, seed=d)
+    c.run()
+    c.check()
