@@ -207,6 +207,9 @@ struct MaskedLayout {
     static constexpr bool kEightK = !FP4 && D >= 128;
     static constexpr bool kUnitV = !FP4;
     static constexpr int kUnit = 16 * D * 2;
+    // At d = 256 a chain bounds a tile: scores, softmax, P V, and the next scores into the buffer that P V has read.  P is
+    // handed over in halves there, so that P V begins under the second half's exponentials.
+    static constexpr bool kHalves = D == 256 && !FP4;
     static constexpr bool kQT = NQ == 1 && DEEP && (kStreams == 1 || D == 64);   // the query tile in tensor memory
     // S buffers of a tile (a power of two); with four, S_{t+1} does not wait for P V of tile t - 1
     static constexpr int kBufShift = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
@@ -252,6 +255,7 @@ struct MaskedAux {
     uint64_t q_ready;                   // the query tile is in tensor memory (four softmax warps)
     uint64_t s_full[2][4];              // [tile][buffer] scores written
     uint64_t p_full[2][4];              // P written over them (four softmax warps)
+    uint64_t p_half[2];                 // its first 32 keys (kHalves)
     uint64_t raw_full[kMaxRaw];
     uint64_t raw_empty[kMaxRaw];        // four decoding warps
     uint64_t drain[2];
@@ -345,6 +349,8 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             }
         }
         mbar_init(&aux->q_ready, 4);
+        mbar_init(&aux->p_half[0], 4);
+        mbar_init(&aux->p_half[1], 4);
         mbar_init(&aux->drain[0], 1);
         mbar_init(&aux->drain[1], 1);
         aux->abort = 0;
@@ -587,14 +593,19 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         auto do_pv = [&](int t) {
             const int b = t & (NB - 1);
             if (NQ == 1 && !wait(&aux->full[vs.slot], vs.par)) return false;
-            if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
+            if (!wait(L::kHalves ? &aux->p_half[b] : &aux->p_full[i][b], (t >> SH) & 1)) return false;
             tc_fence_after();
             const uint32_t v_lo = v_lo0 + (vs.slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes) / 16;
             const uint32_t p_tmem = tmem + L::s_col(i, b), o_tmem = tmem + (KS == 2 ? t & 1 : i) * D;
             const int steps = t == T - 1 ? last_steps : kBN / 16;
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
+            for (int kk = 0; kk < kBN / 16; ++kk) {
+                if (L::kHalves && kk == kBN / 32) {
+                    if (!wait(&aux->p_full[i][b], (t >> SH) & 1)) return false;
+                    tc_fence_after();
+                }
                 if (kk < steps) mma_ts_lo(o_tmem, p_tmem + kk * 8, v_lo + kk * kVStep, idesc_o, t >= KS || kk > 0, go);
+            }
             commit_if(&aux->pv_done[i][done.slot], go);
             if (NQ == 1) commit_if(&aux->empty[vs.slot], go);
             vs.next();
@@ -722,6 +733,26 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             const uint32_t s_tmem = lane_tmem + L::s_col(i, b);
             if (!(ok = wait_warp(&aux->s_full[i][b], (t >> SH) & 1, abort))) break;
             tc_fence_after();
+            if (!FP4 && dead) {
+                // V rows that no row of the CTA may see.  (P V of tile t - lead is done, or S_t could not have been made, and with
+                // it the slot's earlier tile was here: the parity names this phase.  Both tiles' warps write the same zeros.)
+                constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
+                const int slot = L::v_slot(t);
+                if (!(ok = wait_warp(&aux->full[slot], (t / L::kRingV) & 1, abort))) break;
+                const uint32_t v_addr = smem_addr(ring + slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
+                for (int u = m; u < kBN * C8; u += 128)
+                    if ((dead >> (u / C8)) & 1)
+                        st_shared_v4(v_addr + (u / C8 >> 4) * L::kUnit + ((u % C8) >> 3) * 2048 + (u / C8 & 15) * 128 + (u & 7) * 16,
+                                     make_uint4(0u, 0u, 0u, 0u));
+                fence_proxy_async_smem();
+            }
+            // what the warp has stored, and the V rows it has zeroed, before its arrival
+            auto hand_over = [&](uint64_t* bar) {
+                if (live) tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar);
+            };
             if (live) {
                 __syncwarp();
                 float sv[kBN];
@@ -752,10 +783,33 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 // infinity makes the sum and with it the log-sum-exp infinite, and O, times 1 / inf, NaN.)
                 const float nref = fabsf(ref) == INFINITY ? 0.f : -ref;
                 const uint64_t nref2 = pack2(nref, nref);
+                auto rescale = [&] {
+                    if (t < KS || !__any_sync(kFullMask, valid && need)) return true;
+                    // every earlier P V of the O tile has to be in
+                    if (!wait_warp(&aux->pv_done[i][(t - KS) % PV], ((t - KS) / PV) & 1, abort)) return false;
+                    tc_fence_after();
+                    __syncwarp();
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        float ov[32];
+                        tmem_ld32(lane_tmem + g * D + ch * 32, ov);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
+                        tmem_st32(lane_tmem + g * D + ch * 32, ov);
+                    }
+                    return true;
+                };
+                if (L::kHalves && !(ok = rescale())) break;
                 uint32_t pk[kBN / 2];
                 uint64_t ps[2] = {0, 0};   // two fp32 zeros each
 #pragma unroll
                 for (int c = 0; c < kBN; c += 2) {
+                    if (L::kHalves && c == kBN / 2) {
+                        tmem_st16u(s_tmem, pk);
+                        hand_over(&aux->p_half[b]);
+                        __syncwarp();
+                    }
                     const float2 x = unpack2(fma2(pack2(sv[c], sv[c + 1]), sc2, nref2));
                     const float p0 = fast_exp2(x.x), p1 = fast_exp2(x.y);
                     ps[(c >> 1) & 1] = add2(ps[(c >> 1) & 1], pack2(p0, p1));
@@ -769,40 +823,13 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 const float2 psum = unpack2(add2(ps[0], ps[1]));
                 l_sum = l_sum * alpha + (psum.x + psum.y);
                 m_ref = ref;
-                if (t >= KS && __any_sync(kFullMask, valid && need)) {
-                    // every earlier P V of the O tile has to be in
-                    if (!(ok = wait_warp(&aux->pv_done[i][(t - KS) % PV], ((t - KS) / PV) & 1, abort))) break;
-                    tc_fence_after();
-                    __syncwarp();
-#pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        float ov[32];
-                        tmem_ld32(lane_tmem + g * D + ch * 32, ov);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                        tmem_st32(lane_tmem + g * D + ch * 32, ov);
-                    }
-                }
-                tmem_st32u(s_tmem, pk);
+                if (!L::kHalves && !(ok = rescale())) break;
+                if (L::kHalves) tmem_st16u(s_tmem + 16, pk + 16);
+                else tmem_st32u(s_tmem, pk);
+            } else if (L::kHalves) {
+                hand_over(&aux->p_half[b]);
             }
-            if (!FP4 && dead) {
-                // V rows that no row of the CTA may see.  (P V of tile t - lead is done, or S_t could not have been made, and with
-                // it the slot's earlier tile was here: the parity names this phase.  Both tiles' warps write the same zeros.)
-                constexpr int C8 = L::kChunks * 8;         // 16-byte pieces of a row
-                const int slot = L::v_slot(t);
-                if (!(ok = wait_warp(&aux->full[slot], (t / L::kRingV) & 1, abort))) break;
-                const uint32_t v_addr = smem_addr(ring + slot * L::kSlotBytes + (NQ - 1) * L::kTileBytes);
-                for (int u = m; u < kBN * C8; u += 128)
-                    if ((dead >> (u / C8)) & 1)
-                        st_shared_v4(v_addr + (u / C8 >> 4) * L::kUnit + ((u % C8) >> 3) * 2048 + (u / C8 & 15) * 128 + (u & 7) * 16,
-                                     make_uint4(0u, 0u, 0u, 0u));
-                fence_proxy_async_smem();
-            }
-            if (live) tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&aux->p_full[i][b]);
+            hand_over(&aux->p_full[i][b]);
         }
         // every product is done: the query tiles and the ring are free.  (A stream that does not have the last tile waits
         // for its own first: P V is done in order, so that the last one's parity names its phase.)
