@@ -208,8 +208,9 @@ struct MaskedLayout {
     static constexpr bool kUnitV = !FP4;
     static constexpr int kUnit = 16 * D * 2;
     // At d = 256 a chain bounds a tile: scores, softmax, P V, and the next scores into the buffer that P V has read.  P is
-    // handed over in halves there, so that P V begins under the second half's exponentials.
-    static constexpr bool kHalves = D == 256 && !FP4;
+    // handed over in halves there, so that P V begins under the second half's exponentials (a tile 0.84 -> 0.79 us, NVFP4
+    // 0.85 -> 0.79).
+    static constexpr bool kHalves = D == 256;
     static constexpr bool kQT = NQ == 1 && DEEP && (kStreams == 1 || D == 64);   // the query tile in tensor memory
     // S buffers of a tile (a power of two); with four, S_{t+1} does not wait for P V of tile t - 1
     static constexpr int kBufShift = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
@@ -266,7 +267,6 @@ struct MaskedAux {
 };
 static_assert(sizeof(MaskedAux) <= 2048, "aux region");
 
-
 // 16 bytes to shared memory, and an arrival on `bar` once this thread's copies so far are there (counted in its initial
 // count).
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
@@ -277,36 +277,57 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Four e4m3 scales (a word's bytes), each as a pair of equal fp16.
+__device__ __forceinline__ void e4m3x4_pairs_f16x2(uint32_t w, uint32_t (&s2)[4]) {
+    uint32_t lo, hi;
+    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    s2[0] = __byte_perm(lo, 0, 0x1010);
+    s2[1] = __byte_perm(lo, 0, 0x3232);
+    s2[2] = __byte_perm(hi, 0, 0x1010);
+    s2[3] = __byte_perm(hi, 0, 0x3232);
+}
+
 // Two decoding warps' work on a tile: the K or V codes of the raw slot into the fp16 operand tile, chunk-major, 128-byte
 // swizzle; columns that no row may see as zeros.  A unit is one key's 64 elements (32 code bytes, 4 scales, one 128-byte
-// row); eight consecutive keys run side by side, so that the row stores hit distinct banks.
+// row); eight consecutive keys run side by side, so that the row stores hit distinct banks.  A thread's keys lie a constant
+// apart: with the passes unrolled every address is a constant off one of a few registers (a tile of d 256 0.92 -> 0.85 us).
 template <int D>
 __device__ __forceinline__ void decode_tile(const unsigned char* codes, const unsigned char* scales, unsigned char* tile,
                                             uint64_t live, int dt) {
     using R = MaskedRaw<D>;
-    constexpr int CPK = D / 64;
-    for (int u = dt; u < kBN * CPK; u += 64) {
-        const int j = (u / (8 * CPK)) * 8 + (u & 7), c = (u >> 3) % CPK;
-        const int unit = j >> 4, sl = j & 15;
-        uint4 outp[8];
-        if ((live >> j) & 1) {
-            const unsigned char* kr = codes + unit * R::kCodes + sl * (D / 2);
-            const uint4 w0 = *reinterpret_cast<const uint4*>(kr + raw_code_chunk<D>(sl, 2 * c) * 16);
-            const uint4 w1 = *reinterpret_cast<const uint4*>(kr + raw_code_chunk<D>(sl, 2 * c + 1) * 16);
-            const uint32_t sc4 = *reinterpret_cast<const uint32_t*>(scales + unit * R::kScales + sl * (D / 16) + c * 4);
+    constexpr int CPK = D / 64, kRows = 64 / CPK;   // rows a pass: multiples of 16, so that passes differ by constants
+    const int j0 = dt / (8 * CPK) * 8 + (dt & 7), c = (dt >> 3) % CPK, unit = j0 >> 4, sl = j0 & 15;
+    const unsigned char* kr = codes + unit * R::kCodes + sl * (D / 2);
+    const int w0_at = raw_code_chunk<D>(sl, 2 * c) * 16, w1_at = raw_code_chunk<D>(sl, 2 * c + 1) * 16;
+    const unsigned char* sr = scales + unit * R::kScales + sl * (D / 16) + c * 4;
+    unsigned char* row = tile + c * (kBN * 128) + j0 * 128;
+    int at[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) at[q] = (q ^ (j0 & 7)) << 4;
+    const bool whole = live == ~0ull;
+#pragma unroll
+    for (int i = 0; i < CPK; ++i) {
+        constexpr int kUnits = kRows / 16;
+        if (whole || (live >> (j0 + i * kRows) & 1)) {
+            const uint4 w0 = *reinterpret_cast<const uint4*>(kr + i * kUnits * R::kCodes + w0_at);
+            const uint4 w1 = *reinterpret_cast<const uint4*>(kr + i * kUnits * R::kCodes + w1_at);
+            const uint32_t sc4 = *reinterpret_cast<const uint32_t*>(sr + i * kUnits * R::kScales);
             const uint32_t words[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+            uint32_t s2[4];
+            e4m3x4_pairs_f16x2(sc4, s2);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const uint32_t s2 = e4m3_pair_f16x2((sc4 >> (8 * (q >> 1))) & 0xFFu);
-                e2m1x8_f16(words[q], s2, outp[q].x, outp[q].y, outp[q].z, outp[q].w);
+                uint4 x;
+                e2m1x8_f16(words[q], s2[q >> 1], x.x, x.y, x.z, x.w);
+                *reinterpret_cast<uint4*>(row + i * kRows * 128 + at[q]) = x;
             }
         } else {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) outp[q] = make_uint4(0u, 0u, 0u, 0u);
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(row + i * kRows * 128 + at[q]) = make_uint4(0u, 0u, 0u, 0u);
         }
-        unsigned char* row = tile + c * (kBN * 128) + j * 128;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) *reinterpret_cast<uint4*>(row + ((q ^ (j & 7)) << 4)) = outp[q];
     }
 }
 
@@ -783,6 +804,8 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 // infinity makes the sum and with it the log-sum-exp infinite, and O, times 1 / inf, NaN.)
                 const float nref = fabsf(ref) == INFINITY ? 0.f : -ref;
                 const uint64_t nref2 = pack2(nref, nref);
+                // (beside a row's 64 scores, 128 registers a thread leave room for 8 columns without spills)
+                constexpr int kCols = FP4 && L::kHalves ? 8 : 32;
                 auto rescale = [&] {
                     if (t < KS || !__any_sync(kFullMask, valid && need)) return true;
                     // every earlier P V of the O tile has to be in
@@ -790,13 +813,16 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                     tc_fence_after();
                     __syncwarp();
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        float ov[32];
-                        tmem_ld32(lane_tmem + g * D + ch * 32, ov);
+                    for (int ch = 0; ch < D / kCols; ++ch) {
+                        uint32_t ov[kCols];
+                        const uint32_t at = lane_tmem + g * D + ch * kCols;
+                        if constexpr (kCols == 8) tmem_ld8u(at, ov);
+                        else tmem_ld32(at, reinterpret_cast<float(&)[kCols]>(ov));
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-                        tmem_st32(lane_tmem + g * D + ch * 32, ov);
+                        for (int e = 0; e < kCols; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                        if constexpr (kCols == 8) tmem_st8u(at, ov);
+                        else tmem_st32u(at, ov);
                     }
                     return true;
                 };
@@ -1175,9 +1201,9 @@ struct MaskedChoice {
 };
 
 // Key tiles a split takes with nq query tiles a CTA, of `units` at most (and `mean` of it over the CTAs: a prompt's rows see
-// half its own keys), and the call's time by a model (us, fitted to measurements): a CTA has a start and an end that grow with its rows, and a time for each tile of 64 keys (longer beside
-// another CTA with many rows); splits add their combination, in the cluster or by a second kernel; the keys come from HBM at
-// best at its rate.
+// half its own keys), and the call's time by a model (us, fitted to measurements): a CTA has a start and an end that grow
+// with its rows, and a time for each tile of 64 keys (longer beside another CTA with many rows); splits add their
+// combination, in the cluster or by a second kernel; the keys come from HBM at best at its rate.
 MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, double mean, int rows, int nq, int num_sms) {
     const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
     const spec_attn::MaskedVariant deep = spec_attn::masked_variant(p.head_dim, fp4, nq, true);
@@ -1188,7 +1214,11 @@ MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, doub
     const bool whole = nq == 2 || fp4 || d == 256;
     const double fixed_alone = nq == 2 ? 12.0 : 4.3 + (fp4 ? 2.4 : 2.0) * part, cluster = 1.1 + 1.1 * part;
     const double fixed_shared = whole ? fixed_alone : fixed_alone + 3.5 * part * part;
-    const double tile_alone = nq == 2 ? 0.71 : fp4 ? (d == 64 ? 0.55 : d == 128 ? 0.64 : 0.91) : d == 64 ? 0.44 : d == 128 ? 0.46 + 0.12 * part : 0.81;
+    const double tile_alone = nq == 2    ? 0.71
+                              : d == 256 ? 0.79
+                              : fp4      ? (d == 64 ? 0.54 : 0.60)
+                              : d == 64  ? 0.44
+                                         : 0.46 + 0.12 * part;
     const double tile_shared = whole ? tile_alone : (d == 64 ? 0.33 : 0.42) * (1.0 + cta_rows / 128.0);
     const double hbm = static_cast<double>(p.num_reqs) * units * 64 * p.num_kv_heads * (fp4 ? d * 1.125 : d * 4.0) / 6.2e6;
     MaskedChoice best = {1e300, static_cast<int>(units)};
