@@ -242,8 +242,9 @@ struct MaskedLayout {
     static_assert(FP4 || kRingV >= kLead, "V of tile t - kRingV was here when S_t is made");
     // P V barriers in use: one a slot (NQ = 2), or one an S buffer and at least four
     static constexpr int kPv = NQ == 2 ? kRing : 4;
-    // the epilogue's fp32 rows, 16 bytes apart beyond their length (no bank conflict), their log2 sums and largest elements
-    static constexpr int kRowFloats = D + 4;
+    // the epilogue's rows (fp32, or bytes of bf16), 16 bytes apart beyond their length (no bank conflict), their log2 sums and
+    // largest elements
+    static constexpr int kRowFloats = D + 4, kRow16 = D * 2 + 16;
     static_assert(kGroups * kM * (kRowFloats + 2) * 4 <= kQSmem + kTail, "epilogue staging");
     static constexpr int kThreads = FP4 ? 512 : 128 + kGroups * 128;
 };
@@ -450,6 +451,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         const unsigned w = m * by_g >> 16;
         return (size_t)(ri.row0 + lo + w) * p.num_q_heads + kvh * G + (m - w * G);
     };
+    auto pair = [](float x, float y) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    };
+    // Rows wait in shared memory to leave in memory order: of one stream and one split as bf16 already, otherwise in fp32.
+    const bool rounded = KS == 1 && nsplits == 1;
     float* stage = reinterpret_cast<float*>(smem + L::kAux);   // (epilogue)
     float* stage_lse = stage + L::kGroups * kM * L::kRowFloats;
     float* stage_max = stage_lse + L::kGroups * kM;
@@ -864,10 +871,25 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         for (int j = 0; j < NQ; ++j)
             if (ok && j < nact) ok = wait_warp(&aux->pv_done[j][(T - 1) % PV], ((T - 1) / PV) & 1, abort);
         tc_fence_after();
+        const int sr = (KS == 2 ? g * kM : i * p.wt * G) + m;       // (rows past the tile's wt * G are not written)
+        float* row = stage + sr * L::kRowFloats;
+        if (KS == 2) {                                     // the streams' maxima and sums meet behind their rows' elements
+            if (ok) *reinterpret_cast<float2*>(row + D) = make_float2(m_ref, l_sum);
+            named_barrier_sync(1, 2 * kM);
+        }
         if (ok) {
-            const int sr = (KS == 2 ? g * kM : i * p.wt * G) + m;   // (rows past the tile's wt * G are not written)
-            float* row = stage + sr * L::kRowFloats;
-            const float inv = l_sum == 0.f ? 0.f : p.out_scale / l_sum;
+            unsigned char* row16 = reinterpret_cast<unsigned char*>(stage) + sr * L::kRow16;
+            float inv, lse;
+            if (KS == 2) {
+                const float2 other = *reinterpret_cast<const float2*>(stage + (sr ^ kM) * L::kRowFloats + D);
+                const float mx = fmaxf(m_ref, other.x), ref = fabsf(mx) == INFINITY ? 0.f : mx;   // (as in the softmax)
+                const float own = fast_exp2(m_ref - ref), sum = fmaf(l_sum, own, other.y * fast_exp2(other.x - ref));
+                inv = sum == 0.f ? 0.f : own * (p.out_scale / sum);
+                lse = mx + log2f(sum);
+            } else {
+                inv = l_sum == 0.f ? 0.f : p.out_scale / l_sum;
+                lse = m_ref + log2f(l_sum);
+            }
             float most = 0.f;
             if (live) {
 #pragma unroll 1
@@ -880,7 +902,13 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 64; ++e) ov[e] = 0.f;
                     }
-                    if (valid) {
+                    if (valid && rounded) {
+#pragma unroll
+                        for (int e = 0; e < 64; e += 8)
+                            *reinterpret_cast<uint4*>(row16 + (ch * 32 + e) * 2) =
+                                make_uint4(pair(ov[e] * inv, ov[e + 1] * inv), pair(ov[e + 2] * inv, ov[e + 3] * inv),
+                                           pair(ov[e + 4] * inv, ov[e + 5] * inv), pair(ov[e + 6] * inv, ov[e + 7] * inv));
+                    } else if (valid) {
 #pragma unroll
                         for (int e = 0; e < 64; e += 4) {
                             const float4 x = make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
@@ -892,7 +920,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 }
             }
             if (valid) {
-                stage_lse[sr] = m_ref + log2f(l_sum);
+                stage_lse[sr] = lse;
                 stage_max[sr] = most;
             }
         }
@@ -905,12 +933,31 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     }
     if (tid == 0 && *abort) atomicOr(p.status, kDevWaitTimeout);
     // ---------------------------------------------------------------- rows out
-    auto pair = [](float x, float y) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        return *reinterpret_cast<const uint32_t*>(&h);
-    };
     const bool clustered = p.cluster && nsplits > 1;
-    if (!*abort && !(clustered && KS == 1)) {
+    if (rounded) {
+        if (!*abort) {
+            constexpr int C8 = D / 8, kAtOnce = 4;
+            const int pieces = rows * C8;
+            for (int u0 = tid; u0 < pieces; u0 += kAtOnce * L::kThreads) {
+                uint4 x[kAtOnce];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int u = u0 + k * L::kThreads;
+                    if (u < pieces)
+                        x[k] = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(stage) +
+                                                               u / C8 * L::kRow16 + u % C8 * 16);
+                }
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int u = u0 + k * L::kThreads, m = u / C8, c = u % C8;
+                    if (u >= pieces) break;
+                    const size_t at = place(m);
+                    st_global_v4(p.o + at * D + c * 8, x[k]);
+                    if (c == 0 && p.lse) p.lse[at] = stage_lse[m] * kLn2;
+                }
+            }
+        }
+    } else if (!*abort && !(clustered && KS == 1)) {
         constexpr int C8 = D / 8, kAtOnce = 4;             // pieces of 8 elements; a thread's loads before its first store
         const size_t part = (size_t)split * p.total_rows * p.num_q_heads;
         const int pieces = rows * C8;
@@ -922,30 +969,32 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 const int u = u0 + k * L::kThreads, m = u / C8, c = u % C8;
                 if (u >= pieces) break;
                 const float4* src = reinterpret_cast<const float4*>(stage + m * L::kRowFloats + c * 8);
-                a[k] = src[0];
-                b[k] = src[1];
+                // (a piece is two 16-byte words; every other four lanes take the second first, so that eight lanes' reads hit
+                // distinct banks)
+                const int first = c >> 2 & 1;
+                a[k] = src[first];
+                b[k] = src[first ^ 1];
                 lse[k] = stage_lse[m];
                 if (KS == 2) {
                     const float4* other = src + kM * L::kRowFloats / 4;
-                    const float4 a1 = other[0], b1 = other[1];
-                    const float l1 = stage_lse[kM + m], mx = fmaxf(lse[k], l1), ref = fabsf(mx) == INFINITY ? 0.f : mx;
-                    const float e0 = fast_exp2(lse[k] - ref), e1 = fast_exp2(l1 - ref), sum = e0 + e1;
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum, w0 = e0 * inv, w1 = e1 * inv;
-                    auto mix = [&](float x, float y) { return fmaf(w0, x, w1 * y); };
-                    a[k] = make_float4(mix(a[k].x, a1.x), mix(a[k].y, a1.y), mix(a[k].z, a1.z), mix(a[k].w, a1.w));
-                    b[k] = make_float4(mix(b[k].x, b1.x), mix(b[k].y, b1.y), mix(b[k].z, b1.z), mix(b[k].w, b1.w));
-                    lse[k] = mx + log2f(sum);
+                    const float4 a1 = other[first], b1 = other[first ^ 1];
+                    a[k] = make_float4(a[k].x + a1.x, a[k].y + a1.y, a[k].z + a1.z, a[k].w + a1.w);
+                    b[k] = make_float4(b[k].x + b1.x, b[k].y + b1.y, b[k].z + b1.z, b[k].w + b1.w);
+                }
+                if (first) {
+                    const float4 x = a[k];
+                    a[k] = b[k];
+                    b[k] = x;
                 }
             }
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const int u = u0 + k * L::kThreads, m = u / C8, c = u % C8;
                 if (u >= pieces) break;
-                if (clustered) {                           // (the rows stay here for the cluster, their sums where most was)
+                if (clustered) {                           // (the rows stay here for the cluster)
                     float4* to = reinterpret_cast<float4*>(stage + m * L::kRowFloats + c * 8);
                     to[0] = a[k];
                     to[1] = b[k];
-                    if (c == 0) stage_max[m] = lse[k];
                     continue;
                 }
                 const size_t at = place(m);
@@ -955,7 +1004,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                     if (c == 0 && p.lse) p.lse[at] = lse[k] * kLn2;
                 } else {
                     // (two streams' joined row: its largest element or more)
-                    const float most = KS == 2 ? fmaxf(stage_max[m], stage_max[kM + m]) : stage_max[m];
+                    const float most = KS == 2 ? stage_max[m] + stage_max[kM + m] : stage_max[m];
                     const float s = most > 0.f ? 1.f / most : 0.f;
                     st_global_v4(p.ws_o + (part + at) * D + c * 8,
                                  make_uint4(pack_half2(a[k].x * s, a[k].y * s), pack_half2(a[k].z * s, a[k].w * s),
@@ -973,12 +1022,11 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             constexpr int N = decltype(most)::value, C4 = D / 4;
             // Every load of a unit is on its way before the first is used, and each CTA begins with its own rows.
             uint32_t rows_at[N], lse_at[N];
-            const float* sums = KS == 2 ? stage_max : stage_lse;
 #pragma unroll
             for (int k = 0; k < N; ++k) {
                 const int rank = split + k < nsplits ? split + k : split + k - nsplits;
                 rows_at[k] = peer_addr(smem_addr(stage), k < nsplits ? rank : split);
-                lse_at[k] = peer_addr(smem_addr(sums), k < nsplits ? rank : split);
+                lse_at[k] = peer_addr(smem_addr(stage_lse), k < nsplits ? rank : split);
             }
             for (int u = split * L::kThreads + tid; u < rows * C4; u += nsplits * L::kThreads) {
                 const int m = u / C4, c = u % C4;
