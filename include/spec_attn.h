@@ -704,12 +704,13 @@ int spec_attn_masked_plan_destroy(spec_attn_masked_plan* plan);
 
 /*
  * Arguments as spec_attn_run, the NVFP4 global scales positive and finite; row_mask
- * for trees only (NULL for chains), positions [total_q_rows] int32 for trees with a
- * window only (NULL otherwise).  lse may be NULL.  o, lse and workspace share no byte
- * with an input or with each other (SPEC_ATTN_E_INVALID_ARG).  Up to 8 splits need
- * 256 bytes of workspace, the device-status word; more leave partial rows in it, and
- * runs that may overlap on the GPU then need workspaces of their own.  Asynchronous on `stream`, allocation-free, graph
- * capturable.
+ * for trees only (ignored for chains), positions [total_q_rows] int32 for trees with
+ * a window only (ignored otherwise).  lse may be NULL.  o, lse and workspace share no
+ * byte with an input or with each other (SPEC_ATTN_E_INVALID_ARG).  NVFP4 caches:
+ * elements of q beyond +-65504 count as that.  Up to 8 splits need 256 bytes of
+ * workspace, the device-status word; more leave partial rows in it, and runs that may
+ * overlap on the GPU then need workspaces of their own.  Asynchronous on `stream`,
+ * allocation-free, graph capturable.
  */
 int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const void* k_pool, const void* v_pool,
                          const void* k_scales, const void* v_scales, float k_gscale, float v_gscale,
@@ -727,8 +728,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
  *   positions[row] = ctx_r + depth (a root's depth is 0), and
  *   row_mask[row]: the node and its ancestors -- with window_left = n > 0 only those
  *   fewer than n levels above the node, or at a position below sink_keys --
- * in mask_row_words words a row (0: ceil(max_w / 32)), unused bits 0.  Rows of no
- * request get position 0 and an empty mask.  ctx_r = seq_lens[r] - W_r.
+ * in mask_row_words words a row (0: ceil(max_w / 32)), unused bits 0.  The rows from
+ * q_indptr[P] on get position 0 and an empty mask.  ctx_r = seq_lens[r] - W_r.
  *
  * spec_attn_accept_tree walks each tree from node 0: the next node is the lowest
  * child whose draft token is the target token of its parent (the token that the
@@ -745,8 +746,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
  * seq_len below its window SPEC_ATTN_DEV_BAD_SEQ_LEN; such a request's rows are left
  * as they were, its path is empty, accept_lens 0, next_tokens -1 and ctx_lens its
  * seq_len.  Outputs share no byte with an input (ctx_lens apart) or with each other
- * (SPEC_ATTN_E_INVALID_ARG).  workspace: 256 bytes holding the device-status word.  Asynchronous on
- * `stream`, one kernel, allocation-free, graph capturable.
+ * (SPEC_ATTN_E_INVALID_ARG).  workspace: 256 bytes holding the device-status word.
+ * Asynchronous on `stream`, one kernel, allocation-free, graph capturable.
  */
 #define SPEC_ATTN_TREE_MAX_W 1024
 #define SPEC_ATTN_DEV_BAD_TREE      0x40u /* a parent that is no earlier node; a path that does not ascend */

@@ -274,6 +274,17 @@ def test_growing_scores_move_the_reference(hq, hkv, d, rows):
         c.check()
 
 
+@pytest.mark.parametrize("hq,hkv,d,rows", [(8, 2, 64, 9), (8, 2, 128, 70), (6, 2, 256, 9), (6, 2, 256, 60), (6, 1, 256, 21)])
+def test_growing_scores_of_an_nvfp4_cache(hq, hkv, d, rows):
+    """K's block scales grow from 2^-4 to 8 along the context."""
+    for splits in (0, 1, 2):
+        c = Case([rows], [1500], hq, hkv, d, tree=True, kv="nvfp4", sm_scale=0.2, force_splits=splits, seed=17)
+        for j, s in enumerate(c.slots[0]):
+            c.scales[0][s // c.ps, :, s % c.ps] = 0x18 + 0x38 * j // c.lens[0]
+        c.run()
+        c.check()
+
+
 @pytest.mark.parametrize("splits", [0, 1, 3])
 @pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (32, 8, 128), (6, 2, 256)])
 def test_rows_that_see_nothing(hq, hkv, d, splits):
