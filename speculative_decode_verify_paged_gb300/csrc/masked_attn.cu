@@ -11,7 +11,8 @@
 // One CTA = (NQ query tiles of 128 rows) x (one KV head) x (a split of the keys).  A
 // tile holds 128 / G whole window rows with their G heads, so K and V are read once
 // for the G heads; NQ = 2 (d = 128) shares every K and V tile between two query tiles,
-// one's products under the other's softmax.
+// one's products under the other's softmax.  The plan takes the query tiles and the
+// splits by a model of the call's time (choose_split).
 //
 // Keys.  The pages a CTA's rows can see are at most two runs: the sinks' and those
 // from its first row's window on.  They are walked as one list of pages, 64 keys a
@@ -24,26 +25,39 @@
 // NaN); masked scores are replaced, so K may hold anything there.
 //
 // Warp roles:
-//   warp 0      the query tiles, then the K tiles, by TMA into one ring of slots with
-//               the V tiles of warp 3, 128-byte swizzle.  NVFP4: codes and scales into a
-//               raw ring.
+//   warp 0      the query tiles, then the K tiles, by TMA, 128-byte swizzle.  NVFP4:
+//               codes by TMA and scales by plain asynchronous copies into a raw ring.
 //   warps 1, 2  issue the products, one elected thread each.  NQ = 2: warp 1 + i
 //               issues S_{t+1} and then P_t V_t of tile i.  NQ = 1: warp 1 issues
 //               S = Q K^T and warp 2 O += P V.
 //   warp 3      owns tensor memory; the V tiles.
-//   warps 4-7 (and 8-11 for the second tile)   softmax, a row a thread, and epilogue.
-//   NVFP4: warps 8-11 decode K and 12-15 V into fp16 operand tiles of the same ring;
-//               query rows and weights are fp16 too.
+//   warps 4-7   softmax, a row a thread, and epilogue; 8-11 the same for the second
+//               query tile, or for every other key tile of the only one (kStreams).
+//   NVFP4: warps 8-11 decode K and 12-15 V into fp16 operand tiles; query rows and
+//               weights are fp16 too.
 //
 // Tensor memory: O tiles [0, NQ d), two or four S buffers of 64 columns a tile, P in the
 // first half of its S buffer, and where there is room (one tile, the SM to itself) the
 // query tile, which frees its shared memory and doubles the first product's rate.
+//
+// Epilogue.  Rows wait in shared memory so that they leave in memory order, 16 bytes a
+// thread: as bf16 where the CTA's row is the result, else in fp32.
 //
 // Splits.  Up to 8 of them form a cluster: each leaves its normalised rows in fp32 with
 // their log-sum-exps in its own shared memory, and after a cluster barrier every CTA
 // combines a share of the rows from its peers' shared memory.  More leave their rows
 // in the workspace as fp16 of the row's largest element (off by at most 2^-12 of it),
 // and a second kernel joins them.  Both in an order that the split fixes.
+//
+// Bound, with times of a launch in a graph.  A tile of 64 keys takes 0.44 us at d 64,
+// 0.51 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.54, 0.60,
+// 0.79; a launch starts and ends in 5-8 us beside its tiles.  At d 256 bf16 the copies
+// bound it: 64 KB a tile at 43 bytes a clock into an SM (48 nodes over 64K keys 77 us).
+// At d 128 two query tiles keep the tensor cores busy for 1280 of 1490 clocks (a prompt
+// of 2049 rows under a window of 2048: 67 us, 1.7 rounds of CTAs taking 2).  NVFP4 is bound
+// by the chain scores, softmax, P V beside the decoders (4 trees of 32 nodes over 16384
+// keys of d 256: 64 us).  One token of a request reads at 91 % of a copy's rate (64 of
+// them under a window of 4096: 153 us).
 //
 // Every wait is bounded; on time-out the CTA sets the device-status bit, drains its
 // copies and products, frees its tensor memory and leaves.
