@@ -52,7 +52,7 @@
 // Bound, with times of a launch in a graph.  A tile of 64 keys takes 0.44 us at d 64,
 // 0.51 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.54, 0.60,
 // 0.79; a launch starts and ends in 5-8 us beside its tiles.  At d 256 bf16 the copies
-// bound it: 64 KB a tile at 43 bytes a clock into an SM (48 nodes over 64K keys 77 us).
+// bound it: 64 KB a tile at 43 bytes a clock into an SM (48 nodes over 64K keys 75 us).
 // At d 128 two query tiles keep the tensor cores busy for 1280 of 1490 clocks (a prompt
 // of 2049 rows under a window of 2048: 67 us, 1.7 rounds of CTAs taking 2).  NVFP4 is bound
 // by the chain scores, softmax, P V beside the decoders (4 trees of 32 nodes over 16384
@@ -89,6 +89,7 @@ constexpr int kMaxRing = 14;
 constexpr int kMaxRaw = 8;
 constexpr int kMaxSorted = 256;         // requests put in order by one CTA's threads
 constexpr int kMaxCluster = 8;          // CTAs of a cluster that any GPU schedules
+constexpr int kJoinBatch = 16;          // splits whose rows a joining thread has on their way at once (8: 19 splits 15.5 us, not 13.4)
 constexpr float kRescale = 8.0f;        // log2 units: O is rescaled when a row's maximum grows by more
 
 struct MaskedParams {
@@ -1084,7 +1085,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 // Joins the splits' rows: O = sum_s 2^(lse_s - lse) O_s, in split order.  A thread an 8-element piece of a (row, head).
 template <int D>
 __global__ void __launch_bounds__(256) masked_join_kernel(const __grid_constant__ MaskedParams p) {
-    constexpr int C8 = D / 8, kBatch = 8;
+    constexpr int C8 = D / 8, kBatch = kJoinBatch;
     pdl_wait_primary();
     pdl_launch_dependents();
     ReqInfo ri;
@@ -1296,10 +1297,13 @@ MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, doub
         const double waves = std::ceil(static_cast<double>(ctas) * (splits > 1 ? mean : 1.0) / static_cast<double>(at_once));
         const double tiles = static_cast<double>(u) * (splits == 1 && waves > 1.0 ? mean : 1.0);
         const double cta = alone ? fixed_alone + tiles * tile_alone : fixed_shared + tiles * tile_shared;
+        const int64_t batches = (splits + spec_attn::kJoinBatch - 1) / spec_attn::kJoinBatch;
         const double join = splits == 1                        ? 0.0
                             : splits <= spec_attn::kMaxCluster ? cluster
-                                                               : 2.6 + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * d * 4.0 / 1e7;
-        const double cost = std::max(waves * cta, hbm + fixed_alone) + join;
+                                                               : 2.1 + 0.95 * batches + static_cast<double>(splits) * p.num_reqs * rows * p.num_q_heads * d * 4.0 / 1e7;
+        // (HBM's time and the SMs' overlap, not wholly)
+        const double inside = waves * cta, outside = hbm + fixed_alone;
+        const double cost = std::max(inside, outside) + 0.3 * std::min(inside, outside) + join;
         if (cost < best.cost * 0.98) best = {cost, static_cast<int>(u)};
     }
     return best;
