@@ -33,8 +33,9 @@
 //   warp 3      owns tensor memory; the V tiles.
 //   warps 4-7   softmax, a row a thread, and epilogue; 8-11 the same for the second
 //               query tile, or for every other key tile of the only one (kStreams).
-//   NVFP4: warps 8-11 decode K and 12-15 V into fp16 operand tiles; query rows and
-//               weights are fp16 too.
+//   NVFP4: the warps behind them decode K and V into fp16 operand tiles (8 warps at
+//               d 256, 4 otherwise, in teams that take the tiles in turn); query rows
+//               and weights are fp16 too.
 //
 // Tensor memory: O tiles [0, NQ d), two or four S buffers of 64 columns a tile, P in the
 // first half of its S buffer, and where there is room (one tile, the SM to itself) the
@@ -50,8 +51,8 @@
 // and a second kernel joins them.  Both in an order that the split fixes.
 //
 // Bound, with times of a launch in a graph.  A tile of 64 keys takes 0.44 us at d 64,
-// 0.51 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.54, 0.60,
-// 0.79; a launch starts and ends in 5-8 us beside its tiles.  At d 256 bf16 the copies
+// 0.52 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.47, 0.53,
+// 0.80; a launch starts and ends in 5-8 us beside its tiles.  At d 256 bf16 the copies
 // bound it: 64 KB a tile at 43 bytes a clock into an SM (48 nodes over 64K keys 75 us).
 // At d 128 two query tiles keep the tensor cores busy for 1280 of 1490 clocks (a prompt
 // of 2049 rows under a window of 2048: 67 us, 1.7 rounds of CTAs taking 2).  NVFP4 is bound
@@ -212,7 +213,7 @@ struct MaskedLayout {
     // Key streams: two softmax warpgroups take the query tile's key tiles in turn, each with an O tile and a running
     // maximum and sum of its own, and their rows are joined at the end.  A lone group is bound by its chain of latencies
     // (barrier, scores, maximum, exponentials, weights, barrier: 950 clocks a tile, of them 350 exponentials).
-    static constexpr int kStreams = NQ == 1 && DEEP && !FP4 && D <= 128 ? 2 : 1;
+    static constexpr int kStreams = NQ == 1 && DEEP && D <= 128 ? 2 : 1;
     static constexpr int kGroups = NQ * kStreams;          // softmax warpgroups, and O tiles
     // Layout of a bf16 tile: unit-major, a unit 16 keys, [unit][chunk][16 keys][128 bytes], so that a copy takes a whole unit
     // of V (4 KB at d = 128).  K comes 8 keys a copy, [8 keys' group][chunk][8][128 bytes]: its groups then have one stride
@@ -249,8 +250,8 @@ struct MaskedLayout {
     static constexpr int kRingK = NQ == 2 ? kRing : (kRing + 1) / 2, kRingV = NQ == 2 ? kRing : kRing / 2;
     __host__ __device__ static constexpr int k_slot(int t) { return t % kRingK; }
     __host__ __device__ static constexpr int v_slot(int t) { return NQ == 2 ? t % kRing : kRingK + t % kRingV; }
-    static constexpr int kRawFit = (kMax - 1024 - kAux - kRing * kTileBytes) / MaskedRaw<D>::kSlot;
-    static constexpr int kRaw = !FP4 ? 0 : kRawFit > kMaxRaw ? kMaxRaw : kRawFit & ~1;   // (even: a slot is one pair's of decoders)
+    static constexpr int kRawFit = (kMax - 1024 - kAux - kQSmem - kRing * kSlotBytes) / MaskedRaw<D>::kSlot;
+    static constexpr int kRaw = !FP4 ? 0 : kRawFit > kMaxRaw ? kMaxRaw : kRawFit & ~1;   // (even: a slot is one team's of two)
     static constexpr int kTail = kRing * kSlotBytes + kRaw * MaskedRaw<D>::kSlot;   // ring and raw ring, adjacent
     static constexpr int kSmem = 1024 + kAux + kQSmem + kTail;
     static constexpr int kLead = kBufs;                    // tiles by which S leads P V at most
@@ -261,7 +262,11 @@ struct MaskedLayout {
     // largest elements
     static constexpr int kRowFloats = D + 4, kRow16 = D * 2 + 16;
     static_assert(kGroups * kM * (kRowFloats + 2) * 4 <= kQSmem + kTail, "epilogue staging");
-    static constexpr int kThreads = FP4 ? 512 : 128 + kGroups * 128;
+    // NVFP4: two teams of decoding warps for K and two for V take the tiles in turn.  (What a tile takes a team is mostly
+    // waits, stores and the fence behind them, 800 clocks: two teams of a warp at d 128 0.53 us a tile, one of two 0.60.)
+    static constexpr int kTeam = D == 256 ? 2 : 1;         // warps of a team
+    static constexpr int kDecoder0 = 4 + 4 * kGroups;      // the first of them: K's, then as many of V's
+    static constexpr int kThreads = 128 + kGroups * 128 + (FP4 ? 4 * kTeam * 32 : 0);
 };
 
 struct MaskedAux {
@@ -269,12 +274,12 @@ struct MaskedAux {
     uint64_t empty[kMaxRing];           // NQ = 1
     uint64_t pv_done[2][kMaxRing];      // P_t V_t of tile i done: O, P_t's buffer and (NQ = 2) the slot; by t mod kPv
     uint64_t q_full[2];
-    uint64_t q_ready;                   // the query tile is in tensor memory (four softmax warps)
+    uint64_t q_ready;                   // the query tile is in tensor memory, or converted (four softmax warps)
     uint64_t s_full[2][4];              // [tile][buffer] scores written
     uint64_t p_full[2][4];              // P written over them (four softmax warps)
     uint64_t p_half[2];                 // its first 32 keys (kHalves)
     uint64_t raw_full[kMaxRaw];
-    uint64_t raw_empty[kMaxRaw];        // four decoding warps
+    uint64_t raw_empty[kMaxRaw];        // the decoding warps of a tile's K and V
     uint64_t drain[2];
     uint32_t tmem_base;
     int abort;
@@ -305,15 +310,15 @@ __device__ __forceinline__ void e4m3x4_pairs_f16x2(uint32_t w, uint32_t (&s2)[4]
     s2[3] = __byte_perm(hi, 0, 0x3232);
 }
 
-// Two decoding warps' work on a tile: the K or V codes of the raw slot into the fp16 operand tile, chunk-major, 128-byte
+// A decoding team's work on a tile: the K or V codes of the raw slot into the fp16 operand tile, chunk-major, 128-byte
 // swizzle; columns that no row may see as zeros.  A unit is one key's 64 elements (32 code bytes, 4 scales, one 128-byte
 // row); eight consecutive keys run side by side, so that the row stores hit distinct banks.  A thread's keys lie a constant
 // apart: with the passes unrolled every address is a constant off one of a few registers (a tile of d 256 0.92 -> 0.85 us).
-template <int D>
+template <int D, int Threads>
 __device__ __forceinline__ void decode_tile(const unsigned char* codes, const unsigned char* scales, unsigned char* tile,
                                             uint64_t live, int dt) {
     using R = MaskedRaw<D>;
-    constexpr int CPK = D / 64, kRows = 64 / CPK;   // rows a pass: multiples of 16, so that passes differ by constants
+    constexpr int CPK = D / 64, kRows = Threads / CPK;   // rows a pass: multiples of 16, so that passes differ by constants
     const int j0 = dt / (8 * CPK) * 8 + (dt & 7), c = (dt >> 3) % CPK, unit = j0 >> 4, sl = j0 & 15;
     const unsigned char* kr = codes + unit * R::kCodes + sl * (D / 2);
     const int w0_at = raw_code_chunk<D>(sl, 2 * c) * 16, w1_at = raw_code_chunk<D>(sl, 2 * c + 1) * 16;
@@ -324,7 +329,7 @@ __device__ __forceinline__ void decode_tile(const unsigned char* codes, const un
     for (int q = 0; q < 8; ++q) at[q] = (q ^ (j0 & 7)) << 4;
     const bool whole = live == ~0ull;
 #pragma unroll
-    for (int i = 0; i < CPK; ++i) {
+    for (int i = 0; i < kBN / kRows; ++i) {
         constexpr int kUnits = kRows / 16;
         if (whole || (live >> (j0 + i * kRows) & 1)) {
             const uint4 w0 = *reinterpret_cast<const uint4*>(kr + i * kUnits * R::kCodes + w0_at);
@@ -370,12 +375,12 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 
     if (tid == 0) {
         for (int s = 0; s < RING; ++s) {
-            mbar_init(&aux->full[s], FP4 ? 2 : NQ);
+            mbar_init(&aux->full[s], FP4 ? L::kTeam : NQ);
             mbar_init(&aux->empty[s], 1);
         }
         for (int s = 0; s < L::kRaw; ++s) {
             mbar_init(&aux->raw_full[s], 2 + 64);          // codes by either producer, scales by all their lanes
-            mbar_init(&aux->raw_empty[s], 4);
+            mbar_init(&aux->raw_empty[s], 2 * L::kTeam);
         }
         for (int i = 0; i < NQ; ++i) {
             for (int s = 0; s < PV; ++s) mbar_init(&aux->pv_done[i][s], 1);
@@ -656,7 +661,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             return true;
         };
         bool ok = true;
-        if (NQ == 2 || warp == 1) ok = wait(L::kQT ? &aux->q_ready : &aux->q_full[i], 0);
+        if (NQ == 2 || warp == 1) ok = wait(L::kQT || FP4 ? &aux->q_ready : &aux->q_full[i], 0);
         tc_fence_after();
         if (NQ == 2) {
             ok = ok && do_s(0);
@@ -672,21 +677,20 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         volatile int no_abort = 0;
         mbar_wait(drain, 0, &no_abort, kDrainLimit);
         __syncwarp();
-    } else if (FP4 && warp >= 8) {
-        // ------------------------------------------------------------ NVFP4: K (warps 8-11) and V (12-15) into operand tiles,
-        // two warps a tile, the pairs in turn: what a tile takes a warp is mostly waits, stores and the fence behind them
-        const bool is_v = warp >= 12;
+    } else if (FP4 && warp >= L::kDecoder0) {
+        // ------------------------------------------------------------ NVFP4: K and V into operand tiles
+        const bool is_v = warp >= L::kDecoder0 + 2 * L::kTeam;
         const Tiles whole = tiles_within(span, p.page_shift, span.base, span.hi);
-        for (int t = warp >> 1 & 1; t < T; t += 2) {
+        for (int t = warp / L::kTeam & 1; t < T; t += 2) {
             const int slot = is_v ? L::v_slot(t) : L::k_slot(t), lap = t / (is_v ? L::kRingV : L::kRingK), rs = t % max(1, L::kRaw);
             const uint64_t live = whole.has(t0 + t) ? ~0ull : live_columns(p, span, columns_of(span, p.page_shift, t0 + t));
             if (!wait_warp(&aux->raw_full[rs], (t / max(1, L::kRaw)) & 1, abort)) break;
             if (lap > 0 && !wait_warp(&aux->empty[slot], (lap - 1) & 1, abort)) break;
             // (the query tile has to leave the last two slots first)
-            if (is_v && t >= L::kRingV - 2 && t < L::kRingV && !wait_warp(&aux->q_ready, 0, abort)) break;
+            if (L::kQT && is_v && t >= L::kRingV - 2 && t < L::kRingV && !wait_warp(&aux->q_ready, 0, abort)) break;
             const unsigned char* src = raw + rs * R::kSlot;
-            decode_tile<D>(src + (is_v ? R::kVC : 0), src + (is_v ? R::kVS : R::kKS), ring + slot * L::kTileBytes, live,
-                           tid & 63);
+            decode_tile<D, L::kTeam * 32>(src + (is_v ? R::kVC : 0), src + (is_v ? R::kVS : R::kKS), ring + slot * L::kTileBytes,
+                                          live, tid & (L::kTeam * 32 - 1));
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
@@ -728,6 +732,25 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                 tmem_wait_st();
                 fence_proxy_async_smem();                  // (the slots are written by copies next)
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->q_ready);
+            }
+        }
+        if (FP4 && !L::kQT && g == 0) {
+            // the query row to fp16 in its place (as above)
+            if ((ok = wait_warp(&aux->q_full[0], 0, abort))) {
+                const uint32_t row = smem_addr(sQ) + m * 128;
+#pragma unroll 1
+                for (int c = 0; c < L::kChunks; ++c) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t at = row + c * (kM * 128) + ((q ^ (m & 7)) << 4);
+                        const uint4 v = valid ? ld_shared_v4(at) : make_uint4(0u, 0u, 0u, 0u);
+                        st_shared_v4(at, make_uint4(bf16x2_to_f16x2_sat(v.x), bf16x2_to_f16x2_sat(v.y),
+                                                    bf16x2_to_f16x2_sat(v.z), bf16x2_to_f16x2_sat(v.w)));
+                    }
+                }
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&aux->q_ready);
             }
@@ -1279,7 +1302,7 @@ MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, doub
     const double fixed_shared = whole ? fixed_alone : fixed_alone + 3.5 * part * part;
     const double tile_alone = nq == 2    ? 0.71
                               : d == 256 ? 0.79
-                              : fp4      ? (d == 64 ? 0.54 : 0.60)
+                              : fp4      ? (d == 64 ? 0.47 : 0.53)
                               : d == 64  ? 0.44
                                          : 0.46 + 0.12 * part;
     const double tile_shared = whole ? tile_alone : (d == 64 ? 0.33 : 0.42) * (1.0 + cta_rows / 128.0);
