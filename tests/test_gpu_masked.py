@@ -429,6 +429,30 @@ def test_more_work_than_the_gpu_holds(hq, hkv, d, P, rows, kv):
     c.check()
 
 
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("hq,hkv,d,P", [(16, 8, 64, 45), (32, 8, 128, 45), (24, 4, 256, 45), (6, 1, 256, 256)])
+def test_requests_of_all_lengths_in_rounds(hq, hkv, d, P, kv):
+    """More CTAs than the GPU holds, of spans long enough that the longest requests go first: lengths of every size, equal
+    ones, requests without rows or keys."""
+    rng = random.Random(P + d)
+    rows = [rng.choice((0, 1, 1, 2)) for _ in range(P)]
+    for lens in ([rng.choice((0, 1, 63, 64, 100, 700, 700, 1400)) for _ in range(P)], [1000] * P):
+        ctx = [1400] + lens[1:]
+        c = Case([1] + rows[1:], ctx, hq, hkv, d, tree=True, kv=kv, seed=P)
+        c.run()
+        c.check()
+        c.o.fill_(MARK), c.lse.fill_(MARK)
+        c.seq[7] = 2 ** 30                                 # a length that cannot be
+        c.run()
+        at = sum(c.rows[:7])
+        assert bool((c.o[at:at + c.rows[7]] == MARK).all())
+        want = sa.SPEC_ATTN_DEV_BAD_SEQ_LEN if c.rows[7] else 0
+        assert sa.spec_attn_check_device_status(c.ws) == want
+        sa.spec_attn_reset_device_status(c.ws)
+        c.seq[7] = c.lens[7]
+        c.check(skip=(7,) if c.rows[7] else ())
+
+
 def test_a_chain_without_a_window_is_the_window_attention():
     """Every window of up to 16 rows: the same numbers as spec_attn_run's, as far as both are rounded."""
     c = Case([9, 16, 1], [500, 33, 700], 32, 8, 128, seed=15)
