@@ -65,6 +65,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -102,7 +103,7 @@ struct MaskedParams {
     uint16_t* o;
     float* lse;
     unsigned int* status;
-    float2* ws_ls;              // partials: per split and (row, head): (log2 of the sum, largest |element|)
+    float2* ws_ls;              // partials: per split and (row, head): (log2 of the sum, largest |element|, at least FLT_MIN)
     uint16_t* ws_o;             //   and the row's elements over it, fp16
     int total_rows, max_w, num_q_heads, num_kv_heads, group;
     int page_shift;             // log2(page_size)
@@ -1074,8 +1075,10 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                     if (c == 0 && p.lse) p.lse[at] = lse[k] * kLn2;
                 } else {
                     // (two streams' joined row: its largest element or more)
-                    const float most = KS == 2 ? stage_max[m] + stage_max[kM + m] : stage_max[m];
-                    const float s = most > 0.f ? 1.f / most : 0.f;
+                    // (at least the smallest normal number: its reciprocal is finite, where 1 / 2^-129 would make infinities of
+                    // the row's elements and NaN of its zeros)
+                    const float most = fmaxf(KS == 2 ? stage_max[m] + stage_max[kM + m] : stage_max[m], FLT_MIN);
+                    const float s = 1.f / most;
                     st_global_v4(p.ws_o + (part + at) * D + c * 8,
                                  make_uint4(pack_half2(a[k].x * s, a[k].y * s), pack_half2(a[k].z * s, a[k].w * s),
                                             pack_half2(b[k].x * s, b[k].y * s), pack_half2(b[k].z * s, b[k].w * s)));
