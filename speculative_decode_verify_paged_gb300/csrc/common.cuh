@@ -156,6 +156,11 @@ __device__ __forceinline__ bool load_request(const int32_t* seq_lens, const int3
     return true;
 }
 
+// The scale of a split's partial row, O_s = inv * acc: its largest |O_s|, but not so small that inv / scale, by which the
+// accumulated elements are multiplied, could be infinite (0 x infinity would be NaN).  From 2^-124 inv on it is below 2^125;
+// where that product is 0, inv is below 2^-25 and inv / scale below 2^124 for every scale there is.
+__device__ __forceinline__ float partial_scale(float largest, float inv) { return fmaxf(largest, inv * 0x1p-124f); }
+
 // Programmatic dependent launch controls (sm_90+).
 __device__ __forceinline__ void pdl_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -117,7 +117,8 @@ struct AppendParams {
 };
 
 // Split partials.  A split leaves, per (window row, query head) pair, its
-// normalised partial output O_s (d values), lse_s and scale_s = max_e |O_s[e]|;
+// normalised partial output O_s (d values), lse_s and scale_s = max_e |O_s[e]|
+// (not below a floor: partial_scale in common.cuh);
 // O_s is stored as d fp16 values of O_s / scale_s (in [-1, 1]), so a stored
 // value is off by at most scale_s * 2^-12, and the partials take half the bytes
 // of fp32 for the split kernel to write and the merge to read.

@@ -379,6 +379,7 @@ split_attn_cc_kernel(const SplitParams p, const int stages) {
             for (int e = 0; e < DPL; ++e) amax = fmaxf(amax, fabsf(o_acc[t][e] * inv_l));
 #pragma unroll
             for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, off));
+            amax = partial_scale(amax, inv_l);
             const float sc = amax > 0.f ? inv_l / amax : 0.f;
             // this lane's DPL values: elements lane * DPL .. of the row, inside
             // chunk lane * DPL / 8 of the request's chunk-major block

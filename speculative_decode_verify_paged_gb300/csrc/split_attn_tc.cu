@@ -1033,6 +1033,7 @@ split_attn_tc_kernel(const SplitParams p, const __grid_constant__ CUtensorMap tm
         named_barrier_sync(1, 256);
         if (rows_here) {
             amax = fmaxf(ep[kM + mrow], ep[2 * kM + mrow]);
+            amax = partial_scale(amax, inv);
             const float rsc = amax > 0.f ? inv / amax : 0.f;
             const bool row_ok = mrow < R;
             if (warp >= 4 && row_ok)

@@ -1,7 +1,8 @@
 """Rows of splits that wait in 16 bits, with values below the smallest normal number.
 
-A split's row is held as fp16 of a scale that is its largest element, at least 2^-126.  A row whose values are all below
-that may also be taken as zeros by the products: such results are compared to 2^-126."""
+A split's row is held as fp16 of a scale that is its largest element, but not below 2^-126 (under masks) or 2^-124 over its
+sum of weights (the draft's windows).  A row whose values are all below 2^-126 may also be taken as zeros by the products:
+such results are compared to 2^-126."""
 import math
 
 import pytest
@@ -66,3 +67,30 @@ def test_one_smallest_normal_element_among_zeros(hq, hkv, d):
     c.pools[1][s // c.ps, :, s % c.ps, 3] = TINY
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
+@pytest.mark.parametrize("mode", ["cuda_core", "tcgen05", "w_invariant"])
+@pytest.mark.parametrize("hq,hkv,d", [(8, 2, 64), (32, 8, 128), (6, 2, 256)])
+def test_values_below_the_normal_range_in_windows(hq, hkv, d, mode, kv):
+    """The same for the draft's windows, split by either kernel; a 4-bit cache by its global scale."""
+    for keys in (1409, 700):
+        if kv == "nvfp4" and keys == 700:
+            continue
+        c = Case([3, 9], [1200, 1400], hq, hkv, d, kv=kv, seed=5)
+        if kv == "bf16":
+            make_tiny(c, keys)
+        else:
+            c.gscale = (0.3, 2.0 ** -140)
+        over = dict(w_invariant=1, fixed_keys_per_split=128) if mode == "w_invariant" else dict(
+            force_splits=11, kernel_variant=sa.SPEC_ATTN_VARIANT_TCGEN05 if mode == "tcgen05" else
+            sa.SPEC_ATTN_VARIANT_CUDA_CORE)
+        plan = sa.spec_attn_plan_create(
+            num_reqs=2, total_q_rows=c.q.shape[0], max_w=9, num_q_heads=hq, num_kv_heads=hkv, head_dim=d,
+            num_pages=c.pages, block_table_stride=c.table.shape[1], max_seq_len=1409, kv_dtype=int(kv == "nvfp4"), **over)
+        assert plan.info["max_splits"] > 1
+        ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
+        sa.spec_attn_run(plan, c.q, *c.pools, c.table, c.seq, c.indptr, c.o, c.lse, ws, *c.scales, *c.gscale)
+        assert sa.spec_attn_check_device_status(ws) == 0
+        tol = TINY if keys == 1409 else 2.0 ** -6 * float(c.pools[1].nan_to_num(0).abs().max())
+        assert float((c.o[:12].double() - attention(c)).abs().max()) <= tol
