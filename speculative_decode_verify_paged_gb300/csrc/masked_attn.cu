@@ -47,8 +47,8 @@
 // Splits.  Up to 8 of them form a cluster: each leaves its normalised rows in fp32 with
 // their log-sum-exps in its own shared memory, and after a cluster barrier every CTA
 // combines a share of the rows from its peers' shared memory.  More leave their rows
-// in the workspace as fp16 of the row's largest element (off by at most 2^-12 of it),
-// and a second kernel joins them.  Both in an order that the split fixes.
+// in the workspace as fp16 of the row's largest element (off by at most 2^-12 of it, and of
+// 2^-126), and a second kernel joins them.  Both in an order that the split fixes.
 //
 // Bound, with times of a launch in a graph.  A tile of 64 keys takes 0.44 us at d 64,
 // 0.52 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.47, 0.53,
@@ -983,7 +983,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 64; e += 4) {
                             const float4 x = make_float4(ov[e] * inv, ov[e + 1] * inv, ov[e + 2] * inv, ov[e + 3] * inv);
-                            most = fmaxf(fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
+                            if (KS == 1) most = fmaxf(fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(x.z), fabsf(x.w)));
                             *reinterpret_cast<float4*>(row + ch * 32 + e) = x;
                         }
                     }
@@ -992,7 +992,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             }
             if (valid) {
                 stage_lse[sr] = lse;
-                stage_max[sr] = most;
+                if (KS == 1) stage_max[sr] = most;
             }
         }
     }
@@ -1074,10 +1074,19 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
                                                                   pair(b[k].x, b[k].y), pair(b[k].z, b[k].w)));
                     if (c == 0 && p.lse) p.lse[at] = lse[k] * kLn2;
                 } else {
-                    // (two streams' joined row: its largest element or more)
+                    // the row's largest element; of two streams' joined row, whose parts may cancel, by the lanes that hold it
+                    float most = KS == 2 ? 0.f : stage_max[m];
+                    if (KS == 2) {
+                        most = fmaxf(fmaxf(fmaxf(fabsf(a[k].x), fabsf(a[k].y)), fmaxf(fabsf(a[k].z), fabsf(a[k].w))),
+                                     fmaxf(fmaxf(fabsf(b[k].x), fabsf(b[k].y)), fmaxf(fabsf(b[k].z), fabsf(b[k].w))));
+                        // (a row's C8 pieces are in as many neighbouring lanes, which go on or leave together)
+                        const unsigned lanes = static_cast<unsigned>(low_bits(C8)) << (lane & ~(C8 - 1));
+#pragma unroll
+                        for (int x = 1; x < C8; x <<= 1) most = fmaxf(most, __shfl_xor_sync(lanes, most, x));
+                    }
                     // (at least the smallest normal number: its reciprocal is finite, where 1 / 2^-129 would make infinities of
                     // the row's elements and NaN of its zeros)
-                    const float most = fmaxf(KS == 2 ? stage_max[m] + stage_max[kM + m] : stage_max[m], FLT_MIN);
+                    most = fmaxf(most, FLT_MIN);
                     const float s = 1.f / most;
                     st_global_v4(p.ws_o + (part + at) * D + c * 8,
                                  make_uint4(pack_half2(a[k].x * s, a[k].y * s), pack_half2(a[k].z * s, a[k].w * s),

@@ -1,4 +1,4 @@
-"""Rows of splits that wait in 16 bits, with values below the smallest normal number.
+"""Rows of splits that wait in 16 bits, with values below the smallest normal number and with streams of keys that cancel.
 
 A split's row is held as fp16 of a scale that is its largest element, but not below 2^-126 (under masks) or 2^-124 over its
 sum of weights (the draft's windows).  A row whose values are all below 2^-126 may also be taken as zeros by the products:
@@ -67,6 +67,23 @@ def test_one_smallest_normal_element_among_zeros(hq, hkv, d):
     c.pools[1][s // c.ps, :, s % c.ps, 3] = TINY
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (32, 8, 128)])
+def test_streams_of_keys_that_cancel(hq, hkv, d):
+    """Nine splits of two tiles of 64 keys, of equal weights: the first tile's values are 4096 sixty-three times, the
+    second's -4096, and one key of the first is s = 1 + e / 64.  All sums are exact in 32 bits, so that a split's row is
+    s / 128, off by at most 2^-12 of its largest element, below 2 / 128, and the result rounded once."""
+    c = Case([1], [9 * 128 - 1], hq, hkv, d, force_splits=9, seed=3)
+    c.q[:1] = 0
+    e = 1 + (torch.arange(d, device="cuda") % 64) / 64
+    for j, s in enumerate(c.slots[0]):
+        big = 4096.0 if j % 128 < 64 else -4096.0
+        c.pools[1][s // c.ps, :, s % c.ps] = (e if j % 128 == 63 else e * 0 if j % 128 == 127 else e * 0 + big).bfloat16()
+    c.run()
+    want = (e.double() / 128).expand(hq, d)
+    assert bool(((c.o[0].double() - want).abs() <= 2.0 ** -8 * want + (2.0 ** -12 + 2.0 ** -20) * 2 / 128).all())
+    assert float((c.lse[0].double() - math.log(9 * 128)).abs().max()) <= 1e-5
 
 
 @pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
