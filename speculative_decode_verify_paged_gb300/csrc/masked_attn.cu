@@ -453,15 +453,6 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         __syncthreads();
         r = aux->request;
     }
-    // Without a window a split's first table entries sit at a known place: the producers fetch them in the same round trip as
-    // the request's window and length (entries past its pages are not used).
-    const int32_t* const table = p.block_table + (size_t)r * p.bt_stride;
-    const int v0 = split * p.tiles_per_split << (6 - p.page_shift);   // the split's first page in the list
-    int early0 = 0, early1 = 0;
-    if (!p.window && (warp == 0 || warp == 3)) {
-        if (v0 + lane < p.bt_stride) early0 = ld_volatile_i32(table + v0 + lane);
-        if (v0 + 32 + lane < p.bt_stride) early1 = ld_volatile_i32(table + v0 + 32 + lane);
-    }
     ReqInfo ri;
     const bool reporter = tid == 0 && blockIdx.x == 0 && kvh == 0;
     bool active = load_request(p.seq_lens, p.q_indptr, r, p.max_w, p.total_rows, p.max_seq_len,
@@ -469,11 +460,29 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     const int lo = tile * p.cta_rows;                      // first window row of the CTA
     active = active && lo < ri.w;
     Span span = {};
-    int nsplits = 0;
+    int nsplits = 0, T = 0;
+    const int t0 = split * p.tiles_per_split;              // its key tiles: T from here on
     if (active) {
         span = span_of(p, ri, lo);
         nsplits = (span.tiles + p.tiles_per_split - 1) / p.tiles_per_split;
-        active = split < nsplits;
+        T = min(p.tiles_per_split, span.tiles - t0);
+        active = T > 0;
+    }
+    // The split's pages, 32 at a time in the producers' lanes.  The first are asked for here, so that they come while the CTA
+    // meets; only entries of the request's pages are read: a table may end with the last of them.  (Without a window they could
+    // be asked for beside the lengths, a round trip earlier, whatever they hold: one tile of d 128 5.08 us, not 5.16.)
+    const int32_t* const table = p.block_table + (size_t)r * p.bt_stride;
+    const int v0 = t0 << (6 - p.page_shift);               // the split's first page in the list
+    const int pages = min(span.pages - v0, T << (6 - p.page_shift));
+    auto fetch = [&](int k) {
+        if (k >= pages) return 0;
+        const int v = v0 + k;
+        return ld_volatile_i32(table + (v < span.sink_pages ? v : v - span.sink_pages + span.first));
+    };
+    int early0 = 0, early1 = 0;
+    if (active && (warp == 0 || warp == 3)) {
+        early0 = fetch(lane);
+        early1 = fetch(32 + lane);
     }
     tc_fence_before();
     __syncthreads();
@@ -489,8 +498,6 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     const int G = p.group;
     const int nact = (NQ == 2 && lo + p.wt < ri.w) ? 2 : 1;
     const int rows = min(ri.w - lo, p.cta_rows) * G;       // query rows of the CTA, wt * G of them in its first tile
-    const int t0 = split * p.tiles_per_split;              // its key tiles
-    const int T = min(p.tiles_per_split, span.tiles - t0);
     // products of P V take whole 16-key steps: those of the request's last tile end with its keys
     int last_steps = kBN / 16;
     if (t0 + T == span.tiles) {
@@ -518,20 +525,13 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
         // ------------------------------------------------------------ copies: K by warp 0, V by warp 3
         const bool is_v = warp == 3;
         int issued = 0;
-        // the split's pages, 32 at a time in the lanes' registers, the next 32 on their way
         const int shift = p.page_shift, per_tile = 64 >> shift;
-        const int pages = min(span.pages - v0, T * per_tile);
-        auto fetch = [&](int k) {
-            if (k >= pages) return 0;
-            const int v = v0 + k;
-            return ld_volatile_i32(table + (v < span.sink_pages ? v : v - span.sink_pages + span.first));
-        };
         auto checked = [&](int k, int page) {
             if (k >= pages || (page >= 0 && page < p.num_pages)) return k < pages ? page : 0;
             atomicOr(p.status, kDevBadPage);
             return 0;
         };
-        int cur = p.window ? fetch(lane) : early0, next = p.window ? fetch(32 + lane) : early1, batch = 0;
+        int cur = early0, next = early1, batch = 0;        // (the next 32 on their way)
         if (warp == 0 && lane == 0) {
             const uint32_t qbytes = static_cast<uint32_t>(L::kChunks * 128 * G * p.wt);
             for (int i = 0; i < nact; ++i) {
