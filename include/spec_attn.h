@@ -706,11 +706,21 @@ int spec_attn_masked_plan_destroy(spec_attn_masked_plan* plan);
  * Arguments as spec_attn_run, the NVFP4 global scales positive and finite; row_mask
  * for trees only (ignored for chains), positions [total_q_rows] int32 for trees with
  * a window only (ignored otherwise).  lse may be NULL.  o, lse and workspace share no
- * byte with an input or with each other (SPEC_ATTN_E_INVALID_ARG).  NVFP4 caches:
- * elements of q beyond +-65504 count as that.  Up to 8 splits need 256 bytes of
- * workspace, the device-status word; more leave partial rows in it, and runs that may
- * overlap on the GPU then need workspaces of their own.  Asynchronous on `stream`,
- * allocation-free, graph capturable.
+ * byte with an input or with each other (SPEC_ATTN_E_INVALID_ARG).  Up to 8 splits need
+ * 256 bytes of workspace, the device-status word; more leave partial rows in it, and
+ * runs that may overlap on the GPU then need workspaces of their own.  Asynchronous on
+ * `stream`, allocation-free, graph capturable.
+ *
+ * What is held in 16 bits, beside O itself:
+ *   weights: bf16 in O's sum, unrounded in its divisor and in LSE.  NVFP4 caches: fp16
+ *     of the weight relative to a running reference that is at most a factor 256 below
+ *     the largest weight so far; what is below 2^-25 of it counts in the divisor but not
+ *     in O, which moves O by up to 2^-25 sum_j |v_j| of a split's keys.
+ *   q over NVFP4 caches: fp16; elements beyond +-65504 count as that, those below 2^-14
+ *     are rounded to multiples of 2^-24 (below 2^-25: to 0).
+ *   partial rows of more than 8 splits: fp16 of the row's largest element (or of 2^-126,
+ *     if that is larger), 2^-12 of which each split may be off; up to 8 splits keep fp32.
+ *     The number of splits is the plan's choice, or force_splits.
  */
 int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const void* k_pool, const void* v_pool,
                          const void* k_scales, const void* v_scales, float k_gscale, float v_gscale,
@@ -739,8 +749,10 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
  *   next_tokens[r]: the target token of the last (-1 without rows)
  *   ctx_lens[r] = ctx_r + accept_lens[r], the ctx_lens of the next step's
  *                 spec_attn_build_tables (whose prev_seq_lens are these seq_lens)
- * ctx_lens may be seq_lens.  draft_tokens [total_rows], target_tokens [total_rows] and
- * next_tokens [P] int64.
+ * draft_tokens [total_rows], target_tokens [total_rows] and next_tokens [P] int64.
+ * ctx_lens may be seq_lens, for a caller that keeps those lengths elsewhere: what
+ * comes next takes them as they were, window included -- spec_attn_move_kv as its
+ * seq_lens, the next step's spec_attn_build_tables as its prev_seq_lens.
  *
  * A window below 0, above max_w or past total_rows sets SPEC_ATTN_DEV_BAD_WINDOW, a
  * seq_len below its window SPEC_ATTN_DEV_BAD_SEQ_LEN; such a request's rows are left
@@ -776,6 +788,11 @@ int spec_attn_accept_tree(const spec_attn_tree_problem* problem, const int32_t* 
  * key ctx_r + i, for every KV head (NVFP4 caches: codes and scales, byte for byte).
  * Afterwards the request's first ctx_r + accept_lens[r] keys are its accepted text; a
  * chain needs no such call.  Nothing else is written.
+ *
+ * seq_lens are those that spec_attn_accept_tree took, window included: ctx_r =
+ * seq_lens[r] - W_r.  (Not the ctx_lens that it wrote, in a buffer of their own or over
+ * seq_lens: every key would be taken from and put W_r - accept_lens[r] places too low,
+ * over accepted text, and unless that lies before key 0 no check can tell.)
  *
  * h_k_pools, h_v_pools, h_k_scales, h_v_scales: host arrays of num_layers device
  * pointers, read before the call returns (the scales' NULL for bf16).  All layers

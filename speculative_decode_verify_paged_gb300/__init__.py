@@ -708,7 +708,8 @@ def spec_attn_build_tree(parents, seq_lens, q_indptr, positions, row_mask, works
 def spec_attn_accept_tree(parents, draft_tokens, target_tokens, seq_lens, q_indptr, path, accept_lens, next_tokens,
                           ctx_lens, workspace, *, max_w, stream=None):
     """The accepted path of every request's tree (asynchronous).  Tokens int64;
-    ctx_lens may be seq_lens."""
+    ctx_lens may be seq_lens if the caller keeps a copy of those: the move and
+    the next step's tables take the lengths as they were."""
     _check((_calls or _native()).accept_tree((max_w,), parents, draft_tokens, target_tokens, seq_lens, q_indptr, path,
                                              accept_lens, next_tokens, ctx_lens, workspace, stream),
            "spec_attn_accept_tree")
@@ -718,7 +719,9 @@ def spec_attn_move_kv(k_pools, v_pools, block_table, seq_lens, q_indptr, path, a
                       k_scales=None, v_scales=None, stream=None):
     """Move the accepted nodes' keys and values into place in every layer's
     cache (asynchronous).  Pools and scales: lists of one tensor [pages, Hkv,
-    page_size, row] a layer; layers share shapes and strides."""
+    page_size, row] a layer; layers share shapes and strides.  ``seq_lens`` as
+    spec_attn_accept_tree took them, window included, not the ctx_lens that it
+    wrote: with those, accepted text would be overwritten."""
     _check((_calls or _native()).move_kv((max_seq_len,), k_pools, v_pools, k_scales, v_scales, block_table, seq_lens,
                                          q_indptr, path, accept_lens, workspace, stream), "spec_attn_move_kv")
 
