@@ -702,6 +702,29 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
                                  size_t* workspace_bytes);
 int spec_attn_masked_plan_destroy(spec_attn_masked_plan* plan);
 
+/* What a plan decided; for tests, benches and logs. */
+typedef struct spec_attn_masked_plan_info {
+    int32_t query_tiles;         /* query tiles of 128 (row, head) pairs of a CTA: 1, or 2 that share its K and V tiles */
+    int32_t key_streams;         /* softmax groups that take a query tile's key tiles in turn: 1 or 2 */
+    int32_t ctas_per_sm;         /* 1 or 2 */
+    int32_t tiles_per_split;     /* tiles of 64 keys */
+    int32_t max_splits;          /* splits of the longest span */
+    int32_t join;                /* how splits are joined: 0 (one split), 1 (in a cluster), 2 (by a second kernel) */
+    int32_t longest_first;       /* 1: the requests with the most keys go first */
+    int32_t grid_x, grid_y, grid_z;
+    int32_t block_threads;
+    int32_t smem_bytes;          /* dynamic shared memory of the attention kernel */
+    int32_t num_sms;
+    size_t workspace_bytes;
+} spec_attn_masked_plan_info;
+
+int spec_attn_masked_plan_get_info(const spec_attn_masked_plan* plan, spec_attn_masked_plan_info* info);
+
+/* Testing only: with stall = 1 the plan's calls copy no K, so that the bounded waits behind
+ * it run out after about a second; a call then sets SPEC_ATTN_DEV_WAIT_TIMEOUT, frees its
+ * tensor memory and returns, leaving O undefined and the context usable.  0: as ever. */
+int spec_attn_masked_plan_set_test_stall(spec_attn_masked_plan* plan, int stall);
+
 /*
  * Arguments as spec_attn_run, the NVFP4 global scales positive and finite; row_mask
  * for trees only (ignored for chains), positions [total_q_rows] int32 for trees with

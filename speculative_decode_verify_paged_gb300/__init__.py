@@ -60,7 +60,8 @@ EXPORTED_SYMBOLS = (
     "spec_attn_run_append", "spec_attn_run_dense_block", "spec_attn_build_tables",
     "spec_attn_norm_rope_plan_create", "spec_attn_norm_rope_plan_destroy", "spec_attn_norm_rope",
     "spec_attn_norm_rope_append", "spec_attn_cross_plan_create", "spec_attn_cross_plan_destroy",
-    "spec_attn_run_cross", "spec_attn_masked_plan_create", "spec_attn_masked_plan_destroy", "spec_attn_run_masked",
+    "spec_attn_run_cross", "spec_attn_masked_plan_create", "spec_attn_masked_plan_destroy",
+    "spec_attn_masked_plan_get_info", "spec_attn_masked_plan_set_test_stall", "spec_attn_run_masked",
     "spec_attn_build_tree", "spec_attn_accept_tree", "spec_attn_move_kv",
 )
 
@@ -136,6 +137,16 @@ class spec_attn_masked_problem(ctypes.Structure):
         ("window_left", ctypes.c_int32), ("sink_keys", ctypes.c_int32), ("mask_row_words", ctypes.c_int32),
         ("force_splits", ctypes.c_int32), ("max_seq_len", ctypes.c_int64), ("kv_page_stride", ctypes.c_int64),
         ("scale_page_stride", ctypes.c_int64),
+    ]
+
+
+class spec_attn_masked_plan_info(ctypes.Structure):
+    _fields_ = [
+        ("query_tiles", ctypes.c_int32), ("key_streams", ctypes.c_int32), ("ctas_per_sm", ctypes.c_int32),
+        ("tiles_per_split", ctypes.c_int32), ("max_splits", ctypes.c_int32), ("join", ctypes.c_int32),
+        ("longest_first", ctypes.c_int32), ("grid_x", ctypes.c_int32), ("grid_y", ctypes.c_int32),
+        ("grid_z", ctypes.c_int32), ("block_threads", ctypes.c_int32), ("smem_bytes", ctypes.c_int32),
+        ("num_sms", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -232,6 +243,10 @@ def load_library(path: Optional[str] = None):
                                                      ctypes.POINTER(sz)]
         lib.spec_attn_masked_plan_destroy.restype = i32
         lib.spec_attn_masked_plan_destroy.argtypes = [vp]
+        lib.spec_attn_masked_plan_get_info.restype = i32
+        lib.spec_attn_masked_plan_get_info.argtypes = [vp, ctypes.POINTER(spec_attn_masked_plan_info)]
+        lib.spec_attn_masked_plan_set_test_stall.restype = i32
+        lib.spec_attn_masked_plan_set_test_stall.argtypes = [vp, i32]
         lib.spec_attn_run_masked.restype = i32
         lib.spec_attn_run_masked.argtypes = [vp] * 6 + [ctypes.c_float, ctypes.c_float] + [vp] * 8 + [sz, vp]
         lib.spec_attn_build_tree.restype = i32
@@ -663,6 +678,19 @@ class MaskedPlan:
         self.spec = (handle.value, p.num_reqs, p.total_q_rows, p.num_q_heads, p.num_kv_heads, p.head_dim, p.num_pages,
                      p.page_size, p.block_table_stride, p.kv_dtype, p.kv_page_stride, p.scale_page_stride, p.tree,
                      p.mask_row_words or -(-p.max_w // 32))
+
+    @property
+    def info(self):
+        """What the plan decided (spec_attn_masked_plan_info), by name."""
+        info = spec_attn_masked_plan_info()
+        _check(self._lib.spec_attn_masked_plan_get_info(self.handle, ctypes.byref(info)),
+               "spec_attn_masked_plan_get_info")
+        return {name: getattr(info, name) for name, _ in spec_attn_masked_plan_info._fields_}
+
+    def set_test_stall(self, stall):
+        """Testing only: let the waits of this plan's calls run out."""
+        _check(self._lib.spec_attn_masked_plan_set_test_stall(self.handle, int(stall)),
+               "spec_attn_masked_plan_set_test_stall")
 
     def __del__(self):
         h, self.handle = getattr(self, "handle", None), None

@@ -105,7 +105,7 @@ struct MaskedParams {
     unsigned int* status;
     float2* ws_ls;              // partials: per split and (row, head): (log2 of the sum, largest |element|, at least FLT_MIN)
     uint16_t* ws_o;             //   and the row's elements over it, fp16
-    int total_rows, max_w, num_q_heads, num_kv_heads, group;
+    int total_rows, max_w, num_q_heads, group;
     int page_shift;             // log2(page_size)
     int num_pages, bt_stride, tree, window, sinks, mask_words;
     int wt;                     // window rows of a query tile: 128 / group
@@ -115,6 +115,7 @@ struct MaskedParams {
     int max_splits;
     int cluster;                // the splits of a CTA's rows form a cluster
     int longest_first;          // requests to put in order of length (0: as they come)
+    int test_stall;             // testing: no K is copied
     const uint8_t* k_scales;    // NVFP4
     const uint8_t* v_scales;
     long long scale_page_stride;
@@ -524,6 +525,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
     if (warp == 0 || warp == 3) {
         // ------------------------------------------------------------ copies: K by warp 0, V by warp 3
         const bool is_v = warp == 3;
+        const int todo = p.test_stall && !is_v ? 0 : T;
         int issued = 0;
         const int shift = p.page_shift, per_tile = 64 >> shift;
         auto checked = [&](int k, int page) {
@@ -550,7 +552,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             next = fetch(32 * (batch + 1) + lane);
         };
         if constexpr (FP4) {
-            for (int t = 0; t < T; ++t) {
+            for (int t = 0; t < todo; ++t) {
                 const int slot = t % L::kRaw, k = t * per_tile;
                 if (t >= L::kRaw && !wait_warp(&aux->raw_empty[slot], ((t / L::kRaw) - 1) & 1, abort)) break;
                 turn(k);
@@ -588,7 +590,7 @@ masked_attn_kernel(const __grid_constant__ MaskedParams p, const __grid_constant
             const CUtensorMap* const map = is_v ? &tmv : &tmk;
             int slot = first, k = 0;
             uint32_t gone = 1;                             // parity of the phase that lets the slot go (none in the first lap)
-            for (int t = 0; t < T; ++t, k += per_tile) {
+            for (int t = 0; t < todo; ++t, k += per_tile) {
                 if (t >= end - first) {
                     if (NQ == 1 && !wait_warp(&aux->empty[slot], gone, abort)) break;
                     if (NQ == 2 && !(wait_warp(&aux->pv_done[0][slot], gone, abort) &&
@@ -1220,11 +1222,12 @@ struct MaskedVariant {
     MaskedKernel kernel;
     int threads, smem, ctas;   // ctas: on one SM
     int keys_k;                // keys of a copy of K (bf16)
+    int streams;               // key streams
 };
 template <int D, bool FP4, int NQ, bool DEEP>
 MaskedVariant variant_of() {
     using L = MaskedLayout<D, FP4, NQ, DEEP>;
-    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kEightK ? 8 : 16};
+    return {&masked_attn_kernel<D, FP4, NQ, DEEP>, L::kThreads, L::kSmem, L::kCtas, L::kEightK ? 8 : 16, L::kStreams};
 }
 MaskedVariant masked_variant(int d, bool fp4, int nq, bool deep) {
     if (fp4) return d == 64 ? variant_of<64, true, 1, true>() : d == 128 ? variant_of<128, true, 1, true>() : variant_of<256, true, 1, true>();
@@ -1297,6 +1300,8 @@ struct spec_attn_masked_plan {
     int tiles;
     int tiles_per_split;
     int max_splits;
+    int longest_first;
+    int test_stall;
     float sm_scale;
     size_t workspace_bytes;
     spec_attn::MaskedVariant variant;
@@ -1463,8 +1468,14 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
         delete plan;
         return SPEC_ATTN_E_UNSUPPORTED;
     }
-    plan->variant = spec_attn::masked_variant(
-        p.head_dim, fp4, plan->nq, static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs <= sms);
+    const int64_t ctas = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs;
+    plan->variant = spec_attn::masked_variant(p.head_dim, fp4, plan->nq, ctas <= sms);
+    // Longest first: where the CTAs come in rounds.  It takes a CTA 0.4 us and more and shortens the last round's tail, so not
+    // for many rounds of short CTAs (64 tokens over 1-3000 keys 78 -> 71 us, 250 over 50-900 keys 91 -> 102).
+    const int64_t at_once = static_cast<int64_t>(sms) * plan->variant.ctas;
+    plan->longest_first = p.num_reqs > 1 && p.num_reqs <= spec_attn::kMaxSorted && ctas > at_once && plan->tiles_per_split * at_once >= 8 * ctas
+                          ? p.num_reqs
+                          : 0;
     // partials: the pairs of every split, then their elements (a multiple of 256 bytes each)
     const size_t pairs = static_cast<size_t>(plan->max_splits) * p.total_q_rows * p.num_q_heads;
     plan->workspace_bytes = 256 + (plan->max_splits > spec_attn::kMaxCluster ? (pairs * 8 + 255) / 256 * 256 + pairs * p.head_dim * 2 : 0);
@@ -1475,6 +1486,32 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
 
 int spec_attn_masked_plan_destroy(spec_attn_masked_plan* plan) {
     delete plan;
+    return SPEC_ATTN_OK;
+}
+
+int spec_attn_masked_plan_get_info(const spec_attn_masked_plan* plan, spec_attn_masked_plan_info* info) {
+    if (!plan || !info) return SPEC_ATTN_E_INVALID_ARG;
+    *info = {};
+    info->query_tiles = plan->nq;
+    info->key_streams = plan->variant.streams;
+    info->ctas_per_sm = plan->variant.ctas;
+    info->tiles_per_split = plan->tiles_per_split;
+    info->max_splits = plan->max_splits;
+    info->join = plan->max_splits == 1 ? 0 : plan->max_splits <= spec_attn::kMaxCluster ? 1 : 2;
+    info->longest_first = plan->longest_first > 0;
+    info->grid_x = plan->tiles * plan->max_splits;
+    info->grid_y = plan->prob.num_kv_heads;
+    info->grid_z = plan->prob.num_reqs;
+    info->block_threads = plan->variant.threads;
+    info->smem_bytes = plan->variant.smem;
+    info->num_sms = plan->num_sms;
+    info->workspace_bytes = plan->workspace_bytes;
+    return SPEC_ATTN_OK;
+}
+
+int spec_attn_masked_plan_set_test_stall(spec_attn_masked_plan* plan, int stall) {
+    if (!plan || (stall != 0 && stall != 1)) return SPEC_ATTN_E_INVALID_ARG;
+    plan->test_stall = stall;
     return SPEC_ATTN_OK;
 }
 
@@ -1532,7 +1569,6 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     m.total_rows = p.total_q_rows;
     m.max_w = p.max_w;
     m.num_q_heads = p.num_q_heads;
-    m.num_kv_heads = p.num_kv_heads;
     m.group = p.num_q_heads / p.num_kv_heads;
     m.page_shift = p.page_size == 64 ? 6 : p.page_size == 32 ? 5 : 4;
     m.num_pages = p.num_pages;
@@ -1547,13 +1583,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     m.tiles_per_split = plan->tiles_per_split;
     m.max_splits = plan->max_splits;
     m.cluster = plan->max_splits > 1 && plan->max_splits <= kMaxCluster;
-    // Longest first: where the CTAs come in rounds.  It takes a CTA 0.4 us and more and shortens the last round's tail, so not
-    // for many rounds of short CTAs (64 tokens over 1-3000 keys 78 -> 71 us, 250 over 50-900 keys 91 -> 102).
-    const int64_t ctas = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs;
-    const int64_t at_once = static_cast<int64_t>(plan->num_sms) * plan->variant.ctas;
-    m.longest_first = p.num_reqs > 1 && p.num_reqs <= kMaxSorted && ctas > at_once && plan->tiles_per_split * at_once >= 8 * ctas
-                          ? p.num_reqs
-                          : 0;
+    m.longest_first = plan->longest_first;
+    m.test_stall = plan->test_stall;
     m.k_scales = static_cast<const uint8_t*>(k_scales);
     m.v_scales = static_cast<const uint8_t*>(v_scales);
     m.scale_page_stride = p.scale_page_stride;
