@@ -762,7 +762,8 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
  *   row_mask[row]: the node and its ancestors -- with window_left = n > 0 only those
  *   fewer than n levels above the node, or at a position below sink_keys --
  * in mask_row_words words a row (0: ceil(max_w / 32)), unused bits 0.  The rows from
- * q_indptr[P] on get position 0 and an empty mask.  ctx_r = seq_lens[r] - W_r.
+ * q_indptr[P] on get position 0 and an empty mask, unless the last window is below 0.
+ * ctx_r = seq_lens[r] - W_r.
  *
  * spec_attn_accept_tree walks each tree from node 0: the next node is the lowest
  * child whose draft token is the target token of its parent (the token that the

@@ -86,9 +86,10 @@ __global__ void build_tree_kernel(const TreeParams p) {
     pdl_wait_primary();
     pdl_launch_dependents();
     const int r = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
-    // rows of no request, shared by all CTAs
-    const int end = max(p.q_indptr[p.num_reqs], 0);
-    for (long long row = end + (long long)r * threads + tid; row < p.total_rows; row += (long long)gridDim.x * threads) {
+    // rows of no request, shared by all CTAs (none where the last window is below 0: they might be another request's)
+    const int last = p.num_reqs ? p.q_indptr[p.num_reqs - 1] : 0, end = p.q_indptr[p.num_reqs];
+    for (long long row = end < max(last, 0) ? p.total_rows : end + (long long)r * threads + tid; row < p.total_rows;
+         row += (long long)gridDim.x * threads) {
         p.positions[row] = 0;
         for (int k = 0; k < p.words; ++k) p.row_mask[row * p.words + k] = 0;
     }

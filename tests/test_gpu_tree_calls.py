@@ -1,4 +1,5 @@
-"""The accepted path written over the lengths, and the move behind it: the caller keeps the lengths of before."""
+"""Calls of the tree's operators that their documentation allows: the accepted path written over the lengths, and the move
+behind it, for which the caller keeps the lengths of before; a last request that cannot be."""
 import random
 
 import pytest
@@ -39,3 +40,24 @@ def test_lengths_written_in_place_and_a_kept_copy(kv):
     # the new lengths in their place lie before key 0 for a context shorter than what was not accepted: refused there
     c.move(table[2:].cuda(), seq[2:], indptr_of(rows[2:]), path[2:], taken[2:], ws, max_seq_len=96)
     assert sa.spec_attn_check_device_status(ws) == sa.SPEC_ATTN_DEV_BAD_SEQ_LEN
+
+
+@pytest.mark.parametrize("end", [5, -1])
+def test_a_last_window_below_zero_leaves_the_others_rows(end):
+    """The rows from q_indptr[P] on are other requests' then, of more CTAs than the GPU holds at once."""
+    P, w = 2000, 1024
+    i = torch.arange(w, **I32)
+    parents = torch.where(i > 0, 0, -1).int().repeat(P)                        # stars
+    ptr = torch.arange(P + 1, **I32) * w
+    ptr[P] = end
+    pos, mask, ws = torch.full((P * w,), 99, **I32), torch.full((P * w, 32), 99, **I32), workspace()
+    sa.spec_attn_build_tree(parents, torch.full((P,), w + 7, **I32), ptr, pos, mask, ws, max_w=w)
+    assert sa.spec_attn_check_device_status(ws) == sa.SPEC_ATTN_DEV_BAD_WINDOW
+    pos = pos.view(P, w)
+    assert bool((pos[:-1] == 7 + (i > 0)).all()) and bool((pos[-1] == 99).all())
+    mask = mask.view(P, w, 32)
+    want = torch.zeros(w, 32, dtype=torch.int64, device="cuda")
+    want[i.long(), i.long() // 32] = 1 << (i.long() % 32)
+    want[:, 0] |= 1
+    want = torch.where(want >= 2 ** 31, want - 2 ** 32, want).int()
+    assert bool((mask[:-1] == want).all()) and bool((mask[-1] == 99).all())
