@@ -726,7 +726,8 @@ int spec_attn_masked_plan_get_info(const spec_attn_masked_plan* plan, spec_attn_
 int spec_attn_masked_plan_set_test_stall(spec_attn_masked_plan* plan, int stall);
 
 /*
- * Arguments as spec_attn_run, the NVFP4 global scales positive and finite; row_mask
+ * Arguments as spec_attn_run, the NVFP4 global scales positive and finite, and so in
+ * fp32 sm_scale x log2(e) (x k_gscale); row_mask
  * for trees only (ignored for chains), positions [total_q_rows] int32 for trees with
  * a window only (ignored otherwise).  lse may be NULL.  o, lse and workspace share no
  * byte with an input or with each other (SPEC_ATTN_E_INVALID_ARG).  Up to 8 splits need

@@ -1532,6 +1532,9 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
         return SPEC_ATTN_E_INVALID_ARG;
     if (fp4 && (!(k_gscale > 0.f) || !(v_gscale > 0.f) || std::isinf(k_gscale) || std::isinf(v_gscale)))
         return SPEC_ATTN_E_INVALID_ARG;
+    // (the scale of the scores in base 2: as 0 or infinity it would make NaN of masked and of zero scores)
+    const float score_scale = plan->sm_scale * 1.4426950408889634f * (fp4 ? k_gscale : 1.f);
+    if (!(score_scale > 0.f) || std::isinf(score_scale)) return SPEC_ATTN_E_INVALID_ARG;
     for (const void* x : {q, k_pool, v_pool, static_cast<const void*>(o), fp4 ? k_scales : nullptr, fp4 ? v_scales : nullptr})
         if (!masked_aligned(x, 16)) return SPEC_ATTN_E_INVALID_ARG;
     for (const void* x : {static_cast<const void*>(block_table), static_cast<const void*>(seq_lens),
@@ -1589,7 +1592,7 @@ int spec_attn_run_masked(const spec_attn_masked_plan* plan, const void* q, const
     m.v_scales = static_cast<const uint8_t*>(v_scales);
     m.scale_page_stride = p.scale_page_stride;
     m.max_seq_len = p.max_seq_len;
-    m.score_scale_log2 = plan->sm_scale * 1.4426950408889634f * (fp4 ? k_gscale : 1.f);
+    m.score_scale_log2 = score_scale;
     m.out_scale = fp4 ? v_gscale : 1.f;
 
     CUtensorMap maps[3] = {};

@@ -1,9 +1,10 @@
-"""Calls of the attention under masks that its documentation allows: tables that end with the last request's last page."""
+"""Calls of the attention under masks at the edges of its documentation: tables that end with the last request's last page,
+scales whose product leaves the range of fp32."""
 import pytest
 import torch
 
 import speculative_decode_verify_paged_gb300 as sa
-from test_gpu_masked import Case, KV
+from test_gpu_masked import MARK, Case, KV
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,16 @@ def test_a_table_that_ends_with_the_last_page(kv, window, sinks, splits):
         used = (P - 1) * stride2 + -(-lens[-1] // 16)
         call(c, table.flatten()[:used].clone())
         c.check()
+
+
+@pytest.mark.parametrize("kv,sm_scale,k_gscale", [
+    ("nvfp4", 0.05, 2.0 ** -149), ("nvfp4", 2.0 ** -100, 2.0 ** -60), ("bf16", 2.0 ** 128 - 2.0 ** 104, 1.0),
+    ("nvfp4", 2.0 ** 100, 2.0 ** 60)])
+def test_scales_whose_product_is_zero_or_infinite_are_refused(kv, sm_scale, k_gscale):
+    c = Case([4], [100], 8, 2, 64, tree=True, kv=kv, sm_scale=sm_scale, seed=13)
+    c.gscale = (k_gscale, 1.0)
+    with pytest.raises(sa.SpecAttnError) as e:
+        c.run()
+    assert e.value.status == sa.SPEC_ATTN_E_INVALID_ARG
+    torch.cuda.synchronize()
+    assert bool((c.o == MARK).all())
