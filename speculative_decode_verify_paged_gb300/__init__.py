@@ -709,6 +709,14 @@ def spec_attn_masked_plan_create(*, num_reqs, total_q_rows, max_w, num_q_heads, 
                                     num_pages, block_table_stride, kv_dtype, float(sm_scale), int(tree), window_left,
                                     sink_keys, mask_row_words, force_splits, int(max_seq_len), int(kv_page_stride),
                                     int(scale_page_stride))
+    # (ctypes drops the bits that a field does not hold: a window of 2^32 would be none)
+    given = dict(num_reqs=num_reqs, total_q_rows=total_q_rows, max_w=max_w, num_q_heads=num_q_heads,
+                 num_kv_heads=num_kv_heads, head_dim=head_dim, page_size=page_size, num_pages=num_pages,
+                 block_table_stride=block_table_stride, kv_dtype=kv_dtype, tree=tree, window_left=window_left,
+                 sink_keys=sink_keys, mask_row_words=mask_row_words, force_splits=force_splits, max_seq_len=max_seq_len,
+                 kv_page_stride=kv_page_stride, scale_page_stride=scale_page_stride)
+    if any(getattr(prob, name) != int(value) for name, value in given.items()):
+        _check(SPEC_ATTN_E_UNSUPPORTED, "spec_attn_masked_plan_create")
     handle, ws = ctypes.c_void_p(), ctypes.c_size_t()
     _check(load_library().spec_attn_masked_plan_create(ctypes.byref(prob), ctypes.byref(handle), ctypes.byref(ws)),
            "spec_attn_masked_plan_create")

@@ -1,5 +1,5 @@
 """CPU-side checks of the masked plan's info and of its stall hook: the binding's struct has the header's layout, and what is
-no plan is refused."""
+no plan is refused; and numbers that the problem's fields do not hold."""
 import ctypes
 import os
 import subprocess
@@ -40,3 +40,14 @@ def test_null_arguments(lib):
     assert lib.spec_attn_masked_plan_get_info(None, None) == sa.SPEC_ATTN_E_INVALID_ARG
     for stall in (0, 1, 2):
         assert lib.spec_attn_masked_plan_set_test_stall(None, stall) == sa.SPEC_ATTN_E_INVALID_ARG
+
+
+@pytest.mark.parametrize("over", [dict(window_left=2 ** 32), dict(sink_keys=2 ** 32 + 4), dict(max_w=2 ** 32 + 1),
+                                  dict(tree=2 ** 32), dict(force_splits=-2 ** 32), dict(max_seq_len=2 ** 64 + 60),
+                                  dict(kv_page_stride=2 ** 64), dict(num_reqs=2 ** 32 + 1), dict(head_dim=2 ** 32 + 64)])
+def test_numbers_that_their_fields_do_not_hold_are_refused(lib, over):
+    prob = dict(num_reqs=1, total_q_rows=4, max_w=4, num_q_heads=8, num_kv_heads=2, head_dim=64, num_pages=4,
+                block_table_stride=4, max_seq_len=60)
+    with pytest.raises(sa.SpecAttnError) as e:
+        sa.spec_attn_masked_plan_create(**{**prob, **over})
+    assert e.value.status == sa.SPEC_ATTN_E_UNSUPPORTED
