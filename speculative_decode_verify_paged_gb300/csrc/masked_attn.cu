@@ -53,7 +53,8 @@
 // Bound, with times of a launch in a graph.  A tile of 64 keys takes 0.44 us at d 64,
 // 0.52 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.47, 0.53,
 // 0.80; a launch starts and ends in 5-8 us beside its tiles.  At d 256 bf16 the copies
-// bound it: 64 KB a tile at 43 bytes a clock into an SM (48 nodes over 64K keys 75 us).
+// bound it: 64 KB a tile at 43 bytes a clock into an SM (48 nodes over 64K keys 75 us; in
+// long loops of calls 79-81, the power limit).
 // At d 128 two query tiles keep the tensor cores busy for 1280 of 1490 clocks (a prompt
 // of 2049 rows under a window of 2048: 67 us, 1.7 rounds of CTAs taking 2).  NVFP4 is bound
 // by the chain scores, softmax, P V beside the decoders (4 trees of 32 nodes over 16384
@@ -89,7 +90,9 @@ constexpr int kM = 128;
 constexpr int kBN = 64;                 // keys a tile
 constexpr int kMaxRing = 14;
 constexpr int kMaxRaw = 8;
-constexpr int kMaxSorted = 256;         // requests put in order by one CTA's threads, a multiple of 32
+// requests put in order by one CTA's threads, a multiple of 32 (tokens over 100-12000 keys of d 256: 256 of them 238-241 us in
+// whatever order they come; 257 as they come 237 to 278)
+constexpr int kMaxSorted = 256;
 constexpr int kMaxCluster = 8;          // CTAs of a cluster that any GPU schedules
 constexpr int kJoinBatch = 16;          // splits whose rows a joining thread has on their way at once (8: 19 splits 15.5 us, not 13.4)
 constexpr float kRescale = 8.0f;        // log2 units: O is rescaled when a row's maximum grows by more
@@ -1336,9 +1339,10 @@ struct MaskedChoice {
 };
 
 // Key tiles a split takes with nq query tiles a CTA, of `units` at most (and `mean` of it over the CTAs: a prompt's rows see
-// half its own keys), and the call's time by a model (us, fitted to measurements): a CTA has a start and an end that grow
-// with its rows, and a time for each tile of 64 keys (longer beside another CTA with many rows); splits add their
-// combination, in the cluster or by a second kernel; the keys come from HBM at best at its rate.
+// half its own keys), and a figure (us) to rank the choices by: a CTA has a start and an end that grow with its rows, and a
+// time for each tile of 64 keys (longer beside another CTA with many rows); splits add their combination, in the cluster or by a
+// second kernel; the keys come from HBM at best at its rate.  Its parts were fitted to measurements; as a prediction it is up
+// to a third too high (64 tokens under a window of 4096 200 us, measured 152), in part since all lengths count as the longest.
 MaskedChoice choose_split(const spec_attn_masked_problem& p, int64_t units, double mean, int rows, int nq, int num_sms) {
     const bool fp4 = p.kv_dtype == SPEC_ATTN_KV_NVFP4;
     const spec_attn::MaskedVariant deep = spec_attn::masked_variant(p.head_dim, fp4, nq, true);
@@ -1471,11 +1475,13 @@ int spec_attn_masked_plan_create(const spec_attn_masked_problem* problem, spec_a
     const int64_t ctas = static_cast<int64_t>(plan->tiles) * plan->max_splits * p.num_kv_heads * p.num_reqs;
     plan->variant = spec_attn::masked_variant(p.head_dim, fp4, plan->nq, ctas <= sms);
     // Longest first: where the CTAs come in rounds.  It takes a CTA 0.4 us and more and shortens the last round's tail, so not
-    // for many rounds of short CTAs (64 tokens over 1-3000 keys 78 -> 71 us, 250 over 50-900 keys 91 -> 102).
+    // for many rounds of short CTAs (64 tokens over 1-3000 keys 78 -> 71 us, 250 over 50-900 keys 91 -> 102), and not beyond
+    // kMaxSorted requests.
     const int64_t at_once = static_cast<int64_t>(sms) * plan->variant.ctas;
-    plan->longest_first = p.num_reqs > 1 && p.num_reqs <= spec_attn::kMaxSorted && ctas > at_once && plan->tiles_per_split * at_once >= 8 * ctas
-                          ? p.num_reqs
-                          : 0;
+    plan->longest_first = p.num_reqs > 1 && p.num_reqs <= spec_attn::kMaxSorted && ctas > at_once &&
+                                  plan->tiles_per_split * at_once >= 8 * ctas
+                              ? p.num_reqs
+                              : 0;
     // partials: the pairs of every split, then their elements (a multiple of 256 bytes each)
     const size_t pairs = static_cast<size_t>(plan->max_splits) * p.total_q_rows * p.num_q_heads;
     plan->workspace_bytes = 256 + (plan->max_splits > spec_attn::kMaxCluster ? (pairs * 8 + 255) / 256 * 256 + pairs * p.head_dim * 2 : 0);
