@@ -47,8 +47,9 @@
 // Splits.  Up to 8 of them form a cluster: each leaves its normalised rows in fp32 with
 // their log-sum-exps in its own shared memory, and after a cluster barrier every CTA
 // combines a share of the rows from its peers' shared memory.  More leave their rows
-// in the workspace as fp16 of the row's largest element (off by at most 2^-12 of it, and of
-// 2^-126), and a second kernel joins them.  Both in an order that the split fixes.
+// in the workspace as fp16 of the row's largest element, or of 2^-126 if that is larger (off
+// by at most 2^-12 of it), and a second kernel joins them.  Both in an order that the split
+// fixes.
 //
 // Bound, with times of a launch in a graph.  A tile of 64 keys takes 0.44 us at d 64,
 // 0.52 at d 128 (two query tiles: 0.71 for both), 0.75-0.80 at d 256; NVFP4 0.47, 0.53,
